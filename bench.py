@@ -40,7 +40,8 @@ sys.path.insert(0, str(ROOT))
 HBM_PEAK_GBS = 8000.0  # MI355X HBM3E, vendor figure
 METRIC = "logits GB/s + tokens/s, fwd+bwd selected-token logp, V=151936; % HBM peak"
 KERNEL_SOURCE = ROOT / "vocab_selected_token_amd" / "csrc" / "rlk_kernels.hip"
-LMHEAD_SOURCE = ROOT / "vocab_selected_token_amd" / "csrc" / "rlk_lmhead.hip"
+LMHEAD_SOURCE = tuple(ROOT / "vocab_selected_token_amd" / "csrc" / name for name in
+                      ("rlk_lmhead.hip", "rlk_lmhead_segments.h", "rlk_tile.h"))
 TRAFFIC_FILE = ROOT / "profiles" / "traffic_large_32k.txt"
 LMHEAD_TRAFFIC_FILE = ROOT / "profiles" / "traffic_lmhead_4096.txt"
 
@@ -71,10 +72,11 @@ def algorithmic_bytes_one_pass(wl) -> int:
     return n * wl.real_vocab * 2 + n * wl.padded_vocab * out_b + 17 * n
 
 
-def kernel_source_sha(source: Path = KERNEL_SOURCE) -> str:
-    """Hash of a kernel source with comments and whitespace removed: it changes
-    exactly when the code the counters were taken on changes."""
-    text = source.read_text()
+def kernel_source_sha(source: Path | tuple[Path, ...] = KERNEL_SOURCE) -> str:
+    """Hash of a kernel source (or of several: a kernel and its headers) with comments
+    and whitespace removed: it changes exactly when the code the counters were taken on
+    changes."""
+    text = "\n".join(s.read_text() for s in ([source] if isinstance(source, Path) else source))
     text = re.sub(r"/\*.*?\*/", " ", text, flags=re.S)
     text = re.sub(r"//[^\n]*", " ", text)
     return hashlib.sha256(" ".join(text.split()).encode()).hexdigest()
@@ -107,7 +109,7 @@ def measured_ceilings():
 
 
 def read_traffic(kernel: str, workload: str, path: Path = TRAFFIC_FILE,
-                 source: Path = KERNEL_SOURCE):
+                 source: Path | tuple[Path, ...] = KERNEL_SOURCE):
     """HBM bytes per launch of `kernel` from a committed counter summary, or None
     when the summary is missing, was taken on another workload or on a different
     kernel source."""

@@ -348,6 +348,45 @@ rlk_status rlk_logp_fused_lmhead(const rlk_logp_desc* desc, const void* hidden,
                                  const uint8_t* active_mask, float* logp, float* lse,
                                  void* workspace, size_t workspace_bytes, void* stream);
 
+/* Gradients of the fused LM-head: from logp and LSE back to the hidden states
+ * and the weight, without keeping the logits.  With p_rj = exp(z_rj - LSE_r),
+ *   dz[r, j]  = a_r g_r ([j == target[r]] - p_rj) + gl_r p_rj      (j < V_real)
+ *   dhidden   = dz . weight          dweight = dz^T . hidden
+ * where g = grad_logp, gl = grad_lse and a_r is effective-active; the softmax
+ * cross entropy of a row is -logp_r.  z is computed again in pieces of the
+ * vocabulary (16384 columns, or more for few tokens) and each piece's dz, rounded
+ * to bf16, serves both products; the sums are fp32.  The pages have no such step;
+ * the contract is rlk_logp_bwd_ex's, taken back through the product.
+ *   desc, hidden, weight, hidden_dim, targets, active_mask   as for
+ *               rlk_logp_fused_lmhead, with num_tokens <= 2^21 and
+ *               padded_vocab * hidden_dim / 8 < 2^31.  A row that no term reaches
+ *               (not effective-active or g == 0, and gl == 0) takes no part: its
+ *               hidden state and LSE are not read, so they may hold anything.
+ *               The tiling is validated and changes nothing (tiles may be of any
+ *               width).
+ *   lse         (device) float [N]: the forward's LSE.
+ *   grad_logp, grad_lse  (device) float [N] each, or NULL for zero; at least one
+ *               must be given.
+ *   dhidden     (device) bf16 [N, hidden_dim], 16-byte aligned, out; +0 on rows
+ *               that no term reaches.  NULL: not wanted, and not computed.
+ *   dweight     (device) bf16 [padded_vocab, hidden_dim], 16-byte aligned, out;
+ *               +0 on rows >= real_vocab (and everywhere for N == 0).  NULL: not
+ *               wanted, and not computed.  At least one of the two must be given.
+ *   workspace   >= rlk_logp_fused_lmhead_bwd_workspace_bytes(desc, hidden_dim,
+ *               dhidden != NULL, dweight != NULL), 256-byte aligned; calls that
+ *               share one must not overlap.
+ * Repeated calls give the same bits.  A row with a bad target gives NaN to its row
+ * of dhidden and to all real rows of dweight (RLK_ERR_TARGET_RANGE under
+ * RLK_FLAG_VALIDATE), and so does one whose LSE is not finite. */
+size_t rlk_logp_fused_lmhead_bwd_workspace_bytes(const rlk_logp_desc* desc, int64_t hidden_dim,
+                                                 int32_t want_dhidden, int32_t want_dweight);
+rlk_status rlk_logp_fused_lmhead_bwd(const rlk_logp_desc* desc, const void* hidden,
+                                     const void* weight, int64_t hidden_dim,
+                                     const int32_t* targets, const uint8_t* active_mask,
+                                     const float* lse, const float* grad_logp,
+                                     const float* grad_lse, void* dhidden, void* dweight,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
 /* Host-only geometry (no device access): writes T+1 tile bounds
  * floor(t*V_pad/T) to `bounds` and S+1 shard starts floor(s*T/S) to
  * `shard_first_tile` (either may be NULL).  Same limits as the descriptor. */

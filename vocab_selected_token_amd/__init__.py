@@ -39,6 +39,7 @@ EXPORTED = ("rlk_logp_workspace_bytes", "rlk_logp_fwd", "rlk_logp_bwd",
             "rlk_logp_fwd_bwd_workspace_bytes", "rlk_logp_fwd_bwd",
             "rlk_logp_fwd_bwd_ex_workspace_bytes", "rlk_logp_fwd_bwd_ex",
             "rlk_logp_fused_lmhead_workspace_bytes", "rlk_logp_fused_lmhead",
+            "rlk_logp_fused_lmhead_bwd_workspace_bytes", "rlk_logp_fused_lmhead_bwd",
             "rlk_logp_tile_geometry", "rlk_status_string", "rlk_last_error_detail",
             "rlk_logp_fwd_noalloc")
 
@@ -93,6 +94,11 @@ def _load() -> ctypes.CDLL:
     lib.rlk_logp_fused_lmhead_workspace_bytes.restype = sz
     lib.rlk_logp_fused_lmhead.argtypes = [dp, vp, vp, i64, vp, vp, vp, vp, vp, sz, vp]
     lib.rlk_logp_fused_lmhead.restype = ctypes.c_int
+    lib.rlk_logp_fused_lmhead_bwd_workspace_bytes.argtypes = [dp, i64, i32, i32]
+    lib.rlk_logp_fused_lmhead_bwd_workspace_bytes.restype = sz
+    lib.rlk_logp_fused_lmhead_bwd.argtypes = [dp, vp, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, sz,
+                                              vp]
+    lib.rlk_logp_fused_lmhead_bwd.restype = ctypes.c_int
     lib.rlk_logp_tile_geometry.argtypes = [i64, i32, i32, vp, vp]
     lib.rlk_logp_tile_geometry.restype = ctypes.c_int
     lib.rlk_status_string.argtypes = [ctypes.c_int]
@@ -219,6 +225,24 @@ def rlk_logp_fused_lmhead(desc, hidden, weight, hidden_dim: int, targets, active
     _check(_lib.rlk_logp_fused_lmhead(ctypes.byref(desc), _ptr(hidden), _ptr(weight), hidden_dim,
                                       _ptr(targets), _ptr(active_mask), _ptr(logp), _ptr(lse),
                                       _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def rlk_logp_fused_lmhead_bwd_workspace_bytes(desc: rlk_logp_desc, hidden_dim: int,
+                                              want_dhidden: bool, want_dweight: bool) -> int:
+    return int(_lib.rlk_logp_fused_lmhead_bwd_workspace_bytes(ctypes.byref(desc), hidden_dim,
+                                                              int(want_dhidden),
+                                                              int(want_dweight)))
+
+
+def rlk_logp_fused_lmhead_bwd(desc, hidden, weight, hidden_dim: int, targets, active_mask, lse,
+                              grad_logp, grad_lse, dhidden, dweight, workspace,
+                              stream=None) -> None:
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.rlk_logp_fused_lmhead_bwd(ctypes.byref(desc), _ptr(hidden), _ptr(weight),
+                                          hidden_dim, _ptr(targets), _ptr(active_mask), _ptr(lse),
+                                          _ptr(grad_logp), _ptr(grad_lse), _ptr(dhidden),
+                                          _ptr(dweight), _ptr(workspace), ws_bytes,
+                                          _stream(stream)))
 
 
 def rlk_logp_tile_geometry(padded_vocab: int, num_vocab_tiles: int, num_virtual_shards: int = 1):
@@ -543,13 +567,9 @@ def forward_backward_ex(logits: torch.Tensor, targets: torch.Tensor, active_mask
     return logp, lse, ent, dl[:, :v_pad]
 
 
-def fused_lmhead(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
-                 active_mask=None, *, real_vocab: int, padded_vocab: int | None = None,
-                 num_vocab_tiles: int = 64, num_virtual_shards: int = 1,
-                 ignore_index: int = -100, validate: bool = False,
-                 workspace: torch.Tensor | None = None, stream=None):
-    """(logp, lse) of z = hidden . weight^T without materialising z.
-    hidden: bf16 [N, K] contiguous; weight: bf16 [V_pad, K] contiguous."""
+def _check_lmhead(hidden, weight, targets, active_mask, real_vocab, **vectors):
+    """hidden bf16 [N, K], weight bf16 [>= real_vocab, K], both contiguous; targets, mask and
+    vectors as in _check_inputs.  All on the hidden states' GPU."""
     for name, t in (("hidden", hidden), ("weight", weight)):
         _check_logits(t, name)
         if not t.is_contiguous():
@@ -563,7 +583,19 @@ def fused_lmhead(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tens
     if targets is None:
         raise TypeError("targets must be a torch.Tensor")
     _check_rows("active_mask", active_mask, n, _MASK)
-    _check_device(hidden, weight=weight, targets=targets, active_mask=active_mask)
+    for name, t in vectors.items():
+        _check_rows(name, t, n, _F32)
+    _check_device(hidden, weight=weight, targets=targets, active_mask=active_mask, **vectors)
+
+
+def fused_lmhead(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
+                 active_mask=None, *, real_vocab: int, padded_vocab: int | None = None,
+                 num_vocab_tiles: int = 64, num_virtual_shards: int = 1,
+                 ignore_index: int = -100, validate: bool = False,
+                 workspace: torch.Tensor | None = None, stream=None):
+    """(logp, lse) of z = hidden . weight^T without materialising z.
+    hidden: bf16 [N, K] contiguous; weight: bf16 [V_pad, K] contiguous."""
+    _check_lmhead(hidden, weight, targets, active_mask, real_vocab)
     n, k = hidden.shape
     v_pad = padded_vocab or weight.shape[0]
     desc = make_desc(n, real_vocab, v_pad, v_pad, num_vocab_tiles, num_virtual_shards,
@@ -578,3 +610,83 @@ def fused_lmhead(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tens
     rlk_logp_fused_lmhead(desc, hidden, weight, k, targets, _u8_mask(active_mask), logp, lse,
                           workspace, stream)
     return logp, lse
+
+
+def fused_lmhead_backward(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
+                          active_mask, lse: torch.Tensor, grad_logp=None, grad_lse=None, *,
+                          real_vocab: int, want_hidden: bool = True, want_weight: bool = True,
+                          ignore_index: int = -100, validate: bool = False,
+                          workspace: torch.Tensor | None = None, stream=None):
+    """(dhidden, dweight) in bf16, with the shapes of hidden and weight, of a loss on
+    fused_lmhead's logp and LSE; absent gradients are zero.  The one that is not wanted
+    is not computed and comes back as None."""
+    if lse is None:
+        raise TypeError("lse must be a torch.Tensor")
+    if grad_logp is None and grad_lse is None:
+        raise TypeError("at least one of grad_logp and grad_lse must be a torch.Tensor")
+    if not (want_hidden or want_weight):
+        raise ValueError("at least one of want_hidden and want_weight must be true")
+    _check_lmhead(hidden, weight, targets, active_mask, real_vocab, lse=lse, grad_logp=grad_logp,
+                  grad_lse=grad_lse)
+    n, k = hidden.shape
+    rows = weight.shape[0]
+    desc = make_desc(n, real_vocab, rows, rows, 1, 1, ignore_index, validate)
+    dh = torch.empty_like(hidden) if want_hidden else None
+    dw = torch.empty_like(weight) if want_weight else None
+    if workspace is None:
+        nbytes = rlk_logp_fused_lmhead_bwd_workspace_bytes(desc, k, want_hidden, want_weight)
+        if nbytes == 0:
+            raise ValueError(f"invalid rlk_logp_desc: {rlk_last_error_detail()}")
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=hidden.device)
+    rlk_logp_fused_lmhead_bwd(desc, hidden, weight, k, targets, _u8_mask(active_mask), lse,
+                              grad_logp, grad_lse, dh, dw, workspace, stream)
+    return dh, dw
+
+
+class _LmheadSelectedTokenLogprob(torch.autograd.Function):
+    """(logp, lse) of bf16 hidden states and weight, differentiable in both; the forward
+    and the backward are rlk_logp_fused_lmhead and rlk_logp_fused_lmhead_bwd."""
+
+    @staticmethod
+    def forward(ctx, hidden, weight, targets, active_mask, real_vocab, padded_vocab,
+                num_vocab_tiles, ignore_index):
+        logp, lse = fused_lmhead(hidden, weight, targets, active_mask, real_vocab=real_vocab,
+                                 padded_vocab=padded_vocab, num_vocab_tiles=num_vocab_tiles,
+                                 ignore_index=ignore_index)
+        ctx.save_for_backward(hidden, weight, targets, active_mask, lse)
+        ctx.cfg = (real_vocab, ignore_index)
+        ctx.set_materialize_grads(False)
+        return logp, lse
+
+    @staticmethod
+    def backward(ctx, g_logp, g_lse):
+        hidden, weight, targets, active_mask, lse = ctx.saved_tensors
+        real_vocab, ignore_index = ctx.cfg
+
+        def vec(t):
+            return None if t is None else t.contiguous().float()
+        g_logp, g_lse = vec(g_logp), vec(g_lse)
+        want_hidden, want_weight = ctx.needs_input_grad[:2]
+        if (g_logp is None and g_lse is None) or not (want_hidden or want_weight):
+            return (None,) * 8
+        dh, dw = fused_lmhead_backward(hidden, weight, targets, active_mask, lse, g_logp, g_lse,
+                                       real_vocab=real_vocab, want_hidden=want_hidden,
+                                       want_weight=want_weight, ignore_index=ignore_index)
+        return dh, dw, None, None, None, None, None, None
+
+
+def lmhead_selected_token_logprob(hidden: torch.Tensor, weight: torch.Tensor,
+                                  targets: torch.Tensor, active_mask=None, *, real_vocab: int,
+                                  padded_vocab: int | None = None, num_vocab_tiles: int = 64,
+                                  ignore_index: int = -100):
+    """fused_lmhead as a differentiable torch function: returns (logp, lse), fp32 [N].
+
+    The logits z = hidden . weight^T are never kept: the backward takes them again in
+    pieces of the vocabulary.  The softmax cross entropy of a token is -logp; a loss
+    on logp and LSE hands its gradients to rlk_logp_fused_lmhead_bwd, which computes
+    only the gradients that autograd asks for.  hidden: bf16 [N, K] contiguous;
+    weight: bf16 [V_pad, K] contiguous; their gradients are bf16.
+    """
+    _check_lmhead(hidden, weight, targets, active_mask, real_vocab)
+    return _LmheadSelectedTokenLogprob.apply(hidden, weight, targets, active_mask, real_vocab,
+                                             padded_vocab, num_vocab_tiles, ignore_index)

@@ -598,7 +598,9 @@ rlk_status rlk_logp_fwd_bwd_ex(const rlk_logp_desc* desc, const void* logits,
 // ---------------------------------------------------------------------------
 namespace {
 
-rlk_status check_fused_desc(const rlk_logp_desc* d) {
+// min_tile: least columns a tile may have (the forward's blocks hold at most one
+// tile bound; the gradients have no tiles).
+rlk_status check_fused_desc(const rlk_logp_desc* d, int32_t min_tile = rlk::kLmheadBlockVocab) {
   if (!d) return fail(RLK_ERR_NULL_POINTER, "desc is NULL");
   if (d->num_tokens < 0 || d->num_tokens > kI32Max)
     return fail(RLK_ERR_BAD_SHAPE, "num_tokens=%lld outside [0, 2^31-1]",
@@ -609,11 +611,11 @@ rlk_status check_fused_desc(const rlk_logp_desc* d) {
   if (d->num_vocab_tiles < 1 || (int64_t)d->num_vocab_tiles > d->padded_vocab)
     return fail(RLK_ERR_BAD_TILING, "num_vocab_tiles=%d outside [1, padded_vocab]",
                 d->num_vocab_tiles);
-  if (d->padded_vocab / d->num_vocab_tiles < rlk::kLmheadBlockVocab)
+  if (d->padded_vocab / d->num_vocab_tiles < min_tile)
     return fail(RLK_ERR_BAD_TILING,
                 "fused LM-head needs tiles of at least %d columns (padded_vocab / "
                 "num_vocab_tiles = %lld)",
-                rlk::kLmheadBlockVocab, (long long)(d->padded_vocab / d->num_vocab_tiles));
+                min_tile, (long long)(d->padded_vocab / d->num_vocab_tiles));
   if (d->num_virtual_shards < 1 || d->num_virtual_shards > d->num_vocab_tiles)
     return fail(RLK_ERR_BAD_TILING, "num_virtual_shards=%d outside [1, num_vocab_tiles=%d]",
                 d->num_virtual_shards, d->num_vocab_tiles);
@@ -727,6 +729,109 @@ rlk_status rlk_logp_fused_lmhead(const rlk_logp_desc* desc, const void* hidden,
   e = rlk::launch_stage2(a2, stream);
   if (e != hipSuccess) return hip_fail(e, "stage2_merge launch");
   if (validate) return finish_validate(status, stream, true);
+  return ok();
+}
+
+// ---------------------------------------------------------------------------
+// Gradients of the fused LM-head.
+// ---------------------------------------------------------------------------
+namespace {
+
+rlk_status check_hidden_dim(int64_t hidden_dim, int32_t multiple) {
+  if (hidden_dim < multiple || hidden_dim % multiple != 0 || hidden_dim > rlk::kLmheadMaxHidden)
+    return fail(RLK_ERR_BAD_SHAPE, "hidden_dim=%lld must be a positive multiple of %d, at most %lld",
+                (long long)hidden_dim, multiple, (long long)rlk::kLmheadMaxHidden);
+  return RLK_OK;
+}
+
+rlk_status check_lmhead_bwd(const rlk_logp_desc* desc, int64_t hidden_dim) {
+  rlk_status st = check_fused_desc(desc, 1);
+  if (st != RLK_OK) return st;
+  st = check_hidden_dim(hidden_dim, rlk::kLmheadSlabK);
+  if (st != RLK_OK) return st;
+  if (desc->num_tokens > rlk::kLmheadBwdMaxTokens)
+    return fail(RLK_ERR_BAD_SHAPE, "num_tokens=%lld exceeds %lld", (long long)desc->num_tokens,
+                (long long)rlk::kLmheadBwdMaxTokens);
+  if (desc->padded_vocab * (hidden_dim / 8) > kI32Max ||
+      desc->num_tokens * (hidden_dim / 8) > kI32Max)
+    return fail(RLK_ERR_BAD_SHAPE, "hidden or weight holds 2^31 or more 16-byte chunks");
+  return RLK_OK;
+}
+
+}  // namespace
+
+size_t rlk_logp_fused_lmhead_bwd_workspace_bytes(const rlk_logp_desc* desc, int64_t hidden_dim,
+                                                 int32_t want_dhidden, int32_t want_dweight) {
+  if (check_lmhead_bwd(desc, hidden_dim) != RLK_OK) return 0;
+  return rlk::lmhead_bwd_layout(desc->num_tokens, hidden_dim, desc->padded_vocab,
+                                want_dhidden != 0, want_dweight != 0)
+      .total;
+}
+
+rlk_status rlk_logp_fused_lmhead_bwd(const rlk_logp_desc* desc, const void* hidden,
+                                     const void* weight, int64_t hidden_dim,
+                                     const int32_t* targets, const uint8_t* active_mask,
+                                     const float* lse, const float* grad_logp,
+                                     const float* grad_lse, void* dhidden, void* dweight,
+                                     void* workspace, size_t workspace_bytes, void* stream_ptr) {
+  rlk_status st = check_lmhead_bwd(desc, hidden_dim);
+  if (st != RLK_OK) return st;
+  if (!dhidden && !dweight)
+    return fail(RLK_ERR_NULL_POINTER, "at least one of dhidden and dweight must be non-NULL");
+  hipStream_t stream = reinterpret_cast<hipStream_t>(stream_ptr);
+  const int64_t n = desc->num_tokens;
+  hipError_t e;
+  if (n == 0) {  // no token: dweight is zero
+    if (!dweight) return ok();
+    if (!aligned(dweight, 16)) return fail(RLK_ERR_ALIGNMENT, "dweight must be 16-byte aligned");
+    e = rlk::launch_fill_zero(dweight, desc->padded_vocab * hidden_dim * 2, stream);
+    if (e != hipSuccess) return hip_fail(e, "fill_zero launch");
+    return ok();
+  }
+  if (!hidden || !weight || !targets || !lse)
+    return fail(RLK_ERR_NULL_POINTER, "hidden, weight, targets and lse must be non-NULL");
+  if (!grad_logp && !grad_lse)
+    return fail(RLK_ERR_NULL_POINTER, "at least one of grad_logp and grad_lse must be non-NULL");
+  const rlk::LmheadBwdLayout lay = rlk::lmhead_bwd_layout(n, hidden_dim, desc->padded_vocab,
+                                                          dhidden != nullptr, dweight != nullptr);
+  if (!workspace) return fail(RLK_ERR_WORKSPACE, "workspace is NULL");
+  if (workspace_bytes < lay.total)
+    return fail(RLK_ERR_WORKSPACE, "workspace_bytes=%zu < required %zu", workspace_bytes,
+                lay.total);
+  if (!aligned(hidden, 16) || !aligned(weight, 16) || !aligned(dhidden, 16) ||
+      !aligned(dweight, 16))
+    return fail(RLK_ERR_ALIGNMENT, "hidden, weight, dhidden and dweight must be 16-byte aligned");
+  if (!aligned(workspace, 256)) return fail(RLK_ERR_ALIGNMENT, "workspace not 256-byte aligned");
+  if (!aligned(targets, 4) || !aligned(lse, 4) || !aligned(grad_logp, 4) || !aligned(grad_lse, 4))
+    return fail(RLK_ERR_ALIGNMENT, "targets, lse and the gradients must be 4-byte aligned");
+
+  uint32_t* status = reinterpret_cast<uint32_t*>(workspace);
+  const bool validate = (desc->flags & RLK_FLAG_VALIDATE) != 0;
+  if (validate) {
+    e = rlk::launch_clear_status(status, stream);
+    if (e != hipSuccess) return hip_fail(e, "clear_status launch");
+  }
+  rlk::LmheadBwdArgs a;
+  a.hidden = hidden;
+  a.weight = weight;
+  a.hidden_dim = (int32_t)hidden_dim;
+  a.num_tokens = (int32_t)n;
+  a.real_vocab = (int32_t)desc->real_vocab;
+  a.padded_vocab = (int32_t)desc->padded_vocab;
+  a.targets = targets;
+  a.mask = active_mask;
+  a.ignore_index = desc->ignore_index;
+  a.lse = lse;
+  a.grad = grad_logp;
+  a.grad_lse = grad_lse;
+  a.dhidden = dhidden;
+  a.dweight = dweight;
+  a.workspace = static_cast<char*>(workspace);
+  a.layout = lay;
+  a.status = status;
+  e = rlk::launch_lmhead_bwd(a, stream);
+  if (e != hipSuccess) return hip_fail(e, "lmhead_bwd launch");
+  if (validate) return finish_validate(status, stream, false);
   return ok();
 }
 

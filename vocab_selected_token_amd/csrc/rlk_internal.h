@@ -133,6 +133,41 @@ struct LmheadArgs {
   float* psum;
 };
 
+// Gradients of the fused LM-head.  Byte offsets into its workspace (the status
+// words come first): what is known of the live rows, their hidden states by
+// tokens and by columns, a piece of dz by tokens and by columns, the piece of W
+// by columns and the fp32 partials of dh.
+struct LmheadBwdLayout {
+  int32_t padded_tokens;  // num_tokens rounded up to 256
+  int32_t piece;          // vocabulary columns at a time (a multiple of 256)
+  int32_t splits;         // dh: parts a piece's columns are summed in
+  size_t head, idx, tgt, lse, cg, cc, resid, inv;
+  size_t hc, ht, dzn, dzt, wt, part, total;
+};
+
+// hc and dzn rows of padded_tokens elements must span under 2^31 bytes by 256.
+constexpr int64_t kLmheadBwdMaxTokens = int64_t{1} << 21;
+
+struct LmheadBwdArgs {
+  const void* hidden;  // bf16 [num_tokens, hidden_dim]
+  const void* weight;  // bf16 [>= real_vocab, hidden_dim]
+  int32_t hidden_dim;
+  int32_t num_tokens;
+  int32_t real_vocab;
+  int32_t padded_vocab;
+  const int32_t* targets;
+  const uint8_t* mask;  // may be null
+  int32_t ignore_index;
+  const float* lse;
+  const float* grad;      // null = zero
+  const float* grad_lse;  // null = zero
+  void* dhidden;          // bf16 [num_tokens, hidden_dim], or null: not wanted
+  void* dweight;          // bf16 [padded_vocab, hidden_dim], or null: not wanted
+  char* workspace;
+  LmheadBwdLayout layout;
+  uint32_t* status;
+};
+
 // Most threads one launch may have.  A dispatch holds its grid size in 32 bits
 // of threads: at 2^32 the launch fails, and above it the size wraps around and
 // the kernel silently runs on a fraction of the grid.  Every launcher splits
@@ -151,6 +186,10 @@ hipError_t noalloc_scratch(void** ptr);
 int64_t stage1_blocks(int64_t items);
 int64_t lmhead_grid_blocks(int32_t num_tokens, int32_t real_vocab);
 hipError_t launch_lmhead(const LmheadArgs& a, hipStream_t stream);
+LmheadBwdLayout lmhead_bwd_layout(int64_t num_tokens, int64_t hidden_dim, int64_t padded_vocab,
+                                  bool want_dhidden, bool want_dweight);
+hipError_t launch_lmhead_bwd(const LmheadBwdArgs& a, hipStream_t stream);
+hipError_t launch_fill_zero(void* out, int64_t bytes, hipStream_t stream);  // bytes % 16 == 0
 int64_t bwd_col_blocks(int32_t padded_vocab);
 hipError_t launch_stage1(const Stage1Args& a, hipStream_t stream);
 hipError_t launch_stage2(const Stage2Args& a, hipStream_t stream);

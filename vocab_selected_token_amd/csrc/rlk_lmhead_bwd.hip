@@ -1,0 +1,606 @@
+// rlk_lmhead_bwd.hip -- gradients of the fused LM-head for gfx950: from logp and
+// LSE of z = h . W^T back to h and W, without keeping the logits.
+//
+// With p = exp(z - LSE), g and gl the upstream gradients of logp and LSE and a
+// the effective-active flag of a row,
+//   dz = a g (onehot(target) - p) + gl p,   dh = dz . W,   dW = dz^T . h.
+// z is computed again, a piece of the vocabulary at a time, and each piece's dz
+// is used for both products while it is at hand.
+//
+// Only rows that some term reaches ("live": effective-active with g != 0, or gl
+// != 0) take part.  They are gathered to the front first, in ascending order, so
+// that prompt and padding tokens cost nothing in the three products and a NaN in
+// a hidden state that is masked out meets no product (0 * NaN would be NaN).
+//
+// dz is rounded to bf16 for the matrix cores: half a step, 2^-9 relative, once
+// per element, as much as rounding the results to bf16 does.  Two things keep
+// that rounding from adding up.  All rows are divided by the largest |g|, |gl|
+// before it (and the results multiplied by it), so that the equal gradients of a
+// mean become +-1 and a target's entry near 1 - p rounds without a bias that
+// every row shares; and for dh what the rounding took from the target's entry,
+// which dominates its row, is added back in fp32 (dh_finish).
+//
+// Sums over K, over the vocabulary and over tokens are held in fp32, in a fixed
+// order: repeated calls give the same bits.  No atomics.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "rlk_internal.h"
+#include "rlk_tile.h"
+
+namespace rlk {
+namespace {
+
+static_assert(kBK == kLmheadSlabK, "slab width shared with the boundary");
+
+constexpr int kT = 64;  // tile edge of the gather and transpose kernels
+constexpr int kScanThreads = 1024;
+
+__device__ __forceinline__ uint16_t bf16_bits(float x) {
+  const __bf16 b = (__bf16)x;  // to nearest even
+  return __builtin_bit_cast(uint16_t, b);
+}
+__device__ __forceinline__ float bf16_float(uint16_t b) {
+  return __uint_as_float((uint32_t)b << 16);
+}
+
+// What the kernels know of one live row, normalised by the call's scale.
+struct LiveRows {
+  int32_t* idx;    // its row in the batch
+  int32_t* tgt;    // its target column, or -1 (not active)
+  float* lse;
+  float* cg;       // a g / scale: added at the target
+  float* cc;       // (gl - a g) / scale: times p
+  float* resid;    // the target entry of dz less its bf16 rounding
+  int32_t* inv;    // [num_tokens] batch row -> live row, or -1
+  uint32_t* head;  // [0] number of live rows, [1] the scale's bits
+};
+
+__device__ __forceinline__ LiveRows live_rows(char* ws, const LmheadBwdLayout& l) {
+  return {reinterpret_cast<int32_t*>(ws + l.idx),   reinterpret_cast<int32_t*>(ws + l.tgt),
+          reinterpret_cast<float*>(ws + l.lse),     reinterpret_cast<float*>(ws + l.cg),
+          reinterpret_cast<float*>(ws + l.cc),      reinterpret_cast<float*>(ws + l.resid),
+          reinterpret_cast<int32_t*>(ws + l.inv),   reinterpret_cast<uint32_t*>(ws + l.head)};
+}
+
+// ---------------------------------------------------------------------------
+// live_rows_scan: one block.  The scale (largest finite |a g|, |gl|; 1 if all are
+// 0), then the live rows in ascending order.  Slots from the last live row up to
+// a multiple of 256 hold rows that give dz = 0.  An effective-active row with a
+// target outside [0, V_real) is live with NaN factors: its dz is NaN.
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(kScanThreads) void live_rows_scan(
+    int32_t num_tokens, int32_t padded_tokens, int32_t real_vocab,
+    const int32_t* __restrict__ targets, const uint8_t* __restrict__ mask, int32_t ignore_index,
+    const float* __restrict__ lse, const float* __restrict__ grad,
+    const float* __restrict__ grad_lse, char* ws, LmheadBwdLayout lay,
+    uint32_t* __restrict__ status) {
+  __shared__ float wmax[kScanThreads / 64];
+  __shared__ int32_t wsum[kScanThreads / 64];
+  const LiveRows live = live_rows(ws, lay);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+
+  auto row = [&](int32_t r, float& g, float& gl, int32_t& tgt, bool& act, bool& bad) {
+    act = (mask == nullptr || mask[r] != 0);
+    tgt = act ? targets[r] : -1;
+    act = act && tgt != ignore_index;
+    bad = act && (tgt < 0 || tgt >= real_vocab);
+    g = (act && grad) ? grad[r] : 0.0f;
+    gl = grad_lse ? grad_lse[r] : 0.0f;
+  };
+
+  float top = 0.0f;
+  for (int32_t r = tid; r < num_tokens; r += kScanThreads) {
+    float g, gl;
+    int32_t tgt;
+    bool act, bad;
+    row(r, g, gl, tgt, act, bad);
+    const float m = fmaxf(isfinite(g) ? fabsf(g) : 0.0f, isfinite(gl) ? fabsf(gl) : 0.0f);
+    top = fmaxf(top, m);
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+  if (lane == 0) wmax[wave] = top;
+  __syncthreads();
+  for (int w = 0; w < kScanThreads / 64; ++w) top = fmaxf(top, wmax[w]);
+  const float scale = top > 0.0f ? top : 1.0f;
+
+  int32_t base = 0;
+  for (int32_t r0 = 0; r0 < num_tokens; r0 += kScanThreads) {
+    const int32_t r = r0 + tid;
+    float g = 0.0f, gl = 0.0f;
+    int32_t tgt = -1;
+    bool act = false, bad = false;
+    if (r < num_tokens) row(r, g, gl, tgt, act, bad);
+    const bool on = bad || g != 0.0f || gl != 0.0f;
+    const uint64_t votes = __ballot(on);
+    const int32_t before = __popcll(votes & ((1ull << lane) - 1));
+    __syncthreads();  // the previous round's sums have been read
+    if (lane == 0) wsum[wave] = __popcll(votes);
+    __syncthreads();
+    int32_t at = base + before;
+    for (int w = 0; w < kScanThreads / 64; ++w) {
+      if (w < wave) at += wsum[w];
+      base += wsum[w];
+    }
+    if (on) {
+      const float nan = __builtin_nanf("");
+      live.idx[at] = r;
+      live.tgt[at] = (act && !bad) ? tgt : -1;
+      live.lse[at] = lse[r];
+      live.cg[at] = bad ? nan : g / scale;
+      live.cc[at] = bad ? nan : gl / scale - g / scale;
+      live.resid[at] = 0.0f;
+      if (bad) status[0] = 1u;
+    }
+    if (r < num_tokens) live.inv[r] = on ? at : -1;
+  }
+  const int32_t end = min((base + 255) / 256 * 256, padded_tokens);
+  for (int32_t i = base + tid; i < end; i += kScanThreads) {
+    live.idx[i] = -1;
+    live.tgt[i] = -1;
+    live.lse[i] = 0.0f;
+    live.cg[i] = 0.0f;
+    live.cc[i] = 0.0f;
+    live.resid[i] = 0.0f;
+  }
+  if (tid == 0) {
+    live.head[0] = (uint32_t)base;
+    live.head[1] = __float_as_uint(scale);
+  }
+}
+
+// A 64 x 64 bf16 tile read by rows (row r of the source at src[r], or zeros) and
+// written by columns: dst[c][r] = src[r][c].  256 threads; rows of 72 elements
+// in LDS keep both directions at most 2-way conflicting.
+struct Tile64 {
+  uint16_t v[kT][kT + 8];
+};
+
+// ---------------------------------------------------------------------------
+// gather_rows: hc[i] = h[idx[i]] (zeros in the slots behind the last live row)
+// and, when asked for, its transpose ht[k][i].
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(256) void gather_rows(const u32x4* __restrict__ h, int32_t ldc,
+                                                   u32x4* __restrict__ hc, uint16_t* ht,
+                                                   int32_t padded_tokens, int32_t k_tiles,
+                                                   char* ws, LmheadBwdLayout lay,
+                                                   int64_t blk_begin) {
+  __shared__ Tile64 t;
+  const LiveRows live = live_rows(ws, lay);
+  const int64_t blk = blk_begin + blockIdx.x;
+  const int32_t i0 = (int32_t)(blk / k_tiles) * kT;
+  const int32_t kc0 = (int32_t)(blk % k_tiles) * (kT / 8);
+  const int32_t end = (int32_t)(live.head[0] + 255) / 256 * 256;
+  if (i0 >= end) return;
+  for (int q = threadIdx.x; q < kT * kT / 8; q += 256) {
+    const int r = q >> 3, c = q & 7;
+    const int32_t from = live.idx[i0 + r];
+    u32x4 x = {0, 0, 0, 0};
+    if (from >= 0) x = h[(int64_t)from * ldc + kc0 + c];
+    hc[(int64_t)(i0 + r) * ldc + kc0 + c] = x;
+    if (ht) *reinterpret_cast<u32x4*>(&t.v[r][c * 8]) = x;
+  }
+  if (!ht) return;
+  __syncthreads();
+  for (int q = threadIdx.x; q < kT * kT / 8; q += 256) {
+    const int c = q >> 3, r = (q & 7) * 8;
+    union {
+      uint16_t e[8];
+      u32x4 x;
+    } o;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o.e[i] = t.v[r + i][c];
+    *reinterpret_cast<u32x4*>(ht + (int64_t)(kc0 * 8 + c) * padded_tokens + i0 + r) = o.x;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// transpose_weight: wt[k][c] = W[c0 + c][k] of one piece, zeros from the real
+// vocabulary's end on.
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(256) void transpose_weight(const u32x4* __restrict__ w, int32_t ldc,
+                                                        int32_t c0, int32_t real_vocab,
+                                                        int32_t piece, int32_t k_tiles,
+                                                        uint16_t* __restrict__ wt,
+                                                        int64_t blk_begin) {
+  __shared__ Tile64 t;
+  const int64_t blk = blk_begin + blockIdx.x;
+  const int32_t r0 = (int32_t)(blk / k_tiles) * kT;
+  const int32_t kc0 = (int32_t)(blk % k_tiles) * (kT / 8);
+  for (int q = threadIdx.x; q < kT * kT / 8; q += 256) {
+    const int r = q >> 3, c = q & 7;
+    u32x4 x = {0, 0, 0, 0};
+    if (c0 + r0 + r < real_vocab) x = w[(int64_t)(c0 + r0 + r) * ldc + kc0 + c];
+    *reinterpret_cast<u32x4*>(&t.v[r][c * 8]) = x;
+  }
+  __syncthreads();
+  for (int q = threadIdx.x; q < kT * kT / 8; q += 256) {
+    const int c = q >> 3, r = (q & 7) * 8;
+    union {
+      uint16_t e[8];
+      u32x4 x;
+    } o;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o.e[i] = t.v[r + i][c];
+    *reinterpret_cast<u32x4*>(wt + (int64_t)(kc0 * 8 + c) * piece + r0 + r) = o.x;
+  }
+}
+
+// Work index -> (tile of A, tile of B): strips of 4 A tiles, B-major inside, so
+// that the blocks resident on one XCD share operand rows (see lmhead_segments).
+__device__ __forceinline__ void tile_of(int64_t blk, int32_t n_a, int32_t n_b, int32_t& ta,
+                                        int32_t& tb) {
+  constexpr int32_t kGroup = 4;
+  const int64_t strip = blk / ((int64_t)kGroup * n_b);
+  const int32_t r_in = (int32_t)(blk - strip * kGroup * n_b);
+  const int32_t strip_w = min(kGroup, n_a - (int32_t)strip * kGroup);
+  ta = (int32_t)strip * kGroup + r_in % strip_w;
+  tb = r_in / strip_w;
+}
+
+// ---------------------------------------------------------------------------
+// dz_piece: dz of the columns [c0, c0 + piece) for the live rows, in bf16, by
+// tokens (dzn[i][c], ld = piece) and by columns (dzt[c][i], ld = padded_tokens).
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(kThreads) void dz_piece(
+    const u32x4* __restrict__ hc, const u32x4* __restrict__ w, int32_t hidden_dim,
+    int32_t real_vocab, int32_t c0, int32_t piece, int32_t padded_tokens,
+    uint16_t* __restrict__ dzn, uint16_t* __restrict__ dzt, char* ws, LmheadBwdLayout lay,
+    int64_t blk_begin) {
+  __shared__ __attribute__((aligned(16))) char smem[kTileLds];
+  const LiveRows live = live_rows(ws, lay);
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wv = wave >> 2, wt = wave & 3;
+  int32_t va, tb;
+  tile_of(blk_begin + xcd_local_block(blockIdx.x, gridDim.x), piece / kBA, padded_tokens / kBB, va,
+          tb);
+  const int32_t t0 = tb * kBB, v0 = va * kBA;  // v0: column inside the piece
+  if (t0 >= (int32_t)live.head[0]) return;
+  f32x4 acc[kVS][kTS];
+  if (c0 + v0 < real_vocab) {
+    const int64_t row_bytes = (int64_t)hidden_dim * 2;
+    const TileOperand wo(reinterpret_cast<const char*>(w) + (int64_t)(c0 + v0) * row_bytes,
+                         row_bytes, min(kBA, real_vocab - c0 - v0), 0, wave, lane);
+    const TileOperand ho(reinterpret_cast<const char*>(hc) + (int64_t)t0 * row_bytes, row_bytes,
+                         kBB, 0, wave, lane);
+    tile_product(smem, wo, ho, 0, hidden_dim / kBK, wave, lane, acc);
+  }
+  uint16_t* tr = reinterpret_cast<uint16_t*>(smem);  // [256 columns][256 tokens]
+  static_assert(kTileLds >= kBA * kBB * 2, "the transpose fits");
+#pragma unroll
+  for (int ts = 0; ts < kTS; ++ts) {
+    const int32_t ti = (wt * kTS + ts) * 16 + (lane & 15);
+    const int32_t i = t0 + ti;
+    const float L = live.lse[i], cg = live.cg[i], cc = live.cc[i];
+    const int32_t tgt = live.tgt[i] - c0;
+#pragma unroll
+    for (int vs = 0; vs < kVS; ++vs) {
+      const int32_t cl = wv * 128 + vs * 16 + 4 * (lane >> 4);  // column inside the block
+      union {
+        uint16_t e[4];
+        uint64_t x;
+      } o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int32_t c = v0 + cl + e;
+        float d = 0.0f;
+        if (c0 + c < real_vocab) {
+          const float p = exp2_hw((acc[vs][ts][e] - L) * kLog2e);
+          d = p * cc;
+          if (c == tgt) d = fmaf(p, cc, cg);
+        }
+        o.e[e] = bf16_bits(d);
+        if (c == tgt) live.resid[i] = d - bf16_float(o.e[e]);
+        if (dzt) tr[(cl + e) * kBB + ti] = o.e[e];
+      }
+      *reinterpret_cast<uint64_t*>(dzn + (int64_t)i * piece + v0 + cl) = o.x;
+    }
+  }
+  if (!dzt) return;
+  __syncthreads();
+  for (int q = tid; q < kBA * kBB / 8; q += kThreads) {
+    const int c = q / (kBB / 8), r = q % (kBB / 8);
+    *reinterpret_cast<u32x4*>(dzt + (int64_t)(v0 + c) * padded_tokens + t0 + r * 8) =
+        *reinterpret_cast<const u32x4*>(tr + c * kBB + r * 8);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dw_piece: dW[c0 + c][k] = scale * sum_i dzt[c][i] ht[k][i], in bf16; +0 from
+// the real vocabulary's end on.  Operand A is ht, so a lane holds 4 consecutive
+// k of one column.
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(kThreads) void dw_piece(
+    const uint16_t* __restrict__ ht, const uint16_t* __restrict__ dzt, int32_t hidden_dim,
+    int32_t real_vocab, int32_t padded_vocab, int32_t c0, int32_t piece, int32_t padded_tokens,
+    uint16_t* __restrict__ dw, char* ws, LmheadBwdLayout lay, int64_t blk_begin) {
+  __shared__ __attribute__((aligned(16))) char smem[kTileLds];
+  const LiveRows live = live_rows(ws, lay);
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wv = wave >> 2, wt = wave & 3;
+  int32_t ka, cb;
+  tile_of(blk_begin + xcd_local_block(blockIdx.x, gridDim.x), (hidden_dim + kBA - 1) / kBA,
+          piece / kBB, ka, cb);
+  const int32_t k0 = ka * kBA, b0 = cb * kBB;
+  if (c0 + b0 >= padded_vocab) return;
+  const int32_t nslab = ((int32_t)live.head[0] + kBK - 1) / kBK;
+  const float scale = __uint_as_float(live.head[1]);
+  f32x4 acc[kVS][kTS];
+  const bool any = nslab > 0 && c0 + b0 < real_vocab;
+  if (any) {
+    const int64_t row_bytes = (int64_t)padded_tokens * 2;
+    const TileOperand ao(ht + (int64_t)k0 * padded_tokens, row_bytes, min(kBA, hidden_dim - k0), 0,
+                         wave, lane);
+    const TileOperand bo(dzt + (int64_t)b0 * padded_tokens, row_bytes, kBB, 0, wave, lane);
+    tile_product(smem, ao, bo, 0, nslab, wave, lane, acc);
+  }
+#pragma unroll
+  for (int ts = 0; ts < kTS; ++ts) {
+    const int32_t c = c0 + b0 + (wt * kTS + ts) * 16 + (lane & 15);
+    if (c >= padded_vocab) continue;
+    const bool on = any && c < real_vocab;
+#pragma unroll
+    for (int vs = 0; vs < kVS; ++vs) {
+      const int32_t k = k0 + wv * 128 + vs * 16 + 4 * (lane >> 4);
+      if (k >= hidden_dim) continue;
+      union {
+        uint16_t e[4];
+        uint64_t x;
+      } o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o.e[e] = on ? bf16_bits(acc[vs][ts][e] * scale) : (uint16_t)0;
+      *reinterpret_cast<uint64_t*>(dw + (int64_t)c * hidden_dim + k) = o.x;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dh_piece: part[s][i][k] (+)= sum over split s of the piece's columns of
+// dzn[i][c] wt[k][c], in fp32.  The first piece writes, the others add.
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(kThreads) void dh_piece(
+    const uint16_t* __restrict__ wt_, const uint16_t* __restrict__ dzn, int32_t hidden_dim,
+    int32_t piece, int32_t padded_tokens, int32_t splits, bool add, float* __restrict__ part,
+    char* ws, LmheadBwdLayout lay, int64_t blk_begin) {
+  __shared__ __attribute__((aligned(16))) char smem[kTileLds];
+  const LiveRows live = live_rows(ws, lay);
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wv = wave >> 2, wt = wave & 3;
+  const int32_t n_a = (hidden_dim + kBA - 1) / kBA, n_b = padded_tokens / kBB;
+  const int64_t blk = blk_begin + xcd_local_block(blockIdx.x, gridDim.x);
+  const int32_t split = (int32_t)(blk / ((int64_t)n_a * n_b));
+  int32_t ka, tb;
+  tile_of(blk - (int64_t)split * n_a * n_b, n_a, n_b, ka, tb);
+  const int32_t k0 = ka * kBA, t0 = tb * kBB;
+  const int32_t count = (int32_t)live.head[0];
+  if (t0 >= count) return;
+  const int32_t slabs = piece / kBK;
+  const int32_t s0 = (int32_t)((int64_t)split * slabs / splits);
+  const int32_t s1 = (int32_t)((int64_t)(split + 1) * slabs / splits);
+  f32x4 acc[kVS][kTS];
+  if (s1 > s0) {
+    const int64_t row_bytes = (int64_t)piece * 2;
+    const TileOperand ao(wt_ + (int64_t)k0 * piece, row_bytes, min(kBA, hidden_dim - k0), 0, wave,
+                         lane);
+    const TileOperand bo(dzn + (int64_t)t0 * piece, row_bytes, kBB, 0, wave, lane);
+    tile_product(smem, ao, bo, s0, s1 - s0, wave, lane, acc);
+  } else {
+#pragma unroll
+    for (int vs = 0; vs < kVS; ++vs)
+#pragma unroll
+      for (int ts = 0; ts < kTS; ++ts) acc[vs][ts] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+#pragma unroll
+  for (int ts = 0; ts < kTS; ++ts) {
+    const int32_t i = t0 + (wt * kTS + ts) * 16 + (lane & 15);
+    if (i >= count) continue;
+    float* out = part + ((int64_t)split * padded_tokens + i) * hidden_dim;
+#pragma unroll
+    for (int vs = 0; vs < kVS; ++vs) {
+      const int32_t k = k0 + wv * 128 + vs * 16 + 4 * (lane >> 4);
+      if (k >= hidden_dim) continue;
+      f32x4* o = reinterpret_cast<f32x4*>(out + k);
+      *o = add ? *o + acc[vs][ts] : acc[vs][ts];
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dh_finish: dh[r] = scale * (sum of the splits' partials in ascending order +
+// resid W[target]) in bf16; +0 on rows that are not live.  8 columns a thread.
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(256) void dh_finish(const float* __restrict__ part, int32_t splits,
+                                                 int32_t num_tokens, int32_t padded_tokens,
+                                                 int32_t ldc, const u32x4* __restrict__ w,
+                                                 u32x4* __restrict__ dh, char* ws,
+                                                 LmheadBwdLayout lay, int64_t idx_begin) {
+  const LiveRows live = live_rows(ws, lay);
+  const int64_t idx = idx_begin + (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (idx >= (int64_t)num_tokens * ldc) return;
+  const int32_t r = (int32_t)(idx / ldc), c = (int32_t)(idx - (int64_t)r * ldc);
+  const int32_t i = live.inv[r];
+  union {
+    uint16_t e[8];
+    u32x4 x;
+  } o;
+  o.x = u32x4{0, 0, 0, 0};
+  if (i >= 0) {
+    const float scale = __uint_as_float(live.head[1]);
+    f32x4 lo = {0.0f, 0.0f, 0.0f, 0.0f}, hi = lo;
+    const float* p = part + ((int64_t)i * ldc + c) * 8;
+    for (int32_t s = 0; s < splits; ++s) {
+      lo += *reinterpret_cast<const f32x4*>(p);
+      hi += *reinterpret_cast<const f32x4*>(p + 4);
+      p += (int64_t)padded_tokens * ldc * 8;
+    }
+    const float rs = live.resid[i];
+    if (rs != 0.0f) {
+      union {
+        u32x4 x;
+        uint16_t e[8];
+      } wr;
+      wr.x = w[(int64_t)live.tgt[i] * ldc + c];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        lo[e] = fmaf(rs, bf16_float(wr.e[e]), lo[e]);
+        hi[e] = fmaf(rs, bf16_float(wr.e[4 + e]), hi[e]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      o.e[e] = bf16_bits(lo[e] * scale);
+      o.e[4 + e] = bf16_bits(hi[e] * scale);
+    }
+  }
+  dh[idx] = o.x;
+}
+
+__global__ __launch_bounds__(256) void fill_zero(u32x4* __restrict__ out, int64_t n,
+                                                 int64_t begin) {
+  const int64_t i = begin + (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i < n) out[i] = u32x4{0, 0, 0, 0};
+}
+
+// Launches `blocks` blocks in pieces of at most the launch limit.
+template <typename F>
+hipError_t in_launches(int64_t blocks, int threads, F&& launch) {
+  const int64_t most = launch_thread_limit() / threads;
+  for (int64_t b = 0; b < blocks; b += most) {
+    launch(b, blocks - b < most ? blocks - b : most);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+}  // namespace
+
+// Piece: 16384 columns, or more where few tokens leave dz small (2^26 elements,
+// 128 MiB of bf16).  Splits: enough blocks of dh for the chip's 256 CUs.
+LmheadBwdLayout lmhead_bwd_layout(int64_t n, int64_t k, int64_t padded_vocab, bool want_dh,
+                                  bool want_dw) {
+  LmheadBwdLayout l{};
+  const int64_t np = (n + 255) / 256 * 256;
+  int64_t piece = (int64_t{1} << 26) / (np > 0 ? np : 1);
+  piece = piece < 16384 ? 16384 : piece;
+  const int64_t most = (padded_vocab + 255) / 256 * 256;
+  piece = piece < most ? piece / 256 * 256 : most;
+  const int64_t blocks = np / 256 * ((k + 255) / 256);
+  const int64_t splits = blocks > 0 ? (blocks < 256 ? 256 / blocks : 1) : 1;
+  l.padded_tokens = (int32_t)np;
+  l.piece = (int32_t)piece;
+  l.splits = (int32_t)splits;
+  size_t at = 256;  // the status words
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += round256(bytes);
+    return here;
+  };
+  l.head = take(8);
+  l.idx = take(np * 4);
+  l.tgt = take(np * 4);
+  l.lse = take(np * 4);
+  l.cg = take(np * 4);
+  l.cc = take(np * 4);
+  l.resid = take(np * 4);
+  l.inv = take(n * 4);
+  l.hc = take((size_t)np * k * 2);
+  l.dzn = take((size_t)np * piece * 2);
+  if (want_dw) {
+    l.ht = take((size_t)np * k * 2);
+    l.dzt = take((size_t)np * piece * 2);
+  }
+  if (want_dh) {
+    l.wt = take((size_t)piece * k * 2);
+    l.part = take((size_t)splits * np * k * 4);
+  }
+  l.total = at;
+  return l;
+}
+
+hipError_t launch_fill_zero(void* out, int64_t bytes, hipStream_t stream) {
+  const int64_t n = bytes / 16;
+  return in_launches((n + 255) / 256, 256, [&](int64_t b, int64_t nb) {
+    hipLaunchKernelGGL(fill_zero, dim3((unsigned)nb), dim3(256), 0, stream,
+                       reinterpret_cast<u32x4*>(out), n, b * 256);
+  });
+}
+
+hipError_t launch_lmhead_bwd(const LmheadBwdArgs& a, hipStream_t stream) {
+  const LmheadBwdLayout& l = a.layout;
+  char* ws = a.workspace;
+  const int32_t np = l.padded_tokens, k = a.hidden_dim, ldc = k / 8;
+  u32x4* hc = reinterpret_cast<u32x4*>(ws + l.hc);
+  uint16_t* dzn = reinterpret_cast<uint16_t*>(ws + l.dzn);
+  uint16_t* ht = a.dweight ? reinterpret_cast<uint16_t*>(ws + l.ht) : nullptr;
+  uint16_t* dzt = a.dweight ? reinterpret_cast<uint16_t*>(ws + l.dzt) : nullptr;
+  const u32x4* w = reinterpret_cast<const u32x4*>(a.weight);
+
+  hipLaunchKernelGGL(live_rows_scan, dim3(1), dim3(kScanThreads), 0, stream, a.num_tokens, np,
+                     a.real_vocab, a.targets, a.mask, a.ignore_index, a.lse, a.grad, a.grad_lse,
+                     ws, l, a.status);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int32_t k_tiles = k / kT;
+  e = in_launches((int64_t)(np / kT) * k_tiles, 256, [&](int64_t b, int64_t nb) {
+    hipLaunchKernelGGL(gather_rows, dim3((unsigned)nb), dim3(256), 0, stream,
+                       reinterpret_cast<const u32x4*>(a.hidden), ldc, hc, ht, np, k_tiles, ws, l,
+                       b);
+  });
+  if (e != hipSuccess) return e;
+
+  const int32_t n_k = (k + kBA - 1) / kBA, n_t = np / kBB;
+  // pieces of the columns that need work: dW's rows go on to V_pad (as +0)
+  const int32_t columns = a.dweight ? a.padded_vocab : a.real_vocab;
+  for (int64_t begin = 0; begin < columns; begin += l.piece) {
+    const int32_t c0 = (int32_t)begin;
+    const int64_t left = (columns - begin + 255) / 256 * 256;
+    const int32_t piece = left < l.piece ? (int32_t)left : l.piece;
+    e = in_launches((int64_t)(piece / kBA) * n_t, kThreads, [&](int64_t b, int64_t nb) {
+      hipLaunchKernelGGL(dz_piece, dim3((unsigned)nb), dim3(kThreads), 0, stream, hc, w, k,
+                         a.real_vocab, c0, piece, np, dzn, dzt, ws, l, b);
+    });
+    if (e != hipSuccess) return e;
+    if (a.dweight) {
+      e = in_launches((int64_t)(piece / kBB) * n_k, kThreads, [&](int64_t b, int64_t nb) {
+        hipLaunchKernelGGL(dw_piece, dim3((unsigned)nb), dim3(kThreads), 0, stream, ht, dzt, k,
+                           a.real_vocab, a.padded_vocab, c0, piece, np,
+                           reinterpret_cast<uint16_t*>(a.dweight), ws, l, b);
+      });
+      if (e != hipSuccess) return e;
+    }
+    if (a.dhidden) {
+      uint16_t* wt = reinterpret_cast<uint16_t*>(ws + l.wt);
+      e = in_launches((int64_t)(piece / kT) * k_tiles, 256, [&](int64_t b, int64_t nb) {
+        hipLaunchKernelGGL(transpose_weight, dim3((unsigned)nb), dim3(256), 0, stream, w, ldc, c0,
+                           a.real_vocab, piece, k_tiles, wt, b);
+      });
+      if (e != hipSuccess) return e;
+      e = in_launches((int64_t)l.splits * n_t * n_k, kThreads, [&](int64_t b, int64_t nb) {
+        hipLaunchKernelGGL(dh_piece, dim3((unsigned)nb), dim3(kThreads), 0, stream, wt, dzn, k,
+                           piece, np, l.splits, c0 > 0, reinterpret_cast<float*>(ws + l.part), ws,
+                           l, b);
+      });
+      if (e != hipSuccess) return e;
+    }
+  }
+  if (a.dhidden) {
+    e = in_launches(((int64_t)a.num_tokens * ldc + 255) / 256, 256, [&](int64_t b, int64_t nb) {
+      hipLaunchKernelGGL(dh_finish, dim3((unsigned)nb), dim3(256), 0, stream,
+                         reinterpret_cast<const float*>(ws + l.part), l.splits, a.num_tokens, np,
+                         ldc, w, reinterpret_cast<u32x4*>(a.dhidden), ws, l, b * 256);
+    });
+  }
+  return e;
+}
+
+}  // namespace rlk
