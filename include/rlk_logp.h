@@ -387,6 +387,72 @@ rlk_status rlk_logp_fused_lmhead_bwd(const rlk_logp_desc* desc, const void* hidd
                                      const float* grad_lse, void* dhidden, void* dweight,
                                      void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- The LM-head in 8-bit floating point (OCP e4m3) --------------------------
+ * A bf16 matrix is cast in blocks of block_rows x 128: the scale of a block is
+ *   s = max(largest magnitude / 448, 2^-126),   q = e4m3(x / s)
+ * both quotients in fp32, correctly rounded, q to nearest even (448 is e4m3's
+ * largest finite value).  The matrix stands for q * s.  A block that holds NaN or
+ * infinity has that as its scale and gives NaN wherever it is used.  The pages
+ * have no 8-bit path; the statistics keep [PR289]'s contract as
+ * rlk_logp_fused_lmhead does. */
+
+/* An 8-bit matrix (host struct, read during the call only): values
+ * (device) e4m3 [rows, columns], contiguous, 16-byte aligned; scales (device)
+ * float, the one of row block r and column block c at
+ * scale[r * scale_row_stride + c * scale_col_stride]. */
+typedef struct rlk_fp8_matrix {
+  const void* q;
+  const float* scale;
+  int64_t scale_row_stride;
+  int64_t scale_col_stride;
+} rlk_fp8_matrix;
+
+/* The cast.
+ *   rows, cols  rows >= 0 (0 enqueues nothing); cols a positive multiple of 128, at
+ *               most 2^21.
+ *   x           (device) bf16 [rows, ld_x], 16-byte aligned; ld_x >= cols, a multiple
+ *               of 8.
+ *   block_rows  1 (hidden states: one scale per token and 128 columns) or 128 (a
+ *               weight); else RLK_ERR_BAD_TILING.  The last block of rows may be short.
+ *   q           (device) e4m3 [rows, cols] out, contiguous, 16-byte aligned.
+ *   scale       (device) float out, ceil(rows / block_rows) x cols / 128 of them at
+ *               these strides (each >= 1; distinct places are the caller's care).
+ *               For hidden states a row stride of 1 (column blocks apart) is what
+ *               the products read fastest. */
+rlk_status rlk_fp8_quantize(int64_t rows, int64_t cols, const void* x, int64_t ld_x,
+                            int32_t block_rows, void* q, float* scale, int64_t scale_row_stride,
+                            int64_t scale_col_stride, void* stream);
+
+/* Logits from 8-bit operands: z = hidden . weight^T, each block of 128 of the sum
+ * taken by the matrix cores, times its two scales and added up in fp32, rounded
+ * once to bf16 -- the logits that rlk_logp_fwd and its kin read.
+ *   desc        num_tokens, real_vocab, padded_vocab, ld_logits as for rlk_logp_fwd
+ *               (the tiling is validated and not used; flags must be 0).
+ *   hidden      [num_tokens, hidden_dim], one scale per token and 128 columns.
+ *   weight      [>= real_vocab, hidden_dim], one scale per 128 x 128; rows >=
+ *               real_vocab are never read.
+ *   hidden_dim  a positive multiple of 128, at most 2^21; num_tokens (and
+ *               real_vocab) * hidden_dim / 16 < 2^31.
+ *   logits      (device) bf16 [num_tokens, ld_logits], 16-byte aligned, out: columns
+ *               [V_real, V_pad) are -inf, columns from V_pad on are not touched.
+ * A token's logits have the same bits whatever other tokens share the call. */
+rlk_status rlk_lmhead_logits_fp8(const rlk_logp_desc* desc, const rlk_fp8_matrix* hidden,
+                                 const rlk_fp8_matrix* weight, int64_t hidden_dim, void* logits,
+                                 void* stream);
+
+/* rlk_logp_fused_lmhead with 8-bit operands (hidden, weight and hidden_dim as for
+ * rlk_lmhead_logits_fp8): logp and LSE of z, taken from the fp32 sums (not rounded to
+ * bf16), never written to memory.  Everything else -- descriptor, tiles of at
+ * least 256 columns, virtual shards, targets, mask, outputs, workspace
+ * (rlk_logp_fused_lmhead_workspace_bytes), errors -- as for rlk_logp_fused_lmhead;
+ * logp and LSE are bitwise the same for every num_virtual_shards and for a row
+ * whatever other rows share the call. */
+rlk_status rlk_logp_fused_lmhead_fp8(const rlk_logp_desc* desc, const rlk_fp8_matrix* hidden,
+                                     const rlk_fp8_matrix* weight, int64_t hidden_dim,
+                                     const int32_t* targets, const uint8_t* active_mask,
+                                     float* logp, float* lse, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
 /* Host-only geometry (no device access): writes T+1 tile bounds
  * floor(t*V_pad/T) to `bounds` and S+1 shard starts floor(s*T/S) to
  * `shard_first_tile` (either may be NULL).  Same limits as the descriptor. */

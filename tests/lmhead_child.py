@@ -23,8 +23,17 @@ def run_all():
                                                      c.gl, real_vocab=2900)
     _, out["dw0"] = rlk.fused_lmhead_backward(c.h[:0], c.w, c.tgt[:0], None, out["lse"][:0],
                                               c.g[:0], real_vocab=2900)
+    wq, ws = rlk.quantize_fp8(c.w[:2900], 128)
+    out["wq"], out["ws"] = wq, ws
+    for n in (300, 20):  # the tile kernel, the streaming one
+        h = c.h[:n]
+        out[f"hq{n}"], out[f"hs{n}"] = rlk.quantize_fp8(h)
+        out[f"logits{n}"] = rlk.lmhead_logits_fp8(h, wq, ws, real_vocab=2900, padded_vocab=3000)
+        out[f"logp{n}"], out[f"lse{n}"] = rlk.fused_lmhead_fp8(
+            h, wq, ws, c.tgt[:n], c.mask[:n], real_vocab=2900, padded_vocab=3000,
+            num_vocab_tiles=7)
     torch.cuda.synchronize()
-    return {k: v.contiguous().view(torch.uint8).cpu() for k, v in out.items()}
+    return {k: v.reshape(-1).view(torch.uint8).cpu() for k, v in out.items()}
 
 
 def main(out_path: str) -> int:

@@ -40,6 +40,7 @@ EXPORTED = ("rlk_logp_workspace_bytes", "rlk_logp_fwd", "rlk_logp_bwd",
             "rlk_logp_fwd_bwd_ex_workspace_bytes", "rlk_logp_fwd_bwd_ex",
             "rlk_logp_fused_lmhead_workspace_bytes", "rlk_logp_fused_lmhead",
             "rlk_logp_fused_lmhead_bwd_workspace_bytes", "rlk_logp_fused_lmhead_bwd",
+            "rlk_fp8_quantize", "rlk_lmhead_logits_fp8", "rlk_logp_fused_lmhead_fp8",
             "rlk_logp_tile_geometry", "rlk_status_string", "rlk_last_error_detail",
             "rlk_logp_fwd_noalloc")
 
@@ -49,6 +50,11 @@ class rlk_logp_desc(ctypes.Structure):  # noqa: N801 - mirrors the C struct name
                 ("padded_vocab", ctypes.c_int64), ("ld_logits", ctypes.c_int64),
                 ("num_vocab_tiles", ctypes.c_int32), ("num_virtual_shards", ctypes.c_int32),
                 ("ignore_index", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class rlk_fp8_matrix(ctypes.Structure):  # noqa: N801 - mirrors the C struct name
+    _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("scale_row_stride", ctypes.c_int64), ("scale_col_stride", ctypes.c_int64)]
 
 
 class RlkError(RuntimeError):
@@ -99,6 +105,13 @@ def _load() -> ctypes.CDLL:
     lib.rlk_logp_fused_lmhead_bwd.argtypes = [dp, vp, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, sz,
                                               vp]
     lib.rlk_logp_fused_lmhead_bwd.restype = ctypes.c_int
+    mp = ctypes.POINTER(rlk_fp8_matrix)
+    lib.rlk_fp8_quantize.argtypes = [i64, i64, vp, i64, i32, vp, vp, i64, i64, vp]
+    lib.rlk_fp8_quantize.restype = ctypes.c_int
+    lib.rlk_lmhead_logits_fp8.argtypes = [dp, mp, mp, i64, vp, vp]
+    lib.rlk_lmhead_logits_fp8.restype = ctypes.c_int
+    lib.rlk_logp_fused_lmhead_fp8.argtypes = [dp, mp, mp, i64, vp, vp, vp, vp, vp, sz, vp]
+    lib.rlk_logp_fused_lmhead_fp8.restype = ctypes.c_int
     lib.rlk_logp_tile_geometry.argtypes = [i64, i32, i32, vp, vp]
     lib.rlk_logp_tile_geometry.restype = ctypes.c_int
     lib.rlk_status_string.argtypes = [ctypes.c_int]
@@ -242,6 +255,39 @@ def rlk_logp_fused_lmhead_bwd(desc, hidden, weight, hidden_dim: int, targets, ac
                                           hidden_dim, _ptr(targets), _ptr(active_mask), _ptr(lse),
                                           _ptr(grad_logp), _ptr(grad_lse), _ptr(dhidden),
                                           _ptr(dweight), _ptr(workspace), ws_bytes,
+                                          _stream(stream)))
+
+
+def make_fp8_matrix(q, scale) -> rlk_fp8_matrix:
+    """The rlk_fp8_matrix of a pair of tensors (either may be None): values [rows, cols],
+    scales [row blocks, column blocks] with any positive strides."""
+    # the stride of a dimension of one does not matter, and need not be positive
+    rs, cs = (1, 1) if scale is None else (st if n > 1 else 1 for n, st in
+                                           zip(scale.shape, scale.stride()))
+    return rlk_fp8_matrix(_ptr(q), _ptr(scale), rs, cs)
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
+def rlk_fp8_quantize(rows: int, cols: int, x, ld_x: int, block_rows: int, q, scale,
+                     scale_row_stride: int, scale_col_stride: int, stream=None) -> None:
+    _check(_lib.rlk_fp8_quantize(rows, cols, _ptr(x), ld_x, block_rows, _ptr(q), _ptr(scale),
+                                 scale_row_stride, scale_col_stride, _stream(stream)))
+
+
+def rlk_lmhead_logits_fp8(desc, hidden, weight, hidden_dim: int, logits, stream=None) -> None:
+    _check(_lib.rlk_lmhead_logits_fp8(ctypes.byref(desc), _ref(hidden), _ref(weight), hidden_dim,
+                                      _ptr(logits), _stream(stream)))
+
+
+def rlk_logp_fused_lmhead_fp8(desc, hidden, weight, hidden_dim: int, targets, active_mask, logp,
+                              lse, workspace, stream=None) -> None:
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.rlk_logp_fused_lmhead_fp8(ctypes.byref(desc), _ref(hidden), _ref(weight),
+                                          hidden_dim, _ptr(targets), _ptr(active_mask),
+                                          _ptr(logp), _ptr(lse), _ptr(workspace), ws_bytes,
                                           _stream(stream)))
 
 
@@ -612,6 +658,17 @@ def fused_lmhead(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tens
     return logp, lse
 
 
+def _scratch(nbytes: int, device, stream) -> torch.Tensor:
+    """A workspace of nbytes (0: the descriptor was refused) for a call on `stream`: the
+    allocator hands its memory out again only when that stream is through with it."""
+    if nbytes == 0:
+        raise ValueError(f"invalid rlk_logp_desc: {rlk_last_error_detail()}")
+    t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 def fused_lmhead_backward(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
                           active_mask, lse: torch.Tensor, grad_logp=None, grad_lse=None, *,
                           real_vocab: int, want_hidden: bool = True, want_weight: bool = True,
@@ -631,15 +688,14 @@ def fused_lmhead_backward(hidden: torch.Tensor, weight: torch.Tensor, targets: t
     n, k = hidden.shape
     rows = weight.shape[0]
     desc = make_desc(n, real_vocab, rows, rows, 1, 1, ignore_index, validate)
-    dh = torch.empty_like(hidden) if want_hidden else None
-    dw = torch.empty_like(weight) if want_weight else None
-    if workspace is None:
-        nbytes = rlk_logp_fused_lmhead_bwd_workspace_bytes(desc, k, want_hidden, want_weight)
-        if nbytes == 0:
-            raise ValueError(f"invalid rlk_logp_desc: {rlk_last_error_detail()}")
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=hidden.device)
-    rlk_logp_fused_lmhead_bwd(desc, hidden, weight, k, targets, _u8_mask(active_mask), lse,
-                              grad_logp, grad_lse, dh, dw, workspace, stream)
+    with torch.cuda.device(hidden.device):
+        dh = torch.empty_like(hidden) if want_hidden else None
+        dw = torch.empty_like(weight) if want_weight else None
+        if workspace is None:
+            workspace = _scratch(rlk_logp_fused_lmhead_bwd_workspace_bytes(
+                desc, k, want_hidden, want_weight), hidden.device, stream)
+        rlk_logp_fused_lmhead_bwd(desc, hidden, weight, k, targets, _u8_mask(active_mask), lse,
+                                  grad_logp, grad_lse, dh, dw, workspace, stream)
     return dh, dw
 
 
@@ -690,3 +746,132 @@ def lmhead_selected_token_logprob(hidden: torch.Tensor, weight: torch.Tensor,
     _check_lmhead(hidden, weight, targets, active_mask, real_vocab)
     return _LmheadSelectedTokenLogprob.apply(hidden, weight, targets, active_mask, real_vocab,
                                              padded_vocab, num_vocab_tiles, ignore_index)
+
+
+# -- the LM-head in 8-bit floating point ----------------------------------------
+FP8_BLOCK = 128  # columns (and weight rows) that share a scale
+
+
+def quantize_fp8(x: torch.Tensor, block_rows: int = 1, *, stream=None):
+    """(q, scale): bf16 x [R, K] as e4m3 values [R, K] and the fp32 scales
+    [ceil(R / block_rows), K / 128] of its block_rows x 128 blocks, so that q * scale stands
+    for x.  block_rows is 1 for hidden states and 128 for a weight.  The scales of 1 x 128
+    blocks lie with the tokens contiguous (a transposed view), as the products read them."""
+    _check_logits(x, "x")
+    if block_rows not in (1, FP8_BLOCK):
+        raise ValueError(f"block_rows must be 1 or {FP8_BLOCK}, got {block_rows!r}")
+    n, k = x.shape
+    if k == 0 or k % FP8_BLOCK:
+        raise ValueError(f"x must have a multiple of {FP8_BLOCK} columns, got {k}")
+    _check_device(x)
+    row_blocks, col_blocks = -(-n // block_rows), k // FP8_BLOCK
+    with torch.cuda.device(x.device):
+        q = torch.empty((n, k), dtype=torch.float8_e4m3fn, device=x.device)
+        if block_rows == 1:
+            scale = torch.empty((col_blocks, row_blocks), device=x.device).t()
+        else:
+            scale = torch.empty((row_blocks, col_blocks), device=x.device)
+        if n:
+            m = make_fp8_matrix(q, scale)
+            rlk_fp8_quantize(n, k, x, x.stride(0) if n > 1 else k, block_rows, q, scale,
+                             m.scale_row_stride, m.scale_col_stride, stream)
+    return q, scale
+
+
+def _check_fp8(name, q, scale, block_rows):
+    """An e4m3 matrix [R, K], contiguous, and its fp32 scales [ceil(R / block_rows), K / 128]."""
+    if not isinstance(q, torch.Tensor) or not isinstance(scale, torch.Tensor):
+        raise TypeError(f"{name} and its scales must be torch.Tensors")
+    if q.dtype != torch.float8_e4m3fn:
+        raise TypeError(f"{name} must be float8_e4m3fn, got {q.dtype}")
+    if scale.dtype != torch.float32:
+        raise TypeError(f"the scales of {name} must be float32, got {scale.dtype}")
+    if q.dim() != 2 or not q.is_contiguous():
+        raise ValueError(f"{name} must be 2-D and contiguous")
+    if q.shape[1] == 0 or q.shape[1] % FP8_BLOCK:
+        raise ValueError(f"{name} must have a multiple of {FP8_BLOCK} columns, got {q.shape[1]}")
+    want = (-(-q.shape[0] // block_rows), q.shape[1] // FP8_BLOCK)
+    if tuple(scale.shape) != want:
+        raise ValueError(f"the scales of {name} must have shape {want}, got {tuple(scale.shape)}")
+    if any(n > 1 and st < 1 for n, st in zip(scale.shape, scale.stride())):
+        raise ValueError(f"the scales of {name} must have positive strides")
+
+
+def _check_lmhead_fp8(hidden, weight_q, weight_scale, real_vocab, **rows):
+    """hidden: bf16 [N, K], or its (q, scale) pair; rows: targets and active_mask, where there
+    are any.  All on one GPU."""
+    _check_fp8("weight_q", weight_q, weight_scale, FP8_BLOCK)
+    if isinstance(hidden, (tuple, list)):
+        _check_fp8("hidden", *hidden, 1)
+        q, parts = hidden[0], {"hidden scales": hidden[1]}
+    else:
+        _check_logits(hidden, "hidden")
+        q, parts = hidden, {}
+    if weight_q.shape[1] != q.shape[1]:
+        raise ValueError(f"weight_q has {weight_q.shape[1]} columns, hidden {q.shape[1]}")
+    if weight_q.shape[0] < real_vocab:
+        raise ValueError(f"weight_q has {weight_q.shape[0]} rows, fewer than "
+                         f"real_vocab={real_vocab}")
+    if rows:
+        if rows["targets"] is None:
+            raise TypeError("targets must be a torch.Tensor")
+        _check_rows("targets", rows["targets"], q.shape[0], _I32)
+        _check_rows("active_mask", rows["active_mask"], q.shape[0], _MASK)
+    _check_device(q, weight_q=weight_q, weight_scale=weight_scale, **parts, **rows)
+    return q
+
+
+def _fp8_pair(hidden, stream):
+    """The (q, scale) pair of the hidden states, cast on `stream` where they are bf16."""
+    if isinstance(hidden, (tuple, list)):
+        return tuple(hidden)
+    pair = quantize_fp8(hidden, 1, stream=stream)
+    if stream is not None:
+        for t in pair:
+            t.record_stream(stream)
+    return pair
+
+
+def lmhead_logits_fp8(hidden, weight_q: torch.Tensor, weight_scale: torch.Tensor, *,
+                      real_vocab: int, padded_vocab: int | None = None, stream=None):
+    """bf16 logits [N, V_pad] of an 8-bit LM-head, as forward() and its kin take them (their
+    rows are padded to a multiple of 8 columns); columns [real_vocab, V_pad) are -inf.
+
+    hidden: bf16 [N, K], cast to e4m3 with one scale per token and 128 columns, or the
+    (q, scale) pair of quantize_fp8(x, 1).  weight_q, weight_scale: quantize_fp8(W, 128)."""
+    _check_lmhead_fp8(hidden, weight_q, weight_scale, real_vocab)
+    with torch.cuda.device(weight_q.device):
+        q, scale = _fp8_pair(hidden, stream)
+        n, k = q.shape
+        v_pad = padded_vocab or weight_q.shape[0]
+        ld = (v_pad + 7) // 8 * 8
+        logits = torch.empty((n, ld), dtype=torch.bfloat16, device=q.device)
+        rlk_lmhead_logits_fp8(make_desc(n, real_vocab, v_pad, ld, 1), make_fp8_matrix(q, scale),
+                              make_fp8_matrix(weight_q, weight_scale), k, logits, stream)
+    return logits[:, :v_pad]
+
+
+def fused_lmhead_fp8(hidden, weight_q: torch.Tensor, weight_scale: torch.Tensor,
+                     targets: torch.Tensor, active_mask=None, *, real_vocab: int,
+                     padded_vocab: int | None = None, num_vocab_tiles: int = 64,
+                     num_virtual_shards: int = 1, ignore_index: int = -100,
+                     validate: bool = False, workspace: torch.Tensor | None = None, stream=None):
+    """fused_lmhead with an 8-bit weight: (logp, lse) of the logits of lmhead_logits_fp8,
+    taken before their rounding and never written.  hidden, weight_q and weight_scale as
+    there; the rest as for fused_lmhead."""
+    x = _check_lmhead_fp8(hidden, weight_q, weight_scale, real_vocab, targets=targets,
+                          active_mask=active_mask)
+    n = x.shape[0]
+    v_pad = padded_vocab or weight_q.shape[0]
+    desc = make_desc(n, real_vocab, v_pad, v_pad, num_vocab_tiles, num_virtual_shards,
+                     ignore_index, validate)
+    with torch.cuda.device(x.device):
+        if workspace is None:
+            workspace = _scratch(rlk_logp_fused_lmhead_workspace_bytes(desc), x.device, stream)
+        q, scale = _fp8_pair(hidden, stream)
+        logp = torch.empty(n, dtype=torch.float32, device=x.device)
+        lse = torch.empty(n, dtype=torch.float32, device=x.device)
+        rlk_logp_fused_lmhead_fp8(desc, make_fp8_matrix(q, scale),
+                                  make_fp8_matrix(weight_q, weight_scale), x.shape[1], targets,
+                                  _u8_mask(active_mask), logp, lse, workspace, stream)
+    return logp, lse

@@ -17,7 +17,8 @@ LIB = PKG / "librlk_logp.so"
 CALIB = PKG / "rlk_calib"  # stream-ceiling probe the benchmark reports beside its rates
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
-HIP_SOURCES = ["rlk_kernels", "rlk_lmhead", "rlk_lmhead_bwd", "rlk_noalloc"]
+HIP_SOURCES = ["rlk_kernels", "rlk_lmhead", "rlk_lmhead_bwd", "rlk_fp8",
+               "rlk_noalloc"]
 
 # -ffp-contract=off: only the explicit fmaf calls fuse, so every tile's
 # arithmetic is fixed by the source.  Packed fp32 VALU ops are disabled.

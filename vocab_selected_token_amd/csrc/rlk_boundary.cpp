@@ -651,33 +651,65 @@ size_t rlk_logp_fused_lmhead_workspace_bytes(const rlk_logp_desc* desc) {
   return fused_layout(desc).total;
 }
 
-rlk_status rlk_logp_fused_lmhead(const rlk_logp_desc* desc, const void* hidden,
-                                 const void* weight, int64_t hidden_dim, const int32_t* targets,
-                                 const uint8_t* active_mask, float* logp, float* lse,
-                                 void* workspace, size_t workspace_bytes, void* stream_ptr) {
-  rlk_status st = check_fused_desc(desc);
-  if (st != RLK_OK) return st;
-  if (hidden_dim < rlk::kLmheadSlabK || hidden_dim % rlk::kLmheadSlabK != 0 ||
-      hidden_dim > rlk::kLmheadMaxHidden)
+namespace {
+
+rlk_status check_hidden_dim(int64_t hidden_dim, int32_t multiple) {
+  if (hidden_dim < multiple || hidden_dim % multiple != 0 || hidden_dim > rlk::kLmheadMaxHidden)
     return fail(RLK_ERR_BAD_SHAPE, "hidden_dim=%lld must be a positive multiple of %d, at most %lld",
-                (long long)hidden_dim, rlk::kLmheadSlabK, (long long)rlk::kLmheadMaxHidden);
+                (long long)hidden_dim, multiple, (long long)rlk::kLmheadMaxHidden);
+  return RLK_OK;
+}
+
+// The operands of an 8-bit LM-head, of num_tokens (> 0) tokens; `rows` of the
+// weight are read.
+rlk_status check_fp8(const rlk_fp8_matrix* hidden, const rlk_fp8_matrix* weight,
+                     int64_t num_tokens, int64_t rows, int64_t hidden_dim, rlk::LmheadFp8Args* out) {
+  if (!hidden || !weight || !hidden->q || !hidden->scale || !weight->q || !weight->scale)
+    return fail(RLK_ERR_NULL_POINTER, "hidden, weight and their values and scales must be "
+                                      "non-NULL");
+  if (!aligned(hidden->q, 16) || !aligned(weight->q, 16))
+    return fail(RLK_ERR_ALIGNMENT, "the values of hidden and weight must be 16-byte aligned");
+  if (!aligned(hidden->scale, 4) || !aligned(weight->scale, 4))
+    return fail(RLK_ERR_ALIGNMENT, "the scales must be 4-byte aligned");
+  for (const rlk_fp8_matrix* m : {hidden, weight})
+    if (m->scale_row_stride < 1 || m->scale_col_stride < 1 || m->scale_row_stride > kI32Max ||
+        m->scale_col_stride > kI32Max)
+      return fail(RLK_ERR_BAD_SHAPE, "scale strides (%lld, %lld) outside [1, 2^31-1]",
+                  (long long)m->scale_row_stride, (long long)m->scale_col_stride);
+  // 32-bit offsets: 16-byte chunks of the values, bytes of a 256-token block's scales
+  if (rows * (hidden_dim / 16) > kI32Max || num_tokens * (hidden_dim / 16) > kI32Max)
+    return fail(RLK_ERR_BAD_SHAPE, "hidden or weight holds 2^31 or more 16-byte chunks");
+  if (255 * hidden->scale_row_stride + hidden_dim / rlk::kFp8Block * hidden->scale_col_stride >
+      kI32Max / 4)
+    return fail(RLK_ERR_BAD_SHAPE, "the scales of 256 tokens span 2^31 bytes or more");
+  out->hidden_q = hidden->q;
+  out->hidden_scale = hidden->scale;
+  out->weight_q = weight->q;
+  out->weight_scale = weight->scale;
+  out->hidden_row_stride = hidden->scale_row_stride;
+  out->hidden_col_stride = hidden->scale_col_stride;
+  out->weight_row_stride = weight->scale_row_stride;
+  out->weight_col_stride = weight->scale_col_stride;
+  out->hidden_dim = (int32_t)hidden_dim;
+  return RLK_OK;
+}
+
+// The forward of rlk_logp_fused_lmhead (fp8 null) and rlk_logp_fused_lmhead_fp8,
+// whose descriptor, hidden_dim and operands have been checked.
+rlk_status run_fused_lmhead(const rlk_logp_desc* desc, const void* hidden, const void* weight,
+                            const rlk::LmheadFp8Args* fp8, int64_t hidden_dim,
+                            const int32_t* targets, const uint8_t* active_mask, float* logp,
+                            float* lse, void* workspace, size_t workspace_bytes,
+                            void* stream_ptr) {
   const int64_t n = desc->num_tokens;
-  if (n == 0) return ok();
-  if (!hidden || !weight || !targets || !logp || !lse)
-    return fail(RLK_ERR_NULL_POINTER, "hidden, weight, targets, logp and lse must be non-NULL");
   const FusedLayout lay = fused_layout(desc);
   if (!workspace) return fail(RLK_ERR_WORKSPACE, "workspace is NULL");
   if (workspace_bytes < lay.total)
     return fail(RLK_ERR_WORKSPACE, "workspace_bytes=%zu < required %zu", workspace_bytes,
                 lay.total);
-  if (!aligned(hidden, 16) || !aligned(weight, 16))
-    return fail(RLK_ERR_ALIGNMENT, "hidden and weight must be 16-byte aligned");
   if (!aligned(workspace, 256)) return fail(RLK_ERR_ALIGNMENT, "workspace not 256-byte aligned");
   if (!aligned(targets, 4) || !aligned(logp, 4) || !aligned(lse, 4))
     return fail(RLK_ERR_ALIGNMENT, "targets, logp and lse must be 4-byte aligned");
-  // the kernel addresses both operands with 32-bit offsets in 16-byte chunks
-  if ((int64_t)desc->real_vocab * (hidden_dim / 8) > kI32Max || n * (hidden_dim / 8) > kI32Max)
-    return fail(RLK_ERR_BAD_SHAPE, "hidden or weight holds 2^31 or more 16-byte chunks");
   if (rlk::lmhead_grid_blocks((int32_t)n, (int32_t)desc->real_vocab) > kI32Max)
     return fail(RLK_ERR_BAD_SHAPE, "num_tokens x vocabulary blocks too large for one launch");
 
@@ -707,7 +739,7 @@ rlk_status rlk_logp_fused_lmhead(const rlk_logp_desc* desc, const void* hidden,
   a.target_logit = reinterpret_cast<float*>(ws + lay.tlogit);
   a.pmax = reinterpret_cast<float*>(ws + lay.pmax);
   a.psum = reinterpret_cast<float*>(ws + lay.psum);
-  e = rlk::launch_lmhead(a, stream);
+  e = rlk::launch_lmhead(a, fp8, stream);
   if (e != hipSuccess) return hip_fail(e, "lmhead launch");
   rlk::Stage2Args a2;
   a2.logits = nullptr;
@@ -732,17 +764,107 @@ rlk_status rlk_logp_fused_lmhead(const rlk_logp_desc* desc, const void* hidden,
   return ok();
 }
 
+}  // namespace
+
+rlk_status rlk_logp_fused_lmhead(const rlk_logp_desc* desc, const void* hidden,
+                                 const void* weight, int64_t hidden_dim, const int32_t* targets,
+                                 const uint8_t* active_mask, float* logp, float* lse,
+                                 void* workspace, size_t workspace_bytes, void* stream_ptr) {
+  rlk_status st = check_fused_desc(desc);
+  if (st != RLK_OK) return st;
+  st = check_hidden_dim(hidden_dim, rlk::kLmheadSlabK);
+  if (st != RLK_OK) return st;
+  const int64_t n = desc->num_tokens;
+  if (n == 0) return ok();
+  if (!hidden || !weight || !targets || !logp || !lse)
+    return fail(RLK_ERR_NULL_POINTER, "hidden, weight, targets, logp and lse must be non-NULL");
+  if (!aligned(hidden, 16) || !aligned(weight, 16))
+    return fail(RLK_ERR_ALIGNMENT, "hidden and weight must be 16-byte aligned");
+  // the kernel addresses both operands with 32-bit offsets in 16-byte chunks
+  if ((int64_t)desc->real_vocab * (hidden_dim / 8) > kI32Max || n * (hidden_dim / 8) > kI32Max)
+    return fail(RLK_ERR_BAD_SHAPE, "hidden or weight holds 2^31 or more 16-byte chunks");
+  return run_fused_lmhead(desc, hidden, weight, nullptr, hidden_dim, targets, active_mask, logp,
+                          lse, workspace, workspace_bytes, stream_ptr);
+}
+
+// ---------------------------------------------------------------------------
+// The LM-head in 8-bit floating point.
+// ---------------------------------------------------------------------------
+rlk_status rlk_logp_fused_lmhead_fp8(const rlk_logp_desc* desc, const rlk_fp8_matrix* hidden,
+                                     const rlk_fp8_matrix* weight, int64_t hidden_dim,
+                                     const int32_t* targets, const uint8_t* active_mask,
+                                     float* logp, float* lse, void* workspace,
+                                     size_t workspace_bytes, void* stream_ptr) {
+  rlk_status st = check_fused_desc(desc);
+  if (st != RLK_OK) return st;
+  st = check_hidden_dim(hidden_dim, rlk::kFp8Block);
+  if (st != RLK_OK) return st;
+  if (desc->num_tokens == 0) return ok();
+  if (!targets || !logp || !lse)
+    return fail(RLK_ERR_NULL_POINTER, "targets, logp and lse must be non-NULL");
+  rlk::LmheadFp8Args f;
+  st = check_fp8(hidden, weight, desc->num_tokens, desc->real_vocab, hidden_dim, &f);
+  if (st != RLK_OK) return st;
+  return run_fused_lmhead(desc, nullptr, nullptr, &f, hidden_dim, targets, active_mask, logp, lse,
+                          workspace, workspace_bytes, stream_ptr);
+}
+
+rlk_status rlk_lmhead_logits_fp8(const rlk_logp_desc* desc, const rlk_fp8_matrix* hidden,
+                                 const rlk_fp8_matrix* weight, int64_t hidden_dim, void* logits,
+                                 void* stream_ptr) {
+  rlk_status st = check_desc(desc);
+  if (st != RLK_OK) return st;
+  if (desc->flags) return fail(RLK_ERR_BAD_SHAPE, "logits have no data errors to validate");
+  st = check_hidden_dim(hidden_dim, rlk::kFp8Block);
+  if (st != RLK_OK) return st;
+  const int64_t n = desc->num_tokens;
+  if (n == 0) return ok();
+  if (!logits) return fail(RLK_ERR_NULL_POINTER, "logits must be non-NULL");
+  if (!aligned(logits, 16)) return fail(RLK_ERR_ALIGNMENT, "logits not 16-byte aligned");
+  rlk::LmheadFp8Args f;
+  st = check_fp8(hidden, weight, n, desc->real_vocab, hidden_dim, &f);
+  if (st != RLK_OK) return st;
+  if (rlk::lmhead_grid_blocks((int32_t)n, (int32_t)desc->padded_vocab) > kI32Max)
+    return fail(RLK_ERR_BAD_SHAPE, "num_tokens x vocabulary blocks too large for one launch");
+  const hipError_t e = rlk::launch_logits_fp8(
+      f, (int32_t)n, (int32_t)desc->real_vocab, (int32_t)desc->padded_vocab, logits,
+      desc->ld_logits, reinterpret_cast<hipStream_t>(stream_ptr));
+  if (e != hipSuccess) return hip_fail(e, "logits_fp8 launch");
+  return ok();
+}
+
+rlk_status rlk_fp8_quantize(int64_t rows, int64_t cols, const void* x, int64_t ld_x,
+                            int32_t block_rows, void* q, float* scale, int64_t scale_row_stride,
+                            int64_t scale_col_stride, void* stream_ptr) {
+  if (rows < 0 || rows > kI32Max)
+    return fail(RLK_ERR_BAD_SHAPE, "rows=%lld outside [0, 2^31-1]", (long long)rows);
+  rlk_status st = check_hidden_dim(cols, rlk::kFp8Block);
+  if (st != RLK_OK) return st;
+  if (block_rows != 1 && block_rows != rlk::kFp8Block)
+    return fail(RLK_ERR_BAD_TILING, "block_rows=%d is neither 1 nor %d", block_rows,
+                rlk::kFp8Block);
+  if (ld_x < cols)
+    return fail(RLK_ERR_BAD_SHAPE, "ld_x=%lld < cols=%lld", (long long)ld_x, (long long)cols);
+  if (ld_x % 8 != 0)
+    return fail(RLK_ERR_ALIGNMENT, "ld_x=%lld is not a multiple of 8 elements", (long long)ld_x);
+  if (scale_row_stride < 1 || scale_col_stride < 1)
+    return fail(RLK_ERR_BAD_SHAPE, "scale strides (%lld, %lld) must be positive",
+                (long long)scale_row_stride, (long long)scale_col_stride);
+  if (rows == 0) return ok();
+  if (!x || !q || !scale) return fail(RLK_ERR_NULL_POINTER, "x, q and scale must be non-NULL");
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4))
+    return fail(RLK_ERR_ALIGNMENT, "x and q must be 16-byte aligned, scale 4-byte aligned");
+  const rlk::Fp8QuantizeArgs a{x,     ld_x, rows, cols, block_rows, q, scale, scale_row_stride,
+                               scale_col_stride};
+  const hipError_t e = rlk::launch_fp8_quantize(a, reinterpret_cast<hipStream_t>(stream_ptr));
+  if (e != hipSuccess) return hip_fail(e, "fp8_quantize launch");
+  return ok();
+}
+
 // ---------------------------------------------------------------------------
 // Gradients of the fused LM-head.
 // ---------------------------------------------------------------------------
 namespace {
-
-rlk_status check_hidden_dim(int64_t hidden_dim, int32_t multiple) {
-  if (hidden_dim < multiple || hidden_dim % multiple != 0 || hidden_dim > rlk::kLmheadMaxHidden)
-    return fail(RLK_ERR_BAD_SHAPE, "hidden_dim=%lld must be a positive multiple of %d, at most %lld",
-                (long long)hidden_dim, multiple, (long long)rlk::kLmheadMaxHidden);
-  return RLK_OK;
-}
 
 rlk_status check_lmhead_bwd(const rlk_logp_desc* desc, int64_t hidden_dim) {
   rlk_status st = check_fused_desc(desc, 1);

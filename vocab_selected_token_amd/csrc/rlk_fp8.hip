@@ -1,0 +1,472 @@
+// rlk_fp8.hip -- the LM-head in 8-bit floating point (OCP e4m3) for gfx950: the
+// cast with one scale per block of 128, and the product of hidden states and
+// weight in that form, as bf16 logits or as selected-token statistics without
+// logits.
+//
+// A value is q * s: q in e4m3, s the fp32 scale of its block -- 1 x 128 for hidden
+// states (a token, 128 columns of the hidden dimension), 128 x 128 for the weight.
+// Both blocks are 128 wide along the dimension that the product sums over, so
+//   z[t][v] = sum_b s_h[t][b] s_w[v / 128][b] sum_{k in block b} q_h[t][k] q_w[v][k]
+// and one v_mfma_f32_16x16x128_f8f6f4 per 16 x 16 outputs covers a block: its fp32
+// result, times the two scales, is added to the fp32 accumulator in ascending b.
+// The sums do not depend on the tile, so a token's outputs have the same bits
+// whatever the batch, whichever of the two kernels computes them:
+//   fp8_tile    256 vocabulary rows x 256 tokens a block, both operands through
+//               LDS (the layout and loads of rlk_tile.h: a slab row is 128 bytes,
+//               here 128 columns).
+//   fp8_stream  256 vocabulary rows x up to 64 tokens a block, for few tokens, where
+//               the weight's bytes bound the time: each wave streams its 128 weight
+//               rows from memory straight into the matrix cores' registers.
+// Lane l of an MFMA supplies row l%16 and the 16-byte chunks l/16 and l/16 + 4 of
+// the 128 columns, for both operands alike; the result's layout is that of the
+// bf16 16 x 16 tiles (4 vocabulary rows of one token per lane).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "rlk_internal.h"
+#include "rlk_lmhead_segments.h"
+#include "rlk_tile.h"
+
+namespace rlk {
+namespace {
+
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
+
+constexpr float kE4m3Max = 448.0f;
+constexpr float kSmallestScale = 0x1p-126f;  // the smallest normal number
+
+static_assert(kRowBytes == kFp8Block, "a slab of the tile is one block of columns");
+
+// ---------------------------------------------------------------------------
+// The cast: s = max(largest magnitude / 448, 2^-126), q = e4m3(x / s), both
+// quotients correctly rounded (many entries lie midway between two e4m3 values,
+// so the last bit of the quotient decides them).  A block that holds NaN or
+// infinity gets that as its scale, and its product is NaN.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float block_scale(uint32_t top_bits) {
+  const float top = __uint_as_float(top_bits << 16);
+  return maxnan(top / kE4m3Max, kSmallestScale);
+}
+
+// Largest magnitude of 8 bf16 values as bf16 bits: as integers, magnitudes order
+// like the values, infinity above them and NaN above that.
+__device__ __forceinline__ uint32_t top_bits(const u32x4& x) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max(m, max((x[i] >> 16) & 0x7fff, x[i] & 0x7fff));
+  return m;
+}
+
+__device__ __forceinline__ uint64_t cast8(const u32x4& x, float s) {
+  union {
+    int32_t w[2];
+    uint64_t q;
+  } o;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float a = __uint_as_float(x[2 * i] << 16) / s;
+    const float b = __uint_as_float(x[2 * i] & 0xffff0000u) / s;
+    const float c = __uint_as_float(x[2 * i + 1] << 16) / s;
+    const float d = __uint_as_float(x[2 * i + 1] & 0xffff0000u) / s;
+    o.w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false),
+                                             true);
+  }
+  return o.q;
+}
+
+// 1 x 128 blocks: 16 lanes of 8 columns each.
+__global__ __launch_bounds__(256) void quantize_rows(const u32x4* __restrict__ x, int64_t ld,
+                                                     int64_t rows, int32_t col_blocks,
+                                                     uint64_t* __restrict__ q,
+                                                     float* __restrict__ scale, int64_t row_stride,
+                                                     int64_t col_stride, int64_t blk_begin) {
+  const int64_t b = (blk_begin + blockIdx.x) * 16 + (threadIdx.x >> 4);  // block of the matrix
+  if (b >= rows * col_blocks) return;
+  const int lane = threadIdx.x & 15;
+  const int64_t r = b / col_blocks;
+  const int32_t c = (int32_t)(b - r * col_blocks);
+  const u32x4 v = x[r * ld + c * 16 + lane];
+  uint32_t m = top_bits(v);
+#pragma unroll
+  for (int o = 8; o >= 1; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o));
+  const float s = block_scale(m);
+  q[b * 16 + lane] = cast8(v, s);
+  if (lane == 0) scale[r * row_stride + c * col_stride] = s;
+}
+
+// 128 x 128 blocks: one per thread block, 8 rows apart per thread, kept in
+// registers between the maximum and the cast.
+__global__ __launch_bounds__(256) void quantize_blocks(
+    const u32x4* __restrict__ x, int64_t ld, int64_t rows, int32_t col_blocks,
+    uint64_t* __restrict__ q, float* __restrict__ scale, int64_t row_stride, int64_t col_stride,
+    int64_t blk_begin) {
+  __shared__ uint32_t part[4];
+  const int64_t b = blk_begin + blockIdx.x;
+  const int64_t rb = b / col_blocks;
+  const int32_t c = (int32_t)(b - rb * col_blocks);
+  const int64_t r0 = rb * kFp8Block + (threadIdx.x >> 4);
+  const int lane = threadIdx.x & 15;
+  u32x4 v[8];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] = u32x4{0, 0, 0, 0};
+    if (r0 + i * 16 < rows) v[i] = x[(r0 + i * 16) * ld + c * 16 + lane];
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, top_bits(v[i]));
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o));
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
+  __syncthreads();
+  m = max(max(part[0], part[1]), max(part[2], part[3]));
+  const float s = block_scale(m);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (r0 + i * 16 < rows) q[(r0 + i * 16) * (col_blocks * 16) + c * 16 + lane] = cast8(v[i], s);
+  if (threadIdx.x == 0) scale[rb * row_stride + c * col_stride] = s;
+}
+
+// ---------------------------------------------------------------------------
+// The product.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ f32x4 mfma_block(const i32x8& a, const i32x8& b) {
+  // both operands e4m3; the MX scales are not used (1)
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0,
+                                                          0, 0, 0, 0, 0);
+}
+
+__device__ __forceinline__ i32x8 join(const i32x4& lo, const i32x4& hi) {
+  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+__device__ __forceinline__ void add_scaled(f32x4& acc, const f32x4& z, float f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = fmaf(z[i], f, acc[i]);
+}
+
+// What both kernels read.
+struct Fp8Operands {
+  const char* __restrict__ hq;     // [num_tokens][hidden_dim]
+  const float* __restrict__ hs;    // (token, block) at token * hs_row + block * hs_col
+  const char* __restrict__ wq;     // [>= real_vocab][hidden_dim]
+  const float* __restrict__ ws;    // (128-row block, block)
+  int64_t hs_row, hs_col, ws_row, ws_col;
+  int32_t hidden_dim;
+};
+
+// Where logits go (kLogits kernels).
+struct LogitsOut {
+  uint16_t* __restrict__ out;  // bf16 [num_tokens][ld]
+  int64_t ld;
+  int32_t num_tokens, real_vocab, padded_vocab;
+};
+
+__device__ __forceinline__ uint16_t bf16_bits(float x) {
+  const __bf16 b = (__bf16)x;  // to nearest even
+  return __builtin_bit_cast(uint16_t, b);
+}
+
+// Work index -> (vocabulary block, token block): see lmhead_segments.
+__device__ __forceinline__ void block_of(int64_t blk, int32_t n_vbs, int32_t n_tb, int32_t& vb,
+                                         int32_t& tb) {
+  constexpr int32_t kGroupV = 4;
+  const int64_t strip = blk / ((int64_t)kGroupV * n_tb);
+  const int32_t r_in = (int32_t)(blk - strip * kGroupV * n_tb);
+  const int32_t strip_w = min(kGroupV, n_vbs - (int32_t)strip * kGroupV);
+  vb = (int32_t)strip * kGroupV + r_in % strip_w;
+  tb = r_in / strip_w;
+}
+
+// This wave's logits of token t (lane's), columns from v on (4 of them), as bf16;
+// -inf from the real vocabulary's end to the padded one's.
+__device__ __forceinline__ void store_logits(const LogitsOut& o, int32_t t, int32_t v,
+                                             const f32x4& z) {
+  if (t >= o.num_tokens || v >= o.padded_vocab) return;
+  union {
+    uint16_t e[4];
+    uint64_t x;
+  } u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) u.e[i] = v + i < o.real_vocab ? bf16_bits(z[i]) : (uint16_t)0xff80;
+  uint16_t* out = o.out + (int64_t)t * o.ld + v;
+  if (v + 4 <= o.padded_vocab) {
+    *reinterpret_cast<uint64_t*>(out) = u.x;
+  } else {
+    for (int i = 0; i < 4; ++i)
+      if (v + i < o.padded_vocab) out[i] = u.e[i];
+  }
+}
+
+constexpr int kScaleLds = kBB * (int)sizeof(float);  // a slab's token scales
+
+template <bool kLogits>
+__global__ __launch_bounds__(kThreads) void fp8_tile(Fp8Operands p, SegmentArgs a, LogitsOut lo,
+                                                     int32_t n_tb, int32_t vb_begin,
+                                                     int32_t n_vbs, int64_t blk_begin) {
+  __shared__ __attribute__((aligned(16))) char smem[kTileLds + 2 * kScaleLds];
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wv = wave >> 2, wt = wave & 3;
+  int32_t vb, tb;
+  block_of(blk_begin + xcd_local_block(blockIdx.x, gridDim.x), n_vbs, n_tb, vb, tb);
+  vb += vb_begin;
+  const int32_t v0 = vb * kBA, t0 = tb * kBB;
+
+  f32x4 acc[kVS][kTS];
+#pragma unroll
+  for (int vs = 0; vs < kVS; ++vs)
+#pragma unroll
+    for (int ts = 0; ts < kTS; ++ts) acc[vs][ts] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  if (!kLogits || v0 < a.row_hi) {  // else a block of padding: only logits has them
+    const int64_t row_bytes = p.hidden_dim;
+    const int32_t w_first = max(v0, a.row_lo);
+    const TileOperand wo(p.wq + (int64_t)w_first * row_bytes, row_bytes,
+                         min(v0 + kBA, a.row_hi) - w_first, v0 - w_first, wave, lane);
+    const TileOperand ho(p.hq + (int64_t)t0 * row_bytes, row_bytes,
+                         min(t0 + kBB, a.num_tokens) - t0, 0, wave, lane);
+    const int nslab = p.hidden_dim / kFp8Block;
+    // token scales: wave w < 4 loads those of tokens [64w, 64w + 64), one per lane
+    const int32_t last = min(t0 + kBB, a.num_tokens) - t0 - 1;
+    const __amdgpu_buffer_rsrc_t srs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<float*>(p.hs + (int64_t)t0 * p.hs_row), 0,
+        (int)((last * p.hs_row + (nslab - 1) * p.hs_col + 1) * 4), kBufferWord3);
+    const uint32_t s_off = (uint32_t)(min(wave * 64 + lane, last) * p.hs_row * 4);
+    // this wave's weight scale: its 128 rows are one block (rows past the real
+    // vocabulary's last block are not used: clamped)
+    const int32_t wb = min(v0 / kFp8Block + wv, (a.row_hi - 1) / kFp8Block);
+    const float* __restrict__ wsp = p.ws + (int64_t)wb * p.ws_row;
+
+    auto issue = [&](int slab, int stage) __attribute__((always_inline)) {
+      char* base = smem + stage * 2 * kSlabBytes;
+      wo.issue(base, wave, (uint32_t)slab * kRowBytes);
+      ho.issue(base + kSlabBytes, wave, (uint32_t)slab * kRowBytes);
+      if (wave < 4)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            srs, (lds_ptr)(smem + kTileLds + stage * kScaleLds + wave * 256), 4, s_off,
+            (uint32_t)(slab * p.hs_col * 4), 0, 0);
+    };
+    const int fr = lane & 15, fc = lane >> 4;
+    auto frag = [&](const char* op, int row) __attribute__((always_inline)) {
+      return join(*reinterpret_cast<const i32x4*>(op + swizzled(row, fc) * 16),
+                  *reinterpret_cast<const i32x4*>(op + swizzled(row, 4 + fc) * 16));
+    };
+
+    issue(0, 0);
+    if (nslab > 1) issue(1, 1);
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    for (int s = 0; s < nslab; ++s) {
+      const char* As = smem + (s & 1) * 2 * kSlabBytes;
+      const char* Bs = As + kSlabBytes;
+      const float* sc = reinterpret_cast<const float*>(smem + kTileLds + (s & 1) * kScaleLds);
+      const float sw = wsp[s * p.ws_col];
+      i32x8 b[kTS];
+      float f[kTS];
+#pragma unroll
+      for (int ts = 0; ts < kTS; ++ts) {
+        b[ts] = frag(Bs, wt * 64 + ts * 16 + fr);
+        f[ts] = sc[wt * 64 + ts * 16 + fr] * sw;
+      }
+#pragma unroll
+      for (int vs = 0; vs < kVS; ++vs) {
+        const i32x8 av = frag(As, wv * 128 + vs * 16 + fr);
+#pragma unroll
+        for (int ts = 0; ts < kTS; ++ts) add_scaled(acc[vs][ts], mfma_block(av, b[ts]), f[ts]);
+      }
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();  // every wave has read slab s, and slab s+1 has landed
+      if (s + 2 < nslab) issue(s + 2, s & 1);
+    }
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+  }
+  if constexpr (kLogits) {
+#pragma unroll
+    for (int ts = 0; ts < kTS; ++ts)
+#pragma unroll
+      for (int vs = 0; vs < kVS; ++vs)
+        store_logits(lo, t0 + (wt * kTS + ts) * 16 + (lane & 15),
+                     v0 + wv * 128 + vs * 16 + 4 * (lane >> 4), acc[vs][ts]);
+  } else {
+    write_segments<kTS>(a, acc, reinterpret_cast<float*>(smem), vb, t0, wv, wt, lane);
+  }
+}
+
+// Few tokens: two waves, each 128 vocabulary rows x all tokens (16 kTok of them at
+// most), operands from global memory into registers, the next slab's while this
+// one's is multiplied.
+template <bool kLogits, int kTok>
+__global__ __launch_bounds__(128) void fp8_stream(Fp8Operands p, SegmentArgs a, LogitsOut lo,
+                                                  int32_t vb_begin, int64_t blk_begin) {
+  __shared__ float xch[16 * kTok * 4];
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int32_t vb = vb_begin + (int32_t)(blk_begin + blockIdx.x);
+  const int32_t v0 = vb * kBA;
+  f32x4 acc[kVS][kTok];
+#pragma unroll
+  for (int vs = 0; vs < kVS; ++vs)
+#pragma unroll
+    for (int ts = 0; ts < kTok; ++ts) acc[vs][ts] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  if (!kLogits || v0 < a.row_hi) {
+    const int64_t row_bytes = p.hidden_dim;
+    const int32_t w_first = max(v0, a.row_lo);
+    const int32_t w_rows = min(v0 + kBA, a.row_hi) - w_first;
+    const __amdgpu_buffer_rsrc_t wrs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(p.wq + (int64_t)w_first * row_bytes), 0, (int)(w_rows * row_bytes),
+        kBufferWord3);
+    const __amdgpu_buffer_rsrc_t hrs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(p.hq), 0, (int)(a.num_tokens * row_bytes), kBufferWord3);
+    const int nslab = p.hidden_dim / kFp8Block;
+    const int fr = lane & 15, fc = (lane >> 4) * 16;
+    uint32_t woff[kVS], hoff[kTok];
+    const float* __restrict__ hsp[kTok];
+#pragma unroll
+    for (int vs = 0; vs < kVS; ++vs)
+      woff[vs] = (uint32_t)(min(max(v0 + wv * 128 + vs * 16 + fr, w_first), w_first + w_rows - 1) -
+                            w_first) * (uint32_t)row_bytes + fc;
+#pragma unroll
+    for (int ts = 0; ts < kTok; ++ts) {
+      const int32_t t = min(ts * 16 + fr, a.num_tokens - 1);
+      hoff[ts] = (uint32_t)t * (uint32_t)row_bytes + fc;
+      hsp[ts] = p.hs + t * p.hs_row;
+    }
+    const int32_t wb = min(v0 / kFp8Block + wv, (a.row_hi - 1) / kFp8Block);
+    const float* __restrict__ wsp = p.ws + (int64_t)wb * p.ws_row;
+
+    i32x4 aw[2][kVS][2], bh[2][kTok][2];
+    float f[2][kTok];
+    auto load = [&](int slab, int at) __attribute__((always_inline)) {
+      const uint32_t soff = (uint32_t)slab * kRowBytes;
+#pragma unroll
+      for (int vs = 0; vs < kVS; ++vs)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          aw[at][vs][c] = __builtin_bit_cast(
+              i32x4, __builtin_amdgcn_raw_buffer_load_b128(wrs, woff[vs] + c * 64, soff, 0));
+#pragma unroll
+      for (int ts = 0; ts < kTok; ++ts) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          bh[at][ts][c] = __builtin_bit_cast(
+              i32x4, __builtin_amdgcn_raw_buffer_load_b128(hrs, hoff[ts] + c * 64, soff, 0));
+        f[at][ts] = hsp[ts][slab * p.hs_col] * wsp[slab * p.ws_col];
+      }
+    };
+    auto multiply = [&](int at) __attribute__((always_inline)) {
+#pragma unroll
+      for (int vs = 0; vs < kVS; ++vs)
+#pragma unroll
+        for (int ts = 0; ts < kTok; ++ts)
+          add_scaled(acc[vs][ts],
+                     mfma_block(join(aw[at][vs][0], aw[at][vs][1]),
+                                join(bh[at][ts][0], bh[at][ts][1])),
+                     f[at][ts]);
+    };
+    load(0, 0);
+    int s = 0;
+    for (; s + 2 <= nslab; s += 2) {
+      load(s + 1, 1);
+      multiply(0);
+      if (s + 2 < nslab) load(s + 2, 0);
+      multiply(1);
+    }
+    if (s < nslab) multiply(0);
+  }
+  if constexpr (kLogits) {
+#pragma unroll
+    for (int ts = 0; ts < kTok; ++ts)
+#pragma unroll
+      for (int vs = 0; vs < kVS; ++vs)
+        store_logits(lo, ts * 16 + (lane & 15), v0 + wv * 128 + vs * 16 + 4 * (lane >> 4),
+                     acc[vs][ts]);
+  } else {
+    write_segments<kTok>(a, acc, xch, vb, 0, wv, 0, lane);
+  }
+}
+
+// Launches the blocks [vb_begin, vb_begin + n_vbs) of the 256-column grid.
+// Up to 64 tokens the weight's bytes bound the time and the streaming kernel's
+// registers hold all tokens; above, the tile shares each weight slab among 256.
+template <bool kLogits>
+hipError_t launch_blocks(const Fp8Operands& p, const SegmentArgs& sa, const LogitsOut& lo,
+                         int32_t vb_begin, int32_t n_vbs, hipStream_t stream) {
+  const int32_t n = sa.num_tokens;
+  const bool few = n <= 64;
+  const int threads = few ? 128 : kThreads;
+  const int32_t n_tb = (n + kBB - 1) / kBB;
+  const int64_t blocks = few ? n_vbs : (int64_t)n_vbs * n_tb;
+  const int64_t most = launch_thread_limit() / threads;
+  for (int64_t b = 0; b < blocks; b += most) {
+    const dim3 grid((unsigned)(blocks - b < most ? blocks - b : most));
+    if (n <= 16)
+      hipLaunchKernelGGL((fp8_stream<kLogits, 1>), grid, dim3(threads), 0, stream, p, sa, lo,
+                         vb_begin, b);
+    else if (n <= 32)
+      hipLaunchKernelGGL((fp8_stream<kLogits, 2>), grid, dim3(threads), 0, stream, p, sa, lo,
+                         vb_begin, b);
+    else if (few)
+      hipLaunchKernelGGL((fp8_stream<kLogits, 4>), grid, dim3(threads), 0, stream, p, sa, lo,
+                         vb_begin, b);
+    else
+      hipLaunchKernelGGL((fp8_tile<kLogits>), grid, dim3(threads), 0, stream, p, sa, lo, n_tb,
+                         vb_begin, n_vbs, b);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+Fp8Operands operands(const LmheadFp8Args& a) {
+  return {static_cast<const char*>(a.hidden_q), a.hidden_scale,
+          static_cast<const char*>(a.weight_q), a.weight_scale,
+          a.hidden_row_stride, a.hidden_col_stride, a.weight_row_stride, a.weight_col_stride,
+          a.hidden_dim};
+}
+
+}  // namespace
+
+hipError_t launch_fp8_quantize(const Fp8QuantizeArgs& a, hipStream_t stream) {
+  const int32_t col_blocks = (int32_t)(a.cols / kFp8Block);
+  const bool wide = a.block_rows > 1;
+  const int64_t items = wide ? (a.rows + kFp8Block - 1) / kFp8Block * col_blocks
+                             : (a.rows * col_blocks + 15) / 16;
+  const int64_t most = launch_thread_limit() / 256;
+  for (int64_t b = 0; b < items; b += most) {
+    const dim3 grid((unsigned)(items - b < most ? items - b : most));
+    const u32x4* x = reinterpret_cast<const u32x4*>(a.x);
+    uint64_t* q = reinterpret_cast<uint64_t*>(a.q);
+    if (wide)
+      hipLaunchKernelGGL(quantize_blocks, grid, dim3(256), 0, stream, x, a.ld / 8, a.rows,
+                         col_blocks, q, a.scale, a.scale_row_stride, a.scale_col_stride, b);
+    else
+      hipLaunchKernelGGL(quantize_rows, grid, dim3(256), 0, stream, x, a.ld / 8, a.rows,
+                         col_blocks, q, a.scale, a.scale_row_stride, a.scale_col_stride, b);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+hipError_t launch_segments_fp8(const LmheadFp8Args& f, const SegmentArgs& sa, int32_t vb_begin,
+                               int32_t n_vbs, hipStream_t stream) {
+  return launch_blocks<false>(operands(f), sa, LogitsOut{}, vb_begin, n_vbs, stream);
+}
+
+hipError_t launch_logits_fp8(const LmheadFp8Args& f, int32_t num_tokens, int32_t real_vocab,
+                             int32_t padded_vocab, void* logits, int64_t ld,
+                             hipStream_t stream) {
+  SegmentArgs sa{};
+  sa.num_tokens = num_tokens;
+  sa.row_hi = real_vocab;
+  const LogitsOut lo{reinterpret_cast<uint16_t*>(logits), ld, num_tokens, real_vocab,
+                     padded_vocab};
+  return launch_blocks<true>(operands(f), sa, lo, 0, (padded_vocab + kBA - 1) / kBA, stream);
+}
+
+}  // namespace rlk

@@ -133,6 +133,48 @@ struct LmheadArgs {
   float* psum;
 };
 
+// Where a block's statistics go, and what they cover.
+struct SegmentArgs {
+  int32_t num_tokens;
+  int32_t padded_vocab;
+  int32_t num_tiles;
+  int32_t n_vb;            // vocabulary blocks of the whole problem
+  int32_t row_lo, row_hi;  // the shard's real rows: others neither read nor counted
+  int32_t col_lo, col_hi;  // the shard's columns: it writes the slots that start there
+  const int32_t* __restrict__ targets;
+  const uint8_t* __restrict__ mask;
+  int32_t ignore_index;
+  float* __restrict__ seg_m;  // [num_tokens][2 * n_vb]
+  float* __restrict__ seg_s;
+  float* __restrict__ tlogit;  // [num_tokens]
+};
+
+// A matrix in 8-bit floating point: columns that share a scale.
+constexpr int32_t kFp8Block = 128;
+
+struct Fp8QuantizeArgs {
+  const void* x;  // bf16 [rows, ld]
+  int64_t ld;
+  int64_t rows;
+  int64_t cols;        // a multiple of 128
+  int32_t block_rows;  // 1 or 128
+  void* q;             // e4m3 [rows, cols]
+  float* scale;        // (row block, column block) at these strides
+  int64_t scale_row_stride;
+  int64_t scale_col_stride;
+};
+
+// The operands of an 8-bit LM-head.
+struct LmheadFp8Args {
+  const void* hidden_q;       // e4m3 [num_tokens, hidden_dim]
+  const float* hidden_scale;  // (token, column block)
+  const void* weight_q;       // e4m3 [>= real_vocab, hidden_dim]
+  const float* weight_scale;  // (128-row block, column block)
+  int64_t hidden_row_stride, hidden_col_stride;
+  int64_t weight_row_stride, weight_col_stride;
+  int32_t hidden_dim;
+};
+
 // Gradients of the fused LM-head.  Byte offsets into its workspace (the status
 // words come first): what is known of the live rows, their hidden states by
 // tokens and by columns, a piece of dz by tokens and by columns, the piece of W
@@ -185,7 +227,15 @@ hipError_t noalloc_scratch(void** ptr);
 
 int64_t stage1_blocks(int64_t items);
 int64_t lmhead_grid_blocks(int32_t num_tokens, int32_t real_vocab);
-hipError_t launch_lmhead(const LmheadArgs& a, hipStream_t stream);
+// The LM-head's segments and tile partials; with fp8 its operands (a.hidden and
+// a.weight are not used).
+hipError_t launch_lmhead(const LmheadArgs& a, const LmheadFp8Args* fp8, hipStream_t stream);
+// One shard's segments: the blocks [vb_begin, vb_begin + n_vbs) of the grid.
+hipError_t launch_segments_fp8(const LmheadFp8Args& f, const SegmentArgs& sa, int32_t vb_begin,
+                               int32_t n_vbs, hipStream_t stream);
+hipError_t launch_logits_fp8(const LmheadFp8Args& f, int32_t num_tokens, int32_t real_vocab,
+                             int32_t padded_vocab, void* logits, int64_t ld, hipStream_t stream);
+hipError_t launch_fp8_quantize(const Fp8QuantizeArgs& a, hipStream_t stream);
 LmheadBwdLayout lmhead_bwd_layout(int64_t num_tokens, int64_t hidden_dim, int64_t padded_vocab,
                                   bool want_dhidden, bool want_dweight);
 hipError_t launch_lmhead_bwd(const LmheadBwdArgs& a, hipStream_t stream);

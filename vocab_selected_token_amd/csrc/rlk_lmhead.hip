@@ -169,13 +169,33 @@ int64_t lmhead_grid_blocks(int32_t num_tokens, int32_t real_vocab) {
   return n_vb * n_tb;
 }
 
-hipError_t launch_lmhead(const LmheadArgs& a, hipStream_t stream) {
+namespace {
+
+// One shard's segments, in launches of at most `limit` threads; a block's work
+// index (and so its tile) does not depend on the split.
+hipError_t launch_segments(const LmheadArgs& a, const SegmentArgs& sa, int32_t vb_begin,
+                           int32_t n_vbs, hipStream_t stream) {
+  const int32_t n_tb = (a.num_tokens + kBT - 1) / kBT;
+  const int64_t max_blocks = launch_thread_limit() / kThreads;
+  const int64_t blocks = (int64_t)n_vbs * n_tb;
+  for (int64_t b0 = 0; b0 < blocks; b0 += max_blocks) {
+    const int64_t nb = blocks - b0 < max_blocks ? blocks - b0 : max_blocks;
+    hipLaunchKernelGGL(lmhead_segments, dim3((unsigned)nb), dim3(kThreads), 0, stream,
+                       reinterpret_cast<const u32x4*>(a.hidden),
+                       reinterpret_cast<const u32x4*>(a.weight), a.hidden_dim, n_tb, vb_begin,
+                       n_vbs, sa, b0);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_lmhead(const LmheadArgs& a, const LmheadFp8Args* fp8, hipStream_t stream) {
   if (a.num_tokens == 0) return hipSuccess;
   const int32_t n_vb = (a.real_vocab + kBV - 1) / kBV;
-  const int32_t n_tb = (a.num_tokens + kBT - 1) / kBT;
-  const int64_t limit = launch_thread_limit();
-  const int64_t max_blocks = limit / kThreads;
-  const int64_t max_items = limit / 256 * 256;
+  const int64_t max_items = launch_thread_limit() / 256 * 256;
   auto bound = [&](int64_t t) { return (int32_t)((t * a.padded_vocab) / a.num_tiles); };
   // Virtual shard s owns tiles [floor(s*T/S), floor((s+1)*T/S)): its GEMM
   // blocks, then its tiles' partials.  A block cut by a shard bound is
@@ -188,21 +208,13 @@ hipError_t launch_lmhead(const LmheadArgs& a, hipStream_t stream) {
     if (col_lo < row_hi) {  // a shard of padding only has no GEMM block
       const int32_t vb_begin = col_lo / kBV;
       const int32_t n_vbs = (row_hi - 1) / kBV + 1 - vb_begin;
-      // launches of at most limit / kThreads blocks; a block's work index (and
-      // so its tile) does not depend on the split
-      const int64_t blocks = (int64_t)n_vbs * n_tb;
-      for (int64_t b0 = 0; b0 < blocks; b0 += max_blocks) {
-        const int64_t nb = blocks - b0 < max_blocks ? blocks - b0 : max_blocks;
-        const SegmentArgs sa{a.num_tokens, a.padded_vocab, a.num_tiles, n_vb,     col_lo,
-                             row_hi,       col_lo,         col_hi,      a.targets, a.mask,
-                             a.ignore_index, a.seg_m,      a.seg_s,     a.target_logit};
-        hipLaunchKernelGGL(lmhead_segments, dim3((unsigned)nb), dim3(kThreads), 0, stream,
-                           reinterpret_cast<const u32x4*>(a.hidden),
-                           reinterpret_cast<const u32x4*>(a.weight), a.hidden_dim, n_tb, vb_begin,
-                           n_vbs, sa, b0);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-      }
+      const SegmentArgs sa{a.num_tokens, a.padded_vocab, a.num_tiles, n_vb,
+                           col_lo,       row_hi,         col_lo,      col_hi,
+                           a.targets,    a.mask,         a.ignore_index,
+                           a.seg_m,      a.seg_s,        a.target_logit};
+      const hipError_t e = fp8 ? launch_segments_fp8(*fp8, sa, vb_begin, n_vbs, stream)
+                               : launch_segments(a, sa, vb_begin, n_vbs, stream);
+      if (e != hipSuccess) return e;
     }
     const int64_t items = (int64_t)a.num_tokens * (tb - ta);
     for (int64_t i0 = 0; i0 < items; i0 += max_items) {

@@ -27,22 +27,6 @@ __device__ __forceinline__ int32_t inner_tile_bound(int32_t v0, int32_t padded_v
   return (b > v0 && b < v0 + kLmheadBlockVocab) ? b : v0 + kLmheadBlockVocab;
 }
 
-// Where a block's statistics go, and what they cover.
-struct SegmentArgs {
-  int32_t num_tokens;
-  int32_t padded_vocab;
-  int32_t num_tiles;
-  int32_t n_vb;            // vocabulary blocks of the whole problem
-  int32_t row_lo, row_hi;  // the shard's real rows: others neither read nor counted
-  int32_t col_lo, col_hi;  // the shard's columns: it writes the slots that start there
-  const int32_t* __restrict__ targets;
-  const uint8_t* __restrict__ mask;
-  int32_t ignore_index;
-  float* __restrict__ seg_m;  // [num_tokens][2 * n_vb]
-  float* __restrict__ seg_s;
-  float* __restrict__ tlogit;  // [num_tokens]
-};
-
 // acc: this wave's z of vocabulary rows [v0 + 128 wv, +128) and tokens
 // [t0 + 16 kTok wt, +16 kTok); xch: 4 floats per token of the block (LDS).
 // Every wave of the block calls it.  `vb` is v0 / 256.
