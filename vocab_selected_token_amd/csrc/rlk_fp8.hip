@@ -199,7 +199,12 @@ __device__ __forceinline__ void store_logits(const LogitsOut& o, int32_t t, int3
   }
 }
 
-constexpr int kScaleLds = kBB * (int)sizeof(float);  // a slab's token scales
+constexpr int kScaleLds = kThreads * (int)sizeof(float);  // a slab's token scales, by wave
+
+// Read through the scalar cache (a uniform address; written before the launch).
+__device__ __forceinline__ float scalar_load(const float* p) {
+  return *(const __attribute__((address_space(4))) float*)(uintptr_t)p;
+}
 
 template <bool kLogits>
 __global__ __launch_bounds__(kThreads) void fp8_tile(Fp8Operands p, SegmentArgs a, LogitsOut lo,
@@ -229,12 +234,13 @@ __global__ __launch_bounds__(kThreads) void fp8_tile(Fp8Operands p, SegmentArgs 
     const TileOperand ho(p.hq + (int64_t)t0 * row_bytes, row_bytes,
                          min(t0 + kBB, a.num_tokens) - t0, 0, wave, lane);
     const int nslab = p.hidden_dim / kFp8Block;
-    // token scales: wave w < 4 loads those of tokens [64w, 64w + 64), one per lane
+    // token scales: each wave loads those of its 64 tokens, one per lane
     const int32_t last = min(t0 + kBB, a.num_tokens) - t0 - 1;
     const __amdgpu_buffer_rsrc_t srs = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<float*>(p.hs + (int64_t)t0 * p.hs_row), 0,
         (int)((last * p.hs_row + (nslab - 1) * p.hs_col + 1) * 4), kBufferWord3);
-    const uint32_t s_off = (uint32_t)(min(wave * 64 + lane, last) * p.hs_row * 4);
+    const uint32_t s_off = (uint32_t)(min(wt * 64 + lane, last) * p.hs_row * 4);
+    const uint32_t s_step = (uint32_t)p.hs_col * 4;
     // this wave's weight scale: its 128 rows are one block (rows past the real
     // vocabulary's last block are not used: clamped)
     const int32_t wb = min(v0 / kFp8Block + wv, (a.row_hi - 1) / kFp8Block);
@@ -244,43 +250,120 @@ __global__ __launch_bounds__(kThreads) void fp8_tile(Fp8Operands p, SegmentArgs 
       char* base = smem + stage * 2 * kSlabBytes;
       wo.issue(base, wave, (uint32_t)slab * kRowBytes);
       ho.issue(base + kSlabBytes, wave, (uint32_t)slab * kRowBytes);
-      if (wave < 4)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            srs, (lds_ptr)(smem + kTileLds + stage * kScaleLds + wave * 256), 4, s_off,
-            (uint32_t)(slab * p.hs_col * 4), 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          srs, (lds_ptr)(smem + kTileLds + stage * kScaleLds + wave * 256), 4, s_off,
+          (uint32_t)slab * s_step, 0, 0);
     };
+    // Fragment reads.  Rows 16 apart have the same swizzle, so a fragment is at a
+    // fixed distance from the wave's first: the lane's offset of its two chunks
+    // (the second's position differs in one bit) plus an immediate.
     const int fr = lane & 15, fc = lane >> 4;
-    auto frag = [&](const char* op, int row) __attribute__((always_inline)) {
-      return join(*reinterpret_cast<const i32x4*>(op + swizzled(row, fc) * 16),
-                  *reinterpret_cast<const i32x4*>(op + swizzled(row, 4 + fc) * 16));
+    const int lo0 = swizzled(fr, fc) * 16, lo1 = lo0 ^ 64;
+    auto frag = [&](const char* first, int tile) __attribute__((always_inline)) {
+      return join(*reinterpret_cast<const i32x4*>(first + lo0 + tile * 16 * kRowBytes),
+                  *reinterpret_cast<const i32x4*>(first + lo1 + tile * 16 * kRowBytes));
+    };
+
+    // A slab's 32 MFMAs go in four quarters of two 16-row tiles of A.  A quarter
+    // reads the next quarter's A fragments while its MFMAs run (two buffers of
+    // two fragments), and the last quarter, which follows the slab's barrier,
+    // also replaces B fragment by fragment as soon as its last MFMA has it: the
+    // whole slab of fragments would not fit beside 128 accumulators.  Each
+    // MFMA's result is scaled and added while the next one runs.
+    i32x8 a0[2], a1[2], b[kTS];
+    float f[kTS];
+    f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};  // the MFMA result not yet added
+    auto read_a = [&](const char* stage, int q, i32x8 (&a)[2]) __attribute__((always_inline)) {
+      a[0] = frag(stage + wv * 128 * kRowBytes, 2 * q);
+      a[1] = frag(stage + wv * 128 * kRowBytes, 2 * q + 1);
+    };
+    auto read_b = [&](const char* stage, int ts) __attribute__((always_inline)) {
+      b[ts] = frag(stage + kSlabBytes + wt * 64 * kRowBytes, ts);
+    };
+    auto scale_of = [&](int s, int ts) __attribute__((always_inline)) {
+      const char* at = smem + kTileLds + (s & 1) * kScaleLds;
+      return reinterpret_cast<const float*>(at)[wave * 64 + ts * 16 + fr];
+    };
+    // MFMA (q, j) of a slab is tile vs = 2q + j%2, ts = j/2
+    auto step = [&](int q, int j, const i32x8 (&a)[2], float fz) __attribute__((always_inline)) {
+      const f32x4 n = mfma_block(a[j & 1], b[j >> 1]);
+      const int pq = j ? q : q - 1, pj = j ? j - 1 : 7;  // the previous one's place
+      add_scaled(acc[2 * (pq < 0 ? 3 : pq) + (pj & 1)][pj >> 1], z, fz);
+      z = n;
+    };
+    auto order = [&](int reads) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                  // MFMA
+        if (i < reads) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
+        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);                  // VALU
+      }
     };
 
     issue(0, 0);
     if (nslab > 1) issue(1, 1);
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
+    read_a(smem, 0, a0);
+#pragma unroll
+    for (int ts = 0; ts < kTS; ++ts) read_b(smem, ts);
+    float fp = 0.0f;  // the factor of z
+    float sw = scalar_load(wsp);
     for (int s = 0; s < nslab; ++s) {
-      const char* As = smem + (s & 1) * 2 * kSlabBytes;
-      const char* Bs = As + kSlabBytes;
-      const float* sc = reinterpret_cast<const float*>(smem + kTileLds + (s & 1) * kScaleLds);
-      const float sw = wsp[s * p.ws_col];
-      i32x8 b[kTS];
-      float f[kTS];
+      const char* cur = smem + (s & 1) * 2 * kSlabBytes;
+      const char* nxt = smem + ((s + 1) & 1) * 2 * kSlabBytes;
+      float g[kTS];
 #pragma unroll
-      for (int ts = 0; ts < kTS; ++ts) {
-        b[ts] = frag(Bs, wt * 64 + ts * 16 + fr);
-        f[ts] = sc[wt * 64 + ts * 16 + fr] * sw;
-      }
+      for (int ts = 0; ts < kTS; ++ts) g[ts] = scale_of(s, ts);
+      __builtin_amdgcn_s_waitcnt(kWaitLds);
 #pragma unroll
-      for (int vs = 0; vs < kVS; ++vs) {
-        const i32x8 av = frag(As, wv * 128 + vs * 16 + fr);
+      for (int ts = 0; ts < kTS; ++ts) f[ts] = g[ts] * sw;
+      sw = scalar_load(wsp + min(s + 1, nslab - 1) * p.ws_col);
+      read_a(cur, 1, a1);
 #pragma unroll
-        for (int ts = 0; ts < kTS; ++ts) add_scaled(acc[vs][ts], mfma_block(av, b[ts]), f[ts]);
-      }
+      for (int j = 0; j < 8; ++j) step(0, j, a0, j ? f[(j - 1) >> 1] : fp);
+      order(4);
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(kWaitLds);
+      read_a(cur, 2, a0);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) step(1, j, a1, j ? f[(j - 1) >> 1] : f[3]);
+      order(4);
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(kWaitLds);
+      read_a(cur, 3, a1);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) step(2, j, a0, j ? f[(j - 1) >> 1] : f[3]);
+      order(4);
+      __builtin_amdgcn_sched_barrier(0);
+      // every wave has read slab s into registers, and slab s+1 has landed
       __builtin_amdgcn_s_waitcnt(0);
-      __syncthreads();  // every wave has read slab s, and slab s+1 has landed
-      if (s + 2 < nslab) issue(s + 2, s & 1);
+      __syncthreads();
+      __builtin_amdgcn_sched_barrier(0);
+      // the last two steps reload the last slab and read fragments that nothing
+      // uses: unconditional, and in bounds
+      issue(min(s + 2, nslab - 1), s & 1);
+      read_a(nxt, 0, a0);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        step(3, j, a1, j ? f[(j - 1) >> 1] : f[3]);
+        if (j & 1) read_b(nxt, j >> 1);
+      }
+#pragma unroll
+      for (int j = 0; j < kTS; ++j) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // MFMA
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // VMEM
+        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);  // VALU
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+      }
+      fp = f[3];
+      __builtin_amdgcn_sched_barrier(0);
     }
+    add_scaled(acc[7][3], z, fp);
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
   }
