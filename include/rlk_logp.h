@@ -442,11 +442,14 @@ rlk_status rlk_lmhead_logits_fp8(const rlk_logp_desc* desc, const rlk_fp8_matrix
 
 /* rlk_logp_fused_lmhead with 8-bit operands (hidden, weight and hidden_dim as for
  * rlk_lmhead_logits_fp8): logp and LSE of z, taken from the fp32 sums (not rounded to
- * bf16), never written to memory.  Everything else -- descriptor, tiles of at
- * least 256 columns, virtual shards, targets, mask, outputs, workspace
- * (rlk_logp_fused_lmhead_workspace_bytes), errors -- as for rlk_logp_fused_lmhead;
+ * bf16).  z is not written to memory, but for at most 64 tokens, whose few it keeps
+ * in the workspace.  Everything else -- descriptor, tiles of at least 256 columns,
+ * virtual shards, targets, mask, outputs, errors, where the status words and the
+ * per-tile partials lie in the workspace -- as for rlk_logp_fused_lmhead;
  * logp and LSE are bitwise the same for every num_virtual_shards and for a row
- * whatever other rows share the call. */
+ * whatever other rows share the call.
+ *   workspace   >= rlk_logp_fused_lmhead_fp8_workspace_bytes(desc), 256-byte aligned. */
+size_t rlk_logp_fused_lmhead_fp8_workspace_bytes(const rlk_logp_desc* desc);
 rlk_status rlk_logp_fused_lmhead_fp8(const rlk_logp_desc* desc, const rlk_fp8_matrix* hidden,
                                      const rlk_fp8_matrix* weight, int64_t hidden_dim,
                                      const int32_t* targets, const uint8_t* active_mask,

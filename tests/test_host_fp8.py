@@ -92,7 +92,12 @@ def test_fused_refuses():
     refused(fused, rlk.RLK_ERR_NULL_POINTER, tgt=None)
     refused(fused, rlk.RLK_ERR_NULL_POINTER, lse=None)
     refused(fused, rlk.RLK_ERR_WORKSPACE, ws=None)
-    need = rlk.rlk_logp_fused_lmhead_workspace_bytes(desc())
+    need = rlk.rlk_logp_fused_lmhead_fp8_workspace_bytes(desc())
+    # z of 8 tokens x 1000 columns, rounded up to 1024, beside the bf16 head's workspace
+    assert need == rlk.rlk_logp_fused_lmhead_workspace_bytes(desc()) + 8 * 1024 * 4
+    many = desc(num_tokens=65)
+    assert rlk.rlk_logp_fused_lmhead_fp8_workspace_bytes(many) == \
+        rlk.rlk_logp_fused_lmhead_workspace_bytes(many)
     refused(fused, rlk.RLK_ERR_WORKSPACE, ws=FakeTensor(0x20000000, need - 1))
     refused(fused, rlk.RLK_ERR_ALIGNMENT, ws=FakeTensor(0x20000010))
     fused(d=desc(num_tokens=0), h=None, w=None, tgt=None, logp=None, lse=None, ws=None)

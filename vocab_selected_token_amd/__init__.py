@@ -40,7 +40,8 @@ EXPORTED = ("rlk_logp_workspace_bytes", "rlk_logp_fwd", "rlk_logp_bwd",
             "rlk_logp_fwd_bwd_ex_workspace_bytes", "rlk_logp_fwd_bwd_ex",
             "rlk_logp_fused_lmhead_workspace_bytes", "rlk_logp_fused_lmhead",
             "rlk_logp_fused_lmhead_bwd_workspace_bytes", "rlk_logp_fused_lmhead_bwd",
-            "rlk_fp8_quantize", "rlk_lmhead_logits_fp8", "rlk_logp_fused_lmhead_fp8",
+            "rlk_fp8_quantize", "rlk_lmhead_logits_fp8",
+            "rlk_logp_fused_lmhead_fp8_workspace_bytes", "rlk_logp_fused_lmhead_fp8",
             "rlk_logp_tile_geometry", "rlk_status_string", "rlk_last_error_detail",
             "rlk_logp_fwd_noalloc")
 
@@ -110,6 +111,8 @@ def _load() -> ctypes.CDLL:
     lib.rlk_fp8_quantize.restype = ctypes.c_int
     lib.rlk_lmhead_logits_fp8.argtypes = [dp, mp, mp, i64, vp, vp]
     lib.rlk_lmhead_logits_fp8.restype = ctypes.c_int
+    lib.rlk_logp_fused_lmhead_fp8_workspace_bytes.argtypes = [dp]
+    lib.rlk_logp_fused_lmhead_fp8_workspace_bytes.restype = sz
     lib.rlk_logp_fused_lmhead_fp8.argtypes = [dp, mp, mp, i64, vp, vp, vp, vp, vp, sz, vp]
     lib.rlk_logp_fused_lmhead_fp8.restype = ctypes.c_int
     lib.rlk_logp_tile_geometry.argtypes = [i64, i32, i32, vp, vp]
@@ -280,6 +283,10 @@ def rlk_fp8_quantize(rows: int, cols: int, x, ld_x: int, block_rows: int, q, sca
 def rlk_lmhead_logits_fp8(desc, hidden, weight, hidden_dim: int, logits, stream=None) -> None:
     _check(_lib.rlk_lmhead_logits_fp8(ctypes.byref(desc), _ref(hidden), _ref(weight), hidden_dim,
                                       _ptr(logits), _stream(stream)))
+
+
+def rlk_logp_fused_lmhead_fp8_workspace_bytes(desc: rlk_logp_desc) -> int:
+    return int(_lib.rlk_logp_fused_lmhead_fp8_workspace_bytes(ctypes.byref(desc)))
 
 
 def rlk_logp_fused_lmhead_fp8(desc, hidden, weight, hidden_dim: int, targets, active_mask, logp,
@@ -867,7 +874,8 @@ def fused_lmhead_fp8(hidden, weight_q: torch.Tensor, weight_scale: torch.Tensor,
                      ignore_index, validate)
     with torch.cuda.device(x.device):
         if workspace is None:
-            workspace = _scratch(rlk_logp_fused_lmhead_workspace_bytes(desc), x.device, stream)
+            workspace = _scratch(rlk_logp_fused_lmhead_fp8_workspace_bytes(desc), x.device,
+                                 stream)
         q, scale = _fp8_pair(hidden, stream)
         logp = torch.empty(n, dtype=torch.float32, device=x.device)
         lse = torch.empty(n, dtype=torch.float32, device=x.device)

@@ -625,10 +625,11 @@ rlk_status check_fused_desc(const rlk_logp_desc* d, int32_t min_tile = rlk::kLmh
 }
 
 struct FusedLayout {
-  size_t pmax, psum, tlogit, seg_m, seg_s, total;
+  size_t pmax, psum, tlogit, seg_m, seg_s, z, total;
 };
 
-FusedLayout fused_layout(const rlk_logp_desc* d) {
+// fp8: the 8-bit head's, which keeps z of few tokens.
+FusedLayout fused_layout(const rlk_logp_desc* d, bool fp8) {
   const size_t n = (size_t)d->num_tokens;
   const size_t n_vb = ((size_t)d->real_vocab + rlk::kLmheadBlockVocab - 1) /
                       rlk::kLmheadBlockVocab;
@@ -640,7 +641,10 @@ FusedLayout fused_layout(const rlk_logp_desc* d) {
   l.tlogit = l.psum + part;
   l.seg_m = l.tlogit + round256(n * sizeof(float));
   l.seg_s = l.seg_m + seg;
-  l.total = l.seg_s + seg;
+  l.z = l.seg_s + seg;
+  l.total = l.z;
+  if (fp8 && d->num_tokens <= rlk::kFp8FewTokens)
+    l.total += round256(n * n_vb * rlk::kLmheadBlockVocab * sizeof(float));
   return l;
 }
 
@@ -648,7 +652,7 @@ FusedLayout fused_layout(const rlk_logp_desc* d) {
 
 size_t rlk_logp_fused_lmhead_workspace_bytes(const rlk_logp_desc* desc) {
   if (check_fused_desc(desc) != RLK_OK) return 0;
-  return fused_layout(desc).total;
+  return fused_layout(desc, false).total;
 }
 
 namespace {
@@ -691,18 +695,19 @@ rlk_status check_fp8(const rlk_fp8_matrix* hidden, const rlk_fp8_matrix* weight,
   out->weight_row_stride = weight->scale_row_stride;
   out->weight_col_stride = weight->scale_col_stride;
   out->hidden_dim = (int32_t)hidden_dim;
+  out->z = nullptr;
   return RLK_OK;
 }
 
 // The forward of rlk_logp_fused_lmhead (fp8 null) and rlk_logp_fused_lmhead_fp8,
 // whose descriptor, hidden_dim and operands have been checked.
 rlk_status run_fused_lmhead(const rlk_logp_desc* desc, const void* hidden, const void* weight,
-                            const rlk::LmheadFp8Args* fp8, int64_t hidden_dim,
+                            rlk::LmheadFp8Args* fp8, int64_t hidden_dim,
                             const int32_t* targets, const uint8_t* active_mask, float* logp,
                             float* lse, void* workspace, size_t workspace_bytes,
                             void* stream_ptr) {
   const int64_t n = desc->num_tokens;
-  const FusedLayout lay = fused_layout(desc);
+  const FusedLayout lay = fused_layout(desc, fp8 != nullptr);
   if (!workspace) return fail(RLK_ERR_WORKSPACE, "workspace is NULL");
   if (workspace_bytes < lay.total)
     return fail(RLK_ERR_WORKSPACE, "workspace_bytes=%zu < required %zu", workspace_bytes,
@@ -739,6 +744,7 @@ rlk_status run_fused_lmhead(const rlk_logp_desc* desc, const void* hidden, const
   a.target_logit = reinterpret_cast<float*>(ws + lay.tlogit);
   a.pmax = reinterpret_cast<float*>(ws + lay.pmax);
   a.psum = reinterpret_cast<float*>(ws + lay.psum);
+  if (fp8) fp8->z = reinterpret_cast<float*>(ws + lay.z);
   e = rlk::launch_lmhead(a, fp8, stream);
   if (e != hipSuccess) return hip_fail(e, "lmhead launch");
   rlk::Stage2Args a2;
@@ -790,6 +796,11 @@ rlk_status rlk_logp_fused_lmhead(const rlk_logp_desc* desc, const void* hidden,
 // ---------------------------------------------------------------------------
 // The LM-head in 8-bit floating point.
 // ---------------------------------------------------------------------------
+size_t rlk_logp_fused_lmhead_fp8_workspace_bytes(const rlk_logp_desc* desc) {
+  if (check_fused_desc(desc) != RLK_OK) return 0;
+  return fused_layout(desc, true).total;
+}
+
 rlk_status rlk_logp_fused_lmhead_fp8(const rlk_logp_desc* desc, const rlk_fp8_matrix* hidden,
                                      const rlk_fp8_matrix* weight, int64_t hidden_dim,
                                      const int32_t* targets, const uint8_t* active_mask,

@@ -14,9 +14,9 @@
 //   fp8_tile    256 vocabulary rows x 256 tokens a block, both operands through
 //               LDS (the layout and loads of rlk_tile.h: a slab row is 128 bytes,
 //               here 128 columns).
-//   fp8_stream  256 vocabulary rows x up to 64 tokens a block, for few tokens, where
-//               the weight's bytes bound the time: each wave streams its 128 weight
-//               rows from memory straight into the matrix cores' registers.
+//   fp8_stream  for up to 64 tokens, where the weight's bytes bound the time: each
+//               wave streams 16 weight rows from memory straight into the
+//               matrix cores' registers and holds all tokens.
 // Lane l of an MFMA supplies row l%16 and the 16-byte chunks l/16 and l/16 + 4 of
 // the 128 columns, for both operands alike; the result's layout is that of the
 // bf16 16 x 16 tiles (4 vocabulary rows of one token per lane).
@@ -379,130 +379,215 @@ __global__ __launch_bounds__(kThreads) void fp8_tile(Fp8Operands p, SegmentArgs 
   }
 }
 
-// Few tokens: two waves, each 128 vocabulary rows x all tokens (16 kTok of them at
-// most), operands from global memory into registers, the next slab's while this
-// one's is multiplied.
-template <bool kLogits, int kTok>
-__global__ __launch_bounds__(128) void fp8_stream(Fp8Operands p, SegmentArgs a, LogitsOut lo,
-                                                  int32_t vb_begin, int64_t blk_begin) {
-  __shared__ float xch[16 * kTok * 4];
-  const int lane = threadIdx.x & 63;
-  const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int32_t vb = vb_begin + (int32_t)(blk_begin + blockIdx.x);
-  const int32_t v0 = vb * kBA;
-  f32x4 acc[kVS][kTok];
-#pragma unroll
-  for (int vs = 0; vs < kVS; ++vs)
-#pragma unroll
-    for (int ts = 0; ts < kTok; ++ts) acc[vs][ts] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+// The stream kernel's fp32 z, kept between it and segments_of_z.
+struct ZOut {
+  float* __restrict__ z;  // [num_tokens][ld]
+  int64_t ld;
+  int32_t num_tokens;
+};
 
-  if (!kLogits || v0 < a.row_hi) {
-    const int64_t row_bytes = p.hidden_dim;
+__device__ __forceinline__ void store_z(const ZOut& o, int32_t t, int32_t v, const f32x4& z) {
+  if (t < o.num_tokens) *reinterpret_cast<f32x4*>(o.z + (int64_t)t * o.ld + v) = z;
+}
+
+// Few tokens (16 kTok at most): four waves, each 16 vocabulary rows x all tokens.
+// The weight is read once, from memory into registers, kBuf - 1 slabs ahead of the
+// one that is multiplied; the hidden states and their scales come through LDS, kBuf
+// slabs at a time, loaded while the previous ones are multiplied (read by every
+// wave from memory they cost as much as the weight: the loads of 16 rows x 64 bytes,
+// not the bytes, bound a CU's rate).  The blocks are small -- 64 rows, thousands of
+// them -- so that every CU ends at about the same time, and none waits for another:
+// the statistics, whose order spans 128 rows, are taken from z by segments_of_z.
+template <bool kLogits, int kTok>
+__global__ __launch_bounds__(256) void fp8_stream(Fp8Operands p, SegmentArgs a, LogitsOut lo,
+                                                  ZOut zo, int32_t v_begin, int64_t blk_begin) {
+  constexpr int kBuf = 4;                           // slabs in registers; slabs per LDS stage
+  constexpr int kTokens = 16 * kTok;
+  constexpr int kBytes = kTokens * kRowBytes;       // a slab's hidden states
+  constexpr int kCopies = kBuf * kBytes / 16 / 256;  // 16-byte loads per thread and stage
+  __shared__ __attribute__((aligned(16))) char hl[2][kBuf * kBytes];
+  __shared__ float sl[2][kBuf * kTokens];
+  static_assert(kBuf * kTokens <= 256, "a scale per thread at most");
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int32_t v0 = v_begin + (int32_t)(blk_begin + blockIdx.x) * 64;
+  const int32_t vw = v0 + wave * 16;
+  f32x4 acc[kTok];
+#pragma unroll
+  for (int ts = 0; ts < kTok; ++ts) acc[ts] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  if (v0 < a.row_hi && v0 + 64 > a.row_lo) {
+    const uint32_t row_bytes = (uint32_t)p.hidden_dim;
+    const int nslab = p.hidden_dim / kFp8Block;
+    // a wave outside the rows reads one of them all the same, unused
     const int32_t w_first = max(v0, a.row_lo);
-    const int32_t w_rows = min(v0 + kBA, a.row_hi) - w_first;
+    const int32_t w_rows = min(v0 + 64, a.row_hi) - w_first;
     const __amdgpu_buffer_rsrc_t wrs = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<char*>(p.wq + (int64_t)w_first * row_bytes), 0, (int)(w_rows * row_bytes),
         kBufferWord3);
     const __amdgpu_buffer_rsrc_t hrs = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<char*>(p.hq), 0, (int)(a.num_tokens * row_bytes), kBufferWord3);
-    const int nslab = p.hidden_dim / kFp8Block;
-    const int fr = lane & 15, fc = (lane >> 4) * 16;
-    uint32_t woff[kVS], hoff[kTok];
-    const float* __restrict__ hsp[kTok];
-#pragma unroll
-    for (int vs = 0; vs < kVS; ++vs)
-      woff[vs] = (uint32_t)(min(max(v0 + wv * 128 + vs * 16 + fr, w_first), w_first + w_rows - 1) -
-                            w_first) * (uint32_t)row_bytes + fc;
-#pragma unroll
-    for (int ts = 0; ts < kTok; ++ts) {
-      const int32_t t = min(ts * 16 + fr, a.num_tokens - 1);
-      hoff[ts] = (uint32_t)t * (uint32_t)row_bytes + fc;
-      hsp[ts] = p.hs + t * p.hs_row;
-    }
-    const int32_t wb = min(v0 / kFp8Block + wv, (a.row_hi - 1) / kFp8Block);
-    const float* __restrict__ wsp = p.ws + (int64_t)wb * p.ws_row;
+    const __amdgpu_buffer_rsrc_t srs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<float*>(p.hs), 0,
+        (int)(((a.num_tokens - 1) * p.hs_row + (nslab - 1) * p.hs_col + 1) * 4), kBufferWord3);
+    const int fr = lane & 15, fc = lane >> 4;
+    const uint32_t woff =
+        (uint32_t)min(max(vw + fr - w_first, 0), w_rows - 1) * row_bytes + fc * 16;
+    const float* __restrict__ wsp = p.ws + (int64_t)(w_first / kFp8Block) * p.ws_row;
 
-    i32x4 aw[2][kVS][2], bh[2][kTok][2];
-    float f[2][kTok];
-    auto load = [&](int slab, int at) __attribute__((always_inline)) {
-      const uint32_t soff = (uint32_t)slab * kRowBytes;
+    // this thread's part of a stage: slab, row and chunk of each copy; one scale
+    u32x4 copy[kCopies];
+    float scale;
+    auto load_stage = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
-      for (int vs = 0; vs < kVS; ++vs)
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          aw[at][vs][c] = __builtin_bit_cast(
-              i32x4, __builtin_amdgcn_raw_buffer_load_b128(wrs, woff[vs] + c * 64, soff, 0));
-#pragma unroll
-      for (int ts = 0; ts < kTok; ++ts) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          bh[at][ts][c] = __builtin_bit_cast(
-              i32x4, __builtin_amdgcn_raw_buffer_load_b128(hrs, hoff[ts] + c * 64, soff, 0));
-        f[at][ts] = hsp[ts][slab * p.hs_col] * wsp[slab * p.ws_col];
+      for (int j = 0; j < kCopies; ++j) {
+        const int e = j * 256 + tid, c = e & 7, r = (e >> 3) % kTokens, i = (e >> 3) / kTokens;
+        copy[j] = __builtin_bit_cast(
+            u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                       hrs,
+                       (uint32_t)min(r, a.num_tokens - 1) * row_bytes +
+                           (uint32_t)min(s + i, nslab - 1) * kRowBytes + c * 16,
+                       0, 0));
       }
+      const int r = tid % kTokens, i = min(tid / kTokens, kBuf - 1);
+      scale = __builtin_bit_cast(
+          float, __builtin_amdgcn_raw_buffer_load_b32(
+                     srs,
+                     (uint32_t)(min(r, a.num_tokens - 1) * p.hs_row +
+                                min(s + i, nslab - 1) * p.hs_col) * 4,
+                     0, 0));
     };
-    auto multiply = [&](int at) __attribute__((always_inline)) {
+    auto store_stage = [&](int at) __attribute__((always_inline)) {
 #pragma unroll
-      for (int vs = 0; vs < kVS; ++vs)
-#pragma unroll
-        for (int ts = 0; ts < kTok; ++ts)
-          add_scaled(acc[vs][ts],
-                     mfma_block(join(aw[at][vs][0], aw[at][vs][1]),
-                                join(bh[at][ts][0], bh[at][ts][1])),
-                     f[at][ts]);
+      for (int j = 0; j < kCopies; ++j) {
+        const int e = j * 256 + tid, c = e & 7, r = (e >> 3) % kTokens, i = (e >> 3) / kTokens;
+        *reinterpret_cast<u32x4*>(hl[at] + i * kBytes + swizzled(r, c) * 16) = copy[j];
+      }
+      if (tid < kBuf * kTokens) sl[at][tid] = scale;
     };
-    load(0, 0);
-    int s = 0;
-    for (; s + 2 <= nslab; s += 2) {
-      load(s + 1, 1);
-      multiply(0);
-      if (s + 2 < nslab) load(s + 2, 0);
-      multiply(1);
+    // LDS is written and read through this barrier; loads in flight stay there
+    auto barrier = [&]() __attribute__((always_inline)) {
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    };
+
+    i32x4 w[kBuf][2];
+    auto load = [&](int slab, int at) __attribute__((always_inline)) {
+      const uint32_t off = (uint32_t)slab * kRowBytes;
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        w[at][c] = __builtin_bit_cast(
+            i32x4, __builtin_amdgcn_raw_buffer_load_b128(wrs, woff + c * 64, off, 0));
+    };
+    load_stage(0);
+    // past the end the last slab is loaded again, unused
+#pragma unroll
+    for (int i = 0; i < kBuf - 1; ++i) load(min(i, nslab - 1), i);
+    store_stage(0);
+    barrier();
+    for (int s = 0, at = 0; s < nslab; s += kBuf, at ^= 1) {
+      load_stage(min(s + kBuf, nslab - 1));
+#pragma unroll
+      for (int i = 0; i < kBuf; ++i) {
+        load(min(s + i + kBuf - 1, nslab - 1), (i + kBuf - 1) % kBuf);
+        __builtin_amdgcn_sched_barrier(0);
+        if (s + i < nslab) {
+          const float sw = scalar_load(wsp + (s + i) * p.ws_col);
+          const char* hs = hl[at] + i * kBytes;
+#pragma unroll
+          for (int ts = 0; ts < kTok; ++ts) {
+            const i32x8 b = join(
+                *reinterpret_cast<const i32x4*>(hs + swizzled(ts * 16 + fr, fc) * 16),
+                *reinterpret_cast<const i32x4*>(hs + swizzled(ts * 16 + fr, 4 + fc) * 16));
+            add_scaled(acc[ts], mfma_block(join(w[i][0], w[i][1]), b),
+                       sl[at][i * kTokens + ts * 16 + fr] * sw);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      store_stage(at ^ 1);
+      barrier();
     }
-    if (s < nslab) multiply(0);
   }
-  if constexpr (kLogits) {
+  if (!kLogits && vw >= a.row_hi) return;  // z ends with the vocabulary's last 256 columns
 #pragma unroll
-    for (int ts = 0; ts < kTok; ++ts)
-#pragma unroll
-      for (int vs = 0; vs < kVS; ++vs)
-        store_logits(lo, ts * 16 + (lane & 15), v0 + wv * 128 + vs * 16 + 4 * (lane >> 4),
-                     acc[vs][ts]);
-  } else {
-    write_segments<kTok>(a, acc, xch, vb, 0, wv, 0, lane);
+  for (int ts = 0; ts < kTok; ++ts) {
+    const int32_t t = ts * 16 + (lane & 15), v = vw + 4 * (lane >> 4);
+    if constexpr (kLogits)
+      store_logits(lo, t, v, acc[ts]);
+    else
+      store_z(zo, t, v, acc[ts]);
   }
 }
 
-// Launches the blocks [vb_begin, vb_begin + n_vbs) of the 256-column grid.
-// Up to 64 tokens the weight's bytes bound the time and the streaming kernel's
-// registers hold all tokens; above, the tile shares each weight slab among 256.
-template <bool kLogits>
-hipError_t launch_blocks(const Fp8Operands& p, const SegmentArgs& sa, const LogitsOut& lo,
-                         int32_t vb_begin, int32_t n_vbs, hipStream_t stream) {
-  const int32_t n = sa.num_tokens;
-  const bool few = n <= 64;
-  const int threads = few ? 128 : kThreads;
-  const int32_t n_tb = (n + kBB - 1) / kBB;
-  const int64_t blocks = few ? n_vbs : (int64_t)n_vbs * n_tb;
+// The segments of a 256-column block from z, in the tile kernel's layout and so
+// with its bits: two waves of 128 vocabulary rows x 16 tokens.
+__global__ __launch_bounds__(128) void segments_of_z(ZOut zo, SegmentArgs a, int32_t vb_begin,
+                                                     int32_t n_tg, int64_t blk_begin) {
+  __shared__ float xch[16 * 4];
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int64_t blk = blk_begin + blockIdx.x;
+  const int32_t vb = vb_begin + (int32_t)(blk / n_tg);
+  const int32_t t0 = (int32_t)(blk % n_tg) * 16;
+  const int32_t t = min(t0 + (lane & 15), a.num_tokens - 1);
+  const float* __restrict__ z =
+      zo.z + (int64_t)t * zo.ld + vb * kBA + wv * 128 + 4 * (lane >> 4);
+  f32x4 acc[kVS][1];
+#pragma unroll
+  for (int vs = 0; vs < kVS; ++vs) acc[vs][0] = *reinterpret_cast<const f32x4*>(z + vs * 16);
+  write_segments<1>(a, acc, xch, vb, t0, wv, 0, lane);
+}
+
+// Launches `blocks` blocks in pieces of at most the launch limit.
+template <typename F>
+hipError_t in_launches(int64_t blocks, int threads, F&& launch) {
   const int64_t most = launch_thread_limit() / threads;
   for (int64_t b = 0; b < blocks; b += most) {
-    const dim3 grid((unsigned)(blocks - b < most ? blocks - b : most));
-    if (n <= 16)
-      hipLaunchKernelGGL((fp8_stream<kLogits, 1>), grid, dim3(threads), 0, stream, p, sa, lo,
-                         vb_begin, b);
-    else if (n <= 32)
-      hipLaunchKernelGGL((fp8_stream<kLogits, 2>), grid, dim3(threads), 0, stream, p, sa, lo,
-                         vb_begin, b);
-    else if (few)
-      hipLaunchKernelGGL((fp8_stream<kLogits, 4>), grid, dim3(threads), 0, stream, p, sa, lo,
-                         vb_begin, b);
-    else
-      hipLaunchKernelGGL((fp8_tile<kLogits>), grid, dim3(threads), 0, stream, p, sa, lo, n_tb,
-                         vb_begin, n_vbs, b);
+    launch(b, dim3((unsigned)(blocks - b < most ? blocks - b : most)));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
+}
+
+template <bool kLogits, int kTok>
+hipError_t launch_stream(const Fp8Operands& p, const SegmentArgs& sa, const LogitsOut& lo,
+                         const ZOut& zo, int32_t v_begin, int32_t columns, hipStream_t stream) {
+  return in_launches(columns / 64, 256, [&](int64_t b, dim3 grid) {
+    hipLaunchKernelGGL((fp8_stream<kLogits, kTok>), grid, dim3(256), 0, stream, p, sa, lo, zo,
+                       v_begin, b);
+  });
+}
+
+// The product over the columns [256 vb_begin, +256 n_vbs).  Up to 64 tokens the
+// weight's bytes bound the time and the stream kernel's registers hold all
+// tokens; above, the tile shares each weight slab among 256.
+template <bool kLogits>
+hipError_t launch_product(const Fp8Operands& p, const SegmentArgs& sa, const LogitsOut& lo,
+                          const ZOut& zo, int32_t vb_begin, int32_t n_vbs, hipStream_t stream) {
+  const int32_t n = sa.num_tokens;
+  if (n > kFp8FewTokens) {
+    const int32_t n_tb = (n + kBB - 1) / kBB;
+    return in_launches((int64_t)n_vbs * n_tb, kThreads, [&](int64_t b, dim3 grid) {
+      hipLaunchKernelGGL((fp8_tile<kLogits>), grid, dim3(kThreads), 0, stream, p, sa, lo, n_tb,
+                         vb_begin, n_vbs, b);
+    });
+  }
+  const int32_t v = vb_begin * kBA, columns = n_vbs * kBA;
+  hipError_t e;
+  if (n <= 16)
+    e = launch_stream<kLogits, 1>(p, sa, lo, zo, v, columns, stream);
+  else if (n <= 32)
+    e = launch_stream<kLogits, 2>(p, sa, lo, zo, v, columns, stream);
+  else
+    e = launch_stream<kLogits, 4>(p, sa, lo, zo, v, columns, stream);
+  if (e != hipSuccess || kLogits) return e;
+  const int32_t n_tg = (n + 15) / 16;
+  return in_launches((int64_t)n_vbs * n_tg, 128, [&](int64_t b, dim3 grid) {
+    hipLaunchKernelGGL(segments_of_z, grid, dim3(128), 0, stream, zo, sa, vb_begin, n_tg, b);
+  });
 }
 
 Fp8Operands operands(const LmheadFp8Args& a) {
@@ -519,26 +604,22 @@ hipError_t launch_fp8_quantize(const Fp8QuantizeArgs& a, hipStream_t stream) {
   const bool wide = a.block_rows > 1;
   const int64_t items = wide ? (a.rows + kFp8Block - 1) / kFp8Block * col_blocks
                              : (a.rows * col_blocks + 15) / 16;
-  const int64_t most = launch_thread_limit() / 256;
-  for (int64_t b = 0; b < items; b += most) {
-    const dim3 grid((unsigned)(items - b < most ? items - b : most));
-    const u32x4* x = reinterpret_cast<const u32x4*>(a.x);
-    uint64_t* q = reinterpret_cast<uint64_t*>(a.q);
+  const u32x4* x = reinterpret_cast<const u32x4*>(a.x);
+  uint64_t* q = reinterpret_cast<uint64_t*>(a.q);
+  return in_launches(items, 256, [&](int64_t b, dim3 grid) {
     if (wide)
       hipLaunchKernelGGL(quantize_blocks, grid, dim3(256), 0, stream, x, a.ld / 8, a.rows,
                          col_blocks, q, a.scale, a.scale_row_stride, a.scale_col_stride, b);
     else
       hipLaunchKernelGGL(quantize_rows, grid, dim3(256), 0, stream, x, a.ld / 8, a.rows,
                          col_blocks, q, a.scale, a.scale_row_stride, a.scale_col_stride, b);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
+  });
 }
 
 hipError_t launch_segments_fp8(const LmheadFp8Args& f, const SegmentArgs& sa, int32_t vb_begin,
                                int32_t n_vbs, hipStream_t stream) {
-  return launch_blocks<false>(operands(f), sa, LogitsOut{}, vb_begin, n_vbs, stream);
+  const ZOut zo{f.z, (int64_t)sa.n_vb * kBA, sa.num_tokens};
+  return launch_product<false>(operands(f), sa, LogitsOut{}, zo, vb_begin, n_vbs, stream);
 }
 
 hipError_t launch_logits_fp8(const LmheadFp8Args& f, int32_t num_tokens, int32_t real_vocab,
@@ -549,7 +630,8 @@ hipError_t launch_logits_fp8(const LmheadFp8Args& f, int32_t num_tokens, int32_t
   sa.row_hi = real_vocab;
   const LogitsOut lo{reinterpret_cast<uint16_t*>(logits), ld, num_tokens, real_vocab,
                      padded_vocab};
-  return launch_blocks<true>(operands(f), sa, lo, 0, (padded_vocab + kBA - 1) / kBA, stream);
+  return launch_product<true>(operands(f), sa, lo, ZOut{}, 0, (padded_vocab + kBA - 1) / kBA,
+                              stream);
 }
 
 }  // namespace rlk

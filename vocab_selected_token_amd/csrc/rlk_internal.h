@@ -164,6 +164,10 @@ struct Fp8QuantizeArgs {
   int64_t scale_col_stride;
 };
 
+// Up to this many tokens the 8-bit LM-head streams the weight, and its statistics
+// take z (fp32) through the workspace.
+constexpr int32_t kFp8FewTokens = 64;
+
 // The operands of an 8-bit LM-head.
 struct LmheadFp8Args {
   const void* hidden_q;       // e4m3 [num_tokens, hidden_dim]
@@ -173,6 +177,7 @@ struct LmheadFp8Args {
   int64_t hidden_row_stride, hidden_col_stride;
   int64_t weight_row_stride, weight_col_stride;
   int32_t hidden_dim;
+  float* z;  // statistics of few tokens: [num_tokens][real_vocab rounded up to 256]
 };
 
 // Gradients of the fused LM-head.  Byte offsets into its workspace (the status
