@@ -11,6 +11,7 @@ outputs and workspace with torch and call them.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from pathlib import Path
 
@@ -137,8 +138,8 @@ def _ptr(t) -> int | None:
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the handle alone: a Stream object takes ten times as long to make
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
 
 
@@ -665,6 +666,13 @@ def fused_lmhead(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tens
     return logp, lse
 
 
+def _device_of(t: torch.Tensor):
+    """The context in which a call on t's GPU is made (none where it is the current one)."""
+    if t.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(t.device)
+
+
 def _scratch(nbytes: int, device, stream) -> torch.Tensor:
     """A workspace of nbytes (0: the descriptor was refused) for a call on `stream`: the
     allocator hands its memory out again only when that stream is through with it."""
@@ -695,7 +703,7 @@ def fused_lmhead_backward(hidden: torch.Tensor, weight: torch.Tensor, targets: t
     n, k = hidden.shape
     rows = weight.shape[0]
     desc = make_desc(n, real_vocab, rows, rows, 1, 1, ignore_index, validate)
-    with torch.cuda.device(hidden.device):
+    with _device_of(hidden):
         dh = torch.empty_like(hidden) if want_hidden else None
         dw = torch.empty_like(weight) if want_weight else None
         if workspace is None:
@@ -772,10 +780,10 @@ def quantize_fp8(x: torch.Tensor, block_rows: int = 1, *, stream=None):
         raise ValueError(f"x must have a multiple of {FP8_BLOCK} columns, got {k}")
     _check_device(x)
     row_blocks, col_blocks = -(-n // block_rows), k // FP8_BLOCK
-    with torch.cuda.device(x.device):
+    with _device_of(x):
         q = torch.empty((n, k), dtype=torch.float8_e4m3fn, device=x.device)
         if block_rows == 1:
-            scale = torch.empty((col_blocks, row_blocks), device=x.device).t()
+            scale = torch.empty_strided((n, col_blocks), (1, max(n, 1)), device=x.device)
         else:
             scale = torch.empty((row_blocks, col_blocks), device=x.device)
         if n:
@@ -847,7 +855,7 @@ def lmhead_logits_fp8(hidden, weight_q: torch.Tensor, weight_scale: torch.Tensor
     hidden: bf16 [N, K], cast to e4m3 with one scale per token and 128 columns, or the
     (q, scale) pair of quantize_fp8(x, 1).  weight_q, weight_scale: quantize_fp8(W, 128)."""
     _check_lmhead_fp8(hidden, weight_q, weight_scale, real_vocab)
-    with torch.cuda.device(weight_q.device):
+    with _device_of(weight_q):
         q, scale = _fp8_pair(hidden, stream)
         n, k = q.shape
         v_pad = padded_vocab or weight_q.shape[0]
@@ -872,7 +880,7 @@ def fused_lmhead_fp8(hidden, weight_q: torch.Tensor, weight_scale: torch.Tensor,
     v_pad = padded_vocab or weight_q.shape[0]
     desc = make_desc(n, real_vocab, v_pad, v_pad, num_vocab_tiles, num_virtual_shards,
                      ignore_index, validate)
-    with torch.cuda.device(x.device):
+    with _device_of(x):
         if workspace is None:
             workspace = _scratch(rlk_logp_fused_lmhead_fp8_workspace_bytes(desc), x.device,
                                  stream)
