@@ -290,8 +290,8 @@ __global__ __launch_bounds__(kThreads) void fp8_tile(Fp8Operands p, SegmentArgs 
 
     auto issue = [&](int slab, int stage) __attribute__((always_inline)) {
       char* base = smem + stage * 2 * kSlabBytes;
-      wo.issue(base, wave, (uint32_t)slab * kRowBytes);
-      ho.issue(base + kSlabBytes, wave, (uint32_t)slab * kRowBytes);
+      wo.issue(base, wave, slab);
+      ho.issue(base + kSlabBytes, wave, slab);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           srs, (lds_ptr)(smem + kTileLds + stage * kScaleLds + wave * 256), 4, s_off,
           (uint32_t)slab * s_step, 0, 0);

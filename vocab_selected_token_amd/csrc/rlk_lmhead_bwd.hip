@@ -195,36 +195,13 @@ __global__ __launch_bounds__(256) void gather_rows(const u32x4* __restrict__ h, 
   }
 }
 
-// ---------------------------------------------------------------------------
-// transpose_weight: wt[k][c] = W[c0 + c][k] of one piece, zeros from the real
-// vocabulary's end on.
-// ---------------------------------------------------------------------------
-__global__ __launch_bounds__(256) void transpose_weight(const u32x4* __restrict__ w, int32_t ldc,
-                                                        int32_t c0, int32_t real_vocab,
-                                                        int32_t piece, int32_t k_tiles,
-                                                        uint16_t* __restrict__ wt,
-                                                        int64_t blk_begin) {
-  __shared__ Tile64 t;
-  const int64_t blk = blk_begin + blockIdx.x;
-  const int32_t r0 = (int32_t)(blk / k_tiles) * kT;
-  const int32_t kc0 = (int32_t)(blk % k_tiles) * (kT / 8);
-  for (int q = threadIdx.x; q < kT * kT / 8; q += 256) {
-    const int r = q >> 3, c = q & 7;
-    u32x4 x = {0, 0, 0, 0};
-    if (c0 + r0 + r < real_vocab) x = w[(int64_t)(c0 + r0 + r) * ldc + kc0 + c];
-    *reinterpret_cast<u32x4*>(&t.v[r][c * 8]) = x;
-  }
-  __syncthreads();
-  for (int q = threadIdx.x; q < kT * kT / 8; q += 256) {
-    const int c = q >> 3, r = (q & 7) * 8;
-    union {
-      uint16_t e[8];
-      u32x4 x;
-    } o;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o.e[i] = t.v[r + i][c];
-    *reinterpret_cast<u32x4*>(wt + (int64_t)(kc0 * 8 + c) * piece + r0 + r) = o.x;
-  }
+// The weight's last rows, those behind the last whole 64, followed by zeros: the
+// slab of dh's sum that they do not fill.
+__global__ __launch_bounds__(256) void tail_rows(const u32x4* __restrict__ w, int32_t ldc,
+                                                 int32_t rows, u32x4* __restrict__ out,
+                                                 int64_t idx_begin) {
+  const int64_t i = idx_begin + (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i < (int64_t)kBK * ldc) out[i] = i < (int64_t)rows * ldc ? w[i] : u32x4{0, 0, 0, 0};
 }
 
 // Work index -> (tile of A, tile of B): strips of 4 A tiles, B-major inside, so
@@ -240,14 +217,13 @@ __device__ __forceinline__ void tile_of(int64_t blk, int32_t n_a, int32_t n_b, i
 }
 
 // ---------------------------------------------------------------------------
-// dz_piece: dz of the columns [c0, c0 + piece) for the live rows, in bf16, by
-// tokens (dzn[i][c], ld = piece) and by columns (dzt[c][i], ld = padded_tokens).
+// dz_piece: dz of the columns [c0, c0 + piece) for the live rows, in bf16
+// (dz[i][c], ld = piece).
 // ---------------------------------------------------------------------------
 __global__ __launch_bounds__(kThreads) void dz_piece(
     const u32x4* __restrict__ hc, const u32x4* __restrict__ w, int32_t hidden_dim,
     int32_t real_vocab, int32_t c0, int32_t piece, int32_t padded_tokens,
-    uint16_t* __restrict__ dzn, uint16_t* __restrict__ dzt, char* ws, LmheadBwdLayout lay,
-    int64_t blk_begin) {
+    uint16_t* __restrict__ dz, char* ws, LmheadBwdLayout lay, int64_t blk_begin) {
   __shared__ __attribute__((aligned(16))) char smem[kTileLds];
   const LiveRows live = live_rows(ws, lay);
   const int tid = threadIdx.x;
@@ -268,12 +244,9 @@ __global__ __launch_bounds__(kThreads) void dz_piece(
                          kBB, 0, wave, lane);
     tile_product(smem, wo, ho, 0, hidden_dim / kBK, wave, lane, acc);
   }
-  uint16_t* tr = reinterpret_cast<uint16_t*>(smem);  // [256 columns][256 tokens]
-  static_assert(kTileLds >= kBA * kBB * 2, "the transpose fits");
 #pragma unroll
   for (int ts = 0; ts < kTS; ++ts) {
-    const int32_t ti = (wt * kTS + ts) * 16 + (lane & 15);
-    const int32_t i = t0 + ti;
+    const int32_t i = t0 + (wt * kTS + ts) * 16 + (lane & 15);
     const float L = live.lse[i], cg = live.cg[i], cc = live.cc[i];
     const int32_t tgt = live.tgt[i] - c0;
 #pragma unroll
@@ -294,172 +267,173 @@ __global__ __launch_bounds__(kThreads) void dz_piece(
         }
         o.e[e] = bf16_bits(d);
         if (c == tgt) live.resid[i] = d - bf16_float(o.e[e]);
-        if (dzt) tr[(cl + e) * kBB + ti] = o.e[e];
       }
-      *reinterpret_cast<uint64_t*>(dzn + (int64_t)i * piece + v0 + cl) = o.x;
+      *reinterpret_cast<uint64_t*>(dz + (int64_t)i * piece + v0 + cl) = o.x;
     }
-  }
-  if (!dzt) return;
-  __syncthreads();
-  for (int q = tid; q < kBA * kBB / 8; q += kThreads) {
-    const int c = q / (kBB / 8), r = q % (kBB / 8);
-    *reinterpret_cast<u32x4*>(dzt + (int64_t)(v0 + c) * padded_tokens + t0 + r * 8) =
-        *reinterpret_cast<const u32x4*>(tr + c * kBB + r * 8);
   }
 }
 
 // ---------------------------------------------------------------------------
-// dw_piece: dW[c0 + c][k] = scale * sum_i dzt[c][i] ht[k][i], in bf16; +0 from
-// the real vocabulary's end on.  Operand A is ht, so a lane holds 4 consecutive
-// k of one column.
+// grad_piece: both products of one piece in one launch, so that the last blocks
+// of one fill the chip beside the other's.  The blocks [0, n_dh) are dh's (the
+// longer sums first), the rest dW's.
+//   dh:  part[s][k][i] (+)= sum over split s of the piece's columns of
+//        dz[i][c] W[c0 + c][k], in fp32; the first piece writes, the others add.
+//        A = dz, B = W by its rows, so a lane holds 4 consecutive tokens of one k.
+//   dW:  dW[c0 + c][k] = scale * sum_i dz[i][c] ht[k][i], in bf16; +0 from the
+//        real vocabulary's end on.  A = ht, B = dz by its rows: 4 consecutive k of
+//        one column.
 // ---------------------------------------------------------------------------
-__global__ __launch_bounds__(kThreads) void dw_piece(
-    const uint16_t* __restrict__ ht, const uint16_t* __restrict__ dzt, int32_t hidden_dim,
-    int32_t real_vocab, int32_t padded_vocab, int32_t c0, int32_t piece, int32_t padded_tokens,
-    uint16_t* __restrict__ dw, char* ws, LmheadBwdLayout lay, int64_t blk_begin) {
+struct GradArgs {
+  const uint16_t* __restrict__ dz;    // [padded_tokens][piece]
+  const uint16_t* __restrict__ ht;    // [hidden_dim][padded_tokens]
+  const uint16_t* __restrict__ w;     // [>= real_vocab][hidden_dim]
+  const uint16_t* __restrict__ tail;  // [64][hidden_dim], see tail_rows
+  float* __restrict__ part;           // [splits][hidden_dim][padded_tokens]
+  uint16_t* __restrict__ dw;          // [padded_vocab][hidden_dim]
+  int32_t hidden_dim, real_vocab, padded_vocab;
+  int32_t c0, piece;
+  int32_t padded_tokens, splits;
+  bool add;
+  int64_t n_dh, n_dw;
+};
+
+__global__ __launch_bounds__(kThreads) void grad_piece(GradArgs a, char* ws, LmheadBwdLayout lay,
+                                                       int64_t blk_begin) {
   __shared__ __attribute__((aligned(16))) char smem[kTileLds];
   const LiveRows live = live_rows(ws, lay);
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wv = wave >> 2, wt = wave & 3;
-  int32_t ka, cb;
-  tile_of(blk_begin + xcd_local_block(blockIdx.x, gridDim.x), (hidden_dim + kBA - 1) / kBA,
-          piece / kBB, ka, cb);
-  const int32_t k0 = ka * kBA, b0 = cb * kBB;
-  if (c0 + b0 >= padded_vocab) return;
-  const int32_t nslab = ((int32_t)live.head[0] + kBK - 1) / kBK;
-  const float scale = __uint_as_float(live.head[1]);
-  f32x4 acc[kVS][kTS];
-  const bool any = nslab > 0 && c0 + b0 < real_vocab;
-  if (any) {
-    const int64_t row_bytes = (int64_t)padded_tokens * 2;
-    const TileOperand ao(ht + (int64_t)k0 * padded_tokens, row_bytes, min(kBA, hidden_dim - k0), 0,
-                         wave, lane);
-    const TileOperand bo(dzt + (int64_t)b0 * padded_tokens, row_bytes, kBB, 0, wave, lane);
-    tile_product(smem, ao, bo, 0, nslab, wave, lane, acc);
-  }
-#pragma unroll
-  for (int ts = 0; ts < kTS; ++ts) {
-    const int32_t c = c0 + b0 + (wt * kTS + ts) * 16 + (lane & 15);
-    if (c >= padded_vocab) continue;
-    const bool on = any && c < real_vocab;
-#pragma unroll
-    for (int vs = 0; vs < kVS; ++vs) {
-      const int32_t k = k0 + wv * 128 + vs * 16 + 4 * (lane >> 4);
-      if (k >= hidden_dim) continue;
-      union {
-        uint16_t e[4];
-        uint64_t x;
-      } o;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o.e[e] = on ? bf16_bits(acc[vs][ts][e] * scale) : (uint16_t)0;
-      *reinterpret_cast<uint64_t*>(dw + (int64_t)c * hidden_dim + k) = o.x;
-    }
-  }
-}
-
-// ---------------------------------------------------------------------------
-// dh_piece: part[s][i][k] (+)= sum over split s of the piece's columns of
-// dzn[i][c] wt[k][c], in fp32.  The first piece writes, the others add.
-// ---------------------------------------------------------------------------
-__global__ __launch_bounds__(kThreads) void dh_piece(
-    const uint16_t* __restrict__ wt_, const uint16_t* __restrict__ dzn, int32_t hidden_dim,
-    int32_t piece, int32_t padded_tokens, int32_t splits, bool add, float* __restrict__ part,
-    char* ws, LmheadBwdLayout lay, int64_t blk_begin) {
-  __shared__ __attribute__((aligned(16))) char smem[kTileLds];
-  const LiveRows live = live_rows(ws, lay);
-  const int tid = threadIdx.x;
-  const int lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wv = wave >> 2, wt = wave & 3;
-  const int32_t n_a = (hidden_dim + kBA - 1) / kBA, n_b = padded_tokens / kBB;
-  const int64_t blk = blk_begin + xcd_local_block(blockIdx.x, gridDim.x);
-  const int32_t split = (int32_t)(blk / ((int64_t)n_a * n_b));
-  int32_t ka, tb;
-  tile_of(blk - (int64_t)split * n_a * n_b, n_a, n_b, ka, tb);
-  const int32_t k0 = ka * kBA, t0 = tb * kBB;
+  const int32_t n_k = (a.hidden_dim + kBA - 1) / kBA, n_t = a.padded_tokens / kBB;
   const int32_t count = (int32_t)live.head[0];
-  if (t0 >= count) return;
-  const int32_t slabs = piece / kBK;
-  const int32_t s0 = (int32_t)((int64_t)split * slabs / splits);
-  const int32_t s1 = (int32_t)((int64_t)(split + 1) * slabs / splits);
+  const int64_t blk = blk_begin + blockIdx.x;
+  const bool is_dh = blk < a.n_dh;
+
+  int32_t ta, tb, s0 = 0, nslab;
+  if (is_dh) {
+    const int64_t b = xcd_local_block(blk, a.n_dh);
+    const int32_t split = (int32_t)(b / ((int64_t)n_k * n_t));
+    tile_of(b - (int64_t)split * n_k * n_t, n_t, n_k, ta, tb);
+    if (ta * kBA >= count) return;
+    const int32_t slabs = (min(a.piece, a.real_vocab - a.c0) + kBK - 1) / kBK;
+    s0 = (int32_t)((int64_t)split * slabs / a.splits);
+    nslab = (int32_t)((int64_t)(split + 1) * slabs / a.splits) - s0;
+    a.part += (int64_t)split * a.hidden_dim * a.padded_tokens;
+  } else {
+    tile_of(xcd_local_block(blk - a.n_dh, a.n_dw), n_k, a.piece / kBB, ta, tb);
+    if (a.c0 + tb * kBB >= a.padded_vocab) return;
+    nslab = a.c0 + tb * kBB < a.real_vocab ? (count + kBK - 1) / kBK : 0;
+  }
+  const int32_t a0 = ta * kBA, b0 = tb * kBB;
+
   f32x4 acc[kVS][kTS];
-  if (s1 > s0) {
-    const int64_t row_bytes = (int64_t)piece * 2;
-    const TileOperand ao(wt_ + (int64_t)k0 * piece, row_bytes, min(kBA, hidden_dim - k0), 0, wave,
-                         lane);
-    const TileOperand bo(dzn + (int64_t)t0 * piece, row_bytes, kBB, 0, wave, lane);
-    tile_product(smem, ao, bo, s0, s1 - s0, wave, lane, acc);
+  if (nslab > 0) {
+    const int64_t k_bytes = (int64_t)a.hidden_dim * 2, t_bytes = (int64_t)a.padded_tokens * 2,
+                  c_bytes = (int64_t)a.piece * 2;
+    const TileOperand ao(is_dh ? a.dz + (int64_t)a0 * a.piece : a.ht + (int64_t)a0 * a.padded_tokens,
+                         is_dh ? c_bytes : t_bytes, is_dh ? kBA : min(kBA, a.hidden_dim - a0), 0,
+                         wave, lane);
+    const TileOperandT bo(is_dh ? a.w + (int64_t)a.c0 * a.hidden_dim + b0 : a.dz + b0,
+                          is_dh ? k_bytes : c_bytes, is_dh ? min(kBB, a.hidden_dim - b0) : kBB,
+                          a.tail + b0, is_dh ? (a.real_vocab - a.c0) / kBK : -1, wave, lane);
+    tile_product(smem, ao, bo, s0, nslab, wave, lane, acc);
   } else {
 #pragma unroll
     for (int vs = 0; vs < kVS; ++vs)
 #pragma unroll
       for (int ts = 0; ts < kTS; ++ts) acc[vs][ts] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
+
+  if (is_dh) {
+#pragma unroll
+    for (int ts = 0; ts < kTS; ++ts) {
+      const int32_t k = b0 + (wt * kTS + ts) * 16 + (lane & 15);
+      if (k >= a.hidden_dim) continue;
+      float* out = a.part + (int64_t)k * a.padded_tokens + a0 + wv * 128 + 4 * (lane >> 4);
+#pragma unroll
+      for (int vs = 0; vs < kVS; ++vs) {
+        f32x4* o = reinterpret_cast<f32x4*>(out + vs * 16);
+        *o = a.add ? *o + acc[vs][ts] : acc[vs][ts];
+      }
+    }
+    return;
+  }
+  const float scale = __uint_as_float(live.head[1]);
 #pragma unroll
   for (int ts = 0; ts < kTS; ++ts) {
-    const int32_t i = t0 + (wt * kTS + ts) * 16 + (lane & 15);
-    if (i >= count) continue;
-    float* out = part + ((int64_t)split * padded_tokens + i) * hidden_dim;
+    const int32_t c = a.c0 + b0 + (wt * kTS + ts) * 16 + (lane & 15);
+    if (c >= a.padded_vocab) continue;
+    const bool on = c < a.real_vocab;
 #pragma unroll
     for (int vs = 0; vs < kVS; ++vs) {
-      const int32_t k = k0 + wv * 128 + vs * 16 + 4 * (lane >> 4);
-      if (k >= hidden_dim) continue;
-      f32x4* o = reinterpret_cast<f32x4*>(out + k);
-      *o = add ? *o + acc[vs][ts] : acc[vs][ts];
+      const int32_t k = a0 + wv * 128 + vs * 16 + 4 * (lane >> 4);
+      if (k >= a.hidden_dim) continue;
+      union {
+        uint16_t e[4];
+        uint64_t x;
+      } o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o.e[e] = on ? bf16_bits(acc[vs][ts][e] * scale) : (uint16_t)0;
+      *reinterpret_cast<uint64_t*>(a.dw + (int64_t)c * a.hidden_dim + k) = o.x;
     }
   }
 }
 
 // ---------------------------------------------------------------------------
 // dh_finish: dh[r] = scale * (sum of the splits' partials in ascending order +
-// resid W[target]) in bf16; +0 on rows that are not live.  8 columns a thread.
+// resid W[target]) in bf16; +0 on rows that are not live.  A block takes 64 live
+// rows x 64 columns, through LDS from the partials' layout to rows, and writes the
+// zeros of the 64 batch rows of the same numbers.
 // ---------------------------------------------------------------------------
 __global__ __launch_bounds__(256) void dh_finish(const float* __restrict__ part, int32_t splits,
                                                  int32_t num_tokens, int32_t padded_tokens,
                                                  int32_t ldc, const u32x4* __restrict__ w,
                                                  u32x4* __restrict__ dh, char* ws,
-                                                 LmheadBwdLayout lay, int64_t idx_begin) {
+                                                 LmheadBwdLayout lay, int64_t blk_begin) {
+  __shared__ float t[kT][kT + 1];  // [k][i]
   const LiveRows live = live_rows(ws, lay);
-  const int64_t idx = idx_begin + (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (idx >= (int64_t)num_tokens * ldc) return;
-  const int32_t r = (int32_t)(idx / ldc), c = (int32_t)(idx - (int64_t)r * ldc);
-  const int32_t i = live.inv[r];
-  union {
-    uint16_t e[8];
-    u32x4 x;
-  } o;
-  o.x = u32x4{0, 0, 0, 0};
-  if (i >= 0) {
-    const float scale = __uint_as_float(live.head[1]);
-    f32x4 lo = {0.0f, 0.0f, 0.0f, 0.0f}, hi = lo;
-    const float* p = part + ((int64_t)i * ldc + c) * 8;
-    for (int32_t s = 0; s < splits; ++s) {
-      lo += *reinterpret_cast<const f32x4*>(p);
-      hi += *reinterpret_cast<const f32x4*>(p + 4);
-      p += (int64_t)padded_tokens * ldc * 8;
-    }
-    const float rs = live.resid[i];
-    if (rs != 0.0f) {
-      union {
-        u32x4 x;
-        uint16_t e[8];
-      } wr;
-      wr.x = w[(int64_t)live.tgt[i] * ldc + c];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        lo[e] = fmaf(rs, bf16_float(wr.e[e]), lo[e]);
-        hi[e] = fmaf(rs, bf16_float(wr.e[4 + e]), hi[e]);
+  const int64_t blk = blk_begin + blockIdx.x;
+  const int32_t k_tiles = ldc * 8 / kT;
+  const int32_t i0 = (int32_t)(blk / k_tiles) * kT;
+  const int32_t kc0 = (int32_t)(blk % k_tiles) * (kT / 8);
+  const int32_t count = (int32_t)live.head[0];
+  if (i0 < count) {
+    for (int q = threadIdx.x; q < kT * kT / 4; q += 256) {
+      const int k = q >> 4, i = (q & 15) * 4;
+      const float* p = part + (int64_t)(kc0 * 8 + k) * padded_tokens + i0 + i;
+      f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int32_t s = 0; s < splits; ++s) {
+        sum += *reinterpret_cast<const f32x4*>(p);
+        p += (int64_t)padded_tokens * ldc * 8;
       }
-    }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      o.e[e] = bf16_bits(lo[e] * scale);
-      o.e[4 + e] = bf16_bits(hi[e] * scale);
+      for (int e = 0; e < 4; ++e) t[k][i + e] = sum[e];
     }
   }
-  dh[idx] = o.x;
+  __syncthreads();
+  const float scale = __uint_as_float(live.head[1]);
+  for (int q = threadIdx.x; q < kT * kT / 8; q += 256) {
+    const int r = q >> 3, c = q & 7;
+    const int32_t at = i0 + r;
+    if (at < num_tokens && live.inv[at] < 0) dh[(int64_t)at * ldc + kc0 + c] = u32x4{0, 0, 0, 0};
+    if (at >= count) continue;
+    const float rs = live.resid[at];
+    union {
+      uint16_t e[8];
+      u32x4 x;
+    } o, wr;
+    wr.x = u32x4{0, 0, 0, 0};
+    if (rs != 0.0f) wr.x = w[(int64_t)live.tgt[at] * ldc + kc0 + c];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float x = t[c * 8 + e][r];
+      if (rs != 0.0f) x = fmaf(rs, bf16_float(wr.e[e]), x);
+      o.e[e] = bf16_bits(x * scale);
+    }
+    dh[(int64_t)live.idx[at] * ldc + kc0 + c] = o.x;
+  }
 }
 
 __global__ __launch_bounds__(256) void fill_zero(u32x4* __restrict__ out, int64_t n,
@@ -514,13 +488,10 @@ LmheadBwdLayout lmhead_bwd_layout(int64_t n, int64_t k, int64_t padded_vocab, bo
   l.resid = take(np * 4);
   l.inv = take(n * 4);
   l.hc = take((size_t)np * k * 2);
-  l.dzn = take((size_t)np * piece * 2);
-  if (want_dw) {
-    l.ht = take((size_t)np * k * 2);
-    l.dzt = take((size_t)np * piece * 2);
-  }
+  l.dz = take((size_t)np * piece * 2);
+  if (want_dw) l.ht = take((size_t)np * k * 2);
   if (want_dh) {
-    l.wt = take((size_t)piece * k * 2);
+    l.tail = take((size_t)kBK * k * 2);
     l.part = take((size_t)splits * np * k * 4);
   }
   l.total = at;
@@ -540,9 +511,8 @@ hipError_t launch_lmhead_bwd(const LmheadBwdArgs& a, hipStream_t stream) {
   char* ws = a.workspace;
   const int32_t np = l.padded_tokens, k = a.hidden_dim, ldc = k / 8;
   u32x4* hc = reinterpret_cast<u32x4*>(ws + l.hc);
-  uint16_t* dzn = reinterpret_cast<uint16_t*>(ws + l.dzn);
+  uint16_t* dz = reinterpret_cast<uint16_t*>(ws + l.dz);
   uint16_t* ht = a.dweight ? reinterpret_cast<uint16_t*>(ws + l.ht) : nullptr;
-  uint16_t* dzt = a.dweight ? reinterpret_cast<uint16_t*>(ws + l.dzt) : nullptr;
   const u32x4* w = reinterpret_cast<const u32x4*>(a.weight);
 
   hipLaunchKernelGGL(live_rows_scan, dim3(1), dim3(kScanThreads), 0, stream, a.num_tokens, np,
@@ -558,46 +528,58 @@ hipError_t launch_lmhead_bwd(const LmheadBwdArgs& a, hipStream_t stream) {
   });
   if (e != hipSuccess) return e;
 
+  if (a.dhidden && a.real_vocab % kBK != 0) {
+    const int32_t whole = a.real_vocab / kBK * kBK;
+    e = in_launches(((int64_t)kBK * ldc + 255) / 256, 256, [&](int64_t b, int64_t nb) {
+      hipLaunchKernelGGL(tail_rows, dim3((unsigned)nb), dim3(256), 0, stream,
+                         w + (int64_t)whole * ldc, ldc, a.real_vocab - whole,
+                         reinterpret_cast<u32x4*>(ws + l.tail), b * 256);
+    });
+    if (e != hipSuccess) return e;
+  }
+
   const int32_t n_k = (k + kBA - 1) / kBA, n_t = np / kBB;
+  GradArgs g;
+  g.dz = dz;
+  g.ht = ht;
+  g.w = static_cast<const uint16_t*>(a.weight);
+  g.tail = reinterpret_cast<const uint16_t*>(ws + l.tail);
+  g.part = reinterpret_cast<float*>(ws + l.part);
+  g.dw = static_cast<uint16_t*>(a.dweight);
+  g.hidden_dim = k;
+  g.real_vocab = a.real_vocab;
+  g.padded_vocab = a.padded_vocab;
+  g.padded_tokens = np;
+  g.splits = l.splits;
   // pieces of the columns that need work: dW's rows go on to V_pad (as +0)
   const int32_t columns = a.dweight ? a.padded_vocab : a.real_vocab;
   for (int64_t begin = 0; begin < columns; begin += l.piece) {
     const int32_t c0 = (int32_t)begin;
     const int64_t left = (columns - begin + 255) / 256 * 256;
     const int32_t piece = left < l.piece ? (int32_t)left : l.piece;
-    e = in_launches((int64_t)(piece / kBA) * n_t, kThreads, [&](int64_t b, int64_t nb) {
-      hipLaunchKernelGGL(dz_piece, dim3((unsigned)nb), dim3(kThreads), 0, stream, hc, w, k,
-                         a.real_vocab, c0, piece, np, dzn, dzt, ws, l, b);
+    if (c0 < a.real_vocab) {
+      e = in_launches((int64_t)(piece / kBA) * n_t, kThreads, [&](int64_t b, int64_t nb) {
+        hipLaunchKernelGGL(dz_piece, dim3((unsigned)nb), dim3(kThreads), 0, stream, hc, w, k,
+                           a.real_vocab, c0, piece, np, dz, ws, l, b);
+      });
+      if (e != hipSuccess) return e;
+    }
+    g.c0 = c0;
+    g.piece = piece;
+    g.add = c0 > 0;
+    // a piece of padding only adds nothing to dh
+    g.n_dh = a.dhidden && c0 < a.real_vocab ? (int64_t)l.splits * n_t * n_k : 0;
+    g.n_dw = a.dweight ? (int64_t)(piece / kBB) * n_k : 0;
+    e = in_launches(g.n_dh + g.n_dw, kThreads, [&](int64_t b, int64_t nb) {
+      hipLaunchKernelGGL(grad_piece, dim3((unsigned)nb), dim3(kThreads), 0, stream, g, ws, l, b);
     });
     if (e != hipSuccess) return e;
-    if (a.dweight) {
-      e = in_launches((int64_t)(piece / kBB) * n_k, kThreads, [&](int64_t b, int64_t nb) {
-        hipLaunchKernelGGL(dw_piece, dim3((unsigned)nb), dim3(kThreads), 0, stream, ht, dzt, k,
-                           a.real_vocab, a.padded_vocab, c0, piece, np,
-                           reinterpret_cast<uint16_t*>(a.dweight), ws, l, b);
-      });
-      if (e != hipSuccess) return e;
-    }
-    if (a.dhidden) {
-      uint16_t* wt = reinterpret_cast<uint16_t*>(ws + l.wt);
-      e = in_launches((int64_t)(piece / kT) * k_tiles, 256, [&](int64_t b, int64_t nb) {
-        hipLaunchKernelGGL(transpose_weight, dim3((unsigned)nb), dim3(256), 0, stream, w, ldc, c0,
-                           a.real_vocab, piece, k_tiles, wt, b);
-      });
-      if (e != hipSuccess) return e;
-      e = in_launches((int64_t)l.splits * n_t * n_k, kThreads, [&](int64_t b, int64_t nb) {
-        hipLaunchKernelGGL(dh_piece, dim3((unsigned)nb), dim3(kThreads), 0, stream, wt, dzn, k,
-                           piece, np, l.splits, c0 > 0, reinterpret_cast<float*>(ws + l.part), ws,
-                           l, b);
-      });
-      if (e != hipSuccess) return e;
-    }
   }
   if (a.dhidden) {
-    e = in_launches(((int64_t)a.num_tokens * ldc + 255) / 256, 256, [&](int64_t b, int64_t nb) {
+    e = in_launches((int64_t)(np / kT) * k_tiles, 256, [&](int64_t b, int64_t nb) {
       hipLaunchKernelGGL(dh_finish, dim3((unsigned)nb), dim3(256), 0, stream,
                          reinterpret_cast<const float*>(ws + l.part), l.splits, a.num_tokens, np,
-                         ldc, w, reinterpret_cast<u32x4*>(a.dhidden), ws, l, b * 256);
+                         ldc, w, reinterpret_cast<u32x4*>(a.dhidden), ws, l, b);
     });
   }
   return e;

@@ -25,6 +25,13 @@
 // released, and the first fragments of slab s+1 are read while the last k-step's
 // MFMAs run.  Inside each k-step the next fragment reads (and the slab loads)
 // are spread between the MFMAs.
+//
+// B may also lie the other way in memory (TileOperandT): rows of the sum's index,
+// its own index contiguous.  A slab is then 64 rows of 512 bytes, and a fragment
+// comes from two transposing LDS reads (ds_read_b64_tr_b16): of 16 lanes, lane i
+// names 4 consecutive columns (4 (i % 4) on) of row i/4, and gets column i of the
+// four rows.  The chunks of row r are XOR-swizzled by 2 (r % 4) + 8 (r / 8 % 2):
+// the 8 rows that 32 lanes read at once lie 32 bytes apart over all 64 banks.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -104,8 +111,11 @@ struct TileOperand {
     }
   }
 
-  // the slab at byte `soff` of the rows into the LDS stage at `stage`
-  __device__ __forceinline__ void issue(char* stage, int wave, uint32_t soff) const {
+  static constexpr int kReadsPerFragment = 1;
+
+  // slab `slab` into the LDS stage at `stage`
+  __device__ __forceinline__ void issue(char* stage, int wave, int slab) const {
+    const uint32_t soff = (uint32_t)slab * kRowBytes;  // the slab's bytes in a row
     char* base = stage + (wave * kRowsPerWave) * kRowBytes;
 #pragma unroll
     for (int j = 0; j < kLoads; ++j)
@@ -113,13 +123,95 @@ struct TileOperand {
                                                (lds_ptr)(base + j * kRowsPerLoad * kRowBytes), 16,
                                                off[j], soff, 0, 0);
   }
+
+  // The fragment of the 16 rows from `row` on for k-step ks: lane l takes row
+  // l%16 at chunk 4ks + l/16 (k in [32ks + 8(l/16), +8)).
+  static __device__ __forceinline__ bf16x8 fragment(const char* stage, int row, int ks, int lane) {
+    return *reinterpret_cast<const bf16x8*>(
+        stage + swizzled(row + (lane & 15), ks * 4 + (lane >> 4)) * 16);
+  }
+};
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
+
+// The restrict pointer tells the compiler that the read's memory is its own:
+// without that (or a type to tell it by) it takes every direct load in flight for
+// a write to what is read here, and waits for it.  tile_product's barrier and
+// waits keep the two apart.
+__device__ __forceinline__ s16x4 transposed_read(lds_s16x4 __restrict__ at) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(at);
+}
+
+// An operand whose rows are the sum's index: row k of the slab holds B[0..255][k].
+// Wave w moves rows [8w, 8w + 8) of a slab, 2 per instruction; lane i of
+// instruction j fetches row 8w + 2j + i/32 at the chunk that belongs at position
+// i%32.  Columns from `cols` (a multiple of 8) on are never read: clamped.  Slab
+// tail_slab, if any, is read at `tail` (64 whole rows) instead: the one that the
+// last rows do not fill.
+struct TileOperandT {
+  const char* first;
+  const char* tail;
+  int tail_slab;
+  int64_t slab_bytes;
+  uint32_t off[kLoads];
+
+  static constexpr int kRowBytesT = kBB * 2;
+  static constexpr int kReadsPerFragment = 2;
+
+  static __device__ __forceinline__ int swizzle(int row) {
+    return ((row & 3) << 1) | (((row >> 3) & 1) << 3);
+  }
+
+  __device__ __forceinline__ TileOperandT(const void* first_, int64_t row_bytes, int32_t cols,
+                                          const void* tail_, int tail_slab_, int wave, int lane)
+      : first(static_cast<const char*>(first_)),
+        tail(static_cast<const char*>(tail_)),
+        tail_slab(tail_slab_),
+        slab_bytes(kBK * row_bytes) {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int row = wave * (kBK / kWaves) + j * 2 + (lane >> 5);
+      const int c = min((lane & 31) ^ swizzle(row), cols / 8 - 1);
+      off[j] = (uint32_t)(row * row_bytes + c * 16);
+    }
+  }
+
+  __device__ __forceinline__ void issue(char* stage, int wave, int slab) const {
+    // (a select, not a branch: the loads stay among the MFMAs)
+    const int64_t from_tail = -(int64_t)(slab == tail_slab);
+    const char* at = first + ((slab * slab_bytes & ~from_tail) | ((tail - first) & from_tail));
+    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(at), 0, (int)slab_bytes, kBufferWord3);
+    char* base = stage + wave * (kBK / kWaves) * kRowBytesT;
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)(base + j * 2 * kRowBytesT), 16,
+                                               off[j], 0, 0, 0);
+  }
+
+  static __device__ __forceinline__ bf16x8 fragment(const char* stage, int row, int ks, int lane) {
+    const int i = lane & 15;
+    // the lane's row in the k-step's first four of its eight, and its column
+    const int r = ks * 32 + (lane >> 4) * 8 + (i >> 2), col = row + (i & 3) * 4;
+    const char* at = stage + r * kRowBytesT + ((col >> 3) ^ swizzle(r)) * 16 + (col & 7) * 2;
+    union {
+      s16x4 half[2];
+      bf16x8 whole;
+    } f;
+    // rows 4 apart have the same swizzle
+    f.half[0] = transposed_read((lds_s16x4)at);
+    f.half[1] = transposed_read((lds_s16x4)(at + 4 * kRowBytesT));
+    return f.whole;
+  }
 };
 
 // acc = the product over the slabs [slab0, slab0 + nslab) (nslab >= 1) of the
 // operands' rows.  smem: kTileLds bytes, free for other use on return (every
 // load has landed and every wave has passed the last barrier).
+template <typename OperandB>
 __device__ __forceinline__ void tile_product(char* smem, const TileOperand& A,
-                                             const TileOperand& B, int slab0, int nslab, int wave,
+                                             const OperandB& B, int slab0, int nslab, int wave,
                                              int lane, f32x4 (&acc)[kVS][kTS]) {
   const int wv = wave >> 2;  // half of A's rows
   const int wt = wave & 3;   // quarter of B's rows
@@ -134,25 +226,17 @@ __device__ __forceinline__ void tile_product(char* smem, const TileOperand& A,
   // all A rows, then all B rows (about 0.6% faster than alternating)
   auto issue = [&](int slab, int stage) __attribute__((always_inline)) {
     char* base = smem + stage * 2 * kSlabBytes;
-    const uint32_t soff = (uint32_t)(slab0 + slab) * kRowBytes;  // the slab's bytes in a row
-    A.issue(base, wave, soff);
-    B.issue(base + kSlabBytes, wave, soff);
+    A.issue(base, wave, slab0 + slab);
+    B.issue(base + kSlabBytes, wave, slab0 + slab);
   };
-  // fragment reads of k-step ks: lane l takes row l%16 of each 16-row tile at
-  // chunk 4ks + l/16 (k in [32ks + 8(l/16), +8))
-  const int frag_row = lane & 15;
-  const int frag_c = lane >> 4;
   auto fetch = [&](const char* As, int ks, bf16x8 (&af)[kVS], bf16x8 (&bf)[kTS])
       __attribute__((always_inline)) {
     const char* Bs = As + kSlabBytes;
 #pragma unroll
     for (int vs = 0; vs < kVS; ++vs)
-      af[vs] = *reinterpret_cast<const bf16x8*>(
-          As + swizzled(wv * 128 + vs * 16 + frag_row, ks * 4 + frag_c) * 16);
+      af[vs] = TileOperand::fragment(As, wv * 128 + vs * 16, ks, lane);
 #pragma unroll
-    for (int ts = 0; ts < kTS; ++ts)
-      bf[ts] = *reinterpret_cast<const bf16x8*>(
-          Bs + swizzled(wt * 64 + ts * 16 + frag_row, ks * 4 + frag_c) * 16);
+    for (int ts = 0; ts < kTS; ++ts) bf[ts] = OperandB::fragment(Bs, wt * 64 + ts * 16, ks, lane);
   };
   auto mma = [&](const bf16x8 (&af)[kVS], const bf16x8 (&bf)[kTS]) __attribute__((always_inline)) {
 #pragma unroll
@@ -161,10 +245,12 @@ __device__ __forceinline__ void tile_product(char* smem, const TileOperand& A,
       for (int ts = 0; ts < kTS; ++ts)
         acc[vs][ts] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[vs], bf[ts], acc[vs][ts], 0, 0, 0);
   };
-  // Instruction order inside a k-step: 4 MFMAs, then one fragment read (and,
-  // after the barrier, one slab load) per 2 MFMAs, then the remaining MFMAs.
-  // The reads thus overlap the MFMAs that do not need them.
-  constexpr int kReads = kVS + kTS, kMfmas = kVS * kTS, kLead = 4, kPer = 2;
+  // Instruction order inside a k-step: 4 MFMAs, then one LDS read (and, after the
+  // barrier, one slab load) per 2 MFMAs -- per MFMA, where B's fragments take two
+  // reads -- then the remaining MFMAs.  The reads thus overlap the MFMAs that do
+  // not need them.
+  constexpr int kReads = kVS + OperandB::kReadsPerFragment * kTS, kMfmas = kVS * kTS, kLead = 4;
+  constexpr int kPer = OperandB::kReadsPerFragment == 1 ? 2 : 1;
   static_assert(kLead + kPer * kReads <= kMfmas, "the reads fit inside the step");
   static_assert(2 * kLoads <= kReads, "one load per read at most");
   auto order_step = [&](bool with_loads) __attribute__((always_inline)) {
