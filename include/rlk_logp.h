@@ -354,8 +354,8 @@ rlk_status rlk_logp_fused_lmhead(const rlk_logp_desc* desc, const void* hidden,
  *   dhidden   = dz . weight          dweight = dz^T . hidden
  * where g = grad_logp, gl = grad_lse and a_r is effective-active; the softmax
  * cross entropy of a row is -logp_r.  z is computed again in pieces of the
- * vocabulary (16384 columns, or more for few tokens) and each piece's dz, rounded
- * to bf16, serves both products; the sums are fp32.  The pages have no such step;
+ * vocabulary (num_tokens x columns of at most 2^28, but 16384 columns or more) and
+ * each piece's dz, rounded to bf16, serves both products; the sums are fp32.  The pages have no such step;
  * the contract is rlk_logp_bwd_ex's, taken back through the product.
  *   desc, hidden, weight, hidden_dim, targets, active_mask   as for
  *               rlk_logp_fused_lmhead, with num_tokens <= 2^21 and

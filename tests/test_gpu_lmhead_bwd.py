@@ -70,10 +70,11 @@ def test_gradients_match_the_formula(c, terms):
     assert torch.equal(bits(dh), bits(dh2)) and torch.equal(bits(dw), bits(dw2))
 
 
-def test_many_pieces():
-    """4352 tokens take the vocabulary in pieces of 16384 columns: two whole ones and the
-    rest, the last of it padding."""
-    case = C.make_case(4352, 64, 33000, 33100, 5, DEV)
+@pytest.mark.parametrize("v", [33000, 5001])
+def test_many_pieces(v):
+    """16500 tokens take the vocabulary in pieces of at most 16384 columns: 33100 columns in
+    three, the last ending in padding or the last two all padding."""
+    case = C.make_case(16500, 64, v, 33100, 5, DEV)
     dh, dw = backward(case, case.g, case.gl)
     rh, eh, rw, ew = C.gradients64(case, case.g, case.gl)
     assert C.worst(dh, rh, eh) <= 1.0 and C.worst(dw, rw, ew) <= 1.0
