@@ -497,7 +497,10 @@ size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 // at least 16384 columns; 4096 tokens take a 151936-column vocabulary in three.
 // Small pieces leave part of the chip idle at the end of every launch (backward of
 // 3405 live tokens: 11.1 ms in ten pieces, 10.95 in five, 10.75 in three, 10.7 in
-// two).  Splits: enough blocks of dh for the chip's 256 CUs.
+// two).  Splits: enough blocks of dh for the chip's 256 CUs, but at least kSplitSlabs
+// slabs to each.
+constexpr int64_t kSplitSlabs = 4;
+
 LmheadBwdLayout lmhead_bwd_layout(int64_t n, int64_t k, int64_t padded_vocab, bool want_dh,
                                   bool want_dw) {
   LmheadBwdLayout l{};
@@ -508,7 +511,9 @@ LmheadBwdLayout lmhead_bwd_layout(int64_t n, int64_t k, int64_t padded_vocab, bo
   const int64_t pieces = (blocks_v * 256 + piece - 1) / piece;
   piece = (blocks_v + pieces - 1) / pieces * 256;
   const int64_t blocks = np / 256 * ((k + 255) / 256);
-  const int64_t splits = blocks > 0 ? (blocks < 256 ? 256 / blocks : 1) : 1;
+  const int64_t most_splits = piece / (kBK * kSplitSlabs) > 1 ? piece / (kBK * kSplitSlabs) : 1;
+  int64_t splits = blocks > 0 && blocks < 256 ? 256 / blocks : 1;
+  splits = splits < most_splits ? splits : most_splits;
   l.padded_tokens = (int32_t)np;
   l.piece = (int32_t)piece;
   l.splits = (int32_t)splits;
