@@ -161,13 +161,13 @@ def test_statistics(s):
 
 
 def test_rows_do_not_depend_on_the_batch():
-    """The streaming kernel (1, 16, 17, 40, 64 tokens) and the tile kernel (65, 300) give a
-    token the same bits: logits, logp and LSE."""
+    """The streaming kernel (1, 16, 17, 40, 64 tokens) and the tile kernel in its widths (65,
+    150, 250, 300) give a token the same bits: logits, logp and LSE."""
     c, (wq, ws), _ = make(300, 384, 2900, 3000, 61)
     kw = dict(real_vocab=2900, padded_vocab=3000)
     full = rlk.lmhead_logits_fp8(c.h, wq, ws, **kw)
     logp, lse = rlk.fused_lmhead_fp8(c.h, wq, ws, c.tgt, c.mask, num_vocab_tiles=7, **kw)
-    for n in (1, 16, 17, 40, 64, 65):
+    for n in (1, 16, 17, 40, 64, 65, 150, 250):
         for at in (0, 300 - n):
             rows = slice(at, at + n)
             h = c.h[rows].contiguous()

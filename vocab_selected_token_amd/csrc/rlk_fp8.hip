@@ -11,7 +11,7 @@
 // result, times the two scales, is added to the fp32 accumulator in ascending b.
 // The sums do not depend on the tile, so a token's outputs have the same bits
 // whatever the batch, whichever of the two kernels computes them:
-//   fp8_tile    256 vocabulary rows x 256 tokens a block, both operands through
+//   fp8_tile    256 vocabulary rows x 128 to 256 tokens a block, both operands through
 //               LDS (the layout and loads of rlk_tile.h: a slab row is 128 bytes,
 //               here 128 columns).
 //   fp8_stream  for up to 64 tokens, where the weight's bytes bound the time: each
@@ -188,6 +188,10 @@ __device__ __forceinline__ void add_scaled(f32x4& acc, const f32x4& z, float f) 
   for (int i = 0; i < 4; ++i) acc[i] = fmaf(z[i], f, acc[i]);
 }
 
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, kBufferWord3);
+}
+
 // What both kernels read.
 struct Fp8Operands {
   const char* __restrict__ hq;     // [num_tokens][hidden_dim]
@@ -241,18 +245,184 @@ __device__ __forceinline__ void store_logits(const LogitsOut& o, int32_t t, int3
   }
 }
 
-constexpr int kScaleLds = kThreads * (int)sizeof(float);  // a slab's token scales, by wave
-
 // Read through the scalar cache (a uniform address; written before the launch).
 __device__ __forceinline__ float scalar_load(const float* p) {
   return *(const __attribute__((address_space(4))) float*)(uintptr_t)p;
 }
 
-template <bool kLogits>
+// What a tile of 64 kTok tokens keeps in LDS, twice over: a slab of 256 weight rows,
+// of its tokens, and the tokens' scales (64 floats a wave).
+template <int kTok>
+struct Fp8Tile {
+  static constexpr int kTokens = 64 * kTok;
+  static constexpr int kStage = kSlabBytes + kTokens * kRowBytes;
+  static constexpr int kScaleBytes = kThreads * 4;
+  static constexpr int kLds = 2 * (kStage + kScaleBytes);
+};
+
+// acc: z of the vocabulary rows [v0, +256) and tokens [t0, +64 kTok), in 2 x 4 waves
+// of 128 x 16 kTok.  Some row and token of the tile exist.
+template <int kTok>
+__device__ __forceinline__ void fp8_product(char* smem, const Fp8Operands& p,
+                                            const SegmentArgs& a, int32_t v0, int32_t t0,
+                                            int wave, int lane, f32x4 (&acc)[kVS][kTok]) {
+#if defined(__HIP_DEVICE_COMPILE__)  // the host pass cannot instantiate the target's builtins
+  typedef Fp8Tile<kTok> T;
+  const int wv = wave >> 2, wt = wave & 3;
+#pragma unroll
+  for (int vs = 0; vs < kVS; ++vs)
+#pragma unroll
+    for (int ts = 0; ts < kTok; ++ts) acc[vs][ts] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const int64_t row_bytes = p.hidden_dim;
+  const int32_t w_first = max(v0, a.row_lo);
+  const TileOperand wo(p.wq + (int64_t)w_first * row_bytes, row_bytes,
+                       min(v0 + kBA, a.row_hi) - w_first, v0 - w_first, wave, lane);
+  const TileOperandOf<kTok> ho(p.hq + (int64_t)t0 * row_bytes, row_bytes,
+                       min(t0 + T::kTokens, a.num_tokens) - t0, 0, wave, lane);
+  const int nslab = p.hidden_dim / kFp8Block;
+  // token scales: each wave loads those of its 16 kTok tokens, one per lane (and
+  // some that it does not use)
+  const int32_t last = min(t0 + T::kTokens, a.num_tokens) - t0 - 1;
+  const __amdgpu_buffer_rsrc_t srs =
+      buffer_of(p.hs + (int64_t)t0 * p.hs_row, (last * p.hs_row + (nslab - 1) * p.hs_col + 1) * 4);
+  const uint32_t s_off = (uint32_t)(min(wt * (16 * kTok) + lane, last) * p.hs_row * 4);
+  const uint32_t s_step = (uint32_t)p.hs_col * 4;
+  // this wave's weight scale: its 128 rows are one block (rows past the real
+  // vocabulary's last block are not used: clamped)
+  const int32_t wb = min(v0 / kFp8Block + wv, (a.row_hi - 1) / kFp8Block);
+  const float* __restrict__ wsp = p.ws + (int64_t)wb * p.ws_row;
+
+  auto issue = [&](int slab, int stage) __attribute__((always_inline)) {
+    char* base = smem + stage * T::kStage;
+    wo.issue(base, wave, slab);
+    ho.issue(base + kSlabBytes, wave, slab);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        srs, (lds_ptr)(smem + 2 * T::kStage + stage * T::kScaleBytes + wave * 256), 4, s_off,
+        (uint32_t)slab * s_step, 0, 0);
+  };
+  // Fragment reads.  Rows 16 apart have the same swizzle, so a fragment is at a
+  // fixed distance from the wave's first: the lane's offset of its two chunks
+  // (the second's position differs in one bit) plus an immediate.
+  const int fr = lane & 15, fc = lane >> 4;
+  const int lo0 = swizzled(fr, fc) * 16, lo1 = lo0 ^ 64;
+  auto frag = [&](const char* first, int tile) __attribute__((always_inline)) {
+    return join(*reinterpret_cast<const i32x4*>(first + lo0 + tile * 16 * kRowBytes),
+                *reinterpret_cast<const i32x4*>(first + lo1 + tile * 16 * kRowBytes));
+  };
+
+  // A slab's 8 kTok MFMAs go in four quarters of two 16-row tiles of A.  A quarter
+  // reads the next quarter's A fragments while its MFMAs run (two buffers of
+  // two fragments), and the last quarter, which follows the slab's barrier,
+  // also replaces B fragment by fragment as soon as its last MFMA has it: the
+  // whole slab of fragments would not fit beside 128 accumulators.  Each
+  // MFMA's result is scaled and added while the next one runs.
+  i32x8 a0[2], a1[2], b[kTok];
+  float f[kTok];
+  f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};  // the MFMA result not yet added
+  auto read_a = [&](const char* stage, int q, i32x8 (&a)[2]) __attribute__((always_inline)) {
+    a[0] = frag(stage + wv * 128 * kRowBytes, 2 * q);
+    a[1] = frag(stage + wv * 128 * kRowBytes, 2 * q + 1);
+  };
+  auto read_b = [&](const char* stage, int ts) __attribute__((always_inline)) {
+    b[ts] = frag(stage + kSlabBytes + wt * (16 * kTok) * kRowBytes, ts);
+  };
+  auto scale_of = [&](int s, int ts) __attribute__((always_inline)) {
+    const char* at = smem + 2 * T::kStage + (s & 1) * T::kScaleBytes;
+    return reinterpret_cast<const float*>(at)[wave * 64 + ts * 16 + fr];
+  };
+  // MFMA (q, j) of a slab is tile vs = 2q + j%2, ts = j/2
+  auto step = [&](int q, int j, const i32x8 (&a)[2], float fz) __attribute__((always_inline)) {
+    const f32x4 n = mfma_block(a[j & 1], b[j >> 1]);
+    const int pq = j ? q : q - 1, pj = j ? j - 1 : 2 * kTok - 1;  // the previous one's place
+    add_scaled(acc[2 * (pq < 0 ? 3 : pq) + (pj & 1)][pj >> 1], z, fz);
+    z = n;
+  };
+  auto order = [&](int reads) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 2 * kTok; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                  // MFMA
+      if (i < reads) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
+      __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);                  // VALU
+    }
+  };
+
+  issue(0, 0);
+  if (nslab > 1) issue(1, 1);
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  read_a(smem, 0, a0);
+#pragma unroll
+  for (int ts = 0; ts < kTok; ++ts) read_b(smem, ts);
+  float fp = 0.0f;  // the factor of z
+  float sw = scalar_load(wsp);
+  for (int s = 0; s < nslab; ++s) {
+    const char* cur = smem + (s & 1) * T::kStage;
+    const char* nxt = smem + ((s + 1) & 1) * T::kStage;
+    float g[kTok];
+#pragma unroll
+    for (int ts = 0; ts < kTok; ++ts) g[ts] = scale_of(s, ts);
+    __builtin_amdgcn_s_waitcnt(kWaitLds);
+#pragma unroll
+    for (int ts = 0; ts < kTok; ++ts) f[ts] = g[ts] * sw;
+    sw = scalar_load(wsp + min(s + 1, nslab - 1) * p.ws_col);
+    read_a(cur, 1, a1);
+#pragma unroll
+    for (int j = 0; j < 2 * kTok; ++j) step(0, j, a0, j ? f[(j - 1) >> 1] : fp);
+    order(4);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(kWaitLds);
+    read_a(cur, 2, a0);
+#pragma unroll
+    for (int j = 0; j < 2 * kTok; ++j) step(1, j, a1, j ? f[(j - 1) >> 1] : f[kTok - 1]);
+    order(4);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(kWaitLds);
+    read_a(cur, 3, a1);
+#pragma unroll
+    for (int j = 0; j < 2 * kTok; ++j) step(2, j, a0, j ? f[(j - 1) >> 1] : f[kTok - 1]);
+    order(4);
+    __builtin_amdgcn_sched_barrier(0);
+    // every wave has read slab s into registers, and slab s+1 has landed
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    __builtin_amdgcn_sched_barrier(0);
+    // the last two steps reload the last slab and read fragments that nothing
+    // uses: unconditional, and in bounds
+    issue(min(s + 2, nslab - 1), s & 1);
+    read_a(nxt, 0, a0);
+#pragma unroll
+    for (int j = 0; j < 2 * kTok; ++j) {
+      step(3, j, a1, j ? f[(j - 1) >> 1] : f[kTok - 1]);
+      if (j & 1) read_b(nxt, j >> 1);
+    }
+#pragma unroll
+    for (int j = 0; j < kTok; ++j) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // MFMA
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
+      __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // VMEM
+      __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);  // VALU
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+    }
+    fp = f[kTok - 1];
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  add_scaled(acc[7][kTok - 1], z, fp);
+  // the reloads of the last two steps land before the stages are used again
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+#endif
+}
+
+template <bool kLogits, int kTok>
 __global__ __launch_bounds__(kThreads) void fp8_tile(Fp8Operands p, SegmentArgs a, LogitsOut lo,
                                                      int32_t n_tb, int32_t vb_begin,
                                                      int32_t n_vbs, int64_t blk_begin) {
-  __shared__ __attribute__((aligned(16))) char smem[kTileLds + 2 * kScaleLds];
+  typedef Fp8Tile<kTok> T;
+  __shared__ __attribute__((aligned(16))) char smem[T::kLds];
+  static_assert(T::kLds >= T::kTokens * 4 * (int)sizeof(float), "epilogue exchange fits");
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -260,164 +430,19 @@ __global__ __launch_bounds__(kThreads) void fp8_tile(Fp8Operands p, SegmentArgs 
   int32_t vb, tb;
   block_of(blk_begin + xcd_local_block(blockIdx.x, gridDim.x), n_vbs, n_tb, vb, tb);
   vb += vb_begin;
-  const int32_t v0 = vb * kBA, t0 = tb * kBB;
-
-  f32x4 acc[kVS][kTS];
-#pragma unroll
-  for (int vs = 0; vs < kVS; ++vs)
-#pragma unroll
-    for (int ts = 0; ts < kTS; ++ts) acc[vs][ts] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-  if (!kLogits || v0 < a.row_hi) {  // else a block of padding: only logits has them
-    const int64_t row_bytes = p.hidden_dim;
-    const int32_t w_first = max(v0, a.row_lo);
-    const TileOperand wo(p.wq + (int64_t)w_first * row_bytes, row_bytes,
-                         min(v0 + kBA, a.row_hi) - w_first, v0 - w_first, wave, lane);
-    const TileOperand ho(p.hq + (int64_t)t0 * row_bytes, row_bytes,
-                         min(t0 + kBB, a.num_tokens) - t0, 0, wave, lane);
-    const int nslab = p.hidden_dim / kFp8Block;
-    // token scales: each wave loads those of its 64 tokens, one per lane
-    const int32_t last = min(t0 + kBB, a.num_tokens) - t0 - 1;
-    const __amdgpu_buffer_rsrc_t srs = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<float*>(p.hs + (int64_t)t0 * p.hs_row), 0,
-        (int)((last * p.hs_row + (nslab - 1) * p.hs_col + 1) * 4), kBufferWord3);
-    const uint32_t s_off = (uint32_t)(min(wt * 64 + lane, last) * p.hs_row * 4);
-    const uint32_t s_step = (uint32_t)p.hs_col * 4;
-    // this wave's weight scale: its 128 rows are one block (rows past the real
-    // vocabulary's last block are not used: clamped)
-    const int32_t wb = min(v0 / kFp8Block + wv, (a.row_hi - 1) / kFp8Block);
-    const float* __restrict__ wsp = p.ws + (int64_t)wb * p.ws_row;
-
-    auto issue = [&](int slab, int stage) __attribute__((always_inline)) {
-      char* base = smem + stage * 2 * kSlabBytes;
-      wo.issue(base, wave, slab);
-      ho.issue(base + kSlabBytes, wave, slab);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          srs, (lds_ptr)(smem + kTileLds + stage * kScaleLds + wave * 256), 4, s_off,
-          (uint32_t)slab * s_step, 0, 0);
-    };
-    // Fragment reads.  Rows 16 apart have the same swizzle, so a fragment is at a
-    // fixed distance from the wave's first: the lane's offset of its two chunks
-    // (the second's position differs in one bit) plus an immediate.
-    const int fr = lane & 15, fc = lane >> 4;
-    const int lo0 = swizzled(fr, fc) * 16, lo1 = lo0 ^ 64;
-    auto frag = [&](const char* first, int tile) __attribute__((always_inline)) {
-      return join(*reinterpret_cast<const i32x4*>(first + lo0 + tile * 16 * kRowBytes),
-                  *reinterpret_cast<const i32x4*>(first + lo1 + tile * 16 * kRowBytes));
-    };
-
-    // A slab's 32 MFMAs go in four quarters of two 16-row tiles of A.  A quarter
-    // reads the next quarter's A fragments while its MFMAs run (two buffers of
-    // two fragments), and the last quarter, which follows the slab's barrier,
-    // also replaces B fragment by fragment as soon as its last MFMA has it: the
-    // whole slab of fragments would not fit beside 128 accumulators.  Each
-    // MFMA's result is scaled and added while the next one runs.
-    i32x8 a0[2], a1[2], b[kTS];
-    float f[kTS];
-    f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};  // the MFMA result not yet added
-    auto read_a = [&](const char* stage, int q, i32x8 (&a)[2]) __attribute__((always_inline)) {
-      a[0] = frag(stage + wv * 128 * kRowBytes, 2 * q);
-      a[1] = frag(stage + wv * 128 * kRowBytes, 2 * q + 1);
-    };
-    auto read_b = [&](const char* stage, int ts) __attribute__((always_inline)) {
-      b[ts] = frag(stage + kSlabBytes + wt * 64 * kRowBytes, ts);
-    };
-    auto scale_of = [&](int s, int ts) __attribute__((always_inline)) {
-      const char* at = smem + kTileLds + (s & 1) * kScaleLds;
-      return reinterpret_cast<const float*>(at)[wave * 64 + ts * 16 + fr];
-    };
-    // MFMA (q, j) of a slab is tile vs = 2q + j%2, ts = j/2
-    auto step = [&](int q, int j, const i32x8 (&a)[2], float fz) __attribute__((always_inline)) {
-      const f32x4 n = mfma_block(a[j & 1], b[j >> 1]);
-      const int pq = j ? q : q - 1, pj = j ? j - 1 : 7;  // the previous one's place
-      add_scaled(acc[2 * (pq < 0 ? 3 : pq) + (pj & 1)][pj >> 1], z, fz);
-      z = n;
-    };
-    auto order = [&](int reads) __attribute__((always_inline)) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                  // MFMA
-        if (i < reads) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
-        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);                  // VALU
-      }
-    };
-
-    issue(0, 0);
-    if (nslab > 1) issue(1, 1);
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    read_a(smem, 0, a0);
-#pragma unroll
-    for (int ts = 0; ts < kTS; ++ts) read_b(smem, ts);
-    float fp = 0.0f;  // the factor of z
-    float sw = scalar_load(wsp);
-    for (int s = 0; s < nslab; ++s) {
-      const char* cur = smem + (s & 1) * 2 * kSlabBytes;
-      const char* nxt = smem + ((s + 1) & 1) * 2 * kSlabBytes;
-      float g[kTS];
-#pragma unroll
-      for (int ts = 0; ts < kTS; ++ts) g[ts] = scale_of(s, ts);
-      __builtin_amdgcn_s_waitcnt(kWaitLds);
-#pragma unroll
-      for (int ts = 0; ts < kTS; ++ts) f[ts] = g[ts] * sw;
-      sw = scalar_load(wsp + min(s + 1, nslab - 1) * p.ws_col);
-      read_a(cur, 1, a1);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) step(0, j, a0, j ? f[(j - 1) >> 1] : fp);
-      order(4);
-      __builtin_amdgcn_sched_barrier(0);
-      __builtin_amdgcn_s_waitcnt(kWaitLds);
-      read_a(cur, 2, a0);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) step(1, j, a1, j ? f[(j - 1) >> 1] : f[3]);
-      order(4);
-      __builtin_amdgcn_sched_barrier(0);
-      __builtin_amdgcn_s_waitcnt(kWaitLds);
-      read_a(cur, 3, a1);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) step(2, j, a0, j ? f[(j - 1) >> 1] : f[3]);
-      order(4);
-      __builtin_amdgcn_sched_barrier(0);
-      // every wave has read slab s into registers, and slab s+1 has landed
-      __builtin_amdgcn_s_waitcnt(0);
-      __syncthreads();
-      __builtin_amdgcn_sched_barrier(0);
-      // the last two steps reload the last slab and read fragments that nothing
-      // uses: unconditional, and in bounds
-      issue(min(s + 2, nslab - 1), s & 1);
-      read_a(nxt, 0, a0);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        step(3, j, a1, j ? f[(j - 1) >> 1] : f[3]);
-        if (j & 1) read_b(nxt, j >> 1);
-      }
-#pragma unroll
-      for (int j = 0; j < kTS; ++j) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // MFMA
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
-        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // VMEM
-        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);  // VALU
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
-      }
-      fp = f[3];
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    add_scaled(acc[7][3], z, fp);
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-  }
+  const int32_t v0 = vb * kBA, t0 = tb * T::kTokens;
+  f32x4 acc[kVS][kTok];
+  // else a block of padding: only logits has them, and stores no sum
+  if (!kLogits || v0 < a.row_hi) fp8_product<kTok>(smem, p, a, v0, t0, wave, lane, acc);
   if constexpr (kLogits) {
 #pragma unroll
-    for (int ts = 0; ts < kTS; ++ts)
+    for (int ts = 0; ts < kTok; ++ts)
 #pragma unroll
       for (int vs = 0; vs < kVS; ++vs)
-        store_logits(lo, t0 + (wt * kTS + ts) * 16 + (lane & 15),
+        store_logits(lo, t0 + (wt * kTok + ts) * 16 + (lane & 15),
                      v0 + wv * 128 + vs * 16 + 4 * (lane >> 4), acc[vs][ts]);
   } else {
-    write_segments<kTS>(a, acc, reinterpret_cast<float*>(smem), vb, t0, wv, wt, lane);
+    write_segments<kTok>(a, acc, reinterpret_cast<float*>(smem), vb, t0, wv, wt, lane);
   }
 }
 
@@ -464,14 +489,11 @@ __global__ __launch_bounds__(256) void fp8_stream(Fp8Operands p, SegmentArgs a, 
     // a wave outside the rows reads one of them all the same, unused
     const int32_t w_first = max(v0, a.row_lo);
     const int32_t w_rows = min(v0 + 64, a.row_hi) - w_first;
-    const __amdgpu_buffer_rsrc_t wrs = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char*>(p.wq + (int64_t)w_first * row_bytes), 0, (int)(w_rows * row_bytes),
-        kBufferWord3);
-    const __amdgpu_buffer_rsrc_t hrs = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char*>(p.hq), 0, (int)(a.num_tokens * row_bytes), kBufferWord3);
-    const __amdgpu_buffer_rsrc_t srs = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<float*>(p.hs), 0,
-        (int)(((a.num_tokens - 1) * p.hs_row + (nslab - 1) * p.hs_col + 1) * 4), kBufferWord3);
+    const __amdgpu_buffer_rsrc_t wrs =
+        buffer_of(p.wq + (int64_t)w_first * row_bytes, (int64_t)w_rows * row_bytes);
+    const __amdgpu_buffer_rsrc_t hrs = buffer_of(p.hq, (int64_t)a.num_tokens * row_bytes);
+    const __amdgpu_buffer_rsrc_t srs = buffer_of(
+        p.hs, ((a.num_tokens - 1) * p.hs_row + (nslab - 1) * p.hs_col + 1) * 4);
     const int fr = lane & 15, fc = lane >> 4;
     const uint32_t woff =
         (uint32_t)min(max(vw + fr - w_first, 0), w_rows - 1) * row_bytes + fc * 16;
@@ -603,19 +625,52 @@ hipError_t launch_stream(const Fp8Operands& p, const SegmentArgs& sa, const Logi
   });
 }
 
+template <bool kLogits, int kTok>
+hipError_t launch_tile(const Fp8Operands& p, const SegmentArgs& sa, const LogitsOut& lo,
+                       int32_t vb_begin, int32_t n_vbs, hipStream_t stream) {
+  const int32_t n_tb = (sa.num_tokens + 64 * kTok - 1) / (64 * kTok);
+  return in_launches((int64_t)n_vbs * n_tb, kThreads, [&](int64_t b, dim3 grid) {
+    hipLaunchKernelGGL((fp8_tile<kLogits, kTok>), grid, dim3(kThreads), 0, stream, p, sa, lo,
+                       n_tb, vb_begin, n_vbs, b);
+  });
+}
+
+// Tokens of a tile, in 64s.  A tile of 128, 192 or 256 tokens takes about 2.3, 3.0
+// and 4.0 units of time (over many rounds of the chip's 256 CUs, one block each:
+// 39, 50 and 67 us a round at hidden_dim 4096), and the last round of blocks and the
+// last tile of tokens are paid in full: 333 tokens x 50021 columns take 66 us in
+// tiles of 256, 56 in tiles of 192 and 63 in tiles of 128; 65 tokens x 151936 columns
+// 226, 193 and 165; 4096 tokens 2480, 2577 and 2883.  The smaller tile has to be
+// clearly ahead, for it reads the weight more often.
+int tile_tokens(int32_t n, int32_t n_vbs) {
+  const double unit[] = {2.3, 3.0, 4.0};
+  int best = 4;
+  double least = 0.0;
+  for (int k = 4; k >= 2; --k) {
+    const int64_t blocks = (int64_t)n_vbs * ((n + 64 * k - 1) / (64 * k));
+    const double cost = (double)((blocks + 255) / 256) * unit[k - 2];
+    if (k == 4 || cost < 0.95 * least) {
+      least = cost;
+      best = k;
+    }
+  }
+  return best;
+}
+
 // The product over the columns [256 vb_begin, +256 n_vbs).  Up to 64 tokens the
 // weight's bytes bound the time and the stream kernel's registers hold all
-// tokens; above, the tile shares each weight slab among 256.
+// tokens (64 tokens x 151936 columns at hidden_dim 4096: 154 us against 165 us for a
+// tile); above, the tile shares each weight slab among its tokens.
 template <bool kLogits>
 hipError_t launch_product(const Fp8Operands& p, const SegmentArgs& sa, const LogitsOut& lo,
                           const ZOut& zo, int32_t vb_begin, int32_t n_vbs, hipStream_t stream) {
   const int32_t n = sa.num_tokens;
   if (n > kFp8FewTokens) {
-    const int32_t n_tb = (n + kBB - 1) / kBB;
-    return in_launches((int64_t)n_vbs * n_tb, kThreads, [&](int64_t b, dim3 grid) {
-      hipLaunchKernelGGL((fp8_tile<kLogits>), grid, dim3(kThreads), 0, stream, p, sa, lo, n_tb,
-                         vb_begin, n_vbs, b);
-    });
+    switch (tile_tokens(n, n_vbs)) {
+      case 2: return launch_tile<kLogits, 2>(p, sa, lo, vb_begin, n_vbs, stream);
+      case 3: return launch_tile<kLogits, 3>(p, sa, lo, vb_begin, n_vbs, stream);
+      default: return launch_tile<kLogits, 4>(p, sa, lo, vb_begin, n_vbs, stream);
+    }
   }
   const int32_t v = vb_begin * kBA, columns = n_vbs * kBA;
   hipError_t e;

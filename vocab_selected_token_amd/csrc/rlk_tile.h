@@ -94,18 +94,20 @@ __device__ __forceinline__ int64_t xcd_local_block(int64_t b, int64_t nb) {
 // that belongs at LDS position i%8.  The resource starts at `first` and covers
 // `rows` (1..256) rows of row_bytes; block row r reads row r + shift of them,
 // clamped into [0, rows): rows outside are never read.  256 rows span less than
-// 2^31 bytes (the boundary limits hidden_dim).
-struct TileOperand {
+// 2^31 bytes (the boundary limits hidden_dim).  (kLoadsT: 8 kLoadsT rows a wave,
+// for tiles of fewer rows.)
+template <int kLoadsT>
+struct TileOperandOf {
   __amdgpu_buffer_rsrc_t rsrc;
-  uint32_t off[kLoads];  // byte offsets from the resource's base
+  uint32_t off[kLoadsT];  // byte offsets from the resource's base
 
-  __device__ __forceinline__ TileOperand(const void* first, int64_t row_bytes, int32_t rows,
-                                         int32_t shift, int wave, int lane) {
+  __device__ __forceinline__ TileOperandOf(const void* first, int64_t row_bytes, int32_t rows,
+                                           int32_t shift, int wave, int lane) {
     rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(first), 0,
                                              (int)((int64_t)rows * row_bytes), kBufferWord3);
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j) {
-      const int row = wave * kRowsPerWave + j * kRowsPerLoad + (lane >> 3);
+    for (int j = 0; j < kLoadsT; ++j) {
+      const int row = wave * (kRowsPerLoad * kLoadsT) + j * kRowsPerLoad + (lane >> 3);
       const int c = (lane & 7) ^ ((row >> 1) & 7);
       off[j] = (uint32_t)((int64_t)min(max(row + shift, 0), rows - 1) * row_bytes + c * 16);
     }
@@ -116,9 +118,9 @@ struct TileOperand {
   // slab `slab` into the LDS stage at `stage`
   __device__ __forceinline__ void issue(char* stage, int wave, int slab) const {
     const uint32_t soff = (uint32_t)slab * kRowBytes;  // the slab's bytes in a row
-    char* base = stage + (wave * kRowsPerWave) * kRowBytes;
+    char* base = stage + wave * (kRowsPerLoad * kLoadsT) * kRowBytes;
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j)
+    for (int j = 0; j < kLoadsT; ++j)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc,
                                                (lds_ptr)(base + j * kRowsPerLoad * kRowBytes), 16,
                                                off[j], soff, 0, 0);
@@ -142,6 +144,8 @@ typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
 __device__ __forceinline__ s16x4 transposed_read(lds_s16x4 __restrict__ at) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16(at);
 }
+
+typedef TileOperandOf<kLoads> TileOperand;
 
 // An operand whose rows are the sum's index: row k of the slab holds B[0..255][k].
 // Wave w moves rows [8w, 8w + 8) of a slab, 2 per instruction; lane i of
