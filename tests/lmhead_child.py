@@ -23,6 +23,8 @@ def run_all():
                                                      c.gl, real_vocab=2900)
     _, out["dw0"] = rlk.fused_lmhead_backward(c.h[:0], c.w, c.tgt[:0], None, out["lse"][:0],
                                               c.g[:0], real_vocab=2900)
+    out["dh20"], out["dw20"] = rlk.fused_lmhead_backward(
+        c.h[:20], c.w, c.tgt[:20], c.mask[:20], out["lse"][:20], c.g[:20], real_vocab=2900)
     wq, ws = rlk.quantize_fp8(c.w[:2900], 128)
     out["wq"], out["ws"] = wq, ws
     for n in (300, 20):  # the tile kernel, the streaming one

@@ -40,6 +40,13 @@ CASES = [
     dict(n=1, k=64, v=256, pad=256, keep=1.0),
     dict(n=2, k=64, v=1, pad=1, keep=1.0),
     dict(n=37, k=64, v=40, pad=77, keep=0.8),
+    # few tokens, in each width of their kernels; 64 of them at most
+    dict(n=5, k=192, v=3001, pad=3100, keep=0.6),
+    dict(n=16, k=320, v=700, pad=1024, keep=1.0),
+    dict(n=17, k=128, v=2500, pad=2560, keep=0.5),
+    dict(n=32, k=1088, v=900, pad=900, keep=1.0),
+    dict(n=64, k=448, v=5000, pad=5001, keep=0.9),
+    dict(n=65, k=448, v=5000, pad=5001, keep=0.9),
     dict(n=300, k=128, v=2500, pad=2560, keep=0.8),
     dict(n=257, k=320, v=3000, pad=3000, keep=0.5),
     dict(n=255, k=192, v=5001, pad=5120, keep=1.0),
@@ -98,9 +105,10 @@ def test_equal_gradients_round_without_bias():
         assert off_h <= (2 / 3) ** 0.5 * 2 ** -8 and off_w <= (2 / 3) ** 0.5 * 2 ** -8
 
 
-def test_masked_rows_may_hold_anything():
+@pytest.mark.parametrize("n", [40, 300])
+def test_masked_rows_may_hold_anything(n):
     """Rows that no term reaches: their hidden states, LSE and gradients are not read."""
-    case = C.make_case(300, 128, 1000, 1024, 7, DEV)
+    case = C.make_case(n, 128, 1000, 1024, 7, DEV)
     lse = lse_of(case)
     kw = dict(real_vocab=1000)
     ref = rlk.fused_lmhead_backward(case.h, case.w, case.tgt, case.mask, lse, case.g, None, **kw)
@@ -128,10 +136,15 @@ def test_masked_rows_may_hold_anything():
 
 
 def test_no_live_row():
-    case = C.make_case(70, 64, 600, 640, 9, DEV)
-    none = torch.zeros(70, dtype=torch.bool, device=DEV)
+    for n in (20, 70):
+        no_live_row(n)
+
+
+def no_live_row(n):
+    case = C.make_case(n, 64, 600, 640, 9, DEV)
+    none = torch.zeros(n, dtype=torch.bool, device=DEV)
     lse = lse_of(case)
-    for mask, g in ((none, case.g), (case.mask, torch.zeros(70, device=DEV))):
+    for mask, g in ((none, case.g), (case.mask, torch.zeros(n, device=DEV))):
         dh, dw = rlk.fused_lmhead_backward(case.h, case.w, case.tgt, mask, lse, g, None,
                                            real_vocab=600)
         assert (bits(dh) == 0).all() and (bits(dw) == 0).all()
@@ -159,16 +172,17 @@ def test_bad_target_and_validate():
                               validate=True)
 
 
-def test_non_finite_rows_stay_in_their_rows():
+@pytest.mark.parametrize("n", [50, 90])
+def test_non_finite_rows_stay_in_their_rows(n):
     """An infinite upstream gradient, or a hidden state that is not finite, reaches its row
     of dhidden; the other rows keep their bits.  The scale is taken from finite gradients."""
-    case = C.make_case(50, 64, 600, 600, 12, DEV, mask_keep=1.0, ignore_frac=0.0)
+    case = C.make_case(n, 64, 600, 600, 12, DEV, mask_keep=1.0, ignore_frac=0.0)
     lse = lse_of(case)
     top = int(case.g.abs().argmax())  # this row keeps the scale what it was
-    row = (top + 1) % 50
+    row = (top + 1) % n
     ref, _ = rlk.fused_lmhead_backward(case.h, case.w, case.tgt, None, lse, case.g, None,
                                        real_vocab=600)
-    rest = torch.arange(50, device=DEV) != row
+    rest = torch.arange(n, device=DEV) != row
     g = case.g.clone()
     g[row] = float("inf")
     dh, _ = rlk.fused_lmhead_backward(case.h, case.w, case.tgt, None, lse, g, None,
@@ -185,10 +199,11 @@ def test_non_finite_rows_stay_in_their_rows():
     assert torch.isnan(dh[row].float()).all() and torch.isnan(dw.float()).all()
 
 
-def test_workspace_contents_do_not_matter():
-    case = C.make_case(300, 128, 1000, 1024, 21, DEV)
+@pytest.mark.parametrize("n", [9, 300])
+def test_workspace_contents_do_not_matter(n):
+    case = C.make_case(n, 128, 1000, 1024, 21, DEV)
     lse = lse_of(case)
-    desc = rlk.make_desc(300, 1000, 1024, 1024, 4)
+    desc = rlk.make_desc(n, 1000, 1024, 1024, 4)
     need = rlk.rlk_logp_fused_lmhead_bwd_workspace_bytes(desc, 128, True, True)
     out = []
     for fill in (0, 255, 127):
@@ -252,10 +267,11 @@ def test_autograd_function():
         assert abs(along - numeric) <= tol
 
 
-def test_other_stream_and_graph_replays():
+@pytest.mark.parametrize("n", [30, 300])
+def test_other_stream_and_graph_replays(n):
     """A captured forward and backward, replayed on changing inputs with eager work between,
     gives the eager bits; a call on a side stream gives them too."""
-    n, k, v, pad = 300, 128, 5000, 5120
+    k, v, pad = 128, 5000, 5120
     sets = [C.make_case(n, k, v, pad, s, DEV, mask_keep=keep)
             for s, keep in ((41, 0.8), (42, 0.2), (43, 1.0))]
     names = ("h", "w", "tgt", "mask", "g", "gl")

@@ -14,9 +14,8 @@
 //   fp8_tile    256 vocabulary rows x 128 to 256 tokens a block, both operands through
 //               LDS (the layout and loads of rlk_tile.h: a slab row is 128 bytes,
 //               here 128 columns).
-//   fp8_stream  for up to 64 tokens, where the weight's bytes bound the time: each
-//               wave streams 16 weight rows from memory straight into the
-//               matrix cores' registers and holds all tokens.
+//   fp8_stream  for up to 64 tokens, where the weight's bytes bound the time
+//               (rlk_stream.h).
 // Lane l of an MFMA supplies row l%16 and the 16-byte chunks l/16 and l/16 + 4 of
 // the 128 columns, for both operands alike; the result's layout is that of the
 // bf16 16 x 16 tiles (4 vocabulary rows of one token per lane).
@@ -25,12 +24,12 @@
 
 #include "rlk_internal.h"
 #include "rlk_lmhead_segments.h"
+#include "rlk_stream.h"
 #include "rlk_tile.h"
 
 namespace rlk {
 namespace {
 
-typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr float kE4m3Max = 448.0f;
@@ -173,23 +172,19 @@ __global__ __launch_bounds__(256) void quantize_blocks(
 // ---------------------------------------------------------------------------
 // The product.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ f32x4 mfma_block(const i32x8& a, const i32x8& b) {
+[[maybe_unused]] __device__ __forceinline__ f32x4 mfma_block(const i32x8& a, const i32x8& b) {
   // both operands e4m3; the MX scales are not used (1)
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0,
                                                           0, 0, 0, 0, 0);
 }
 
-__device__ __forceinline__ i32x8 join(const i32x4& lo, const i32x4& hi) {
+[[maybe_unused]] __device__ __forceinline__ i32x8 join(const i32x4& lo, const i32x4& hi) {
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-__device__ __forceinline__ void add_scaled(f32x4& acc, const f32x4& z, float f) {
+[[maybe_unused]] __device__ __forceinline__ void add_scaled(f32x4& acc, const f32x4& z, float f) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) acc[i] = fmaf(z[i], f, acc[i]);
-}
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, int64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, kBufferWord3);
 }
 
 // What both kernels read.
@@ -243,11 +238,6 @@ __device__ __forceinline__ void store_logits(const LogitsOut& o, int32_t t, int3
     for (int i = 0; i < 4; ++i)
       if (v + i < o.padded_vocab) out[i] = u.e[i];
   }
-}
-
-// Read through the scalar cache (a uniform address; written before the launch).
-__device__ __forceinline__ float scalar_load(const float* p) {
-  return *(const __attribute__((address_space(4))) float*)(uintptr_t)p;
 }
 
 // What a tile of 64 kTok tokens keeps in LDS, twice over: a slab of 256 weight rows,
@@ -457,122 +447,60 @@ __device__ __forceinline__ void store_z(const ZOut& o, int32_t t, int32_t v, con
   if (t < o.num_tokens) *reinterpret_cast<f32x4*>(o.z + (int64_t)t * o.ld + v) = z;
 }
 
-// Few tokens (16 kTok at most): four waves, each 16 vocabulary rows x all tokens.
-// The weight is read once, from memory into registers, kBuf - 1 slabs ahead of the
-// one that is multiplied; the hidden states and their scales come through LDS, kBuf
-// slabs at a time, loaded while the previous ones are multiplied (read by every
-// wave from memory they cost as much as the weight: the loads of 16 rows x 64 bytes,
-// not the bytes, bound a CU's rate).  The blocks are small -- 64 rows, thousands of
-// them -- so that every CU ends at about the same time, and none waits for another:
-// the statistics, whose order spans 128 rows, are taken from z by segments_of_z.
+// What the 8-bit head adds to stream_product: the tokens' scales, staged like the
+// hidden states (one per thread at most), and the weight's.
+template <int kTok>
+struct Fp8Stream {
+  static constexpr int kTokens = 16 * kTok;
+  static_assert(kBuf * kTokens <= kStreamThreads, "a scale per thread at most");
+
+  float (*lds)[kBuf * kTokens];
+  const float* __restrict__ hs;
+  const float* __restrict__ ws;  // the block's: its 64 rows lie in one of 128
+  int64_t hs_row, hs_col, ws_col;
+  int32_t num_tokens, nslab;
+  float scale, sw;
+
+  __device__ __forceinline__ void load_stage(int s) {
+    const int tid = threadIdx.x, r = tid % kTokens, i = min(tid / kTokens, kBuf - 1);
+    scale = hs[min(r, num_tokens - 1) * hs_row + min(s + i, nslab - 1) * hs_col];
+  }
+  __device__ __forceinline__ void store_stage(int at) {
+    if (threadIdx.x < kBuf * kTokens) lds[at][threadIdx.x] = scale;
+  }
+  __device__ __forceinline__ void begin(int slab) { sw = scalar_load(ws + slab * ws_col); }
+  __device__ __forceinline__ void multiply(f32x4& acc, const i32x4& a0, const i32x4& a1,
+                                           const i32x4& b0, const i32x4& b1, int at,
+                                           int place) const {
+    add_scaled(acc, mfma_block(join(a0, a1), join(b0, b1)), lds[at][place] * sw);
+  }
+};
+
+// Few tokens (16 kTok at most).  No block waits for another: the statistics, whose
+// order spans 128 rows, are taken from z by segments_of_z.
 template <bool kLogits, int kTok>
-__global__ __launch_bounds__(256) void fp8_stream(Fp8Operands p, SegmentArgs a, LogitsOut lo,
-                                                  ZOut zo, int32_t v_begin, int64_t blk_begin) {
-  constexpr int kBuf = 4;                           // slabs in registers; slabs per LDS stage
-  constexpr int kTokens = 16 * kTok;
-  constexpr int kBytes = kTokens * kRowBytes;       // a slab's hidden states
-  constexpr int kCopies = kBuf * kBytes / 16 / 256;  // 16-byte loads per thread and stage
-  __shared__ __attribute__((aligned(16))) char hl[2][kBuf * kBytes];
-  __shared__ float sl[2][kBuf * kTokens];
-  static_assert(kBuf * kTokens <= 256, "a scale per thread at most");
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int32_t v0 = v_begin + (int32_t)(blk_begin + blockIdx.x) * 64;
+__global__ __launch_bounds__(kStreamThreads) void fp8_stream(Fp8Operands p, SegmentArgs a,
+                                                             LogitsOut lo, ZOut zo,
+                                                             int32_t v_begin, int64_t blk_begin) {
+  __shared__ StreamLds<kTok> lds;
+  __shared__ float scales[2][kBuf * 16 * kTok];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int32_t v0 = v_begin + (int32_t)(blk_begin + blockIdx.x) * kStreamRows;
   const int32_t vw = v0 + wave * 16;
   f32x4 acc[kTok];
-#pragma unroll
-  for (int ts = 0; ts < kTok; ++ts) acc[ts] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-  if (v0 < a.row_hi && v0 + 64 > a.row_lo) {
-    const uint32_t row_bytes = (uint32_t)p.hidden_dim;
-    const int nslab = p.hidden_dim / kFp8Block;
-    // a wave outside the rows reads one of them all the same, unused
-    const int32_t w_first = max(v0, a.row_lo);
-    const int32_t w_rows = min(v0 + 64, a.row_hi) - w_first;
-    const __amdgpu_buffer_rsrc_t wrs =
-        buffer_of(p.wq + (int64_t)w_first * row_bytes, (int64_t)w_rows * row_bytes);
-    const __amdgpu_buffer_rsrc_t hrs = buffer_of(p.hq, (int64_t)a.num_tokens * row_bytes);
-    const __amdgpu_buffer_rsrc_t srs = buffer_of(
-        p.hs, ((a.num_tokens - 1) * p.hs_row + (nslab - 1) * p.hs_col + 1) * 4);
-    const int fr = lane & 15, fc = lane >> 4;
-    const uint32_t woff =
-        (uint32_t)min(max(vw + fr - w_first, 0), w_rows - 1) * row_bytes + fc * 16;
-    const float* __restrict__ wsp = p.ws + (int64_t)(w_first / kFp8Block) * p.ws_row;
-
-    // this thread's part of a stage: slab, row and chunk of each copy; one scale
-    u32x4 copy[kCopies];
-    float scale;
-    auto load_stage = [&](int s) __attribute__((always_inline)) {
-#pragma unroll
-      for (int j = 0; j < kCopies; ++j) {
-        const int e = j * 256 + tid, c = e & 7, r = (e >> 3) % kTokens, i = (e >> 3) / kTokens;
-        copy[j] = __builtin_bit_cast(
-            u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                       hrs,
-                       (uint32_t)min(r, a.num_tokens - 1) * row_bytes +
-                           (uint32_t)min(s + i, nslab - 1) * kRowBytes + c * 16,
-                       0, 0));
-      }
-      const int r = tid % kTokens, i = min(tid / kTokens, kBuf - 1);
-      scale = __builtin_bit_cast(
-          float, __builtin_amdgcn_raw_buffer_load_b32(
-                     srs,
-                     (uint32_t)(min(r, a.num_tokens - 1) * p.hs_row +
-                                min(s + i, nslab - 1) * p.hs_col) * 4,
-                     0, 0));
-    };
-    auto store_stage = [&](int at) __attribute__((always_inline)) {
-#pragma unroll
-      for (int j = 0; j < kCopies; ++j) {
-        const int e = j * 256 + tid, c = e & 7, r = (e >> 3) % kTokens, i = (e >> 3) / kTokens;
-        *reinterpret_cast<u32x4*>(hl[at] + i * kBytes + swizzled(r, c) * 16) = copy[j];
-      }
-      if (tid < kBuf * kTokens) sl[at][tid] = scale;
-    };
-    // LDS is written and read through this barrier; loads in flight stay there
-    auto barrier = [&]() __attribute__((always_inline)) {
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-      __builtin_amdgcn_s_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-    };
-
-    i32x4 w[kBuf][2];
-    auto load = [&](int slab, int at) __attribute__((always_inline)) {
-      const uint32_t off = (uint32_t)slab * kRowBytes;
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-        w[at][c] = __builtin_bit_cast(
-            i32x4, __builtin_amdgcn_raw_buffer_load_b128(wrs, woff + c * 64, off, 0));
-    };
-    load_stage(0);
-    // past the end the last slab is loaded again, unused
-#pragma unroll
-    for (int i = 0; i < kBuf - 1; ++i) load(min(i, nslab - 1), i);
-    store_stage(0);
-    barrier();
-    for (int s = 0, at = 0; s < nslab; s += kBuf, at ^= 1) {
-      load_stage(min(s + kBuf, nslab - 1));
-#pragma unroll
-      for (int i = 0; i < kBuf; ++i) {
-        load(min(s + i + kBuf - 1, nslab - 1), (i + kBuf - 1) % kBuf);
-        __builtin_amdgcn_sched_barrier(0);
-        if (s + i < nslab) {
-          const float sw = scalar_load(wsp + (s + i) * p.ws_col);
-          const char* hs = hl[at] + i * kBytes;
-#pragma unroll
-          for (int ts = 0; ts < kTok; ++ts) {
-            const i32x8 b = join(
-                *reinterpret_cast<const i32x4*>(hs + swizzled(ts * 16 + fr, fc) * 16),
-                *reinterpret_cast<const i32x4*>(hs + swizzled(ts * 16 + fr, 4 + fc) * 16));
-            add_scaled(acc[ts], mfma_block(join(w[i][0], w[i][1]), b),
-                       sl[at][i * kTokens + ts * 16 + fr] * sw);
-          }
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      store_stage(at ^ 1);
-      barrier();
-    }
+  if (v0 < a.row_hi && v0 + kStreamRows > a.row_lo) {
+    Fp8Stream<kTok> math;
+    math.lds = scales;
+    math.hs = p.hs;
+    math.ws = p.ws + (int64_t)(max(v0, a.row_lo) / kFp8Block) * p.ws_row;
+    math.hs_row = p.hs_row;
+    math.hs_col = p.hs_col;
+    math.ws_col = p.ws_col;
+    math.num_tokens = a.num_tokens;
+    math.nslab = p.hidden_dim / kFp8Block;
+    stream_product(lds, p.wq, p.hq, (uint32_t)p.hidden_dim, a.row_lo, a.row_hi, a.num_tokens, v0,
+                   math, acc);
   }
   if (!kLogits && vw >= a.row_hi) return;  // z ends with the vocabulary's last 256 columns
 #pragma unroll
@@ -619,8 +547,8 @@ hipError_t in_launches(int64_t blocks, int threads, F&& launch) {
 template <bool kLogits, int kTok>
 hipError_t launch_stream(const Fp8Operands& p, const SegmentArgs& sa, const LogitsOut& lo,
                          const ZOut& zo, int32_t v_begin, int32_t columns, hipStream_t stream) {
-  return in_launches(columns / 64, 256, [&](int64_t b, dim3 grid) {
-    hipLaunchKernelGGL((fp8_stream<kLogits, kTok>), grid, dim3(256), 0, stream, p, sa, lo, zo,
+  return in_launches(columns / kStreamRows, kStreamThreads, [&](int64_t b, dim3 grid) {
+    hipLaunchKernelGGL((fp8_stream<kLogits, kTok>), grid, dim3(kStreamThreads), 0, stream, p, sa, lo, zo,
                        v_begin, b);
   });
 }

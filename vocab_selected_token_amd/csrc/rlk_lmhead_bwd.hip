@@ -26,6 +26,7 @@
 #include <stdint.h>
 
 #include "rlk_internal.h"
+#include "rlk_stream.h"
 #include "rlk_tile.h"
 
 namespace rlk {
@@ -216,6 +217,19 @@ __device__ __forceinline__ void tile_of(int64_t blk, int32_t n_a, int32_t n_b, i
   tb = r_in / strip_w;
 }
 
+// dz of one column, and what its rounding to bf16 took where it is the target's.
+__device__ __forceinline__ uint16_t dz_of(float z, float L, float cg, float cc, bool real,
+                                          bool target, float* resid) {
+  float d = 0.0f;
+  if (real) {
+    const float p = exp2_hw((z - L) * kLog2e);
+    d = target ? fmaf(p, cc, cg) : p * cc;
+  }
+  const uint16_t bits = bf16_bits(d);
+  if (target) *resid = d - bf16_float(bits);
+  return bits;
+}
+
 // A wave's 64 rows (of operand B) x 128 columns (of A) in bf16, through LDS: 8 bytes
 // a lane as the accumulators lie, out in 16-byte pieces of whole 256-byte rows.
 // pack(vs, ts) gives 4 columns; to(row, chunk) the place of 8 columns, or null.
@@ -292,14 +306,8 @@ __global__ __launch_bounds__(kThreads) void dz_piece(
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int32_t c = v0 + wv * 128 + vs * 16 + 4 * (lane >> 4) + e;
-          float d = 0.0f;
-          if (c < last) {
-            const float p = exp2_hw((acc[vs][ts][e] - L[ts]) * kLog2e);
-            d = c == tgt[ts] ? fmaf(p, cc[ts], cg[ts]) : p * cc[ts];
-          }
-          o.e[e] = bf16_bits(d);
-          if (c == tgt[ts])
-            live.resid[t0 + (wt * kTS + ts) * 16 + (lane & 15)] = d - bf16_float(o.e[e]);
+          o.e[e] = dz_of(acc[vs][ts][e], L[ts], cg[ts], cc[ts], c < last, c == tgt[ts],
+                         live.resid + t0 + (wt * kTS + ts) * 16 + (lane & 15));
         }
         return o.x;
       },
@@ -329,6 +337,7 @@ struct GradArgs {
   int32_t hidden_dim, real_vocab, padded_vocab;
   int32_t c0, piece;
   int32_t padded_tokens, splits;
+  int32_t dz_rows;  // rows of dz that a tile of tokens has (others are not used)
   bool add;
   int64_t n_dh, n_dw;
 };
@@ -368,7 +377,7 @@ __global__ __launch_bounds__(kThreads) void grad_piece(GradArgs a, char* ws, Lmh
     const int64_t k_bytes = (int64_t)a.hidden_dim * 2, t_bytes = (int64_t)a.padded_tokens * 2,
                   c_bytes = (int64_t)a.piece * 2;
     const TileOperand ao(is_dh ? a.dz + (int64_t)a0 * a.piece : a.ht + (int64_t)a0 * a.padded_tokens,
-                         is_dh ? c_bytes : t_bytes, is_dh ? kBA : min(kBA, a.hidden_dim - a0), 0,
+                         is_dh ? c_bytes : t_bytes, is_dh ? a.dz_rows : min(kBA, a.hidden_dim - a0), 0,
                          wave, lane);
     const TileOperandT bo(is_dh ? a.w + (int64_t)a.c0 * a.hidden_dim + b0 : a.dz + b0,
                           is_dh ? k_bytes : c_bytes, is_dh ? min(kBB, a.hidden_dim - b0) : kBB,
@@ -416,26 +425,160 @@ __global__ __launch_bounds__(kThreads) void grad_piece(GradArgs a, char* ws, Lmh
 }
 
 // ---------------------------------------------------------------------------
+// Few tokens (16 kTok at most): the weight's and dW's bytes bound the time, and the
+// tiles of the kernels above would leave most of their rows empty.
+//   dz_stream  z by stream_product, then dz by tokens (dz[i][c], as dz_piece) and by
+//              columns (dzt[c][i], 64 tokens apart) for dw_few.
+//   dw_few     a block takes 64 columns: dz's fragments stay in registers, and each
+//              of its four waves goes over every fourth 64 of hidden_dim, operands
+//              straight from memory (the L2 holds ht), one or two MFMA steps for a
+//              whole sum, out through LDS in rows of 128 bytes.
+// ---------------------------------------------------------------------------
+struct Bf16Stream {
+  __device__ __forceinline__ void load_stage(int) {}
+  __device__ __forceinline__ void store_stage(int) {}
+  __device__ __forceinline__ void begin(int) {}
+  __device__ __forceinline__ void multiply(f32x4& acc, const i32x4& a0, const i32x4& a1,
+                                           const i32x4& b0, const i32x4& b1, int, int) const {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a0),
+                                                  __builtin_bit_cast(bf16x8, b0), acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a1),
+                                                  __builtin_bit_cast(bf16x8, b1), acc, 0, 0, 0);
+  }
+};
+
+constexpr int kFewLd = 64;  // tokens a row of dzt has room for
+
+template <int kTok>
+__global__ __launch_bounds__(kStreamThreads) void dz_stream(
+    const char* __restrict__ hc, const char* __restrict__ w, int32_t hidden_dim,
+    int32_t real_vocab, int32_t c0, int32_t piece, uint16_t* __restrict__ dz,
+    uint16_t* __restrict__ dzt, char* ws, LmheadBwdLayout lay, int64_t blk_begin) {
+  __shared__ StreamLds<kTok> lds;
+  const LiveRows live = live_rows(ws, lay);
+  if (live.head[0] == 0) return;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int32_t v0 = c0 + (int32_t)(blk_begin + blockIdx.x) * kStreamRows;
+  f32x4 acc[kTok];
+  Bf16Stream math;
+  // the gathered rows behind the last live one are zeros
+  stream_product(lds, w, hc, (uint32_t)hidden_dim * 2, 0, real_vocab, 16 * kTok, v0, math, acc);
+  const int32_t v = v0 + wave * 16 + 4 * (lane >> 4);
+#pragma unroll
+  for (int ts = 0; ts < kTok; ++ts) {
+    const int32_t i = ts * 16 + (lane & 15);
+    const float L = live.lse[i], cg = live.cg[i], cc = live.cc[i];
+    const int32_t tgt = live.tgt[i];
+    union {
+      uint16_t e[4];
+      uint64_t x;
+    } o;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      o.e[e] = dz_of(acc[ts][e], L, cg, cc, v + e < real_vocab, v + e == tgt, live.resid + i);
+      if (dzt) dzt[(int64_t)(v + e - c0) * kFewLd + i] = o.e[e];
+    }
+    *reinterpret_cast<uint64_t*>(dz + (int64_t)i * piece + (v - c0)) = o.x;
+  }
+}
+
+template <int kTok>
+__global__ __launch_bounds__(256) void dw_few(const uint16_t* __restrict__ ht,
+                                              const uint16_t* __restrict__ dzt,
+                                              int32_t hidden_dim, int32_t real_vocab,
+                                              int32_t padded_vocab, int32_t c0,
+                                              int32_t padded_tokens, uint16_t* __restrict__ dw,
+                                              char* ws, LmheadBwdLayout lay, int64_t blk_begin) {
+  constexpr int kSteps = kTok > 2 ? 2 : 1;  // of 32 tokens
+  __shared__ __attribute__((aligned(16))) char stage[4][64 * 128];
+  const LiveRows live = live_rows(ws, lay);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int32_t b0 = (int32_t)(blk_begin + blockIdx.x) * 64;  // column inside the piece
+  const float scale = __uint_as_float(live.head[1]);
+  const bool any = live.head[0] != 0 && c0 + b0 < real_vocab;
+  const int fr = lane & 15, fg = lane >> 4;
+  const i32x4 none = {0, 0, 0, 0};
+  i32x4 b[4][kSteps];
+#pragma unroll
+  for (int ts = 0; ts < 4; ++ts)
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)  // 16 tokens fill half a step
+      b[ts][s] = any && s * 32 + fg * 8 < 16 * kTok
+                     ? *reinterpret_cast<const i32x4*>(
+                           dzt + (int64_t)(b0 + ts * 16 + fr) * kFewLd + s * 32 + fg * 8)
+                     : none;
+  char* own = stage[wave];
+  for (int32_t k0 = wave * 64; k0 < hidden_dim; k0 += 256) {
+    f32x4 acc[4][4];
+#pragma unroll
+    for (int vs = 0; vs < 4; ++vs) {
+      i32x4 a[kSteps];
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+        a[s] = any ? *reinterpret_cast<const i32x4*>(
+                         ht + (int64_t)(k0 + vs * 16 + fr) * padded_tokens + s * 32 + fg * 8)
+                   : none;
+#pragma unroll
+      for (int ts = 0; ts < 4; ++ts) {
+        acc[vs][ts] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+          acc[vs][ts] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              __builtin_bit_cast(bf16x8, a[s]), __builtin_bit_cast(bf16x8, b[ts][s]), acc[vs][ts],
+              0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int ts = 0; ts < 4; ++ts) {
+      const int r = ts * 16 + fr;
+      const bool on = c0 + b0 + r < real_vocab;
+#pragma unroll
+      for (int vs = 0; vs < 4; ++vs) {
+        union {
+          uint16_t e[4];
+          uint64_t x;
+        } o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o.e[e] = on ? bf16_bits(acc[vs][ts][e] * scale) : (uint16_t)0;
+        *reinterpret_cast<uint64_t*>(own + swizzled(r, vs * 2 + (lane >> 5)) * 16 +
+                                     (fg & 1) * 8) = o.x;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int r = j * 8 + (lane >> 3), c = (lane & 7) ^ ((r >> 1) & 7);
+      const u32x4 x = *reinterpret_cast<const u32x4*>(own + r * 128 + (lane & 7) * 16);
+      if (c0 + b0 + r < padded_vocab)
+        *reinterpret_cast<u32x4*>(dw + (int64_t)(c0 + b0 + r) * hidden_dim + k0 + c * 8) = x;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
 // dh_finish: dh[r] = scale * (sum of the splits' partials in ascending order +
 // resid W[target]) in bf16; +0 on rows that are not live.  A block takes 64 live
-// rows x 64 columns, through LDS from the partials' layout to rows, and writes the
-// zeros of the 64 batch rows of the same numbers.
+// rows x kCols columns (few, where few rows make few blocks of many splits), through
+// LDS from the partials' layout to rows, and writes the zeros of the 64 batch rows
+// of the same numbers.
 // ---------------------------------------------------------------------------
+template <int kCols>
 __global__ __launch_bounds__(256) void dh_finish(const float* __restrict__ part, int32_t splits,
                                                  int32_t num_tokens, int32_t padded_tokens,
                                                  int32_t ldc, const u32x4* __restrict__ w,
                                                  u32x4* __restrict__ dh, char* ws,
                                                  LmheadBwdLayout lay, int64_t blk_begin) {
-  __shared__ float t[kT][kT + 1];  // [k][i]
+  __shared__ float t[kCols][kT + 1];  // [k][i]
   const LiveRows live = live_rows(ws, lay);
   const int64_t blk = blk_begin + blockIdx.x;
-  const int32_t k_tiles = ldc * 8 / kT;
+  const int32_t k_tiles = ldc * 8 / kCols;
   const int32_t i0 = (int32_t)(blk / k_tiles) * kT;
-  const int32_t kc0 = (int32_t)(blk % k_tiles) * (kT / 8);
+  const int32_t kc0 = (int32_t)(blk % k_tiles) * (kCols / 8);
   const int32_t count = (int32_t)live.head[0];
   const int64_t split_size = (int64_t)padded_tokens * ldc * 8;
   if (i0 < count) {
-    for (int q = threadIdx.x; q < kT * kT / 4; q += 256) {
+    for (int q = threadIdx.x; q < kT * kCols / 4; q += 256) {
       const int k = q >> 4, i = (q & 15) * 4;
       if (i0 + i >= count) continue;
       const float* p = part + (int64_t)(kc0 * 8 + k) * padded_tokens + i0 + i;
@@ -449,8 +592,8 @@ __global__ __launch_bounds__(256) void dh_finish(const float* __restrict__ part,
   }
   __syncthreads();
   const float scale = __uint_as_float(live.head[1]);
-  for (int q = threadIdx.x; q < kT * kT / 8; q += 256) {
-    const int r = q >> 3, c = q & 7;
+  for (int q = threadIdx.x; q < kT * kCols / 8; q += 256) {
+    const int r = q / (kCols / 8), c = q % (kCols / 8);
     const int32_t at = i0 + r;
     if (at < num_tokens && live.inv[at] < 0) dh[(int64_t)at * ldc + kc0 + c] = u32x4{0, 0, 0, 0};
     if (at >= count) continue;
@@ -534,6 +677,7 @@ LmheadBwdLayout lmhead_bwd_layout(int64_t n, int64_t k, int64_t padded_vocab, bo
   l.hc = take((size_t)np * k * 2);
   l.dz = take((size_t)np * piece * 2);
   if (want_dw) l.ht = take((size_t)np * k * 2);
+  if (want_dw && n <= kFewLd) l.dzt = take((size_t)piece * kFewLd * 2);
   if (want_dh) {
     l.tail = take((size_t)kBK * k * 2);
     l.part = take((size_t)splits * np * k * 4);
@@ -549,6 +693,37 @@ hipError_t launch_fill_zero(void* out, int64_t bytes, hipStream_t stream) {
                        reinterpret_cast<u32x4*>(out), n, b * 256);
   });
 }
+
+namespace {
+
+// dz and dW of one piece for few tokens.
+template <int kTok>
+hipError_t launch_few(const LmheadBwdArgs& a, int32_t c0, int32_t piece, hipStream_t stream) {
+  const LmheadBwdLayout& l = a.layout;
+  char* ws = a.workspace;
+  uint16_t* dzt = a.dweight ? reinterpret_cast<uint16_t*>(ws + l.dzt) : nullptr;
+  const int32_t real = a.real_vocab - c0 < piece ? a.real_vocab - c0 : piece;
+  if (real > 0) {
+    const hipError_t e = in_launches(
+        ((int64_t)real + kStreamRows - 1) / kStreamRows, kStreamThreads,
+        [&](int64_t b, int64_t nb) {
+          hipLaunchKernelGGL(dz_stream<kTok>, dim3((unsigned)nb), dim3(kStreamThreads), 0, stream,
+                             ws + l.hc, static_cast<const char*>(a.weight), a.hidden_dim,
+                             a.real_vocab, c0, piece, reinterpret_cast<uint16_t*>(ws + l.dz), dzt,
+                             ws, l, b);
+        });
+    if (e != hipSuccess) return e;
+  }
+  if (!a.dweight) return hipSuccess;
+  return in_launches(piece / 64, 256, [&](int64_t b, int64_t nb) {
+    hipLaunchKernelGGL(dw_few<kTok>, dim3((unsigned)nb), dim3(256), 0, stream,
+                       reinterpret_cast<const uint16_t*>(ws + l.ht), dzt, a.hidden_dim,
+                       a.real_vocab, a.padded_vocab, c0, l.padded_tokens,
+                       static_cast<uint16_t*>(a.dweight), ws, l, b);
+  });
+}
+
+}  // namespace
 
 hipError_t launch_lmhead_bwd(const LmheadBwdArgs& a, hipStream_t stream) {
   const LmheadBwdLayout& l = a.layout;
@@ -595,13 +770,21 @@ hipError_t launch_lmhead_bwd(const LmheadBwdArgs& a, hipStream_t stream) {
   g.padded_vocab = a.padded_vocab;
   g.padded_tokens = np;
   g.splits = l.splits;
+  // up to 64 tokens, as the 8-bit head's forward; dh's sum stays with the tiles
+  const int few = a.num_tokens <= 16 ? 1 : a.num_tokens <= 32 ? 2 : a.num_tokens <= kFewLd ? 4 : 0;
+  g.dz_rows = few ? 16 * few : kBA;
   // pieces of the columns that need work: dW's rows go on to V_pad (as +0)
   const int32_t columns = a.dweight ? a.padded_vocab : a.real_vocab;
   for (int64_t begin = 0; begin < columns; begin += l.piece) {
     const int32_t c0 = (int32_t)begin;
     const int64_t left = (columns - begin + 255) / 256 * 256;
     const int32_t piece = left < l.piece ? (int32_t)left : l.piece;
-    if (c0 < a.real_vocab) {
+    if (few) {
+      e = few == 1   ? launch_few<1>(a, c0, piece, stream)
+          : few == 2 ? launch_few<2>(a, c0, piece, stream)
+                     : launch_few<4>(a, c0, piece, stream);
+      if (e != hipSuccess) return e;
+    } else if (c0 < a.real_vocab) {
       e = in_launches((int64_t)(piece / kBA) * n_t, kThreads, [&](int64_t b, int64_t nb) {
         hipLaunchKernelGGL(dz_piece, dim3((unsigned)nb), dim3(kThreads), 0, stream, hc, w, k,
                            a.real_vocab, c0, piece, np, dz, ws, l, b);
@@ -613,17 +796,18 @@ hipError_t launch_lmhead_bwd(const LmheadBwdArgs& a, hipStream_t stream) {
     g.add = c0 > 0;
     // a piece of padding only adds nothing to dh
     g.n_dh = a.dhidden && c0 < a.real_vocab ? (int64_t)l.splits * n_t * n_k : 0;
-    g.n_dw = a.dweight ? (int64_t)(piece / kBB) * n_k : 0;
+    g.n_dw = a.dweight && !few ? (int64_t)(piece / kBB) * n_k : 0;
     e = in_launches(g.n_dh + g.n_dw, kThreads, [&](int64_t b, int64_t nb) {
       hipLaunchKernelGGL(grad_piece, dim3((unsigned)nb), dim3(kThreads), 0, stream, g, ws, l, b);
     });
     if (e != hipSuccess) return e;
   }
   if (a.dhidden) {
-    e = in_launches((int64_t)(np / kT) * k_tiles, 256, [&](int64_t b, int64_t nb) {
-      hipLaunchKernelGGL(dh_finish, dim3((unsigned)nb), dim3(256), 0, stream,
-                         reinterpret_cast<const float*>(ws + l.part), l.splits, a.num_tokens, np,
-                         ldc, w, reinterpret_cast<u32x4*>(a.dhidden), ws, l, b);
+    const int32_t cols = few ? 16 : kT;
+    e = in_launches((int64_t)(np / kT) * (k / cols), 256, [&](int64_t b, int64_t nb) {
+      hipLaunchKernelGGL(few ? dh_finish<16> : dh_finish<kT>, dim3((unsigned)nb), dim3(256), 0,
+                         stream, reinterpret_cast<const float*>(ws + l.part), l.splits,
+                         a.num_tokens, np, ldc, w, reinterpret_cast<u32x4*>(a.dhidden), ws, l, b);
     });
   }
   return e;
