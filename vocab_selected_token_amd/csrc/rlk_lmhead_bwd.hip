@@ -233,6 +233,9 @@ __device__ __forceinline__ uint16_t dz_of(float z, float L, float cg, float cc, 
 // A wave's 64 rows (of operand B) x 128 columns (of A) in bf16, through LDS: 8 bytes
 // a lane as the accumulators lie, out in 16-byte pieces of whole 256-byte rows.
 // pack(vs, ts) gives 4 columns; to(row, chunk) the place of 8 columns, or null.
+// (Nontemporal: what is written outlives the caches.  The backward of 1024 tokens x
+// 2048 x 151936 takes 1784 us this way, 1837 us without; dw_few below gains most, 32
+// tokens 228 us for 267.)
 // smem: kTileLds bytes, free; each wave uses its own part.
 template <typename Pack, typename To>
 __device__ __forceinline__ void store_rows(char* smem, int wave, int lane, Pack&& pack, To&& to) {
@@ -250,9 +253,8 @@ __device__ __forceinline__ void store_rows(char* smem, int wave, int lane, Pack&
   for (int j = 0; j < 16; ++j) {
     const int r = j * 4 + (lane >> 4), c = (lane & 15) ^ (r & 15);
     uint16_t* out = to(r, c);
-    if (out)
-      *reinterpret_cast<u32x4*>(out) =
-          *reinterpret_cast<const u32x4*>(own + r * 256 + (lane & 15) * 16);
+    const u32x4 x = *reinterpret_cast<const u32x4*>(own + r * 256 + (lane & 15) * 16);
+    if (out) __builtin_nontemporal_store(x, reinterpret_cast<u32x4*>(out));
   }
 }
 static_assert(kTileLds >= kWaves * 64 * 256, "the rows fit");
@@ -337,7 +339,6 @@ struct GradArgs {
   int32_t hidden_dim, real_vocab, padded_vocab;
   int32_t c0, piece;
   int32_t padded_tokens, splits;
-  int32_t dz_rows;  // rows of dz that a tile of tokens has (others are not used)
   bool add;
   int64_t n_dh, n_dw;
 };
@@ -377,7 +378,7 @@ __global__ __launch_bounds__(kThreads) void grad_piece(GradArgs a, char* ws, Lmh
     const int64_t k_bytes = (int64_t)a.hidden_dim * 2, t_bytes = (int64_t)a.padded_tokens * 2,
                   c_bytes = (int64_t)a.piece * 2;
     const TileOperand ao(is_dh ? a.dz + (int64_t)a0 * a.piece : a.ht + (int64_t)a0 * a.padded_tokens,
-                         is_dh ? c_bytes : t_bytes, is_dh ? a.dz_rows : min(kBA, a.hidden_dim - a0), 0,
+                         is_dh ? c_bytes : t_bytes, is_dh ? kBA : min(kBA, a.hidden_dim - a0), 0,
                          wave, lane);
     const TileOperandT bo(is_dh ? a.w + (int64_t)a.c0 * a.hidden_dim + b0 : a.dz + b0,
                           is_dh ? k_bytes : c_bytes, is_dh ? min(kBB, a.hidden_dim - b0) : kBB,
@@ -551,9 +552,96 @@ __global__ __launch_bounds__(256) void dw_few(const uint16_t* __restrict__ ht,
       const int r = j * 8 + (lane >> 3), c = (lane & 7) ^ ((r >> 1) & 7);
       const u32x4 x = *reinterpret_cast<const u32x4*>(own + r * 128 + (lane & 7) * 16);
       if (c0 + b0 + r < padded_vocab)
-        *reinterpret_cast<u32x4*>(dw + (int64_t)(c0 + b0 + r) * hidden_dim + k0 + c * 8) = x;
+        __builtin_nontemporal_store(
+            x, reinterpret_cast<u32x4*>(dw + (int64_t)(c0 + b0 + r) * hidden_dim + k0 + c * 8));
     }
   }
+}
+
+// dh_few: part[s][k][i] (+)= the sum of dh_piece for the same split, for few tokens:
+// a block takes 256 columns of hidden_dim, its eight waves 32 each with all tokens.
+// W goes through LDS in slabs of 64 of its rows, two stages (64 KB: two blocks a CU,
+// one slab of each in flight); dz's fragments come from memory, a slab ahead.
+template <int kTok>
+__global__ __launch_bounds__(kThreads) void dh_few(GradArgs a, char* ws, LmheadBwdLayout lay,
+                                                   int64_t blk_begin) {
+#if defined(__HIP_DEVICE_COMPILE__)  // the host pass cannot instantiate the target's builtins
+  __shared__ __attribute__((aligned(16))) char smem[2 * kSlabBytes];
+  const LiveRows live = live_rows(ws, lay);
+  if (live.head[0] == 0) return;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int32_t n_k = (a.hidden_dim + kBB - 1) / kBB;
+  const int64_t blk = blk_begin + blockIdx.x;
+  const int32_t split = (int32_t)(blk / n_k), k0 = (int32_t)(blk % n_k) * kBB;
+  const int32_t slabs = (min(a.piece, a.real_vocab - a.c0) + kBK - 1) / kBK;
+  const int32_t s0 = (int32_t)((int64_t)split * slabs / a.splits);
+  const int32_t s1 = (int32_t)((int64_t)(split + 1) * slabs / a.splits);
+  const TileOperandT wo(a.w + (int64_t)a.c0 * a.hidden_dim + k0, (int64_t)a.hidden_dim * 2,
+                        min(kBB, a.hidden_dim - k0), a.tail + k0, (a.real_vocab - a.c0) / kBK,
+                        wave, lane);
+  f32x4 acc[kTok][2];
+#pragma unroll
+  for (int t = 0; t < kTok; ++t) acc[t][0] = acc[t][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  if (s1 > s0) {
+    const uint16_t* dz = a.dz + (int64_t)(lane & 15) * a.piece + (lane >> 4) * 8;
+    bf16x8 d[kTok][2], nd[kTok][2];
+    auto load_dz = [&](int s, bf16x8 (&to)[kTok][2]) __attribute__((always_inline)) {
+#pragma unroll
+      for (int t = 0; t < kTok; ++t)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+          to[t][ks] = *reinterpret_cast<const bf16x8*>(dz + (int64_t)t * 16 * a.piece + s * kBK +
+                                                       ks * 32);
+    };
+    wo.issue(smem, wave, s0);
+    wo.issue(smem + kSlabBytes, wave, min(s0 + 1, s1 - 1));
+    load_dz(s0, d);
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    for (int s = s0; s < s1; ++s) {
+      char* cur = smem + ((s - s0) & 1) * kSlabBytes;
+      bf16x8 b[2][2];
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          b[j][ks] = TileOperandT::fragment(cur, wave * 32 + j * 16, ks, lane);
+      __builtin_amdgcn_sched_barrier(0);
+      // every wave has read slab s into registers, and slab s+1 has landed
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+      __builtin_amdgcn_sched_barrier(0);
+      // the last two steps load the last slab again, unused
+      wo.issue(cur, wave, min(s + 2, s1 - 1));
+      load_dz(min(s + 1, s1 - 1), nd);
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int t = 0; t < kTok; ++t)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            acc[t][j] =
+                __builtin_amdgcn_mfma_f32_16x16x32_bf16(d[t][ks], b[j][ks], acc[t][j], 0, 0, 0);
+#pragma unroll
+      for (int t = 0; t < kTok; ++t)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) d[t][ks] = nd[t][ks];
+    }
+    __builtin_amdgcn_s_waitcnt(0);  // no load into LDS outlives the block
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int32_t k = k0 + wave * 32 + j * 16 + (lane & 15);
+    if (k >= a.hidden_dim) continue;
+    float* out = a.part + ((int64_t)split * a.hidden_dim + k) * a.padded_tokens + 4 * (lane >> 4);
+#pragma unroll
+    for (int t = 0; t < kTok; ++t) {
+      f32x4* o = reinterpret_cast<f32x4*>(out + t * 16);
+      *o = a.add ? *o + acc[t][j] : acc[t][j];
+    }
+  }
+#endif
 }
 
 // ---------------------------------------------------------------------------
@@ -655,7 +743,8 @@ LmheadBwdLayout lmhead_bwd_layout(int64_t n, int64_t k, int64_t padded_vocab, bo
   piece = (blocks_v + pieces - 1) / pieces * 256;
   const int64_t blocks = np / 256 * ((k + 255) / 256);
   const int64_t most_splits = piece / (kBK * kSplitSlabs) > 1 ? piece / (kBK * kSplitSlabs) : 1;
-  int64_t splits = blocks > 0 && blocks < 256 ? 256 / blocks : 1;
+  const int64_t want = n <= kFewLd ? 512 : 256;  // two blocks of dh_few fit a CU
+  int64_t splits = blocks > 0 && blocks < want ? want / blocks : 1;
   splits = splits < most_splits ? splits : most_splits;
   l.padded_tokens = (int32_t)np;
   l.piece = (int32_t)piece;
@@ -696,10 +785,11 @@ hipError_t launch_fill_zero(void* out, int64_t bytes, hipStream_t stream) {
 
 namespace {
 
-// dz and dW of one piece for few tokens.
+// One piece for few tokens.
 template <int kTok>
-hipError_t launch_few(const LmheadBwdArgs& a, int32_t c0, int32_t piece, hipStream_t stream) {
+hipError_t launch_few(const LmheadBwdArgs& a, const GradArgs& g, hipStream_t stream) {
   const LmheadBwdLayout& l = a.layout;
+  const int32_t c0 = g.c0, piece = g.piece;
   char* ws = a.workspace;
   uint16_t* dzt = a.dweight ? reinterpret_cast<uint16_t*>(ws + l.dzt) : nullptr;
   const int32_t real = a.real_vocab - c0 < piece ? a.real_vocab - c0 : piece;
@@ -712,6 +802,13 @@ hipError_t launch_few(const LmheadBwdArgs& a, int32_t c0, int32_t piece, hipStre
                              a.real_vocab, c0, piece, reinterpret_cast<uint16_t*>(ws + l.dz), dzt,
                              ws, l, b);
         });
+    if (e != hipSuccess) return e;
+  }
+  if (a.dhidden && real > 0) {
+    const int64_t n_k = (a.hidden_dim + kBB - 1) / kBB;
+    const hipError_t e = in_launches(l.splits * n_k, kThreads, [&](int64_t b, int64_t nb) {
+      hipLaunchKernelGGL(dh_few<kTok>, dim3((unsigned)nb), dim3(kThreads), 0, stream, g, ws, l, b);
+    });
     if (e != hipSuccess) return e;
   }
   if (!a.dweight) return hipSuccess;
@@ -770,33 +867,33 @@ hipError_t launch_lmhead_bwd(const LmheadBwdArgs& a, hipStream_t stream) {
   g.padded_vocab = a.padded_vocab;
   g.padded_tokens = np;
   g.splits = l.splits;
-  // up to 64 tokens, as the 8-bit head's forward; dh's sum stays with the tiles
   const int few = a.num_tokens <= 16 ? 1 : a.num_tokens <= 32 ? 2 : a.num_tokens <= kFewLd ? 4 : 0;
-  g.dz_rows = few ? 16 * few : kBA;
   // pieces of the columns that need work: dW's rows go on to V_pad (as +0)
   const int32_t columns = a.dweight ? a.padded_vocab : a.real_vocab;
   for (int64_t begin = 0; begin < columns; begin += l.piece) {
     const int32_t c0 = (int32_t)begin;
     const int64_t left = (columns - begin + 255) / 256 * 256;
     const int32_t piece = left < l.piece ? (int32_t)left : l.piece;
+    g.c0 = c0;
+    g.piece = piece;
+    g.add = c0 > 0;
     if (few) {
-      e = few == 1   ? launch_few<1>(a, c0, piece, stream)
-          : few == 2 ? launch_few<2>(a, c0, piece, stream)
-                     : launch_few<4>(a, c0, piece, stream);
+      e = few == 1   ? launch_few<1>(a, g, stream)
+          : few == 2 ? launch_few<2>(a, g, stream)
+                     : launch_few<4>(a, g, stream);
       if (e != hipSuccess) return e;
-    } else if (c0 < a.real_vocab) {
+      continue;
+    }
+    if (c0 < a.real_vocab) {
       e = in_launches((int64_t)(piece / kBA) * n_t, kThreads, [&](int64_t b, int64_t nb) {
         hipLaunchKernelGGL(dz_piece, dim3((unsigned)nb), dim3(kThreads), 0, stream, hc, w, k,
                            a.real_vocab, c0, piece, np, dz, ws, l, b);
       });
       if (e != hipSuccess) return e;
     }
-    g.c0 = c0;
-    g.piece = piece;
-    g.add = c0 > 0;
     // a piece of padding only adds nothing to dh
     g.n_dh = a.dhidden && c0 < a.real_vocab ? (int64_t)l.splits * n_t * n_k : 0;
-    g.n_dw = a.dweight && !few ? (int64_t)(piece / kBB) * n_k : 0;
+    g.n_dw = a.dweight ? (int64_t)(piece / kBB) * n_k : 0;
     e = in_launches(g.n_dh + g.n_dw, kThreads, [&](int64_t b, int64_t nb) {
       hipLaunchKernelGGL(grad_piece, dim3((unsigned)nb), dim3(kThreads), 0, stream, g, ws, l, b);
     });
