@@ -345,12 +345,12 @@ __device__ __forceinline__ void fp8_product(char* smem, const Fp8Operands& p,
   for (int ts = 0; ts < kTok; ++ts) read_b(smem, ts);
   float fp = 0.0f;  // the factor of z
   float sw = scalar_load(wsp);
+  float g[kTok];  // the next slab's token scales
+#pragma unroll
+  for (int ts = 0; ts < kTok; ++ts) g[ts] = scale_of(0, ts);
   for (int s = 0; s < nslab; ++s) {
     const char* cur = smem + (s & 1) * T::kStage;
     const char* nxt = smem + ((s + 1) & 1) * T::kStage;
-    float g[kTok];
-#pragma unroll
-    for (int ts = 0; ts < kTok; ++ts) g[ts] = scale_of(s, ts);
     __builtin_amdgcn_s_waitcnt(kWaitLds);
 #pragma unroll
     for (int ts = 0; ts < kTok; ++ts) f[ts] = g[ts] * sw;
@@ -379,6 +379,8 @@ __device__ __forceinline__ void fp8_product(char* smem, const Fp8Operands& p,
     // the last two steps reload the last slab and read fragments that nothing
     // uses: unconditional, and in bounds
     issue(min(s + 2, nslab - 1), s & 1);
+#pragma unroll
+    for (int ts = 0; ts < kTok; ++ts) g[ts] = scale_of(s + 1, ts);
     read_a(nxt, 0, a0);
 #pragma unroll
     for (int j = 0; j < 2 * kTok; ++j) {
