@@ -24,6 +24,7 @@
 
 #include "rlk_internal.h"
 #include "rlk_lmhead_segments.h"
+#include "rlk_rows.h"
 #include "rlk_stream.h"
 #include "rlk_tile.h"
 
@@ -204,11 +205,6 @@ struct LogitsOut {
   int32_t num_tokens, real_vocab, padded_vocab;
 };
 
-__device__ __forceinline__ uint16_t bf16_bits(float x) {
-  const __bf16 b = (__bf16)x;  // to nearest even
-  return __builtin_bit_cast(uint16_t, b);
-}
-
 // Work index -> (vocabulary block, token block): see lmhead_segments.
 __device__ __forceinline__ void block_of(int64_t blk, int32_t n_vbs, int32_t n_tb, int32_t& vb,
                                          int32_t& tb) {
@@ -220,22 +216,34 @@ __device__ __forceinline__ void block_of(int64_t blk, int32_t n_vbs, int32_t n_t
   tb = r_in / strip_w;
 }
 
-// This wave's logits of token t (lane's), columns from v on (4 of them), as bf16;
-// -inf from the real vocabulary's end to the padded one's.
-__device__ __forceinline__ void store_logits(const LogitsOut& o, int32_t t, int32_t v,
-                                             const f32x4& z) {
-  if (t >= o.num_tokens || v >= o.padded_vocab) return;
+// 4 logits of a token, columns from v on, as bf16; -inf from the real vocabulary's end.
+__device__ __forceinline__ uint64_t logits_of(const LogitsOut& o, int32_t v, const f32x4& z) {
   union {
     uint16_t e[4];
     uint64_t x;
   } u;
 #pragma unroll
   for (int i = 0; i < 4; ++i) u.e[i] = v + i < o.real_vocab ? bf16_bits(z[i]) : (uint16_t)0xff80;
+  return u.x;
+}
+
+// Stores the kCount logits `x` of token t, columns from v on (a multiple of kCount),
+// as far as the padded vocabulary goes.
+template <int kCount, typename T>
+__device__ __forceinline__ void store_logits(const LogitsOut& o, int32_t t, int32_t v,
+                                             const T& x) {
+  static_assert(sizeof(T) == kCount * 2, "bf16");
+  if (t >= o.num_tokens || v >= o.padded_vocab) return;
   uint16_t* out = o.out + (int64_t)t * o.ld + v;
-  if (v + 4 <= o.padded_vocab) {
-    *reinterpret_cast<uint64_t*>(out) = u.x;
+  if (v + kCount <= o.padded_vocab) {
+    *reinterpret_cast<T*>(out) = x;
   } else {
-    for (int i = 0; i < 4; ++i)
+    union {
+      T whole;
+      uint16_t e[kCount];
+    } u;
+    u.whole = x;
+    for (int i = 0; i < kCount; ++i)
       if (v + i < o.padded_vocab) out[i] = u.e[i];
   }
 }
@@ -427,12 +435,15 @@ __global__ __launch_bounds__(kThreads) void fp8_tile(Fp8Operands p, SegmentArgs 
   // else a block of padding: only logits has them, and stores no sum
   if (!kLogits || v0 < a.row_hi) fp8_product<kTok>(smem, p, a, v0, t0, wave, lane, acc);
   if constexpr (kLogits) {
-#pragma unroll
-    for (int ts = 0; ts < kTok; ++ts)
-#pragma unroll
-      for (int vs = 0; vs < kVS; ++vs)
-        store_logits(lo, t0 + (wt * kTok + ts) * 16 + (lane & 15),
-                     v0 + wv * 128 + vs * 16 + 4 * (lane >> 4), acc[vs][ts]);
+    static_assert(T::kLds >= kWaves * 4096 * kTok, "the rows fit");
+    store_rows<kTok>(
+        smem, wave, lane,
+        [&](int vs, int ts) __attribute__((always_inline)) {
+          return logits_of(lo, v0 + wv * 128 + vs * 16 + 4 * (lane >> 4), acc[vs][ts]);
+        },
+        [&](int r, int c, const u32x4& x) __attribute__((always_inline)) {
+          store_logits<8>(lo, t0 + wt * (16 * kTok) + r, v0 + wv * 128 + c * 8, x);
+        });
   } else {
     write_segments<kTok>(a, acc, reinterpret_cast<float*>(smem), vb, t0, wv, wt, lane);
   }
@@ -509,7 +520,7 @@ __global__ __launch_bounds__(kStreamThreads) void fp8_stream(Fp8Operands p, Segm
   for (int ts = 0; ts < kTok; ++ts) {
     const int32_t t = ts * 16 + (lane & 15), v = vw + 4 * (lane >> 4);
     if constexpr (kLogits)
-      store_logits(lo, t, v, acc[ts]);
+      store_logits<4>(lo, t, v, logits_of(lo, v, acc[ts]));
     else
       store_z(zo, t, v, acc[ts]);
   }

@@ -26,6 +26,7 @@
 #include <stdint.h>
 
 #include "rlk_internal.h"
+#include "rlk_rows.h"
 #include "rlk_stream.h"
 #include "rlk_tile.h"
 
@@ -37,10 +38,6 @@ static_assert(kBK == kLmheadSlabK, "slab width shared with the boundary");
 constexpr int kT = 64;  // tile edge of the gather and transpose kernels
 constexpr int kScanThreads = 1024;
 
-__device__ __forceinline__ uint16_t bf16_bits(float x) {
-  const __bf16 b = (__bf16)x;  // to nearest even
-  return __builtin_bit_cast(uint16_t, b);
-}
 __device__ __forceinline__ float bf16_float(uint16_t b) {
   return __uint_as_float((uint32_t)b << 16);
 }
@@ -230,34 +227,13 @@ __device__ __forceinline__ uint16_t dz_of(float z, float L, float cg, float cc, 
   return bits;
 }
 
-// A wave's 64 rows (of operand B) x 128 columns (of A) in bf16, through LDS: 8 bytes
-// a lane as the accumulators lie, out in 16-byte pieces of whole 256-byte rows.
-// pack(vs, ts) gives 4 columns; to(row, chunk) the place of 8 columns, or null.
-// (Nontemporal: what is written outlives the caches.  The backward of 1024 tokens x
-// 2048 x 151936 takes 1784 us this way, 1837 us without; dw_few below gains most, 32
-// tokens 228 us for 267.)
-// smem: kTileLds bytes, free; each wave uses its own part.
-template <typename Pack, typename To>
-__device__ __forceinline__ void store_rows(char* smem, int wave, int lane, Pack&& pack, To&& to) {
-  char* own = smem + wave * (64 * 256);
-#pragma unroll
-  for (int ts = 0; ts < kTS; ++ts)
-#pragma unroll
-    for (int vs = 0; vs < kVS; ++vs) {
-      // chunk c of row r lies at c ^ (r % 16): 16 rows spread over all banks
-      const int r = ts * 16 + (lane & 15), c = vs * 2 + (lane >> 5);
-      *reinterpret_cast<uint64_t*>(own + r * 256 + (c ^ (lane & 15)) * 16 +
-                                   ((lane >> 4) & 1) * 8) = pack(vs, ts);
-    }
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const int r = j * 4 + (lane >> 4), c = (lane & 15) ^ (r & 15);
-    uint16_t* out = to(r, c);
-    const u32x4 x = *reinterpret_cast<const u32x4*>(own + r * 256 + (lane & 15) * 16);
-    if (out) __builtin_nontemporal_store(x, reinterpret_cast<u32x4*>(out));
-  }
+// Whole rows out of a 256 x 256 tile, past the caches (what is written outlives them:
+// the backward of 1024 tokens x 2048 x 151936 takes 1784 us this way, 1837 us with
+// ordinary stores; dw_few below gains most, 32 tokens 228 us for 267).
+static_assert(kTileLds >= kWaves * 4096 * kTS, "the rows fit");
+__device__ __forceinline__ void put_row(uint16_t* out, const u32x4& x) {
+  __builtin_nontemporal_store(x, reinterpret_cast<u32x4*>(out));
 }
-static_assert(kTileLds >= kWaves * 64 * 256, "the rows fit");
 
 // ---------------------------------------------------------------------------
 // dz_piece: dz of the columns [c0, c0 + piece) for the live rows, in bf16
@@ -298,7 +274,7 @@ __global__ __launch_bounds__(kThreads) void dz_piece(
     tgt[ts] = live.tgt[i] - c0;
   }
   const int32_t last = real_vocab - c0;  // columns from here on are padding
-  store_rows(
+  store_rows<kTS>(
       smem, wave, lane,
       [&](int vs, int ts) __attribute__((always_inline)) {
         union {
@@ -313,8 +289,8 @@ __global__ __launch_bounds__(kThreads) void dz_piece(
         }
         return o.x;
       },
-      [&](int r, int c) __attribute__((always_inline)) {
-        return dz + (int64_t)(t0 + wt * 64 + r) * piece + v0 + wv * 128 + c * 8;
+      [&](int r, int c, const u32x4& x) __attribute__((always_inline)) {
+        put_row(dz + (int64_t)(t0 + wt * 64 + r) * piece + v0 + wv * 128 + c * 8, x);
       });
 }
 
@@ -406,7 +382,7 @@ __global__ __launch_bounds__(kThreads) void grad_piece(GradArgs a, char* ws, Lmh
     return;
   }
   const float scale = __uint_as_float(live.head[1]);
-  store_rows(
+  store_rows<kTS>(
       smem, wave, lane,
       [&](int vs, int ts) __attribute__((always_inline)) {
         union {
@@ -418,10 +394,10 @@ __global__ __launch_bounds__(kThreads) void grad_piece(GradArgs a, char* ws, Lmh
         for (int e = 0; e < 4; ++e) o.e[e] = on ? bf16_bits(acc[vs][ts][e] * scale) : (uint16_t)0;
         return o.x;
       },
-      [&](int r, int c) __attribute__((always_inline)) -> uint16_t* {
+      [&](int r, int c, const u32x4& x) __attribute__((always_inline)) {
         const int32_t row = a.c0 + b0 + wt * 64 + r, k = a0 + wv * 128 + c * 8;
-        return row < a.padded_vocab && k < a.hidden_dim ? a.dw + (int64_t)row * a.hidden_dim + k
-                                                        : nullptr;
+        if (row < a.padded_vocab && k < a.hidden_dim)
+          put_row(a.dw + (int64_t)row * a.hidden_dim + k, x);
       });
 }
 
