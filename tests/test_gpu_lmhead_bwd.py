@@ -199,6 +199,22 @@ def test_non_finite_rows_stay_in_their_rows(n):
     assert torch.isnan(dh[row].float()).all() and torch.isnan(dw.float()).all()
 
 
+@pytest.mark.parametrize("n", [20, 300])
+def test_infinite_weight_stays_in_its_row(n):
+    """A weight entry of -inf where every hidden state is positive: that logit is -inf, its
+    probability 0 and its row of dweight 0; the rows gathered behind the last live one meet it
+    with hidden states of zero (0 * inf), which must not show."""
+    case = C.make_case(n, 64, 600, 600, 13, DEV)
+    case.h[:, 7] = case.h[:, 7].abs() + 0.125
+    case.tgt[case.tgt == 100] = 99
+    case.w[100, 7] = float("-inf")
+    lse = lse_of(case)
+    assert lse.isfinite().all()
+    _, dw = rlk.fused_lmhead_backward(case.h, case.w, case.tgt, case.mask, lse, case.g, case.gl,
+                                      real_vocab=600, want_hidden=False)
+    assert dw.float().isfinite().all() and (dw[100] == 0).all()
+
+
 @pytest.mark.parametrize("n", [9, 300])
 def test_workspace_contents_do_not_matter(n):
     case = C.make_case(n, 128, 1000, 1024, 21, DEV)

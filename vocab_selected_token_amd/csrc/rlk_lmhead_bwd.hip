@@ -265,6 +265,9 @@ __global__ __launch_bounds__(kThreads) void dz_piece(
   }
   float L[kTS], cg[kTS], cc[kTS];
   int32_t tgt[kTS];
+  // columns from here on are padding; all of them for a slot behind the last live row
+  // (its z may be NaN: a hidden state of zero times an infinite weight)
+  int32_t last[kTS];
 #pragma unroll
   for (int ts = 0; ts < kTS; ++ts) {
     const int32_t i = t0 + (wt * kTS + ts) * 16 + (lane & 15);
@@ -272,8 +275,8 @@ __global__ __launch_bounds__(kThreads) void dz_piece(
     cg[ts] = live.cg[i];
     cc[ts] = live.cc[i];
     tgt[ts] = live.tgt[i] - c0;
+    last[ts] = i < (int32_t)live.head[0] ? real_vocab - c0 : 0;
   }
-  const int32_t last = real_vocab - c0;  // columns from here on are padding
   store_rows<kTS>(
       smem, wave, lane,
       [&](int vs, int ts) __attribute__((always_inline)) {
@@ -284,7 +287,7 @@ __global__ __launch_bounds__(kThreads) void dz_piece(
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int32_t c = v0 + wv * 128 + vs * 16 + 4 * (lane >> 4) + e;
-          o.e[e] = dz_of(acc[vs][ts][e], L[ts], cg[ts], cc[ts], c < last, c == tgt[ts],
+          o.e[e] = dz_of(acc[vs][ts][e], L[ts], cg[ts], cc[ts], c < last[ts], c == tgt[ts],
                          live.resid + t0 + (wt * kTS + ts) * 16 + (lane & 15));
         }
         return o.x;
@@ -447,13 +450,14 @@ __global__ __launch_bounds__(kStreamThreads) void dz_stream(
     const int32_t i = ts * 16 + (lane & 15);
     const float L = live.lse[i], cg = live.cg[i], cc = live.cc[i];
     const int32_t tgt = live.tgt[i];
+    const int32_t last = i < (int32_t)live.head[0] ? real_vocab : 0;  // as in dz_piece
     union {
       uint16_t e[4];
       uint64_t x;
     } o;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      o.e[e] = dz_of(acc[ts][e], L, cg, cc, v + e < real_vocab, v + e == tgt, live.resid + i);
+      o.e[e] = dz_of(acc[ts][e], L, cg, cc, v + e < last, v + e == tgt, live.resid + i);
       if (dzt) dzt[(int64_t)(v + e - c0) * kFewLd + i] = o.e[e];
     }
     *reinterpret_cast<uint64_t*>(dz + (int64_t)i * piece + (v - c0)) = o.x;
