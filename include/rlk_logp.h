@@ -427,7 +427,8 @@ rlk_status rlk_fp8_quantize(int64_t rows, int64_t cols, const void* x, int64_t l
  * taken by the matrix cores, times its two scales and added up in fp32, rounded
  * once to bf16 -- the logits that rlk_logp_fwd and its kin read.
  *   desc        num_tokens, real_vocab, padded_vocab, ld_logits as for rlk_logp_fwd
- *               (the tiling is validated and not used; flags must be 0).
+ *               (the tiling is validated and not used; flags must be 0), with
+ *               padded_vocab < 2^31 - 512.
  *   hidden      [num_tokens, hidden_dim], one scale per token and 128 columns.
  *   weight      [>= real_vocab, hidden_dim], one scale per 128 x 128; rows >=
  *               real_vocab are never read.

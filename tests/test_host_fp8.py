@@ -109,6 +109,9 @@ def test_logits_refuse():
     refused(logits, rlk.RLK_ERR_BAD_SHAPE, d=desc(ld_logits=1016))
     refused(logits, rlk.RLK_ERR_ALIGNMENT, d=desc(ld_logits=1028))
     refused(logits, rlk.RLK_ERR_BAD_SHAPE, d=desc(validate=True))
+    # column numbers of the last block would pass 2^31
+    refused(logits, rlk.RLK_ERR_BAD_SHAPE, d=desc(padded_vocab=(1 << 31) - 256,
+                                                  ld_logits=(1 << 31) - 256))
     logits(d=desc(num_tokens=0), h=None, w=None, out=None)
 
 

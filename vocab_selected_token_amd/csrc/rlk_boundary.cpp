@@ -826,6 +826,9 @@ rlk_status rlk_lmhead_logits_fp8(const rlk_logp_desc* desc, const rlk_fp8_matrix
   rlk_status st = check_desc(desc);
   if (st != RLK_OK) return st;
   if (desc->flags) return fail(RLK_ERR_BAD_SHAPE, "logits have no data errors to validate");
+  if (desc->padded_vocab > kI32Max - 512)  // 32-bit columns up to the end of the last block
+    return fail(RLK_ERR_BAD_SHAPE, "padded_vocab=%lld exceeds 2^31 - 513",
+                (long long)desc->padded_vocab);
   st = check_hidden_dim(hidden_dim, rlk::kFp8Block);
   if (st != RLK_OK) return st;
   const int64_t n = desc->num_tokens;
