@@ -349,6 +349,57 @@ def test_other_stream_and_graph_replays(n):
         torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("n", [30, 300])
+def test_captured_training_step(n):
+    """Forward, loss and autograd's backward captured as one graph (no eager graph of the same
+    leaves alive), replayed on changing inputs with eager steps on other leaves between."""
+    k, v = 128, 2900
+    sets = [C.make_case(n, k, v, v, s, DEV) for s in (51, 52, 53)]
+    names = ("h", "w", "tgt", "mask", "g", "gl")
+    st = {m: getattr(sets[0], m).clone() for m in names}
+
+    def step(h, w, tgt, mask, g, gl):
+        h, w = h.detach().requires_grad_(True), w.detach().requires_grad_(True)
+        logp, lse = rlk.lmhead_selected_token_logprob(h, w, tgt, mask, real_vocab=v,
+                                                      num_vocab_tiles=7)
+        loss = (logp * g).sum() + (lse * gl).sum()
+        return (loss.detach(), *torch.autograd.grad(loss, (h, w)))
+
+    def eager(i):
+        return [bits(x).clone() for x in step(*(getattr(sets[i], m) for m in names))[1:]]
+
+    refs = [eager(i) for i in range(3)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):  # autograd's own warm-up, off the capturing stream
+        step(*(st[m] for m in names))
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(*(st[m] for m in names))
+    torch.cuda.synchronize()
+    for rep, i in enumerate((1, 0, 2, 2, 1)):
+        print(f"replay {rep} on set {i}", flush=True)
+        for m in names:
+            st[m].copy_(getattr(sets[i], m))
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out[1:], refs[i]):
+            assert torch.equal(bits(a), b), f"replay {rep}"
+        assert all(torch.equal(a, b) for a, b in zip(eager(2 - i), refs[2 - i]))
+
+
+def test_second_derivatives_are_refused():
+    case = C.make_case(20, 64, 300, 300, 3, DEV)
+    h = case.h.clone().requires_grad_(True)
+    logp, _ = rlk.lmhead_selected_token_logprob(h, case.w, case.tgt, case.mask, real_vocab=300,
+                                                num_vocab_tiles=1)
+    (grad,) = torch.autograd.grad(logp.sum(), h, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable|does not require grad"):
+        grad.float().sum().backward()
+
+
 def test_split_launches_give_the_same_bits(tmp_path):
     """Launches of at most so many threads (read once per process: child processes)."""
     ref = lmhead_child.run_all()

@@ -730,6 +730,7 @@ class _LmheadSelectedTokenLogprob(torch.autograd.Function):
         return logp, lse
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, g_logp, g_lse):
         hidden, weight, targets, active_mask, lse = ctx.saved_tensors
         real_vocab, ignore_index = ctx.cfg
