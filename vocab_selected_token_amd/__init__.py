@@ -674,12 +674,16 @@ def _device_of(t: torch.Tensor):
 
 
 def _scratch(nbytes: int, device, stream) -> torch.Tensor:
-    """A workspace of nbytes (0: the descriptor was refused) for a call on `stream`: the
-    allocator hands its memory out again only when that stream is through with it."""
+    """A workspace of nbytes (0: the descriptor was refused) for a call on `stream`."""
     if nbytes == 0:
         raise ValueError(f"invalid rlk_logp_desc: {rlk_last_error_detail()}")
-    t = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream is not None:
+    return _used_on(stream, torch.empty(nbytes, dtype=torch.uint8, device=device))
+
+
+def _used_on(stream, t):
+    """t (or None), whose memory the allocator is to hand out again only when `stream`, where
+    it is not the current one, is through with it."""
+    if stream is not None and t is not None:
         t.record_stream(stream)
     return t
 
@@ -704,8 +708,8 @@ def fused_lmhead_backward(hidden: torch.Tensor, weight: torch.Tensor, targets: t
     rows = weight.shape[0]
     desc = make_desc(n, real_vocab, rows, rows, 1, 1, ignore_index, validate)
     with _device_of(hidden):
-        dh = torch.empty_like(hidden) if want_hidden else None
-        dw = torch.empty_like(weight) if want_weight else None
+        dh = _used_on(stream, torch.empty_like(hidden) if want_hidden else None)
+        dw = _used_on(stream, torch.empty_like(weight) if want_weight else None)
         if workspace is None:
             workspace = _scratch(rlk_logp_fused_lmhead_bwd_workspace_bytes(
                 desc, k, want_hidden, want_weight), hidden.device, stream)
@@ -791,7 +795,7 @@ def quantize_fp8(x: torch.Tensor, block_rows: int = 1, *, stream=None):
             m = make_fp8_matrix(q, scale)
             rlk_fp8_quantize(n, k, x, x.stride(0) if n > 1 else k, block_rows, q, scale,
                              m.scale_row_stride, m.scale_col_stride, stream)
-    return q, scale
+    return _used_on(stream, q), _used_on(stream, scale)
 
 
 def _check_fp8(name, q, scale, block_rows):
@@ -839,13 +843,8 @@ def _check_lmhead_fp8(hidden, weight_q, weight_scale, real_vocab, **rows):
 
 def _fp8_pair(hidden, stream):
     """The (q, scale) pair of the hidden states, cast on `stream` where they are bf16."""
-    if isinstance(hidden, (tuple, list)):
-        return tuple(hidden)
-    pair = quantize_fp8(hidden, 1, stream=stream)
-    if stream is not None:
-        for t in pair:
-            t.record_stream(stream)
-    return pair
+    return tuple(hidden) if isinstance(hidden, (tuple, list)) else \
+        quantize_fp8(hidden, 1, stream=stream)
 
 
 def lmhead_logits_fp8(hidden, weight_q: torch.Tensor, weight_scale: torch.Tensor, *,
@@ -861,7 +860,7 @@ def lmhead_logits_fp8(hidden, weight_q: torch.Tensor, weight_scale: torch.Tensor
         n, k = q.shape
         v_pad = padded_vocab or weight_q.shape[0]
         ld = (v_pad + 7) // 8 * 8
-        logits = torch.empty((n, ld), dtype=torch.bfloat16, device=q.device)
+        logits = _used_on(stream, torch.empty((n, ld), dtype=torch.bfloat16, device=q.device))
         rlk_lmhead_logits_fp8(make_desc(n, real_vocab, v_pad, ld, 1), make_fp8_matrix(q, scale),
                               make_fp8_matrix(weight_q, weight_scale), k, logits, stream)
     return logits[:, :v_pad]
@@ -886,8 +885,8 @@ def fused_lmhead_fp8(hidden, weight_q: torch.Tensor, weight_scale: torch.Tensor,
             workspace = _scratch(rlk_logp_fused_lmhead_fp8_workspace_bytes(desc), x.device,
                                  stream)
         q, scale = _fp8_pair(hidden, stream)
-        logp = torch.empty(n, dtype=torch.float32, device=x.device)
-        lse = torch.empty(n, dtype=torch.float32, device=x.device)
+        logp = _used_on(stream, torch.empty(n, dtype=torch.float32, device=x.device))
+        lse = _used_on(stream, torch.empty(n, dtype=torch.float32, device=x.device))
         rlk_logp_fused_lmhead_fp8(desc, make_fp8_matrix(q, scale),
                                   make_fp8_matrix(weight_q, weight_scale), x.shape[1], targets,
                                   _u8_mask(active_mask), logp, lse, workspace, stream)
