@@ -87,6 +87,21 @@ def test_many_pieces(v):
     assert C.worst(dh, rh, eh) <= 1.0 and C.worst(dw, rw, ew) <= 1.0
 
 
+@pytest.mark.parametrize("live", [1, 200, 256, 257, 800])
+def test_few_live_rows(live):
+    """Of 1100 tokens only `live` are active, anywhere in the batch: dh's sums are then taken
+    in more parts (25 to each tile of 256 tokens if all were live, up to 125)."""
+    case = C.make_case(1100, 320, 33000, 33024, 17, DEV, mask_keep=1.0, ignore_frac=0.0)
+    gen = torch.Generator(device=DEV).manual_seed(live)
+    case.mask[torch.randperm(1100, generator=gen, device=DEV)[live:]] = False
+    dh, dw = backward(case, case.g, None)
+    rh, eh, rw, ew = C.gradients64(case, case.g, None)
+    h, w = C.worst(dh, rh, eh), C.worst(dw, rw, ew)
+    print(f"error over bound: dhidden {h:.3f}, dweight {w:.3f}", flush=True)
+    assert h <= 1.0 and w <= 1.0
+    assert (bits(dh[~case.mask]) == 0).all()
+
+
 def test_equal_gradients_round_without_bias():
     """A mean's gradient is the same for every row.  The target's entry of dz is then near
     that one number in every row; its rounding must not shift all of them alike.  The

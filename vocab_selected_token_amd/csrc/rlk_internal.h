@@ -187,7 +187,8 @@ struct LmheadFp8Args {
 struct LmheadBwdLayout {
   int32_t padded_tokens;  // num_tokens rounded up to 256
   int32_t piece;          // vocabulary columns at a time (a multiple of 256)
-  int32_t splits;         // dh: parts a piece's columns are summed in
+  int32_t splits;         // dh: parts a piece's columns are summed in, if all rows are live
+  int32_t most_splits;    // and at most, if not
   size_t head, idx, tgt, lse, cg, cc, resid, inv;
   size_t hc, ht, dz, dzt, tail, part, total;
 };
