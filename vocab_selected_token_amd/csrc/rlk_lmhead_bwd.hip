@@ -258,19 +258,20 @@ __device__ __forceinline__ void put_row(uint16_t* out, const u32x4& x) {
 // ---------------------------------------------------------------------------
 __global__ __launch_bounds__(kThreads) void dz_piece(
     const u32x4* __restrict__ hc, const u32x4* __restrict__ w, int32_t hidden_dim,
-    int32_t real_vocab, int32_t c0, int32_t piece, int32_t padded_tokens,
-    uint16_t* __restrict__ dz, char* ws, LmheadBwdLayout lay, int64_t blk_begin) {
+    int32_t real_vocab, int32_t c0, int32_t piece, uint16_t* __restrict__ dz, char* ws, LmheadBwdLayout lay, int64_t blk_begin) {
   __shared__ __attribute__((aligned(16))) char smem[kTileLds];
   const LiveRows live = live_rows(ws, lay);
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wv = wave >> 2, wt = wave & 3;
+  // only tiles with a live row
+  const int32_t n_va = piece / kBA, n_tb = ((int32_t)live.head[0] + kBB - 1) / kBB;
+  const int64_t blk = blk_begin + blockIdx.x, used = (int64_t)n_va * n_tb;
+  if (blk >= used) return;
   int32_t va, tb;
-  tile_of(blk_begin + xcd_local_block(blockIdx.x, gridDim.x), piece / kBA, padded_tokens / kBB, va,
-          tb);
+  tile_of(xcd_local_block(blk, used), n_va, n_tb, va, tb);
   const int32_t t0 = tb * kBB, v0 = va * kBA;  // v0: column inside the piece
-  if (t0 >= (int32_t)live.head[0]) return;
   f32x4 acc[kVS][kTS];
   if (c0 + v0 < real_vocab) {
     const int64_t row_bytes = (int64_t)hidden_dim * 2;
@@ -895,7 +896,7 @@ hipError_t launch_lmhead_bwd(const LmheadBwdArgs& a, hipStream_t stream) {
     if (c0 < a.real_vocab) {
       e = in_launches((int64_t)(piece / kBA) * n_t, kThreads, [&](int64_t b, int64_t nb) {
         hipLaunchKernelGGL(dz_piece, dim3((unsigned)nb), dim3(kThreads), 0, stream, hc, w, k,
-                           a.real_vocab, c0, piece, np, dz, ws, l, b);
+                           a.real_vocab, c0, piece, dz, ws, l, b);
       });
       if (e != hipSuccess) return e;
     }
