@@ -745,8 +745,6 @@ rlk_status run_fused_lmhead(const rlk_logp_desc* desc, const void* hidden, const
   a.pmax = reinterpret_cast<float*>(ws + lay.pmax);
   a.psum = reinterpret_cast<float*>(ws + lay.psum);
   if (fp8) fp8->z = reinterpret_cast<float*>(ws + lay.z);
-  e = rlk::launch_lmhead(a, fp8, stream);
-  if (e != hipSuccess) return hip_fail(e, "lmhead launch");
   rlk::Stage2Args a2;
   a2.logits = nullptr;
   a2.target_logit = a.target_logit;
@@ -764,8 +762,8 @@ rlk_status run_fused_lmhead(const rlk_logp_desc* desc, const void* hidden, const
   a2.lse = lse;
   a2.entropy = nullptr;
   a2.status = status;
-  e = rlk::launch_stage2(a2, stream);
-  if (e != hipSuccess) return hip_fail(e, "stage2_merge launch");
+  e = rlk::launch_lmhead(a, fp8, a2, stream);
+  if (e != hipSuccess) return hip_fail(e, "lmhead launch");
   if (validate) return finish_validate(status, stream, true);
   return ok();
 }

@@ -233,9 +233,10 @@ hipError_t noalloc_scratch(void** ptr);
 
 int64_t stage1_blocks(int64_t items);
 int64_t lmhead_grid_blocks(int32_t num_tokens, int32_t real_vocab);
-// The LM-head's segments and tile partials; with fp8 its operands (a.hidden and
+// The LM-head's segments, tile partials and stage-2 merge; with fp8 its operands (a.hidden and
 // a.weight are not used).
-hipError_t launch_lmhead(const LmheadArgs& a, const LmheadFp8Args* fp8, hipStream_t stream);
+hipError_t launch_lmhead(const LmheadArgs& a, const LmheadFp8Args* fp8, const Stage2Args& a2,
+                         hipStream_t stream);
 // One shard's segments: the blocks [vb_begin, vb_begin + n_vbs) of the grid.
 hipError_t launch_segments_fp8(const LmheadFp8Args& f, const SegmentArgs& sa, int32_t vb_begin,
                                int32_t n_vbs, hipStream_t stream);
