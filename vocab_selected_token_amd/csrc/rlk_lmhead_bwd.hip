@@ -37,6 +37,7 @@ static_assert(kBK == kLmheadSlabK, "slab width shared with the boundary");
 
 constexpr int kT = 64;  // tile edge of the gather and transpose kernels
 constexpr int kScanThreads = 1024;
+constexpr int32_t kScanFew = 1024;
 
 __device__ __forceinline__ float bf16_float(uint16_t b) {
   return __uint_as_float((uint32_t)b << 16);
@@ -61,80 +62,96 @@ __device__ __forceinline__ LiveRows live_rows(char* ws, const LmheadBwdLayout& l
           reinterpret_cast<int32_t*>(ws + l.inv),   reinterpret_cast<uint32_t*>(ws + l.head)};
 }
 
-// ---------------------------------------------------------------------------
-// live_rows_scan: one block.  The scale (largest finite |a g|, |gl|; 1 if all are
-// 0), then the live rows in ascending order.  Slots from the last live row up to
-// a multiple of 256 hold rows that give dz = 0.  An effective-active row with a
-// target outside [0, V_real) is live with NaN factors: its dz is NaN.
-// ---------------------------------------------------------------------------
-__global__ __launch_bounds__(kScanThreads) void live_rows_scan(
-    int32_t num_tokens, int32_t padded_tokens, int32_t real_vocab,
-    const int32_t* __restrict__ targets, const uint8_t* __restrict__ mask, int32_t ignore_index,
-    const float* __restrict__ lse, const float* __restrict__ grad,
-    const float* __restrict__ grad_lse, char* ws, LmheadBwdLayout lay,
-    uint32_t* __restrict__ status) {
-  __shared__ float wmax[kScanThreads / 64];
-  __shared__ int32_t wsum[kScanThreads / 64];
-  const LiveRows live = live_rows(ws, lay);
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+// What is known of the batch's rows.
+struct RowArgs {
+  const int32_t* __restrict__ targets;
+  const uint8_t* __restrict__ mask;
+  const float* __restrict__ lse;
+  const float* __restrict__ grad;
+  const float* __restrict__ grad_lse;
+  uint32_t* __restrict__ status;
+  int32_t num_tokens, padded_tokens, real_vocab, ignore_index;
+};
 
+template <int kThr>
+struct ScanLds {
+  float top[kThr / 64];
+  int32_t sum[kThr / 64];
+};
+
+// By a whole block: the scale (largest finite |a g|, |gl|; 1 if all are 0), then the
+// live rows in ascending order.  Returns their number; at(i, r) hears that live row i
+// is row r of the batch.  With `write`, they and the scale go to the workspace; slots
+// from the last live row up to a multiple of 256 hold rows that give dz = 0.  An
+// effective-active row with a target outside [0, V_real) is live with NaN factors:
+// its dz is NaN.
+template <int kThr, typename At>
+__device__ __forceinline__ int32_t scan_rows(const RowArgs& a, const LiveRows& live,
+                                             ScanLds<kThr>& lds, bool write, At&& at_row) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   auto row = [&](int32_t r, float& g, float& gl, int32_t& tgt, bool& act, bool& bad) {
-    act = (mask == nullptr || mask[r] != 0);
-    tgt = act ? targets[r] : -1;
-    act = act && tgt != ignore_index;
-    bad = act && (tgt < 0 || tgt >= real_vocab);
-    g = (act && grad) ? grad[r] : 0.0f;
-    gl = grad_lse ? grad_lse[r] : 0.0f;
+    act = (a.mask == nullptr || a.mask[r] != 0);
+    tgt = act ? a.targets[r] : -1;
+    act = act && tgt != a.ignore_index;
+    bad = act && (tgt < 0 || tgt >= a.real_vocab);
+    g = (act && a.grad) ? a.grad[r] : 0.0f;
+    gl = a.grad_lse ? a.grad_lse[r] : 0.0f;
   };
 
-  float top = 0.0f;
-  for (int32_t r = tid; r < num_tokens; r += kScanThreads) {
-    float g, gl;
-    int32_t tgt;
-    bool act, bad;
-    row(r, g, gl, tgt, act, bad);
-    const float m = fmaxf(isfinite(g) ? fabsf(g) : 0.0f, isfinite(gl) ? fabsf(gl) : 0.0f);
-    top = fmaxf(top, m);
-  }
+  float scale = 1.0f;
+  if (write) {
+    float top = 0.0f;
+    for (int32_t r = tid; r < a.num_tokens; r += kThr) {
+      float g, gl;
+      int32_t tgt;
+      bool act, bad;
+      row(r, g, gl, tgt, act, bad);
+      const float m = fmaxf(isfinite(g) ? fabsf(g) : 0.0f, isfinite(gl) ? fabsf(gl) : 0.0f);
+      top = fmaxf(top, m);
+    }
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-  if (lane == 0) wmax[wave] = top;
-  __syncthreads();
-  for (int w = 0; w < kScanThreads / 64; ++w) top = fmaxf(top, wmax[w]);
-  const float scale = top > 0.0f ? top : 1.0f;
+    for (int o = 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+    if (lane == 0) lds.top[wave] = top;
+    __syncthreads();
+    for (int w = 0; w < kThr / 64; ++w) top = fmaxf(top, lds.top[w]);
+    if (top > 0.0f) scale = top;
+  }
 
   int32_t base = 0;
-  for (int32_t r0 = 0; r0 < num_tokens; r0 += kScanThreads) {
+  for (int32_t r0 = 0; r0 < a.num_tokens; r0 += kThr) {
     const int32_t r = r0 + tid;
     float g = 0.0f, gl = 0.0f;
     int32_t tgt = -1;
     bool act = false, bad = false;
-    if (r < num_tokens) row(r, g, gl, tgt, act, bad);
+    if (r < a.num_tokens) row(r, g, gl, tgt, act, bad);
     const bool on = bad || g != 0.0f || gl != 0.0f;
     const uint64_t votes = __ballot(on);
     const int32_t before = __popcll(votes & ((1ull << lane) - 1));
     __syncthreads();  // the previous round's sums have been read
-    if (lane == 0) wsum[wave] = __popcll(votes);
+    if (lane == 0) lds.sum[wave] = __popcll(votes);
     __syncthreads();
     int32_t at = base + before;
-    for (int w = 0; w < kScanThreads / 64; ++w) {
-      if (w < wave) at += wsum[w];
-      base += wsum[w];
+    for (int w = 0; w < kThr / 64; ++w) {
+      if (w < wave) at += lds.sum[w];
+      base += lds.sum[w];
     }
+    if (on) at_row(at, r);
+    if (!write) continue;
     if (on) {
       const float nan = __builtin_nanf("");
       live.idx[at] = r;
       live.tgt[at] = (act && !bad) ? tgt : -1;
-      live.lse[at] = lse[r];
+      live.lse[at] = a.lse[r];
       live.cg[at] = bad ? nan : g / scale;
       live.cc[at] = bad ? nan : gl / scale - g / scale;
       live.resid[at] = 0.0f;
-      if (bad) status[0] = 1u;
+      if (bad) a.status[0] = 1u;
     }
-    if (r < num_tokens) live.inv[r] = on ? at : -1;
+    if (r < a.num_tokens) live.inv[r] = on ? at : -1;
   }
-  const int32_t end = min((base + 255) / 256 * 256, padded_tokens);
-  for (int32_t i = base + tid; i < end; i += kScanThreads) {
+  if (!write) return base;
+  const int32_t end = min((base + 255) / 256 * 256, a.padded_tokens);
+  for (int32_t i = base + tid; i < end; i += kThr) {
     live.idx[i] = -1;
     live.tgt[i] = -1;
     live.lse[i] = 0.0f;
@@ -146,6 +163,16 @@ __global__ __launch_bounds__(kScanThreads) void live_rows_scan(
     live.head[0] = (uint32_t)base;
     live.head[1] = __float_as_uint(scale);
   }
+  return base;
+}
+
+// ---------------------------------------------------------------------------
+// live_rows_scan: one block, for more than kScanFew tokens.
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(kScanThreads) void live_rows_scan(RowArgs a, char* ws,
+                                                               LmheadBwdLayout lay) {
+  __shared__ ScanLds<kScanThreads> lds;
+  scan_rows(a, live_rows(ws, lay), lds, true, [](int32_t, int32_t) {});
 }
 
 // How dh's blocks share its sums.  The grid is made for tiles of all tokens; where
@@ -171,29 +198,62 @@ struct Tile64 {
 
 // ---------------------------------------------------------------------------
 // gather_rows: hc[i] = h[idx[i]] (zeros in the slots behind the last live row)
-// and, when asked for, its transpose ht[k][i].
+// and, when asked for, its transpose ht[k][i].  The blocks behind those of the rows
+// copy the weight's last rows, those behind the last whole 64, followed by zeros: the
+// slab of dh's sum that they do not fill.
+// kScan: up to kScanFew tokens every block scans the rows itself, and the first
+// writes what the scan found (a launch less: the backward of 1 x 64 x 1000 takes 25.0 us
+// for 30.5, of 64 x 512 x 12003 45.0 for 49.2).
 // ---------------------------------------------------------------------------
-__global__ __launch_bounds__(256) void gather_rows(const u32x4* __restrict__ h, int32_t ldc,
-                                                   u32x4* __restrict__ hc, uint16_t* ht,
-                                                   int32_t padded_tokens, int32_t k_tiles,
-                                                   char* ws, LmheadBwdLayout lay,
-                                                   int64_t blk_begin) {
+struct GatherArgs {
+  const u32x4* __restrict__ h;
+  u32x4* __restrict__ hc;
+  uint16_t* __restrict__ ht;
+  const u32x4* __restrict__ w_tail;  // the weight's last rows
+  u32x4* __restrict__ tail;
+  int64_t n_rows;     // blocks of rows
+  int32_t tail_rows;  // 0: no such slab
+  int32_t ldc;        // 16-byte chunks per row
+};
+
+template <bool kScan>
+__global__ __launch_bounds__(256) void gather_rows(GatherArgs a, RowArgs rows, char* ws,
+                                                   LmheadBwdLayout lay, int64_t blk_begin) {
   __shared__ Tile64 t;
-  const LiveRows live = live_rows(ws, lay);
+  __shared__ int32_t from[kT];
   const int64_t blk = blk_begin + blockIdx.x;
+  if (blk >= a.n_rows) {
+    const int64_t i = (blk - a.n_rows) * 256 + threadIdx.x;
+    if (i < (int64_t)kBK * a.ldc)
+      a.tail[i] = i < (int64_t)a.tail_rows * a.ldc ? a.w_tail[i] : u32x4{0, 0, 0, 0};
+    return;
+  }
+  const LiveRows live = live_rows(ws, lay);
+  const int32_t k_tiles = a.ldc / (kT / 8);
   const int32_t i0 = (int32_t)(blk / k_tiles) * kT;
   const int32_t kc0 = (int32_t)(blk % k_tiles) * (kT / 8);
-  const int32_t end = (int32_t)(live.head[0] + 255) / 256 * 256;
-  if (i0 >= end) return;
+  int32_t count;
+  if constexpr (kScan) {
+    __shared__ ScanLds<256> lds;
+    if (threadIdx.x < kT) from[threadIdx.x] = -1;
+    __syncthreads();
+    count = scan_rows(rows, live, lds, blk == 0, [&](int32_t at, int32_t r) {
+      if (at >= i0 && at < i0 + kT) from[at - i0] = r;
+    });
+  } else {
+    count = (int32_t)live.head[0];
+    if (threadIdx.x < kT) from[threadIdx.x] = live.idx[i0 + threadIdx.x];
+  }
+  if (i0 >= (count + 255) / 256 * 256) return;
+  __syncthreads();
   for (int q = threadIdx.x; q < kT * kT / 8; q += 256) {
     const int r = q >> 3, c = q & 7;
-    const int32_t from = live.idx[i0 + r];
     u32x4 x = {0, 0, 0, 0};
-    if (from >= 0) x = h[(int64_t)from * ldc + kc0 + c];
-    hc[(int64_t)(i0 + r) * ldc + kc0 + c] = x;
-    if (ht) *reinterpret_cast<u32x4*>(&t.v[r][c * 8]) = x;
+    if (from[r] >= 0) x = a.h[(int64_t)from[r] * a.ldc + kc0 + c];
+    a.hc[(int64_t)(i0 + r) * a.ldc + kc0 + c] = x;
+    if (a.ht) *reinterpret_cast<u32x4*>(&t.v[r][c * 8]) = x;
   }
-  if (!ht) return;
+  if (!a.ht) return;
   __syncthreads();
   for (int q = threadIdx.x; q < kT * kT / 8; q += 256) {
     const int c = q >> 3, r = (q & 7) * 8;
@@ -203,17 +263,8 @@ __global__ __launch_bounds__(256) void gather_rows(const u32x4* __restrict__ h, 
     } o;
 #pragma unroll
     for (int i = 0; i < 8; ++i) o.e[i] = t.v[r + i][c];
-    *reinterpret_cast<u32x4*>(ht + (int64_t)(kc0 * 8 + c) * padded_tokens + i0 + r) = o.x;
+    *reinterpret_cast<u32x4*>(a.ht + (int64_t)(kc0 * 8 + c) * rows.padded_tokens + i0 + r) = o.x;
   }
-}
-
-// The weight's last rows, those behind the last whole 64, followed by zeros: the
-// slab of dh's sum that they do not fill.
-__global__ __launch_bounds__(256) void tail_rows(const u32x4* __restrict__ w, int32_t ldc,
-                                                 int32_t rows, u32x4* __restrict__ out,
-                                                 int64_t idx_begin) {
-  const int64_t i = idx_begin + (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i < (int64_t)kBK * ldc) out[i] = i < (int64_t)rows * ldc ? w[i] : u32x4{0, 0, 0, 0};
 }
 
 // Work index -> (tile of A, tile of B): strips of 4 A tiles, B-major inside, so
@@ -338,7 +389,7 @@ struct GradArgs {
   const uint16_t* __restrict__ dz;    // [padded_tokens][piece]
   const uint16_t* __restrict__ ht;    // [hidden_dim][padded_tokens]
   const uint16_t* __restrict__ w;     // [>= real_vocab][hidden_dim]
-  const uint16_t* __restrict__ tail;  // [64][hidden_dim], see tail_rows
+  const uint16_t* __restrict__ tail;  // [64][hidden_dim], see gather_rows
   float* __restrict__ part;           // [DhParts::splits][hidden_dim][DhParts::rows]
   uint16_t* __restrict__ dw;          // [padded_vocab][hidden_dim]
   int32_t hidden_dim, real_vocab, padded_vocab;
@@ -841,28 +892,31 @@ hipError_t launch_lmhead_bwd(const LmheadBwdArgs& a, hipStream_t stream) {
   uint16_t* ht = a.dweight ? reinterpret_cast<uint16_t*>(ws + l.ht) : nullptr;
   const u32x4* w = reinterpret_cast<const u32x4*>(a.weight);
 
-  hipLaunchKernelGGL(live_rows_scan, dim3(1), dim3(kScanThreads), 0, stream, a.num_tokens, np,
-                     a.real_vocab, a.targets, a.mask, a.ignore_index, a.lse, a.grad, a.grad_lse,
-                     ws, l, a.status);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const int32_t k_tiles = k / kT;
-  e = in_launches((int64_t)(np / kT) * k_tiles, 256, [&](int64_t b, int64_t nb) {
-    hipLaunchKernelGGL(gather_rows, dim3((unsigned)nb), dim3(256), 0, stream,
-                       reinterpret_cast<const u32x4*>(a.hidden), ldc, hc, ht, np, k_tiles, ws, l,
-                       b);
-  });
-  if (e != hipSuccess) return e;
-
-  if (a.dhidden && a.real_vocab % kBK != 0) {
-    const int32_t whole = a.real_vocab / kBK * kBK;
-    e = in_launches(((int64_t)kBK * ldc + 255) / 256, 256, [&](int64_t b, int64_t nb) {
-      hipLaunchKernelGGL(tail_rows, dim3((unsigned)nb), dim3(256), 0, stream,
-                         w + (int64_t)whole * ldc, ldc, a.real_vocab - whole,
-                         reinterpret_cast<u32x4*>(ws + l.tail), b * 256);
-    });
+  const RowArgs rows{a.targets, a.mask, a.lse, a.grad, a.grad_lse, a.status, a.num_tokens, np,
+                     a.real_vocab, a.ignore_index};
+  const bool scan = a.num_tokens <= kScanFew;
+  hipError_t e;
+  if (!scan) {
+    hipLaunchKernelGGL(live_rows_scan, dim3(1), dim3(kScanThreads), 0, stream, rows, ws, l);
+    e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
+  const int32_t whole = a.real_vocab / kBK * kBK;
+  GatherArgs ga;
+  ga.h = reinterpret_cast<const u32x4*>(a.hidden);
+  ga.hc = hc;
+  ga.ht = ht;
+  ga.w_tail = w + (int64_t)whole * ldc;
+  ga.tail = reinterpret_cast<u32x4*>(ws + l.tail);
+  ga.n_rows = (int64_t)(np / kT) * (k / kT);
+  ga.tail_rows = a.dhidden ? a.real_vocab - whole : 0;
+  ga.ldc = ldc;
+  const int64_t tail_blocks = ga.tail_rows ? ((int64_t)kBK * ldc + 255) / 256 : 0;
+  e = in_launches(ga.n_rows + tail_blocks, 256, [&](int64_t b, int64_t nb) {
+    hipLaunchKernelGGL(scan ? gather_rows<true> : gather_rows<false>, dim3((unsigned)nb),
+                       dim3(256), 0, stream, ga, rows, ws, l, b);
+  });
+  if (e != hipSuccess) return e;
 
   const int32_t n_k = (k + kBA - 1) / kBA, n_t = np / kBB;
   GradArgs g;
