@@ -266,8 +266,9 @@ def make_fp8_matrix(q, scale) -> rlk_fp8_matrix:
     """The rlk_fp8_matrix of a pair of tensors (either may be None): values [rows, cols],
     scales [row blocks, column blocks] with any positive strides."""
     # the stride of a dimension of one does not matter, and need not be positive
-    rs, cs = (1, 1) if scale is None else (st if n > 1 else 1 for n, st in
-                                           zip(scale.shape, scale.stride()))
+    rs, cs = (1, 1) if scale is None else scale.stride()
+    if scale is not None and 1 in scale.shape:
+        rs, cs = (st if n > 1 else 1 for n, st in zip(scale.shape, (rs, cs)))
     return rlk_fp8_matrix(_ptr(q), _ptr(scale), rs, cs)
 
 
@@ -764,6 +765,7 @@ class _LmheadSelectedTokenLogprob(torch.autograd.Function):
                                       vec(g_logp), vec(g_lse), want_hidden, want_weight)
         return dh, dw, None, None, None, None, None, None
 
+
 def lmhead_selected_token_logprob(hidden: torch.Tensor, weight: torch.Tensor,
                                   targets: torch.Tensor, active_mask=None, *, real_vocab: int,
                                   padded_vocab: int | None = None, num_vocab_tiles: int = 64,
@@ -797,18 +799,26 @@ def quantize_fp8(x: torch.Tensor, block_rows: int = 1, *, stream=None):
     if k == 0 or k % FP8_BLOCK:
         raise ValueError(f"x must have a multiple of {FP8_BLOCK} columns, got {k}")
     _check_device(x)
-    row_blocks, col_blocks = -(-n // block_rows), k // FP8_BLOCK
     with _device_of(x):
-        q = torch.empty((n, k), dtype=torch.float8_e4m3fn, device=x.device)
-        if block_rows == 1:
-            scale = torch.empty_strided((n, col_blocks), (1, max(n, 1)), device=x.device)
-        else:
-            scale = torch.empty((row_blocks, col_blocks), device=x.device)
-        if n:
-            m = make_fp8_matrix(q, scale)
-            rlk_fp8_quantize(n, k, x, x.stride(0) if n > 1 else k, block_rows, q, scale,
-                             m.scale_row_stride, m.scale_col_stride, stream)
-    return _used_on(stream, q), _used_on(stream, scale)
+        return _quantize(x, block_rows, stream)[:2]
+
+
+def _quantize(x, block_rows, stream):
+    """quantize_fp8 of a checked x, and the pair as an rlk_fp8_matrix."""
+    n, k = x.shape
+    col_blocks = k // FP8_BLOCK
+    q = _used_on(stream, torch.empty((n, k), dtype=torch.float8_e4m3fn, device=x.device))
+    if block_rows == 1:
+        strides = 1, n or 1
+        scale = torch.empty_strided((n, col_blocks), strides, device=x.device)
+    else:
+        strides = col_blocks, 1
+        scale = torch.empty((-(-n // block_rows), col_blocks), device=x.device)
+    _used_on(stream, scale)
+    if n:
+        rlk_fp8_quantize(n, k, x, x.stride(0) if n > 1 else k, block_rows, q, scale, *strides,
+                         stream)
+    return q, scale, rlk_fp8_matrix(q.data_ptr(), scale.data_ptr(), *strides)
 
 
 def _check_fp8(name, q, scale, block_rows):
@@ -826,7 +836,8 @@ def _check_fp8(name, q, scale, block_rows):
     want = (-(-q.shape[0] // block_rows), q.shape[1] // FP8_BLOCK)
     if tuple(scale.shape) != want:
         raise ValueError(f"the scales of {name} must have shape {want}, got {tuple(scale.shape)}")
-    if any(n > 1 and st < 1 for n, st in zip(scale.shape, scale.stride())):
+    if min(scale.stride()) < 1 and any(n > 1 and st < 1 for n, st in
+                                       zip(scale.shape, scale.stride())):
         raise ValueError(f"the scales of {name} must have positive strides")
 
 
@@ -854,10 +865,11 @@ def _check_lmhead_fp8(hidden, weight_q, weight_scale, real_vocab, **rows):
     return q
 
 
-def _fp8_pair(hidden, stream):
-    """The (q, scale) pair of the hidden states, cast on `stream` where they are bf16."""
-    return tuple(hidden) if isinstance(hidden, (tuple, list)) else \
-        quantize_fp8(hidden, 1, stream=stream)
+def _fp8_operand(hidden, stream):
+    """(q, scale, rlk_fp8_matrix) of the hidden states, cast on `stream` where they are bf16."""
+    if isinstance(hidden, (tuple, list)):
+        return (*hidden, make_fp8_matrix(*hidden))
+    return _quantize(hidden, 1, stream)
 
 
 def lmhead_logits_fp8(hidden, weight_q: torch.Tensor, weight_scale: torch.Tensor, *,
@@ -869,14 +881,14 @@ def lmhead_logits_fp8(hidden, weight_q: torch.Tensor, weight_scale: torch.Tensor
     (q, scale) pair of quantize_fp8(x, 1).  weight_q, weight_scale: quantize_fp8(W, 128)."""
     _check_lmhead_fp8(hidden, weight_q, weight_scale, real_vocab)
     with _device_of(weight_q):
-        q, scale = _fp8_pair(hidden, stream)
+        q, scale, matrix = _fp8_operand(hidden, stream)
         n, k = q.shape
         v_pad = padded_vocab or weight_q.shape[0]
         ld = (v_pad + 7) // 8 * 8
         logits = _used_on(stream, torch.empty((n, ld), dtype=torch.bfloat16, device=q.device))
-        rlk_lmhead_logits_fp8(make_desc(n, real_vocab, v_pad, ld, 1), make_fp8_matrix(q, scale),
+        rlk_lmhead_logits_fp8(make_desc(n, real_vocab, v_pad, ld, 1), matrix,
                               make_fp8_matrix(weight_q, weight_scale), k, logits, stream)
-    return logits[:, :v_pad]
+    return logits if ld == v_pad else logits[:, :v_pad]
 
 
 def fused_lmhead_fp8(hidden, weight_q: torch.Tensor, weight_scale: torch.Tensor,
@@ -897,10 +909,10 @@ def fused_lmhead_fp8(hidden, weight_q: torch.Tensor, weight_scale: torch.Tensor,
         if workspace is None:
             workspace = _scratch(rlk_logp_fused_lmhead_fp8_workspace_bytes(desc), x.device,
                                  stream)
-        q, scale = _fp8_pair(hidden, stream)
+        q, scale, matrix = _fp8_operand(hidden, stream)
         logp = _used_on(stream, torch.empty(n, dtype=torch.float32, device=x.device))
         lse = _used_on(stream, torch.empty(n, dtype=torch.float32, device=x.device))
-        rlk_logp_fused_lmhead_fp8(desc, make_fp8_matrix(q, scale),
+        rlk_logp_fused_lmhead_fp8(desc, matrix,
                                   make_fp8_matrix(weight_q, weight_scale), x.shape[1], targets,
                                   _u8_mask(active_mask), logp, lse, workspace, stream)
     return logp, lse
