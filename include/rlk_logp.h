@@ -355,8 +355,9 @@ rlk_status rlk_logp_fused_lmhead(const rlk_logp_desc* desc, const void* hidden,
  * where g = grad_logp, gl = grad_lse and a_r is effective-active; the softmax
  * cross entropy of a row is -logp_r.  z is computed again in pieces of the
  * vocabulary (num_tokens x columns of at most 2^28, but 16384 columns or more) and
- * each piece's dz, rounded to bf16, serves both products; the sums are fp32.  The pages have no such step;
- * the contract is rlk_logp_bwd_ex's, taken back through the product.
+ * each piece's dz, rounded to bf16, serves both products; the sums are fp32.  The
+ * pages have no such step; the contract is rlk_logp_bwd_ex's, taken back through the
+ * product.
  *   desc, hidden, weight, hidden_dim, targets, active_mask   as for
  *               rlk_logp_fused_lmhead, with num_tokens <= 2^21 and
  *               padded_vocab * hidden_dim / 8 < 2^31.  A row that no term reaches
@@ -425,7 +426,9 @@ rlk_status rlk_fp8_quantize(int64_t rows, int64_t cols, const void* x, int64_t l
 
 /* Logits from 8-bit operands: z = hidden . weight^T, each block of 128 of the sum
  * taken by the matrix cores, times its two scales and added up in fp32, rounded
- * once to bf16 -- the logits that rlk_logp_fwd and its kin read.
+ * once to bf16 -- the logits that rlk_logp_fwd and its kin read.  (A block's sum of
+ * 128 products is good to about 2^-14 of its largest product, as the matrix cores add
+ * 8-bit products; the rest is fp32.)
  *   desc        num_tokens, real_vocab, padded_vocab, ld_logits as for rlk_logp_fwd
  *               (the tiling is validated and not used; flags must be 0), with
  *               padded_vocab < 2^31 - 512.

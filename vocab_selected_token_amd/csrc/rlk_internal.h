@@ -182,8 +182,8 @@ struct LmheadFp8Args {
 
 // Gradients of the fused LM-head.  Byte offsets into its workspace (the status
 // words come first): what is known of the live rows, their hidden states by
-// tokens and by columns, a piece of dz (also by columns, for few tokens), the weight's last rows and the fp32
-// partials of dh.
+// tokens and by columns, a piece of dz (also by columns, for few tokens), the
+// weight's last rows and the fp32 partials of dh.
 struct LmheadBwdLayout {
   int32_t padded_tokens;  // num_tokens rounded up to 256
   int32_t piece;          // vocabulary columns at a time (a multiple of 256)

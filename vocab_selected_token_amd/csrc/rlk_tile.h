@@ -30,7 +30,8 @@
 // its own index contiguous.  A slab is then 64 rows of 512 bytes, and a fragment
 // comes from two transposing LDS reads (ds_read_b64_tr_b16): of 16 lanes, lane i
 // names 4 consecutive columns (4 (i % 4) on) of row i/4, and gets column i of the
-// four rows.  The chunks of row r are XOR-swizzled by 2 (r % 4) + 8 (r / 8 % 2):
+// four rows.  The product runs as fast as with both operands along the sum, and saves
+// the copy.  The chunks of row r are XOR-swizzled by 2 (r % 4) + 8 (r / 8 % 2):
 // the 8 rows that 32 lanes read at once lie 32 bytes apart over all 64 banks.
 #pragma once
 
