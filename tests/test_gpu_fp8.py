@@ -130,6 +130,39 @@ def test_logits(s):
     assert same(got, out[:, :pad])
 
 
+@pytest.mark.parametrize("n", [1, 70])
+def test_products_meet_in_groups_of_eight(n):
+    """The property on which the products' error bound rests: with one column its LSE is z.
+    A product beside one of 2^14 is kept down to 2^1 in the same 8 columns, and down to 2^-9 in
+    others; what is cut goes towards zero; a subnormal lines the others up as 2^-6 would; a
+    zero does not."""
+    def z(at):
+        """z of products {column: (h, w)}, as the streaming (n = 1) or the tile kernel has it."""
+        h = torch.zeros((n, 128), device=DEV)
+        w = torch.zeros((1, 128), device=DEV)
+        for k, (a, b) in at.items():
+            h[:, k], w[0, k] = a, b
+        hq, wq = h.to(torch.float8_e4m3fn), w.to(torch.float8_e4m3fn)
+        assert (hq.float() == h).all() and (wq.float() == w).all()
+        _, lse = rlk.fused_lmhead_fp8(
+            (hq, torch.ones((n, 1), device=DEV)), wq, torch.ones((1, 1), device=DEV),
+            torch.zeros(n, dtype=torch.int32, device=DEV), real_vocab=1, padded_vocab=256,
+            num_vocab_tiles=1)
+        assert (lse == lse[0]).all()
+        return float(lse[0])
+
+    top = (2.0 ** 7, 2.0 ** 7)
+    for sign in (1.0, -1.0):
+        assert z({8: top, 15: (sign * 2.0, 1.0)}) == 2.0 ** 14 + sign * 2.0
+        assert z({8: top, 15: (sign, 1.0)}) == 2.0 ** 14
+        assert z({8: top, 15: (sign * 1.875, 2.0)}) == 2.0 ** 14 + sign * 2.0
+        for k in (7, 16, 127):
+            assert z({8: top, k: (sign * 2.0 ** -9, 1.0)}) == 2.0 ** 14 + sign * 2.0 ** -9
+    assert z({0: (2.0 ** -9, 2.0 ** 8), 1: (2.0 ** -5, 2.0 ** -6)}) == 0.5 + 2.0 ** -11
+    assert z({0: (2.0 ** -9, 2.0 ** 8), 1: (2.0 ** -6, 2.0 ** -6)}) == 0.5
+    assert z({0: (0.0, 448.0), 1: (2.0 ** -9, 2.0 ** -9)}) == 2.0 ** -18
+
+
 def check_stats(c, logp, lse, z, err):
     """logp and LSE of z (64 bits): LSE moves by no more than z's largest error, the sum of
     exponentials is off by at most 128 half steps and, through the rounding of its

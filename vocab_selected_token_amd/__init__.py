@@ -790,7 +790,8 @@ FP8_BLOCK = 128  # columns (and weight rows) that share a scale
 def quantize_fp8(x: torch.Tensor, block_rows: int = 1, *, stream=None):
     """(q, scale): bf16 x [R, K] as e4m3 values [R, K] and the fp32 scales
     [ceil(R / block_rows), K / 128] of its block_rows x 128 blocks, so that q * scale stands
-    for x.  block_rows is 1 for hidden states and 128 for a weight.  The scales of 1 x 128
+    for x.  block_rows is 1 for hidden states and 128 for a weight (its real rows alone, where
+    the padding may hold anything: they would share a scale).  The scales of 1 x 128
     blocks lie with the tokens contiguous (a transposed view), as the products read them."""
     _check_logits(x, "x")
     if block_rows not in (1, FP8_BLOCK):
