@@ -502,8 +502,9 @@ __global__ __launch_bounds__(kThreads) void grad_piece(GradArgs a, char* ws, Lmh
 //              of its four waves goes over every fourth 64 of hidden_dim, operands
 //              straight from memory (the L2 holds ht), one or two MFMA steps for a
 //              whole sum, out through LDS in rows of 128 bytes.
-// 32 x 1024 x 151936: dz_stream 65 us (the weight at 4.8 TB/s), dw_few 76 us (dW at
-// 4.1 TB/s), dh_few 65 us; the tiles took 340 us for all three, these 228.
+// 32 x 1024 x 151936: dz_stream 65 us (the weight at 4.8 TB/s), dw_few 64 us (dW at
+// 4.9 TB/s; 76 with each step's ht loaded as it is used), dh_few 65 us; the tiles took
+// 340 us for the whole backward, these 215.
 // ---------------------------------------------------------------------------
 struct Bf16Stream {
   __device__ __forceinline__ void load_stage(int) {}
@@ -583,26 +584,34 @@ __global__ __launch_bounds__(256) void dw_few(const uint16_t* __restrict__ ht,
                            dzt + (int64_t)(b0 + ts * 16 + fr) * kFewLd + s * 32 + fg * 8)
                      : none;
   char* own = stage[wave];
+  i32x4 a[4][kSteps];
+  auto load_a = [&](int32_t k0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int vs = 0; vs < 4; ++vs)
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+        a[vs][s] = any ? *reinterpret_cast<const i32x4*>(
+                             ht + (int64_t)(k0 + vs * 16 + fr) * padded_tokens + s * 32 + fg * 8)
+                       : none;
+  };
+  if (wave * 64 < hidden_dim) load_a(wave * 64);
   for (int32_t k0 = wave * 64; k0 < hidden_dim; k0 += 256) {
     f32x4 acc[4][4];
 #pragma unroll
     for (int vs = 0; vs < 4; ++vs) {
-      i32x4 a[kSteps];
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s)
-        a[s] = any ? *reinterpret_cast<const i32x4*>(
-                         ht + (int64_t)(k0 + vs * 16 + fr) * padded_tokens + s * 32 + fg * 8)
-                   : none;
 #pragma unroll
       for (int ts = 0; ts < 4; ++ts) {
         acc[vs][ts] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
           acc[vs][ts] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              __builtin_bit_cast(bf16x8, a[s]), __builtin_bit_cast(bf16x8, b[ts][s]), acc[vs][ts],
-              0, 0, 0);
+              __builtin_bit_cast(bf16x8, a[vs][s]), __builtin_bit_cast(bf16x8, b[ts][s]),
+              acc[vs][ts], 0, 0, 0);
       }
     }
+    // the next step's, on their way while this one's results leave (in place of the last
+    // step's the last 64 again, unused)
+    load_a(min(k0 + 256, hidden_dim - 64));
 #pragma unroll
     for (int ts = 0; ts < 4; ++ts) {
       const int r = ts * 16 + fr;
