@@ -801,11 +801,11 @@ def quantize_fp8(x: torch.Tensor, block_rows: int = 1, *, stream=None):
         raise ValueError(f"x must have a multiple of {FP8_BLOCK} columns, got {k}")
     _check_device(x)
     with _device_of(x):
-        return _quantize(x, block_rows, stream)[:2]
+        return _quantize(x, block_rows, stream)
 
 
 def _quantize(x, block_rows, stream):
-    """quantize_fp8 of a checked x, and the pair as an rlk_fp8_matrix."""
+    """quantize_fp8 of a checked x."""
     n, k = x.shape
     col_blocks = k // FP8_BLOCK
     q = _used_on(stream, torch.empty((n, k), dtype=torch.float8_e4m3fn, device=x.device))
@@ -819,7 +819,7 @@ def _quantize(x, block_rows, stream):
     if n:
         rlk_fp8_quantize(n, k, x, x.stride(0) if n > 1 else k, block_rows, q, scale, *strides,
                          stream)
-    return q, scale, rlk_fp8_matrix(q.data_ptr(), scale.data_ptr(), *strides)
+    return q, scale
 
 
 def _check_fp8(name, q, scale, block_rows):
@@ -866,11 +866,21 @@ def _check_lmhead_fp8(hidden, weight_q, weight_scale, real_vocab, **rows):
     return q
 
 
-def _fp8_operand(hidden, stream):
-    """(q, scale, rlk_fp8_matrix) of the hidden states, cast on `stream` where they are bf16."""
+def _fp8_operand(hidden, nbytes, stream):
+    """(rlk_fp8_matrix of the hidden states, a buffer of at least nbytes): bf16 ones are cast on
+    `stream`, behind the nbytes of that buffer (one allocation costs less than three)."""
     if isinstance(hidden, (tuple, list)):
-        return (*hidden, make_fp8_matrix(*hidden))
-    return _quantize(hidden, 1, stream)
+        return make_fp8_matrix(*hidden), _scratch(nbytes, hidden[0].device, stream) if nbytes \
+            else None
+    n, k = hidden.shape
+    at = -(-nbytes // 256) * 256
+    scales = at + -(-n * k // 256) * 256
+    buffer = _scratch(scales + n * k // FP8_BLOCK * 4 + 256, hidden.device, stream)
+    base = buffer.data_ptr()
+    if n:
+        _check(_lib.rlk_fp8_quantize(n, k, hidden.data_ptr(), hidden.stride(0) if n > 1 else k,
+                                     1, base + at, base + scales, 1, n, _stream(stream)))
+    return rlk_fp8_matrix(base + at, base + scales, 1, n or 1), buffer
 
 
 def lmhead_logits_fp8(hidden, weight_q: torch.Tensor, weight_scale: torch.Tensor, *,
@@ -880,13 +890,13 @@ def lmhead_logits_fp8(hidden, weight_q: torch.Tensor, weight_scale: torch.Tensor
 
     hidden: bf16 [N, K], cast to e4m3 with one scale per token and 128 columns, or the
     (q, scale) pair of quantize_fp8(x, 1).  weight_q, weight_scale: quantize_fp8(W, 128)."""
-    _check_lmhead_fp8(hidden, weight_q, weight_scale, real_vocab)
-    with _device_of(weight_q):
-        q, scale, matrix = _fp8_operand(hidden, stream)
-        n, k = q.shape
+    x = _check_lmhead_fp8(hidden, weight_q, weight_scale, real_vocab)
+    with _device_of(x):
+        matrix, buffer = _fp8_operand(hidden, 0, stream)
+        n, k = x.shape
         v_pad = padded_vocab or weight_q.shape[0]
         ld = (v_pad + 7) // 8 * 8
-        logits = _used_on(stream, torch.empty((n, ld), dtype=torch.bfloat16, device=q.device))
+        logits = _used_on(stream, torch.empty((n, ld), dtype=torch.bfloat16, device=x.device))
         rlk_lmhead_logits_fp8(make_desc(n, real_vocab, v_pad, ld, 1), matrix,
                               make_fp8_matrix(weight_q, weight_scale), k, logits, stream)
     return logits if ld == v_pad else logits[:, :v_pad]
@@ -907,10 +917,12 @@ def fused_lmhead_fp8(hidden, weight_q: torch.Tensor, weight_scale: torch.Tensor,
     desc = make_desc(n, real_vocab, v_pad, v_pad, num_vocab_tiles, num_virtual_shards,
                      ignore_index, validate)
     with _device_of(x):
+        nbytes = rlk_logp_fused_lmhead_fp8_workspace_bytes(desc)
+        if nbytes == 0:
+            raise ValueError(f"invalid rlk_logp_desc: {rlk_last_error_detail()}")
+        matrix, buffer = _fp8_operand(hidden, nbytes if workspace is None else 0, stream)
         if workspace is None:
-            workspace = _scratch(rlk_logp_fused_lmhead_fp8_workspace_bytes(desc), x.device,
-                                 stream)
-        q, scale, matrix = _fp8_operand(hidden, stream)
+            workspace = buffer
         logp = _used_on(stream, torch.empty(n, dtype=torch.float32, device=x.device))
         lse = _used_on(stream, torch.empty(n, dtype=torch.float32, device=x.device))
         rlk_logp_fused_lmhead_fp8(desc, matrix,
