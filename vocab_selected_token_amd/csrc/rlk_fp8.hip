@@ -530,7 +530,7 @@ __global__ __launch_bounds__(kStreamThreads) void fp8_stream(Fp8Operands p, Segm
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int32_t v0 = v_begin + (int32_t)(blk_begin + blockIdx.x) * kStreamRows;
   const int32_t vw = v0 + wave * 16;
-  f32x4 acc[kTok];
+  f32x4 acc[1][kTok];
   if (v0 < a.row_hi && v0 + kStreamRows > a.row_lo) {
     Fp8Stream<kTok> math;
     math.lds = scales;
@@ -549,9 +549,9 @@ __global__ __launch_bounds__(kStreamThreads) void fp8_stream(Fp8Operands p, Segm
   for (int ts = 0; ts < kTok; ++ts) {
     const int32_t t = ts * 16 + (lane & 15), v = vw + 4 * (lane >> 4);
     if constexpr (kLogits)
-      store_logits<4, false>(lo, t, v, logits_of(lo, v, acc[ts]));
+      store_logits<4, false>(lo, t, v, logits_of(lo, v, acc[0][ts]));
     else
-      store_z(zo, t, v, acc[ts]);
+      store_z(zo, t, v, acc[0][ts]);
   }
 }
 

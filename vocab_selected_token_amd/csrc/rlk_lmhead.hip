@@ -23,6 +23,8 @@
 //                    column order into the tile partial, in the same [N][T]
 //                    layout that stage 1 of the materialised path writes.
 //
+// Up to 64 tokens lmhead_stream takes the first kernel's place.
+//
 // The product is the tile product of rlk_tile.h with W rows as operand A and
 // hidden rows as operand B (C[vocab][token]); rlk_lmhead_segments.h turns a
 // block's accumulators into its segments.
@@ -35,6 +37,7 @@
 
 #include "rlk_internal.h"
 #include "rlk_lmhead_segments.h"
+#include "rlk_stream.h"
 #include "rlk_tile.h"
 
 namespace rlk {
@@ -45,6 +48,8 @@ constexpr int kBT = kBB;  // tokens per block
 
 static_assert(kBV == kLmheadBlockVocab, "block width shared with the boundary");
 static_assert(kBK == kLmheadSlabK, "slab width shared with the boundary");
+
+constexpr int32_t kStreamTokens = 64;  // the most that lmhead_stream takes
 
 // ---------------------------------------------------------------------------
 // lmhead_segments
@@ -103,6 +108,45 @@ __global__ __launch_bounds__(kThreads) void lmhead_segments(
   f32x4 acc[kVS][kTS];
   tile_product(smem, wo, ho, 0, hidden_dim / kBK, wave, lane, acc);
   write_segments<kTS>(a, acc, reinterpret_cast<float*>(smem), vb, t0, wave >> 2, wave & 3, lane);
+}
+
+// ---------------------------------------------------------------------------
+// lmhead_stream: lmhead_segments for up to 64 tokens (16 kTok), whose time the weight's
+// bytes bound: stream_product in blocks of 256 rows, then z through LDS into the tile
+// kernel's layout, and so with its bits.  The whole call takes 70 us for 32 x 1024 x
+// 151936 (102 with tiles; the weight at 5.0 TB/s in this kernel), 275 us (327) for 32 x
+// 4096, 77 us (108) for 64 x 1024; 64 tokens need 144 registers, and in 128 they spilled
+// and took 103.
+// ---------------------------------------------------------------------------
+template <int kTok>
+__global__ __launch_bounds__(kThreads, kTok == 4 ? 2 : 4) void lmhead_stream(const char* __restrict__ h,
+                                                             const char* __restrict__ w,
+                                                             int32_t hidden_dim, int32_t vb_begin,
+                                                             SegmentArgs a, int64_t blk_begin) {
+  __shared__ union {
+    StreamLds<kTok> stream;
+    f32x4 z[kBV / 4][16 * kTok];
+  } lds;
+  __shared__ float xch[4 * 16 * 4];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int32_t vb = vb_begin + (int32_t)(blk_begin + blockIdx.x);
+  f32x4 acc[2][kTok];
+  Bf16Stream math;
+  stream_product<2, kThreads>(lds.stream, w, h, (uint32_t)hidden_dim * 2, a.row_lo, a.row_hi,
+                              a.num_tokens, vb * kBV, math, acc);
+#pragma unroll
+  for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+    for (int ts = 0; ts < kTok; ++ts)
+      lds.z[(wave * 2 + rt) * 4 + (lane >> 4)][ts * 16 + (lane & 15)] = acc[rt][ts];
+  __syncthreads();
+  const int wv = wave >> 2, wt = wave & 3;  // (waves without tokens only meet the barrier)
+  f32x4 z[kVS][1];
+#pragma unroll
+  for (int vs = 0; vs < kVS; ++vs)
+    z[vs][0] = lds.z[(wv * kVS + vs) * 4 + (lane >> 4)][min(wt, kTok - 1) * 16 + (lane & 15)];
+  write_segments<1>(a, z, xch, vb, 0, wv, wt, lane);
 }
 
 // The partial (M, S) of tile t of a token from its segments, in ascending columns.  A
@@ -248,6 +292,17 @@ hipError_t launch_segments(const LmheadArgs& a, const SegmentArgs& sa, int32_t v
   const int64_t blocks = (int64_t)n_vbs * n_tb;
   for (int64_t b0 = 0; b0 < blocks; b0 += max_blocks) {
     const int64_t nb = blocks - b0 < max_blocks ? blocks - b0 : max_blocks;
+    if (a.num_tokens <= kStreamTokens) {
+      const auto stream_kernel = a.num_tokens <= 16   ? lmhead_stream<1>
+                                 : a.num_tokens <= 32 ? lmhead_stream<2>
+                                                      : lmhead_stream<4>;
+      hipLaunchKernelGGL(stream_kernel, dim3((unsigned)nb), dim3(kThreads), 0, stream,
+                         static_cast<const char*>(a.hidden), static_cast<const char*>(a.weight),
+                         a.hidden_dim, vb_begin, sa, b0);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      continue;
+    }
     hipLaunchKernelGGL(lmhead_segments, dim3((unsigned)nb), dim3(kThreads), 0, stream,
                        reinterpret_cast<const u32x4*>(a.hidden),
                        reinterpret_cast<const u32x4*>(a.weight), a.hidden_dim, n_tb, vb_begin,

@@ -506,19 +506,6 @@ __global__ __launch_bounds__(kThreads) void grad_piece(GradArgs a, char* ws, Lmh
 // 4.9 TB/s; 76 with each step's ht loaded as it is used), dh_few 65 us; the tiles took
 // 340 us for the whole backward, these 215.
 // ---------------------------------------------------------------------------
-struct Bf16Stream {
-  __device__ __forceinline__ void load_stage(int) {}
-  __device__ __forceinline__ void store_stage(int) {}
-  __device__ __forceinline__ void begin(int) {}
-  __device__ __forceinline__ void multiply(f32x4& acc, const i32x4& a0, const i32x4& a1,
-                                           const i32x4& b0, const i32x4& b1, int, int) const {
-    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a0),
-                                                  __builtin_bit_cast(bf16x8, b0), acc, 0, 0, 0);
-    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a1),
-                                                  __builtin_bit_cast(bf16x8, b1), acc, 0, 0, 0);
-  }
-};
-
 constexpr int kFewLd = 64;  // tokens a row of dzt has room for
 
 template <int kTok>
@@ -532,7 +519,7 @@ __global__ __launch_bounds__(kStreamThreads) void dz_stream(
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int32_t v0 = c0 + (int32_t)(blk_begin + blockIdx.x) * kStreamRows;
-  f32x4 acc[kTok];
+  f32x4 acc[1][kTok];
   Bf16Stream math;
   // the gathered rows behind the last live one are zeros
   stream_product(lds, w, hc, (uint32_t)hidden_dim * 2, 0, real_vocab, 16 * kTok, v0, math, acc);
@@ -550,7 +537,7 @@ __global__ __launch_bounds__(kStreamThreads) void dz_stream(
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       o.e[e] = bf16_bits(
-          dz_of(acc[ts][e], nl, cg, cc, v + e < last, v + e == tgt, live.resid + i));
+          dz_of(acc[0][ts][e], nl, cg, cc, v + e < last, v + e == tgt, live.resid + i));
       if (dzt) dzt[(int64_t)(v + e - c0) * kFewLd + i] = o.e[e];
     }
     *reinterpret_cast<uint64_t*>(dz + (int64_t)i * piece + (v - c0)) = o.x;

@@ -1,7 +1,8 @@
 // rlk_stream.h -- few tokens times a weight that is streamed from memory, shared by
 // the LM-head kernels: the weight's bytes bound the time.
 //
-// A block is four waves of 16 vocabulary rows x all tokens (16 kTok at most).  The
+// A block is four waves of 16 vocabulary rows x all tokens (16 kTok at most), or, where
+// its results belong together, eight of 32.  The
 // weight is read once, from memory into registers, kBuf - 1 slabs (of 128 bytes a
 // row) ahead of the one that is multiplied; the hidden states come through LDS,
 // kBuf slabs at a time, loaded while the previous ones are multiplied (read by every
@@ -40,40 +41,46 @@ struct StreamLds {
   __attribute__((aligned(16))) char hidden[2][kBuf * kBytes];
 };
 
-// acc: C of this wave's 16 rows of the block's [v0, +64) and the tokens.  w: the
-// weight's rows [row_lo, row_hi) (some of them in the block; others are not read: the
-// row is clamped), row_bytes each, a multiple of 128; h: num_tokens rows.  `math`
+// acc: C of this wave's 16 kRT rows of the block's [v0, +kThr / 4 kRT) and the tokens.
+// w: the weight's rows [row_lo, row_hi) (some of them in the block; others are not read:
+// the row is clamped), row_bytes each, a multiple of 128; h: num_tokens rows.  `math`
 // multiplies a slab and may stage data of its own beside the hidden states.
-// Every wave of the block calls it.
-template <int kTok, typename Math>
+// Every wave of the block calls it; on return all have done with `lds`.
+template <int kRT = 1, int kThr = kStreamThreads, int kTok, typename Math>
 __device__ __forceinline__ void stream_product(StreamLds<kTok>& lds, const char* w, const char* h,
                                                uint32_t row_bytes, int32_t row_lo, int32_t row_hi,
                                                int32_t num_tokens, int32_t v0, Math& math,
-                                               f32x4 (&acc)[kTok]) {
+                                               f32x4 (&acc)[kRT][kTok]) {
 #if defined(__HIP_DEVICE_COMPILE__)  // the host pass cannot instantiate the target's builtins
   typedef StreamLds<kTok> T;
-  constexpr int kCopies = kBuf * T::kBytes / 16 / kStreamThreads;  // per thread and stage
+  constexpr int kCopies = kBuf * T::kBytes / 16 / kThr;  // per thread and stage
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nslab = (int)(row_bytes / kRowBytes);
 #pragma unroll
-  for (int ts = 0; ts < kTok; ++ts) acc[ts] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int rt = 0; rt < kRT; ++rt)
+#pragma unroll
+    for (int ts = 0; ts < kTok; ++ts) acc[rt][ts] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
   // a wave outside the rows reads one of them all the same, unused
   const int32_t w_first = max(v0, row_lo);
-  const int32_t w_rows = min(v0 + kStreamRows, row_hi) - w_first;
+  const int32_t w_rows = min(v0 + kThr / 4 * kRT, row_hi) - w_first;
   const __amdgpu_buffer_rsrc_t wrs =
       buffer_of(w + (int64_t)w_first * row_bytes, (int64_t)w_rows * row_bytes);
   const __amdgpu_buffer_rsrc_t hrs = buffer_of(h, (int64_t)num_tokens * row_bytes);
   const int fr = lane & 15, fc = lane >> 4;
-  const uint32_t woff =
-      (uint32_t)min(max(v0 + wave * 16 + fr - w_first, 0), w_rows - 1) * row_bytes + fc * 16;
+  uint32_t woff[kRT];
+#pragma unroll
+  for (int rt = 0; rt < kRT; ++rt)
+    woff[rt] = (uint32_t)min(max(v0 + (wave * kRT + rt) * 16 + fr - w_first, 0), w_rows - 1) *
+                   row_bytes +
+               fc * 16;
 
   u32x4 copy[kCopies];
   auto load_stage = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < kCopies; ++j) {
-      const int e = j * kStreamThreads + tid, c = e & 7, r = (e >> 3) % T::kTokens,
+      const int e = j * kThr + tid, c = e & 7, r = (e >> 3) % T::kTokens,
                 i = (e >> 3) / T::kTokens;
       copy[j] = __builtin_bit_cast(
           u32x4, __builtin_amdgcn_raw_buffer_load_b128(
@@ -87,7 +94,7 @@ __device__ __forceinline__ void stream_product(StreamLds<kTok>& lds, const char*
   auto store_stage = [&](int at) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < kCopies; ++j) {
-      const int e = j * kStreamThreads + tid, c = e & 7, r = (e >> 3) % T::kTokens,
+      const int e = j * kThr + tid, c = e & 7, r = (e >> 3) % T::kTokens,
                 i = (e >> 3) / T::kTokens;
       *reinterpret_cast<u32x4*>(lds.hidden[at] + i * T::kBytes + swizzled(r, c) * 16) = copy[j];
     }
@@ -100,13 +107,15 @@ __device__ __forceinline__ void stream_product(StreamLds<kTok>& lds, const char*
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
   };
 
-  i32x4 a[kBuf][2];
+  i32x4 a[kBuf][kRT][2];
   auto load = [&](int slab, int at) __attribute__((always_inline)) {
     const uint32_t off = (uint32_t)slab * kRowBytes;
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
-      a[at][c] = __builtin_bit_cast(
-          i32x4, __builtin_amdgcn_raw_buffer_load_b128(wrs, woff + c * 64, off, 0));
+    for (int rt = 0; rt < kRT; ++rt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        a[at][rt][c] = __builtin_bit_cast(
+            i32x4, __builtin_amdgcn_raw_buffer_load_b128(wrs, woff[rt] + c * 64, off, 0));
   };
   load_stage(0);
   // past the end the last slab is loaded again, unused
@@ -124,12 +133,15 @@ __device__ __forceinline__ void stream_product(StreamLds<kTok>& lds, const char*
         const char* hs = lds.hidden[at] + i * T::kBytes;
         math.begin(s + i);
 #pragma unroll
-        for (int ts = 0; ts < kTok; ++ts)
-          math.multiply(
-              acc[ts], a[i][0], a[i][1],
-              *reinterpret_cast<const i32x4*>(hs + swizzled(ts * 16 + fr, fc) * 16),
-              *reinterpret_cast<const i32x4*>(hs + swizzled(ts * 16 + fr, 4 + fc) * 16), at,
-              i * T::kTokens + ts * 16 + fr);
+        for (int ts = 0; ts < kTok; ++ts) {
+          const i32x4 b0 = *reinterpret_cast<const i32x4*>(hs + swizzled(ts * 16 + fr, fc) * 16);
+          const i32x4 b1 =
+              *reinterpret_cast<const i32x4*>(hs + swizzled(ts * 16 + fr, 4 + fc) * 16);
+#pragma unroll
+          for (int rt = 0; rt < kRT; ++rt)
+            math.multiply(acc[rt][ts], a[i][rt][0], a[i][rt][1], b0, b1, at,
+                          i * T::kTokens + ts * 16 + fr);
+        }
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -138,6 +150,20 @@ __device__ __forceinline__ void stream_product(StreamLds<kTok>& lds, const char*
   }
 #endif
 }
+
+// bf16: two k-steps of 32 a slab, in the order of the tile product.
+struct Bf16Stream {
+  __device__ __forceinline__ void load_stage(int) {}
+  __device__ __forceinline__ void store_stage(int) {}
+  __device__ __forceinline__ void begin(int) {}
+  __device__ __forceinline__ void multiply(f32x4& acc, const i32x4& a0, const i32x4& a1,
+                                           const i32x4& b0, const i32x4& b1, int, int) const {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a0),
+                                                  __builtin_bit_cast(bf16x8, b0), acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a1),
+                                                  __builtin_bit_cast(bf16x8, b1), acc, 0, 0, 0);
+  }
+};
 
 }  // namespace
 }  // namespace rlk
