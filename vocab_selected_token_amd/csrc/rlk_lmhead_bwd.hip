@@ -713,19 +713,22 @@ __global__ __launch_bounds__(kThreads) void dh_few(GradArgs a, char* ws, LmheadB
 }
 
 // ---------------------------------------------------------------------------
-// dh_finish: dh[r] = scale * (sum of the splits' partials in ascending order +
-// resid W[target]) in bf16; +0 on rows that are not live.  A block takes 64 live
-// rows x kCols columns (few, where few rows make few blocks of many splits), through
-// LDS from the partials' layout to rows, and writes the zeros of the 64 batch rows
-// of the same numbers.  The partials' bytes bound it: 27 us for 3405 rows x 4096 (59 MB of
-// them), 12 us for 32 x 1024 in 128 splits.
+// dh_finish: dh[r] = scale * (sum of the splits' partials in a fixed order + resid
+// W[target]) in bf16; +0 on rows that are not live.  A block takes 64 live rows x kCols
+// columns, through LDS from the partials' layout to rows, and writes the zeros of the 64
+// batch rows of the same numbers.  Few rows make few blocks of many splits: kCols is
+// small then, and kGroups of threads sum a range of the splits each.  The partials'
+// bytes bound it where there are many rows: 27 us for 3405 x 4096 (59 MB of them);
+// 32 x 1024 in 128 splits take 8 us (12 with one group).
 // ---------------------------------------------------------------------------
-template <int kCols>
-__global__ __launch_bounds__(256) void dh_finish(const float* __restrict__ part,
-                                                 int32_t num_tokens, int32_t ldc, const u32x4* __restrict__ w,
-                                                 u32x4* __restrict__ dh, char* ws,
-                                                 LmheadBwdLayout lay, int64_t blk_begin) {
-  __shared__ float t[kCols][kT + 1];  // [k][i]
+template <int kCols, int kGroups>
+__global__ __launch_bounds__(256 * kGroups) void dh_finish(const float* __restrict__ part,
+                                                           int32_t num_tokens, int32_t ldc,
+                                                           const u32x4* __restrict__ w,
+                                                           u32x4* __restrict__ dh, char* ws,
+                                                           LmheadBwdLayout lay,
+                                                           int64_t blk_begin) {
+  __shared__ float t[kGroups][kCols][kT + 1];  // [group of splits][k][i]
   const LiveRows live = live_rows(ws, lay);
   const int64_t blk = blk_begin + blockIdx.x;
   const int32_t k_tiles = ldc * 8 / kCols;
@@ -734,22 +737,24 @@ __global__ __launch_bounds__(256) void dh_finish(const float* __restrict__ part,
   const int32_t count = (int32_t)live.head[0];
   const DhParts parts(count, lay);
   const int64_t split_size = (int64_t)parts.rows * ldc * 8;
+  const int tid = threadIdx.x & 255, group = threadIdx.x >> 8;
+  const int32_t s0 = group * parts.splits / kGroups, s1 = (group + 1) * parts.splits / kGroups;
   if (i0 < count) {
-    for (int q = threadIdx.x; q < kT * kCols / 4; q += 256) {
+    for (int q = tid; q < kT * kCols / 4; q += 256) {
       const int k = q >> 4, i = (q & 15) * 4;
       if (i0 + i >= count) continue;
       const float* p = part + (int64_t)(kc0 * 8 + k) * parts.rows + i0 + i;
       f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 8
-      for (int32_t s = 0; s < parts.splits; ++s)
+      for (int32_t s = s0; s < s1; ++s)
         sum += *reinterpret_cast<const f32x4*>(p + s * split_size);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) t[k][i + e] = sum[e];
+      for (int e = 0; e < 4; ++e) t[group][k][i + e] = sum[e];
     }
   }
   __syncthreads();
   const float scale = __uint_as_float(live.head[1]);
-  for (int q = threadIdx.x; q < kT * kCols / 8; q += 256) {
+  for (int q = threadIdx.x; q < kT * kCols / 8; q += 256 * kGroups) {
     const int r = q / (kCols / 8), c = q % (kCols / 8);
     const int32_t at = i0 + r;
     if (at < num_tokens && live.inv[at] < 0) dh[(int64_t)at * ldc + kc0 + c] = u32x4{0, 0, 0, 0};
@@ -763,7 +768,9 @@ __global__ __launch_bounds__(256) void dh_finish(const float* __restrict__ part,
     if (rs != 0.0f) wr.x = w[(int64_t)live.tgt[at] * ldc + kc0 + c];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      float x = t[c * 8 + e][r];
+      float x = t[0][c * 8 + e][r];
+#pragma unroll
+      for (int g = 1; g < kGroups; ++g) x += t[g][c * 8 + e][r];
       if (rs != 0.0f) x = fmaf(rs, bf16_float(wr.e[e]), x);
       o.e[e] = bf16_bits(x * scale);
     }
@@ -972,11 +979,12 @@ hipError_t launch_lmhead_bwd(const LmheadBwdArgs& a, hipStream_t stream) {
     if (e != hipSuccess) return e;
   }
   if (a.dhidden) {
-    const int32_t cols = few ? 16 : kT;
-    e = in_launches((int64_t)(np / kT) * (k / cols), 256, [&](int64_t b, int64_t nb) {
-      hipLaunchKernelGGL(few ? dh_finish<16> : dh_finish<kT>, dim3((unsigned)nb), dim3(256), 0,
-                         stream, reinterpret_cast<const float*>(ws + l.part),
-                         a.num_tokens, ldc, w, reinterpret_cast<u32x4*>(a.dhidden), ws, l, b);
+    const int32_t cols = few ? 16 : kT, groups = few ? 4 : 1;
+    e = in_launches((int64_t)(np / kT) * (k / cols), 256 * groups, [&](int64_t b, int64_t nb) {
+      hipLaunchKernelGGL((few ? dh_finish<16, 4> : dh_finish<kT, 1>), dim3((unsigned)nb),
+                         dim3(256 * groups), 0, stream,
+                         reinterpret_cast<const float*>(ws + l.part), a.num_tokens, ldc, w,
+                         reinterpret_cast<u32x4*>(a.dhidden), ws, l, b);
     });
   }
   return e;
