@@ -1000,7 +1000,7 @@ int64_t read_thread_limit() {
   char* end = nullptr;
   const long long n = strtoll(v, &end, 10);
   if (end == v) return kLimit;  // not a number: the default
-  if (n < 1024) return 1024;    // at least two blocks of every kernel
+  if (n < 1024) return 1024;    // at least one block of every kernel
   return n < kLimit ? (int64_t)n : kLimit;
 }
 
