@@ -230,7 +230,7 @@ def test_infinite_weight_stays_in_its_row(n):
     assert dw.float().isfinite().all() and (dw[100] == 0).all()
 
 
-@pytest.mark.parametrize("n", [9, 300])
+@pytest.mark.parametrize("n", [9, 100, 300])
 def test_workspace_contents_do_not_matter(n):
     case = C.make_case(n, 128, 1000, 1024, 21, DEV)
     lse = lse_of(case)
@@ -246,6 +246,22 @@ def test_workspace_contents_do_not_matter(n):
         out.append((bits(dh).clone(), bits(dw).clone()))
     for o in out[1:]:
         assert torch.equal(o[0], out[0][0]) and torch.equal(o[1], out[0][1])
+
+
+def test_forward_rows_do_not_depend_on_the_batch():
+    """The forward's streaming kernel (up to 64 tokens) and its tiles of 128 (65, 128 tokens),
+    192 (333, 777) and 256 (1024) give a token the same bits, whatever the virtual shards."""
+    case = C.make_case(1024, 64, 50021, 50176, 19, DEV)
+    kw = dict(real_vocab=50021, num_vocab_tiles=61)
+    logp, lse = rlk.fused_lmhead(case.h, case.w, case.tgt, case.mask, **kw)
+    for n in (1, 16, 17, 40, 64, 65, 128, 333, 777):
+        for at in (0, 1024 - n):
+            rows = slice(at, at + n)
+            for shards in (1, 3):
+                got = rlk.fused_lmhead(case.h[rows], case.w, case.tgt[rows], case.mask[rows],
+                                       num_virtual_shards=shards, **kw)
+                assert torch.equal(bits(got[0]), bits(logp[rows])), (n, shards)
+                assert torch.equal(bits(got[1]), bits(lse[rows])), (n, shards)
 
 
 def test_autograd_function():

@@ -606,27 +606,11 @@ hipError_t launch_tile(const Fp8Operands& p, const SegmentArgs& sa, const Logits
   });
 }
 
-// Tokens of a tile, in 64s.  A tile of 128, 192 or 256 tokens takes about 2.3, 3.0
-// and 4.0 units of time (over many rounds of the chip's 256 CUs, one block each:
-// 39, 50 and 67 us a round at hidden_dim 4096), and the last round of blocks and the
-// last tile of tokens are paid in full: 333 tokens x 50021 columns take 66 us in
-// tiles of 256, 56 in tiles of 192 and 63 in tiles of 128; 65 tokens x 151936 columns
-// 226, 193 and 165; 4096 tokens 2480, 2577 and 2883.  The smaller tile has to be
-// clearly ahead, for it reads the weight more often.
-int tile_tokens(int32_t n, int32_t n_vbs) {
-  const double unit[] = {2.3, 3.0, 4.0};
-  int best = 4;
-  double least = 0.0;
-  for (int k = 4; k >= 2; --k) {
-    const int64_t blocks = (int64_t)n_vbs * ((n + 64 * k - 1) / (64 * k));
-    const double cost = (double)((blocks + 255) / 256) * unit[k - 2];
-    if (k == 4 || cost < 0.95 * least) {
-      least = cost;
-      best = k;
-    }
-  }
-  return best;
-}
+// Time of a round of tiles of 128, 192 and 256 tokens (hidden_dim 4096: 39, 50 and 67
+// us), see tile_tokens: 333 tokens x 50021 columns take 66 us in tiles of 256, 56 in
+// tiles of 192 and 63 in tiles of 128; 65 tokens x 151936 columns 226, 193 and 165;
+// 4096 tokens 2480, 2577 and 2883.
+constexpr double kTileUnits[] = {2.3, 3.0, 4.0};
 
 // The product over the columns [256 vb_begin, +256 n_vbs).  Up to 64 tokens the
 // weight's bytes bound the time and the stream kernel's registers hold all
@@ -637,7 +621,7 @@ hipError_t launch_product(const Fp8Operands& p, const SegmentArgs& sa, const Log
                           const ZOut& zo, int32_t vb_begin, int32_t n_vbs, hipStream_t stream) {
   const int32_t n = sa.num_tokens;
   if (n > kFp8FewTokens) {
-    switch (tile_tokens(n, n_vbs)) {
+    switch (tile_tokens(n, n_vbs, kTileUnits)) {
       case 2: return launch_tile<kLogits, 2>(p, sa, lo, vb_begin, n_vbs, stream);
       case 3: return launch_tile<kLogits, 3>(p, sa, lo, vb_begin, n_vbs, stream);
       default: return launch_tile<kLogits, 4>(p, sa, lo, vb_begin, n_vbs, stream);

@@ -231,6 +231,24 @@ constexpr size_t kNoAllocScratchBytes = (size_t{32} << 20) + 256;
 // Its device address on the current device (looked up once per device).
 hipError_t noalloc_scratch(void** ptr);
 
+// Tokens of an LM-head tile, in 64s (2 to 4), for n tokens and n_vbs vocabulary blocks:
+// unit is the time of a round -- the chip's 256 CUs, a block each -- of such tiles.  The
+// last round of blocks and the last tile of tokens are paid in full, which narrower
+// tiles may save; one has to be clearly ahead, for it reads the weight more often.
+inline int tile_tokens(int32_t n, int32_t n_vbs, const double (&unit)[3]) {
+  int best = 4;
+  double least = 0.0;
+  for (int k = 4; k >= 2; --k) {
+    const int64_t blocks = (int64_t)n_vbs * (((int64_t)n + 64 * k - 1) / (64 * k));
+    const double cost = (double)((blocks + 255) / 256) * unit[k - 2];
+    if (k == 4 || cost < 0.95 * least) {
+      least = cost;
+      best = k;
+    }
+  }
+  return best;
+}
+
 int64_t stage1_blocks(int64_t items);
 int64_t lmhead_grid_blocks(int32_t num_tokens, int32_t real_vocab);
 // The LM-head's segments, tile partials and stage-2 merge; with fp8 its operands (a.hidden and

@@ -12,7 +12,8 @@
 //
 // Two kernels run before the ordinary stage-2 merge (for few tokens the second
 // does that merge as well: lmhead_rows):
-//   lmhead_segments  bf16 MFMA GEMM of a 256-vocab x 256-token block over the
+//   lmhead_segments  bf16 MFMA GEMM of a 256-vocab x 256-token block (or of 128
+//                    or 192 tokens, by how many blocks that makes) over the
 //                    whole hidden dimension, then, per token, the (max, sumexp)
 //                    of each "segment" -- the part of the block's vocabulary
 //                    that lies in one tile (a block holds at most one tile
@@ -44,7 +45,7 @@ namespace rlk {
 namespace {
 
 constexpr int kBV = kBA;  // vocabulary rows per block (= kLmheadBlockVocab)
-constexpr int kBT = kBB;  // tokens per block
+constexpr int kBT = kBB;  // tokens per block, at most
 
 static_assert(kBV == kLmheadBlockVocab, "block width shared with the boundary");
 static_assert(kBK == kLmheadSlabK, "slab width shared with the boundary");
@@ -69,11 +70,13 @@ constexpr int32_t kStreamTokens = 64;  // the most that lmhead_stream takes
 // every grouping of the tiles: the slots, and so the partials, do not depend
 // on the shard count.
 // ---------------------------------------------------------------------------
+template <int kTok>
 __global__ __launch_bounds__(kThreads) void lmhead_segments(
     const u32x4* __restrict__ h, const u32x4* __restrict__ w, int32_t hidden_dim, int32_t n_tb,
     int32_t vb_begin, int32_t n_vbs, SegmentArgs a, int64_t blk_begin) {
-  __shared__ __attribute__((aligned(16))) char smem[kTileLds];
-  static_assert(kTileLds >= kBT * 4 * (int)sizeof(float), "epilogue exchange fits");
+  constexpr int kTokens = 64 * kTok;
+  __shared__ __attribute__((aligned(16))) char smem[2 * kStageBytes<kTok>];
+  static_assert(sizeof(smem) >= kTokens * 4 * sizeof(float), "epilogue exchange fits");
 
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -94,7 +97,7 @@ __global__ __launch_bounds__(kThreads) void lmhead_segments(
   const int32_t vb = vb_begin + (int32_t)strip * kGroupV + r_in % strip_w;
   const int32_t tb = r_in / strip_w;
   const int32_t v0 = vb * kBV;
-  const int32_t t0 = tb * kBT;
+  const int32_t t0 = tb * kTokens;
   const int32_t ldc = hidden_dim / 8;  // 16-byte chunks per row
   const int64_t row_bytes = (int64_t)ldc * 16;
 
@@ -103,11 +106,11 @@ __global__ __launch_bounds__(kThreads) void lmhead_segments(
   const int32_t w_first = max(v0, a.row_lo);
   const TileOperand wo(w + (int64_t)w_first * ldc, row_bytes, min(v0 + kBV, a.row_hi) - w_first,
                        v0 - w_first, wave, lane);
-  const TileOperand ho(h + (int64_t)t0 * ldc, row_bytes, min(t0 + kBT, a.num_tokens) - t0, 0,
-                       wave, lane);
-  f32x4 acc[kVS][kTS];
+  const TileOperandOf<kTok> ho(h + (int64_t)t0 * ldc, row_bytes,
+                               min(t0 + kTokens, a.num_tokens) - t0, 0, wave, lane);
+  f32x4 acc[kVS][kTok];
   tile_product(smem, wo, ho, 0, hidden_dim / kBK, wave, lane, acc);
-  write_segments<kTS>(a, acc, reinterpret_cast<float*>(smem), vb, t0, wave >> 2, wave & 3, lane);
+  write_segments<kTok>(a, acc, reinterpret_cast<float*>(smem), vb, t0, wave >> 2, wave & 3, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -283,30 +286,39 @@ int64_t lmhead_grid_blocks(int32_t num_tokens, int32_t real_vocab) {
 
 namespace {
 
+// Time of a round of tiles of 128, 192 and 256 tokens (hidden_dim 4096: 65, 81 and 100
+// us; 1024: 19, 24 and 31), see tile_tokens.  It takes narrower tiles for 777 tokens x
+// 1088 x 50021 (110 us for the call; 125 with 256 tokens), 333 x 2176 x 50021 (90; 108),
+// 128 x 1024 x 151936 (90; 111) and 200 x 2048 x 12003 (38; 54).
+constexpr double kTileUnits[] = {2.5, 3.15, 4.0};
+
 // One shard's segments, in launches of at most `limit` threads; a block's work
 // index (and so its tile) does not depend on the split.
 hipError_t launch_segments(const LmheadArgs& a, const SegmentArgs& sa, int32_t vb_begin,
                            int32_t n_vbs, hipStream_t stream) {
-  const int32_t n_tb = (a.num_tokens + kBT - 1) / kBT;
+  const int32_t n = a.num_tokens;
+  const bool few = n <= kStreamTokens;
+  const int k_tok = few ? 0 : tile_tokens(n, n_vbs, kTileUnits);
+  const int32_t n_tb = few ? 1 : (n + 64 * k_tok - 1) / (64 * k_tok);
+  const auto stream_kernel = n <= 16   ? lmhead_stream<1>
+                             : n <= 32 ? lmhead_stream<2>
+                                       : lmhead_stream<4>;
+  const auto tile_kernel = k_tok == 2   ? lmhead_segments<2>
+                           : k_tok == 3 ? lmhead_segments<3>
+                                        : lmhead_segments<4>;
   const int64_t max_blocks = launch_thread_limit() / kThreads;
   const int64_t blocks = (int64_t)n_vbs * n_tb;
   for (int64_t b0 = 0; b0 < blocks; b0 += max_blocks) {
-    const int64_t nb = blocks - b0 < max_blocks ? blocks - b0 : max_blocks;
-    if (a.num_tokens <= kStreamTokens) {
-      const auto stream_kernel = a.num_tokens <= 16   ? lmhead_stream<1>
-                                 : a.num_tokens <= 32 ? lmhead_stream<2>
-                                                      : lmhead_stream<4>;
-      hipLaunchKernelGGL(stream_kernel, dim3((unsigned)nb), dim3(kThreads), 0, stream,
+    const dim3 grid((unsigned)(blocks - b0 < max_blocks ? blocks - b0 : max_blocks));
+    if (few)
+      hipLaunchKernelGGL(stream_kernel, grid, dim3(kThreads), 0, stream,
                          static_cast<const char*>(a.hidden), static_cast<const char*>(a.weight),
                          a.hidden_dim, vb_begin, sa, b0);
-      const hipError_t e = hipGetLastError();
-      if (e != hipSuccess) return e;
-      continue;
-    }
-    hipLaunchKernelGGL(lmhead_segments, dim3((unsigned)nb), dim3(kThreads), 0, stream,
-                       reinterpret_cast<const u32x4*>(a.hidden),
-                       reinterpret_cast<const u32x4*>(a.weight), a.hidden_dim, n_tb, vb_begin,
-                       n_vbs, sa, b0);
+    else
+      hipLaunchKernelGGL(tile_kernel, grid, dim3(kThreads), 0, stream,
+                         reinterpret_cast<const u32x4*>(a.hidden),
+                         reinterpret_cast<const u32x4*>(a.weight), a.hidden_dim, n_tb, vb_begin,
+                         n_vbs, sa, b0);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

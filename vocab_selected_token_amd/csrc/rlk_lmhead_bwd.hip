@@ -313,35 +313,39 @@ __device__ __forceinline__ void put_row(uint16_t* out, const u32x4& x) {
 // column (777 tokens x 1088 x 50021: backward 249 -> 225 us; 1024 x 2048 x 151936:
 // 1744 -> 1718 us).
 // ---------------------------------------------------------------------------
+template <int kTok>
 __global__ __launch_bounds__(kThreads) void dz_piece(
     const u32x4* __restrict__ hc, const u32x4* __restrict__ w, int32_t hidden_dim,
-    int32_t real_vocab, int32_t c0, int32_t piece, uint16_t* __restrict__ dz, char* ws, LmheadBwdLayout lay, int64_t blk_begin) {
-  __shared__ __attribute__((aligned(16))) char smem[kTileLds];
+    int32_t real_vocab, int32_t c0, int32_t piece, uint16_t* __restrict__ dz, char* ws,
+    LmheadBwdLayout lay, int64_t blk_begin) {
+  constexpr int kTokens = 64 * kTok;
+  __shared__ __attribute__((aligned(16))) char smem[2 * kStageBytes<kTok>];
+  static_assert(sizeof(smem) >= kWaves * 4096 * kTok, "the rows fit");
   const LiveRows live = live_rows(ws, lay);
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wv = wave >> 2, wt = wave & 3;
   // only tiles with a live row
-  const int32_t n_va = piece / kBA, n_tb = ((int32_t)live.head[0] + kBB - 1) / kBB;
+  const int32_t n_va = piece / kBA, n_tb = ((int32_t)live.head[0] + kTokens - 1) / kTokens;
   const int64_t blk = blk_begin + blockIdx.x, used = (int64_t)n_va * n_tb;
   if (blk >= used) return;
   int32_t va, tb;
   tile_of(xcd_local_block(blk, used), n_va, n_tb, va, tb);
-  const int32_t t0 = tb * kBB, v0 = va * kBA;  // v0: column inside the piece
-  f32x4 acc[kVS][kTS];
+  const int32_t t0 = tb * kTokens, v0 = va * kBA;  // v0: column inside the piece
+  f32x4 acc[kVS][kTok];
   if (c0 + v0 < real_vocab) {
     const int64_t row_bytes = (int64_t)hidden_dim * 2;
     const TileOperand wo(reinterpret_cast<const char*>(w) + (int64_t)(c0 + v0) * row_bytes,
                          row_bytes, min(kBA, real_vocab - c0 - v0), 0, wave, lane);
-    const TileOperand ho(reinterpret_cast<const char*>(hc) + (int64_t)t0 * row_bytes, row_bytes,
-                         kBB, 0, wave, lane);
+    const TileOperandOf<kTok> ho(reinterpret_cast<const char*>(hc) + (int64_t)t0 * row_bytes,
+                                 row_bytes, kTokens, 0, wave, lane);
     tile_product(smem, wo, ho, 0, hidden_dim / kBK, wave, lane, acc);
   }
   const int32_t cw = v0 + wv * 128;  // this wave's first column
 #pragma unroll
-  for (int ts = 0; ts < kTS; ++ts) {
-    const int32_t i = t0 + (wt * kTS + ts) * 16 + (lane & 15);
+  for (int ts = 0; ts < kTok; ++ts) {
+    const int32_t i = t0 + (wt * kTok + ts) * 16 + (lane & 15);
     const float nl = -live.lse[i] * kLog2e, cg = live.cg[i], cc = live.cc[i];
     const int32_t tgt = live.tgt[i] - c0;
     // columns from here on are padding; all of them for a slot behind the last live row
@@ -364,7 +368,7 @@ __global__ __launch_bounds__(kThreads) void dz_piece(
         }
     }
   }
-  store_rows<kTS>(
+  store_rows<kTok>(
       smem, wave, lane,
       [&](int vs, int ts) __attribute__((always_inline)) {
         union {
@@ -376,7 +380,7 @@ __global__ __launch_bounds__(kThreads) void dz_piece(
         return o.x;
       },
       [&](int r, int c, const u32x4& x) __attribute__((always_inline)) {
-        put_row(dz + (int64_t)(t0 + wt * 64 + r) * piece + v0 + wv * 128 + c * 8, x);
+        put_row(dz + (int64_t)(t0 + wt * (16 * kTok) + r) * piece + v0 + wv * 128 + c * 8, x);
       });
 }
 
@@ -964,9 +968,14 @@ hipError_t launch_lmhead_bwd(const LmheadBwdArgs& a, hipStream_t stream) {
       continue;
     }
     if (c0 < a.real_vocab) {
-      e = in_launches((int64_t)(piece / kBA) * n_t, kThreads, [&](int64_t b, int64_t nb) {
-        hipLaunchKernelGGL(dz_piece, dim3((unsigned)nb), dim3(kThreads), 0, stream, hc, w, k,
-                           a.real_vocab, c0, piece, dz, ws, l, b);
+      // tiles of 128 tokens where one holds them all (128 x 1024 x 151936: backward 305 us
+      // for 331; 90 x 512 x 12003: 62 for 71)
+      const bool narrow = a.num_tokens <= 128;
+      const int64_t tiles = (int64_t)(piece / kBA) * (narrow ? 1 : n_t);
+      e = in_launches(tiles, kThreads, [&](int64_t b, int64_t nb) {
+        hipLaunchKernelGGL((narrow ? dz_piece<2> : dz_piece<4>), dim3((unsigned)nb),
+                           dim3(kThreads), 0, stream, hc, w, k, a.real_vocab, c0, piece, dz, ws,
+                           l, b);
       });
       if (e != hipSuccess) return e;
     }

@@ -211,59 +211,66 @@ struct TileOperandT {
   }
 };
 
+// LDS of a tile whose B has 64 kTok rows (each wave takes 16 kTok of them).
+template <int kTok>
+constexpr int kStageBytes = kSlabBytes + 64 * kTok * kRowBytes;
+
 // acc = the product over the slabs [slab0, slab0 + nslab) (nslab >= 1) of the
-// operands' rows.  smem: kTileLds bytes, free for other use on return (every
+// operands' rows.  smem: two stages, free for other use on return (every
 // load has landed and every wave has passed the last barrier).
-template <typename OperandB>
+template <int kTok, typename OperandB>
 __device__ __forceinline__ void tile_product(char* smem, const TileOperand& A,
                                              const OperandB& B, int slab0, int nslab, int wave,
-                                             int lane, f32x4 (&acc)[kVS][kTS]) {
+                                             int lane, f32x4 (&acc)[kVS][kTok]) {
+  constexpr int kStage = kStageBytes<kTok>;
   const int wv = wave >> 2;  // half of A's rows
   const int wt = wave & 3;   // quarter of B's rows
 #pragma unroll
   for (int a = 0; a < kVS; ++a)
 #pragma unroll
-    for (int b = 0; b < kTS; ++b)
+    for (int b = 0; b < kTok; ++b)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[a][b][i] = 0.0f;
 
   // slab `slab` into LDS stage `stage` (A rows at the stage base, B rows after);
   // all A rows, then all B rows (about 0.6% faster than alternating)
   auto issue = [&](int slab, int stage) __attribute__((always_inline)) {
-    char* base = smem + stage * 2 * kSlabBytes;
+    char* base = smem + stage * kStage;
     A.issue(base, wave, slab0 + slab);
     B.issue(base + kSlabBytes, wave, slab0 + slab);
   };
-  auto fetch = [&](const char* As, int ks, bf16x8 (&af)[kVS], bf16x8 (&bf)[kTS])
+  auto fetch = [&](const char* As, int ks, bf16x8 (&af)[kVS], bf16x8 (&bf)[kTok])
       __attribute__((always_inline)) {
     const char* Bs = As + kSlabBytes;
 #pragma unroll
     for (int vs = 0; vs < kVS; ++vs)
       af[vs] = TileOperand::fragment(As, wv * 128 + vs * 16, ks, lane);
 #pragma unroll
-    for (int ts = 0; ts < kTS; ++ts) bf[ts] = OperandB::fragment(Bs, wt * 64 + ts * 16, ks, lane);
+    for (int ts = 0; ts < kTok; ++ts)
+      bf[ts] = OperandB::fragment(Bs, wt * (16 * kTok) + ts * 16, ks, lane);
   };
-  auto mma = [&](const bf16x8 (&af)[kVS], const bf16x8 (&bf)[kTS]) __attribute__((always_inline)) {
+  auto mma = [&](const bf16x8 (&af)[kVS], const bf16x8 (&bf)[kTok]) __attribute__((always_inline)) {
 #pragma unroll
     for (int vs = 0; vs < kVS; ++vs)
 #pragma unroll
-      for (int ts = 0; ts < kTS; ++ts)
+      for (int ts = 0; ts < kTok; ++ts)
         acc[vs][ts] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[vs], bf[ts], acc[vs][ts], 0, 0, 0);
   };
   // Instruction order inside a k-step: 4 MFMAs, then one LDS read (and, after the
   // barrier, one slab load) per 2 MFMAs -- per MFMA, where B's fragments take two
-  // reads -- then the remaining MFMAs.  The reads thus overlap the MFMAs that do
-  // not need them.
-  constexpr int kReads = kVS + OperandB::kReadsPerFragment * kTS, kMfmas = kVS * kTS, kLead = 4;
-  constexpr int kPer = OperandB::kReadsPerFragment == 1 ? 2 : 1;
+  // reads, and in narrower tiles -- then the remaining MFMAs.  The reads thus overlap
+  // the MFMAs that do not need them.
+  constexpr int kReads = kVS + OperandB::kReadsPerFragment * kTok, kMfmas = kVS * kTok, kLead = 4;
+  constexpr int kPer = OperandB::kReadsPerFragment == 1 && kTok == kTS ? 2 : 1;
+  constexpr int kSlabLoads = kLoads + kTok;
   static_assert(kLead + kPer * kReads <= kMfmas, "the reads fit inside the step");
-  static_assert(2 * kLoads <= kReads, "one load per read at most");
+  static_assert(kSlabLoads <= kReads, "one load per read at most");
   auto order_step = [&](bool with_loads) __attribute__((always_inline)) {
     __builtin_amdgcn_sched_group_barrier(0x008, kLead, 0);  // MFMA
 #pragma unroll
     for (int i = 0; i < kReads; ++i) {
       __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
-      if (with_loads && i < 2 * kLoads) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // VMEM
+      if (with_loads && i < kSlabLoads) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // VMEM
       __builtin_amdgcn_sched_group_barrier(0x008, kPer, 0);
     }
     __builtin_amdgcn_sched_group_barrier(0x008, kMfmas - kLead - kPer * kReads, 0);
@@ -273,11 +280,11 @@ __device__ __forceinline__ void tile_product(char* smem, const TileOperand& A,
   if (nslab > 1) issue(1, 1);
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
-  bf16x8 a0[kVS], b0[kTS], a1[kVS], b1[kTS];
+  bf16x8 a0[kVS], b0[kTok], a1[kVS], b1[kTok];
   fetch(smem, 0, a0, b0);
   for (int s = 0; s < nslab; ++s) {
-    const char* cur = smem + (s & 1) * 2 * kSlabBytes;
-    const char* nxt = smem + ((s + 1) & 1) * 2 * kSlabBytes;
+    const char* cur = smem + (s & 1) * kStage;
+    const char* nxt = smem + ((s + 1) & 1) * kStage;
     // the fragments of this k-step were read during the previous one; wait for
     // them before more reads go out (the LDS counter holds at most 15)
     __builtin_amdgcn_s_waitcnt(kWaitLds);
