@@ -380,6 +380,38 @@ def test_other_stream_and_graph_replays(n):
         torch.cuda.synchronize()
 
 
+def test_calls_on_several_streams_at_once():
+    """Gradients and 8-bit statistics of three batches, each on a stream of its own, in turn
+    and without waiting: the bits of the calls made alone."""
+    kw = dict(real_vocab=12003)
+    runs = []
+    for n in (30, 100, 500):
+        case = C.make_case(n, 512, 12003, 12003, n, DEV)
+        pair = rlk.quantize_fp8(case.w, 128)
+        _, lse = rlk.fused_lmhead(case.h, case.w, case.tgt, case.mask, num_vocab_tiles=40, **kw)
+
+        def call(stream=None, case=case, pair=pair, lse=lse):
+            return (*rlk.fused_lmhead_backward(case.h, case.w, case.tgt, case.mask, lse, case.g,
+                                               case.gl, stream=stream, **kw),
+                    *rlk.fused_lmhead_fp8(case.h, *pair, case.tgt, case.mask, stream=stream,
+                                          num_vocab_tiles=40, **kw))
+        runs.append((call, call(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = [(call(stream), ref) for _ in range(10) for call, ref, stream in runs]
+    torch.cuda.synchronize()
+    for i, (out, ref) in enumerate(got):
+        assert all(torch.equal(bits(a), bits(b)) for a, b in zip(out, ref)), i
+
+
+def test_no_token_through_autograd():
+    case = C.make_case(5, 64, 300, 300, 8, DEV)
+    h, w = case.h[:0].clone().requires_grad_(True), case.w.clone().requires_grad_(True)
+    logp, lse = rlk.lmhead_selected_token_logprob(h, w, case.tgt[:0], None, real_vocab=300,
+                                                  num_vocab_tiles=1)
+    (logp.sum() + lse.sum()).backward()
+    assert h.grad.shape == (0, 64) and (bits(w.grad) == 0).all()
+
+
 @pytest.mark.parametrize("n", [30, 300])
 def test_captured_training_step(n):
     """Forward, loss and autograd's backward captured as one graph (no eager graph of the same
