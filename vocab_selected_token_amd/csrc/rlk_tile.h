@@ -90,17 +90,6 @@ __device__ __forceinline__ int64_t xcd_local_block(int64_t b, int64_t nb) {
   return x * per + (x < rem ? x : rem) + l;
 }
 
-// A barrier behind all of each wave's loads but the last kLater: the first slab is
-// multiplied while the second arrives (forward of 1024 tokens x 2048 x 151936: 574 us
-// for 588, of 4096 x 4096: 3914 for 3957).  In assembly, since the compiler's own barrier
-// waits for every load into LDS.
-template <int kLater>
-__device__ __forceinline__ void barrier_after_loads() {
-#if defined(__HIP_DEVICE_COMPILE__)
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLater) : "memory");
-#endif
-}
-
 // One operand's slab loads.  Wave w moves rows [32w, 32w + 32), 8 rows per
 // instruction; lane i of instruction j fetches row 32w + 8j + i/8 at the chunk
 // that belongs at LDS position i%8.  The resource starts at `first` and covers
@@ -288,12 +277,9 @@ __device__ __forceinline__ void tile_product(char* smem, const TileOperand& A,
   };
 
   issue(0, 0);
-  if (nslab > 1) {
-    issue(1, 1);
-    barrier_after_loads<kSlabLoads>();  // slab 1 is waited for before slab 0's last k-step
-  } else {
-    barrier_after_loads<0>();
-  }
+  if (nslab > 1) issue(1, 1);
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
   bf16x8 a0[kVS], b0[kTok], a1[kVS], b1[kTok];
   fetch(smem, 0, a0, b0);
   for (int s = 0; s < nslab; ++s) {
