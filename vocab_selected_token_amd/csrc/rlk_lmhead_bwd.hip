@@ -26,7 +26,7 @@
 //
 // What it costs: three products of the live rows, one of them the forward's again; the
 // alternative, logits kept from the forward, is what the caller comes here to avoid.
-// 4096 tokens (3405 live) x 4096 x 151936 take 10.05 ms, 1.27 PFLOP/s in the products; a
+// 4096 tokens (3405 live) x 4096 x 151936 take 10.1 ms, 1.26 PFLOP/s in the products; a
 // library's bf16 product of that size runs at 1.43.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -184,9 +184,9 @@ __global__ __launch_bounds__(kScanThreads) void live_rows_scan(RowArgs a, char* 
 // How dh's blocks share its sums.  The grid is made for tiles of all tokens; where
 // some have no live row, their blocks take a part of the others' sums: `splits` parts
 // to each of `tiles` tiles of live rows, padded to `rows` (777 tokens, 660 of them live,
-// x 1088 x 50021: backward 237 -> 205 us; the blocks that are left over end at once, and
+// x 1088 x 50021: grad_piece 108 -> 89 us; the blocks that are left over end at once, and
 // the others are numbered without them, so that every XCD gets its share: 4096 x 4096 x
-// 151936, 3405 live, 10305 -> 10035 us).
+// 151936, 3405 live, backward 10.40 -> 10.14 ms).
 struct DhParts {
   int32_t tiles, splits, rows;
   __device__ __forceinline__ DhParts(int32_t count, const LmheadBwdLayout& l)
@@ -310,8 +310,8 @@ __device__ __forceinline__ void put_row(uint16_t* out, const u32x4& x) {
 // dz_piece: dz of the columns [c0, c0 + piece) for the live rows, in bf16
 // (dz[i][c], ld = piece).  The exponentials and the stores of a tile follow its
 // product and nothing hides them, so a wave without target and padding tests no
-// column (777 tokens x 1088 x 50021: backward 249 -> 225 us; 1024 x 2048 x 151936:
-// 1744 -> 1718 us).
+// column (this kernel for 1024 x 64 x 65536: 69 -> 45 us; 777 x 1088 x 50021: 111 -> 101;
+// 1024 x 2048 x 151936: 629 -> 577).
 // ---------------------------------------------------------------------------
 template <int kTok>
 __global__ __launch_bounds__(kThreads) void dz_piece(
