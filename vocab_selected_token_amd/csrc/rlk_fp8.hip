@@ -7,7 +7,7 @@
 // states (a token, 128 columns of the hidden dimension), 128 x 128 for the weight.
 // Both blocks are 128 wide along the dimension that the product sums over, so
 //   z[t][v] = sum_b s_h[t][b] s_w[v / 128][b] sum_{k in block b} q_h[t][k] q_w[v][k]
-// and one v_mfma_f32_16x16x128_f8f6f4 per 16 x 16 outputs covers a block: its fp32
+// and four v_mfma_f32_16x16x32_bf16 per 16 x 16 outputs cover a block: its fp32
 // result, times the two scales, is added to the fp32 accumulator in ascending b.
 // The sums do not depend on the tile, so a token's outputs have the same bits
 // whatever the batch, whichever of the two kernels computes them:
@@ -16,18 +16,20 @@
 //               here 128 columns).
 //   fp8_stream  for up to 64 tokens, where the weight's bytes bound the time
 //               (rlk_stream.h).
-// Precision: the matrix cores add 8-bit products in groups of 8 columns and cut each
-// towards zero 13 bits below the group's largest exponent (found with single products;
-// the tests pin it); the groups' sums are added like fp32.  A product loses bits only
-// beside one 2^7 times as large, less than 2^-13 of that one; the sum of a random block
-// of 128 is off by 5.4e-5 of the largest product, root mean square.  Nothing is summed
-// in them beyond a block: its result is scaled and added in fp32.  logp ends up 1.8e-6
-// (relative) from 64 bits, where fp32 products give 4e-7; the operands' own rounding
-// to e4m3 is 2^-4 at most.  The same products through bf16 MFMAs (e4m3 fits in bf16)
-// would lose nothing and take twice the time.
+// Precision: the values stay in 8 bits in memory, in LDS and on their way, and become
+// bf16, which holds every e4m3 value, in the registers in front of the matrix cores.
+// Their products are then exact and all sums fp32: z is 1.4e-7 from 64 bits (root mean
+// square, logits of 1.3, hidden_dim 4096).  The 8-bit MFMA (v_mfma_f32_16x16x128_f8f6f4)
+// would save the conversions and half of the matrix cores' time, but adds products in groups
+// of 8 columns and cuts each towards zero 13 bits below the group's largest exponent: z
+// was 1.9e-5 off with it, at any hidden_dim, which is 1e-5 and more of the logp of a token
+// that the model is sure of.  4096 tokens x 4096 x 151936 took 2.3 ms that way and take
+// 4.0 ms now; 1 token 127 us and 123.
 //
-// Lane l of an MFMA supplies row l%16 and the 16-byte chunks l/16 and l/16 + 4 of
-// the 128 columns, for both operands alike; the result's layout is that of the
+// Operand layout of a block: lane l supplies row/column l%16, and of the 128 bytes of
+// its row the 16-byte chunks l/16 (the first 8 columns for step 0, the others for step 1)
+// and l/16 + 4 (steps 2 and 3).  The matrix cores see the 128 columns in another order
+// than they lie in, but in the same for both operands; the result's layout is that of the
 // bf16 16 x 16 tiles (4 vocabulary rows of one token per lane).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -41,7 +43,7 @@
 namespace rlk {
 namespace {
 
-typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
+typedef int32_t i32x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kE4m3Max = 448.0f;
 constexpr float kSmallestScale = 0x1p-126f;  // the smallest normal number
@@ -183,14 +185,27 @@ __global__ __launch_bounds__(256) void quantize_blocks(
 // ---------------------------------------------------------------------------
 // The product.
 // ---------------------------------------------------------------------------
-[[maybe_unused]] __device__ __forceinline__ f32x4 mfma_block(const i32x8& a, const i32x8& b) {
-  // both operands e4m3; the MX scales are not used (1)
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0,
-                                                          0, 0, 0, 0, 0);
+// 8 e4m3 values as bf16, which holds each of them exactly (NaN stays NaN).
+[[maybe_unused]] __device__ __forceinline__ bf16x8 widen(int32_t lo, int32_t hi) {
+#if defined(__HIP_DEVICE_COMPILE__)  // the host pass has no such builtins
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  union {
+    bf16x2 pair[4];
+    bf16x8 whole;
+  } w;
+  w.pair[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+  w.pair[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+  w.pair[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+  w.pair[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+  return w.whole;
+#else
+  return bf16x8{};
+#endif
 }
 
-[[maybe_unused]] __device__ __forceinline__ i32x8 join(const i32x4& lo, const i32x4& hi) {
-  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+[[maybe_unused]] __device__ __forceinline__ f32x4 mfma_step(const bf16x8& a, const bf16x8& b,
+                                                            const f32x4& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
 [[maybe_unused]] __device__ __forceinline__ void add_scaled(f32x4& acc, const f32x4& z, float f) {
@@ -275,14 +290,16 @@ struct Fp8Tile {
 
 // acc: z of the vocabulary rows [v0, +256) and tokens [t0, +64 kTok), in 2 x 4 waves
 // of 128 x 16 kTok.  Some row and token of the tile exist.
-// What bounds it: the MFMAs keep the matrix cores busy for half of the cycles (4096 x
-// 4096 x 151936: 2.25-2.35 ms, 2.2 PFLOP/s; the chip runs at 1.86 GHz under it); without
-// the four fmas by which each lane scales an MFMA's result it takes 2.09 ms, without
-// them and the loads into LDS 1.67-1.70.  A library's product of the same shape with
-// one scale in all takes 1.95 ms.  Registers decide the shape: 128 accumulators leave
-// room for half a slab of fragments, and a version that held a whole one spilled and
-// took 14.7 ms; addresses are one offset and immediates, scales come from LDS and
-// the scalar cache, and the body has no branch, for the same reason.
+// A wave takes a slab in eight 16-row tiles of A, a tile in four steps of 32 columns, a
+// step in kTok MFMAs.  Beside these it widens the next step of A (4 conversions) and adds
+// the previous tile's block sums, scaled, to the accumulators; B is widened once a slab, step
+// by step as the last tile has done with it.
+// What bounds it: 128 MFMAs a slab and wave (kTok = 4) take 2048 cycles of a SIMD, their issue
+// with 192 conversions and 128 fmas 1792, with two waves on it: 4096 x 4096 x 151936 in 4.0
+// ms, 1.27 PFLOP/s, where a library's bf16 product reaches 1.43.  Registers decide the
+// shape: 128 accumulators, 64 of B and 16 sums leave no room to hold A's raw chunks a tile
+// ahead (255 of 256 are in use, none spilled); addresses are one offset and immediates,
+// scales come from LDS and the scalar cache, and the body has no branch, for the same reason.
 template <int kTok>
 __device__ __forceinline__ void fp8_product(char* smem, const Fp8Operands& p,
                                             const SegmentArgs& a, int32_t v0, int32_t t0,
@@ -326,113 +343,102 @@ __device__ __forceinline__ void fp8_product(char* smem, const Fp8Operands& p,
   // (the second's position differs in one bit) plus an immediate.
   const int fr = lane & 15, fc = lane >> 4;
   const int lo0 = swizzled(fr, fc) * 16, lo1 = lo0 ^ 64;
-  auto frag = [&](const char* first, int tile) __attribute__((always_inline)) {
-    return join(*reinterpret_cast<const i32x4*>(first + lo0 + tile * 16 * kRowBytes),
-                *reinterpret_cast<const i32x4*>(first + lo1 + tile * 16 * kRowBytes));
+  // chunk `c` (columns for the steps 2c and 2c + 1) of A's 16-row tile `at`
+  auto read_a = [&](const char* stage, int at, int c) __attribute__((always_inline)) {
+    return *reinterpret_cast<const i32x4*>(stage + wv * 128 * kRowBytes + (c ? lo1 : lo0) +
+                                           at * 16 * kRowBytes);
   };
-
-  // A slab's 8 kTok MFMAs go in four quarters of two 16-row tiles of A.  A quarter
-  // reads the next quarter's A fragments while its MFMAs run (two buffers of
-  // two fragments), and the last quarter, which follows the slab's barrier,
-  // also replaces B fragment by fragment as soon as its last MFMA has it: the
-  // whole slab of fragments would not fit beside 128 accumulators.  Each
-  // MFMA's result is scaled and added while the next one runs.
-  i32x8 a0[2], a1[2], b[kTok];
-  float f[kTok];
-  f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};  // the MFMA result not yet added
-  auto read_a = [&](const char* stage, int q, i32x8 (&a)[2]) __attribute__((always_inline)) {
-    a[0] = frag(stage + wv * 128 * kRowBytes, 2 * q);
-    a[1] = frag(stage + wv * 128 * kRowBytes, 2 * q + 1);
-  };
-  auto read_b = [&](const char* stage, int ts) __attribute__((always_inline)) {
-    b[ts] = frag(stage + kSlabBytes + wt * (16 * kTok) * kRowBytes, ts);
+  // step ks of B's tile `ts`
+  auto read_b = [&](const char* stage, int ts, int ks) __attribute__((always_inline)) {
+    return *reinterpret_cast<const i32x2*>(stage + kSlabBytes + wt * (16 * kTok) * kRowBytes +
+                                           (ks < 2 ? lo0 : lo1) + ts * 16 * kRowBytes +
+                                           (ks & 1) * 8);
   };
   auto scale_of = [&](int s, int ts) __attribute__((always_inline)) {
     const char* at = smem + 2 * T::kStage + (s & 1) * T::kScaleBytes;
     return reinterpret_cast<const float*>(at)[wave * 64 + ts * 16 + fr];
   };
-  // MFMA (q, j) of a slab is tile vs = 2q + j%2, ts = j/2
-  auto step = [&](int q, int j, const i32x8 (&a)[2], float fz) __attribute__((always_inline)) {
-    const f32x4 n = mfma_block(a[j & 1], b[j >> 1]);
-    const int pq = j ? q : q - 1, pj = j ? j - 1 : 2 * kTok - 1;  // the previous one's place
-    add_scaled(acc[2 * (pq < 0 ? 3 : pq) + (pj & 1)][pj >> 1], z, fz);
-    z = n;
-  };
-  auto order = [&](int reads) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < 2 * kTok; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                  // MFMA
-      if (i < reads) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
-      __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);                  // VALU
-    }
-  };
 
+  i32x4 ra[2];         // A's chunks as they are read, the next steps' still to be widened
+  i32x2 rb[kTok];      // a step of B's
+  bf16x8 fa, b[kTok][4];
+  f32x4 z[kTok];       // the tile's block sums
+  float f[kTok], g[kTok];
   issue(0, 0);
   if (nslab > 1) issue(1, 1);
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
-  read_a(smem, 0, a0);
+  ra[0] = read_a(smem, 0, 0);
+  ra[1] = read_a(smem, 0, 1);
+  fa = widen(ra[0][0], ra[0][1]);
 #pragma unroll
-  for (int ts = 0; ts < kTok; ++ts) read_b(smem, ts);
-  float fp = 0.0f;  // the factor of z
+  for (int ts = 0; ts < kTok; ++ts) {
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      rb[ts] = read_b(smem, ts, ks);
+      if (ks < 3) b[ts][ks] = widen(rb[ts][0], rb[ts][1]);
+    }
+    z[ts] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    f[ts] = 0.0f;
+  }
   float sw = scalar_load(wsp);
-  float g[kTok];  // the next slab's token scales
-#pragma unroll
-  for (int ts = 0; ts < kTok; ++ts) g[ts] = scale_of(0, ts);
   for (int s = 0; s < nslab; ++s) {
     const char* cur = smem + (s & 1) * T::kStage;
     const char* nxt = smem + ((s + 1) & 1) * T::kStage;
-    __builtin_amdgcn_s_waitcnt(kWaitLds);
 #pragma unroll
-    for (int ts = 0; ts < kTok; ++ts) f[ts] = g[ts] * sw;
-    sw = scalar_load(wsp + min(s + 1, nslab - 1) * p.ws_col);
-    read_a(cur, 1, a1);
+    for (int at = 0; at < kVS; ++at) {
+      const char* from = at < kVS - 1 ? cur : nxt;  // A's next tile
+      const int to = (at + 1) % kVS;
+      if (at == kVS - 1) {
+        // every wave has read slab s into registers, and slab s+1 has landed
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);
+        // the last two steps reload the last slab and read fragments that nothing
+        // uses: unconditional, and in bounds
+        issue(min(s + 2, nslab - 1), s & 1);
+      }
 #pragma unroll
-    for (int j = 0; j < 2 * kTok; ++j) step(0, j, a0, j ? f[(j - 1) >> 1] : fp);
-    order(4);
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(kWaitLds);
-    read_a(cur, 2, a0);
+      for (int ks = 0; ks < 4; ++ks) {
+        // the next step's fragment of A
+        const bf16x8 an = ks == 0   ? widen(ra[0][2], ra[0][3])
+                          : ks == 1 ? widen(ra[1][0], ra[1][1])
+                          : ks == 2 ? widen(ra[1][2], ra[1][3])
+                                    : widen(ra[0][0], ra[0][1]);
+        if (ks == 1) ra[0] = read_a(from, to, 0);
+        if (ks == 3) ra[1] = read_a(from, to, 1);
+        // B's steps are replaced one by one once the last tile has them
+        if (at == 0 && ks == 0)
 #pragma unroll
-    for (int j = 0; j < 2 * kTok; ++j) step(1, j, a1, j ? f[(j - 1) >> 1] : f[kTok - 1]);
-    order(4);
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(kWaitLds);
-    read_a(cur, 3, a1);
+          for (int ts = 0; ts < kTok; ++ts) {
+            b[ts][3] = widen(rb[ts][0], rb[ts][1]);
+            g[ts] = scale_of(s, ts);
+          }
+        if (at == kVS - 1) {
+          if (ks > 0)
 #pragma unroll
-    for (int j = 0; j < 2 * kTok; ++j) step(2, j, a0, j ? f[(j - 1) >> 1] : f[kTok - 1]);
-    order(4);
-    __builtin_amdgcn_sched_barrier(0);
-    // every wave has read slab s into registers, and slab s+1 has landed
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    __builtin_amdgcn_sched_barrier(0);
-    // the last two steps reload the last slab and read fragments that nothing
-    // uses: unconditional, and in bounds
-    issue(min(s + 2, nslab - 1), s & 1);
+            for (int ts = 0; ts < kTok; ++ts) b[ts][ks - 1] = widen(rb[ts][0], rb[ts][1]);
 #pragma unroll
-    for (int ts = 0; ts < kTok; ++ts) g[ts] = scale_of(s + 1, ts);
-    read_a(nxt, 0, a0);
+          for (int ts = 0; ts < kTok; ++ts) rb[ts] = read_b(nxt, ts, ks);
+        }
 #pragma unroll
-    for (int j = 0; j < 2 * kTok; ++j) {
-      step(3, j, a1, j ? f[(j - 1) >> 1] : f[kTok - 1]);
-      if (j & 1) read_b(nxt, j >> 1);
+        for (int ts = 0; ts < kTok; ++ts) {
+          if (ks == 0) add_scaled(acc[(at + kVS - 1) % kVS][ts], z[ts], f[ts]);
+          z[ts] = mfma_step(fa, b[ts][ks], ks ? z[ts] : f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+        }
+        fa = an;
+        if (at == 0 && ks == 2) {
+#pragma unroll
+          for (int ts = 0; ts < kTok; ++ts) f[ts] = g[ts] * sw;
+          sw = scalar_load(wsp + min(s + 1, nslab - 1) * p.ws_col);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
-#pragma unroll
-    for (int j = 0; j < kTok; ++j) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // MFMA
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
-      __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // VMEM
-      __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);  // VALU
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-      __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
-    }
-    fp = f[kTok - 1];
-    __builtin_amdgcn_sched_barrier(0);
   }
-  add_scaled(acc[7][kTok - 1], z, fp);
+#pragma unroll
+  for (int ts = 0; ts < kTok; ++ts) add_scaled(acc[kVS - 1][ts], z[ts], f[ts]);
   // the reloads of the last two steps land before the stages are used again
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
@@ -440,9 +446,7 @@ __device__ __forceinline__ void fp8_product(char* smem, const Fp8Operands& p,
 }
 
 // A tile's fixed part -- first loads, exponentials or stores, drain -- takes 8 us
-// (statistics) or 10 (logits) beside 1.7-2 us a slab: a third of the time at hidden_dim
-// 1024.  Blocks that stay and load their next tile's first slabs before that part were
-// no faster (1024 tokens x 2048 x 151936: 353 us for 342, at 252 registers for 231).
+// (statistics) or 10 (logits) beside 3 us a slab.
 template <bool kLogits, int kTok>
 __global__ __launch_bounds__(kThreads) void fp8_tile(Fp8Operands p, SegmentArgs a, LogitsOut lo,
                                                      int32_t n_tb, int32_t vb_begin,
@@ -512,14 +516,20 @@ struct Fp8Stream {
   __device__ __forceinline__ void multiply(f32x4& acc, const i32x4& a0, const i32x4& a1,
                                            const i32x4& b0, const i32x4& b1, int at,
                                            int place) const {
-    add_scaled(acc, mfma_block(join(a0, a1), join(b0, b1)), lds[at][place] * sw);
+    f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+    z = mfma_step(widen(a0[0], a0[1]), widen(b0[0], b0[1]), z);
+    z = mfma_step(widen(a0[2], a0[3]), widen(b0[2], b0[3]), z);
+    z = mfma_step(widen(a1[0], a1[1]), widen(b1[0], b1[1]), z);
+    z = mfma_step(widen(a1[2], a1[3]), widen(b1[2], b1[3]), z);
+    add_scaled(acc, z, lds[at][place] * sw);
   }
 };
 
 // Few tokens (16 kTok at most).  No block waits for another: the statistics, whose
 // order spans 128 rows, are taken from z by segments_of_z.  The weight's bytes bound it:
-// 1 token x 4096 x 151936 in 111-115 us, 5.4-5.6 TB/s;
-// reading alone, row pieces in this order, reaches 6.1.
+// 1 token x 4096 x 151936 in 111-115 us, 5.4-5.6 TB/s; reading alone, row pieces in this
+// order, reaches 6.1.  From 32 tokens on every wave's conversions of the hidden states weigh
+// as well (64 tokens: 172 us).
 template <bool kLogits, int kTok>
 __global__ __launch_bounds__(kStreamThreads) void fp8_stream(Fp8Operands p, SegmentArgs a,
                                                              LogitsOut lo, ZOut zo,
@@ -606,15 +616,16 @@ hipError_t launch_tile(const Fp8Operands& p, const SegmentArgs& sa, const Logits
   });
 }
 
-// Time of a round of tiles of 128, 192 and 256 tokens (hidden_dim 4096: 39, 50 and 67
-// us), see tile_tokens: 333 tokens x 50021 columns take 66 us in tiles of 256, 56 in
-// tiles of 192 and 63 in tiles of 128; 65 tokens x 151936 columns 226, 193 and 165;
-// 4096 tokens 2480, 2577 and 2883.
-constexpr double kTileUnits[] = {2.3, 3.0, 4.0};
+// Time of a round of tiles of 128, 192 and 256 tokens, see tile_tokens: 68, 87 and 107 us
+// at hidden_dim 4096, 37, 47 and 58 at 2048, 23, 29 and 35 at 1024, 15, 19 and 23 at 512 (logits
+// of 65536 columns): near the same ratios throughout.  333 tokens x 2176 x 50021 take 118 us
+// in tiles of 256, 97 in tiles of 192 and 111 in tiles of 128; 65 tokens x 4096 x 151936 317, 260
+// and 211; 4096 tokens 4.02, 4.38 and 4.77 ms.
+constexpr double kTileUnits[] = {2.55, 3.2, 4.0};
 
 // The product over the columns [256 vb_begin, +256 n_vbs).  Up to 64 tokens the
 // weight's bytes bound the time and the stream kernel's registers hold all
-// tokens (64 tokens x 151936 columns at hidden_dim 4096: 154 us against 165 us for a
+// tokens (64 tokens x 151936 columns at hidden_dim 4096: 187 us against 211 us for a
 // tile); above, the tile shares each weight slab among its tokens.
 template <bool kLogits>
 hipError_t launch_product(const Fp8Operands& p, const SegmentArgs& sa, const LogitsOut& lo,
