@@ -398,6 +398,48 @@ def _u8_mask(mask):
     return mask.view(torch.uint8) if mask.dtype == torch.bool else mask
 
 
+# A convenience given a `stream` other than the current one launches there, and takes the
+# memory of its results and workspace there too: the allocator hands a freed block out
+# again to the stream it was taken on, whose own work is through with it by then, and to no
+# other.  (Taken on the current stream, a block could still be in use by work queued there
+# that `stream` does not wait for.)  The inputs are the caller's to order: ready on `stream`
+# when the call is made, and kept until it is done.
+def _torch_stream(stream, device):
+    """`stream` as torch knows it; anything with a cuda_stream handle will do."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+
+
+def _call_on(t: torch.Tensor, stream):
+    """The context in which memory for a call on t's GPU and `stream` is taken and the call
+    is made (none where both are the current ones)."""
+    if stream is not None:
+        return torch.cuda.stream(_torch_stream(stream, t.device))
+    if t.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(t.device)
+
+
+def _handed_over(t: torch.Tensor, stream, *results):
+    """Records what a call on `stream` returns (Nones apart) on the current stream, where it is
+    read: freed, it goes back to the pool of `stream` once the work queued here is through."""
+    if stream is None:
+        return
+    current = torch.cuda.current_stream(t.device)
+    if current.cuda_stream != stream.cuda_stream:
+        for r in results:
+            if r is not None:
+                r.record_stream(current)
+
+
+def _bytes_for(nbytes: int, device) -> torch.Tensor:
+    """A workspace of nbytes (0: the descriptor was refused)."""
+    if nbytes == 0:
+        raise ValueError(f"invalid rlk_logp_desc: {rlk_last_error_detail()}")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def workspace_for(desc: rlk_logp_desc, device) -> torch.Tensor:
     """A fresh workspace of rlk_logp_workspace_bytes(desc) bytes for rlk_logp_fwd
     (its contents on entry do not matter)."""
@@ -659,38 +701,15 @@ def fused_lmhead(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tens
 
 def _run_lmhead(desc, hidden, weight, targets, active_mask, workspace=None, stream=None):
     n, k = hidden.shape
-    logp = torch.empty(n, dtype=torch.float32, device=hidden.device)
-    lse = torch.empty(n, dtype=torch.float32, device=hidden.device)
-    if workspace is None:
-        nbytes = rlk_logp_fused_lmhead_workspace_bytes(desc)
-        if nbytes == 0:
-            raise ValueError(f"invalid rlk_logp_desc: {rlk_last_error_detail()}")
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=hidden.device)
-    rlk_logp_fused_lmhead(desc, hidden, weight, k, targets, _u8_mask(active_mask), logp, lse,
-                          workspace, stream)
+    with _call_on(hidden, stream):
+        logp = torch.empty(n, dtype=torch.float32, device=hidden.device)
+        lse = torch.empty(n, dtype=torch.float32, device=hidden.device)
+        if workspace is None:
+            workspace = _bytes_for(rlk_logp_fused_lmhead_workspace_bytes(desc), hidden.device)
+        rlk_logp_fused_lmhead(desc, hidden, weight, k, targets, _u8_mask(active_mask), logp, lse,
+                              workspace, stream)
+    _handed_over(hidden, stream, logp, lse)
     return logp, lse
-
-
-def _device_of(t: torch.Tensor):
-    """The context in which a call on t's GPU is made (none where it is the current one)."""
-    if t.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(t.device)
-
-
-def _scratch(nbytes: int, device, stream) -> torch.Tensor:
-    """A workspace of nbytes (0: the descriptor was refused) for a call on `stream`."""
-    if nbytes == 0:
-        raise ValueError(f"invalid rlk_logp_desc: {rlk_last_error_detail()}")
-    return _used_on(stream, torch.empty(nbytes, dtype=torch.uint8, device=device))
-
-
-def _used_on(stream, t):
-    """t (or None), whose memory the allocator is to hand out again only when `stream`, where
-    it is not the current one, is through with it."""
-    if stream is not None and t is not None:
-        t.record_stream(stream)
-    return t
 
 
 def fused_lmhead_backward(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
@@ -718,14 +737,15 @@ def fused_lmhead_backward(hidden: torch.Tensor, weight: torch.Tensor, targets: t
 def _run_lmhead_backward(desc, hidden, weight, targets, active_mask, lse, grad_logp, grad_lse,
                          want_hidden, want_weight, workspace=None, stream=None):
     k = hidden.shape[1]
-    with _device_of(hidden):
-        dh = _used_on(stream, torch.empty_like(hidden) if want_hidden else None)
-        dw = _used_on(stream, torch.empty_like(weight) if want_weight else None)
+    with _call_on(hidden, stream):
+        dh = torch.empty_like(hidden) if want_hidden else None
+        dw = torch.empty_like(weight) if want_weight else None
         if workspace is None:
-            workspace = _scratch(rlk_logp_fused_lmhead_bwd_workspace_bytes(
-                desc, k, want_hidden, want_weight), hidden.device, stream)
+            workspace = _bytes_for(rlk_logp_fused_lmhead_bwd_workspace_bytes(
+                desc, k, want_hidden, want_weight), hidden.device)
         rlk_logp_fused_lmhead_bwd(desc, hidden, weight, k, targets, _u8_mask(active_mask), lse,
                                   grad_logp, grad_lse, dh, dw, workspace, stream)
+    _handed_over(hidden, stream, dh, dw)
     return dh, dw
 
 
@@ -738,10 +758,9 @@ class _LmheadSelectedTokenLogprob(torch.autograd.Function):
                 num_vocab_tiles, ignore_index):
         n, rows = hidden.shape[0], weight.shape[0]
         v_pad = padded_vocab or rows
-        with _device_of(hidden):
-            logp, lse = _run_lmhead(make_desc(n, real_vocab, v_pad, v_pad, num_vocab_tiles, 1,
-                                              ignore_index),
-                                    hidden, weight, targets, active_mask)
+        logp, lse = _run_lmhead(make_desc(n, real_vocab, v_pad, v_pad, num_vocab_tiles, 1,
+                                          ignore_index),
+                                hidden, weight, targets, active_mask)
         ctx.save_for_backward(hidden, weight, targets, active_mask, lse)
         ctx.desc = make_desc(n, real_vocab, rows, rows, 1, 1, ignore_index)
         ctx.set_materialize_grads(False)
@@ -800,25 +819,19 @@ def quantize_fp8(x: torch.Tensor, block_rows: int = 1, *, stream=None):
     if k == 0 or k % FP8_BLOCK:
         raise ValueError(f"x must have a multiple of {FP8_BLOCK} columns, got {k}")
     _check_device(x)
-    with _device_of(x):
-        return _quantize(x, block_rows, stream)
-
-
-def _quantize(x, block_rows, stream):
-    """quantize_fp8 of a checked x."""
-    n, k = x.shape
     col_blocks = k // FP8_BLOCK
-    q = _used_on(stream, torch.empty((n, k), dtype=torch.float8_e4m3fn, device=x.device))
-    if block_rows == 1:
-        strides = 1, n or 1
-        scale = torch.empty_strided((n, col_blocks), strides, device=x.device)
-    else:
-        strides = col_blocks, 1
-        scale = torch.empty((-(-n // block_rows), col_blocks), device=x.device)
-    _used_on(stream, scale)
-    if n:
-        rlk_fp8_quantize(n, k, x, x.stride(0) if n > 1 else k, block_rows, q, scale, *strides,
-                         stream)
+    with _call_on(x, stream):
+        q = torch.empty((n, k), dtype=torch.float8_e4m3fn, device=x.device)
+        if block_rows == 1:
+            strides = 1, n or 1
+            scale = torch.empty_strided((n, col_blocks), strides, device=x.device)
+        else:
+            strides = col_blocks, 1
+            scale = torch.empty((-(-n // block_rows), col_blocks), device=x.device)
+        if n:
+            rlk_fp8_quantize(n, k, x, x.stride(0) if n > 1 else k, block_rows, q, scale, *strides,
+                             stream)
+    _handed_over(x, stream, q, scale)
     return q, scale
 
 
@@ -870,12 +883,11 @@ def _fp8_operand(hidden, nbytes, stream):
     """(rlk_fp8_matrix of the hidden states, a buffer of at least nbytes): bf16 ones are cast on
     `stream`, behind the nbytes of that buffer (one allocation costs less than three)."""
     if isinstance(hidden, (tuple, list)):
-        return make_fp8_matrix(*hidden), _scratch(nbytes, hidden[0].device, stream) if nbytes \
-            else None
+        return make_fp8_matrix(*hidden), _bytes_for(nbytes, hidden[0].device) if nbytes else None
     n, k = hidden.shape
     at = -(-nbytes // 256) * 256
     scales = at + -(-n * k // 256) * 256
-    buffer = _scratch(scales + n * k // FP8_BLOCK * 4 + 256, hidden.device, stream)
+    buffer = _bytes_for(scales + n * k // FP8_BLOCK * 4 + 256, hidden.device)
     base = buffer.data_ptr()
     if n:
         _check(_lib.rlk_fp8_quantize(n, k, hidden.data_ptr(), hidden.stride(0) if n > 1 else k,
@@ -891,14 +903,15 @@ def lmhead_logits_fp8(hidden, weight_q: torch.Tensor, weight_scale: torch.Tensor
     hidden: bf16 [N, K], cast to e4m3 with one scale per token and 128 columns, or the
     (q, scale) pair of quantize_fp8(x, 1).  weight_q, weight_scale: quantize_fp8(W, 128)."""
     x = _check_lmhead_fp8(hidden, weight_q, weight_scale, real_vocab)
-    with _device_of(x):
+    with _call_on(x, stream):
         matrix, buffer = _fp8_operand(hidden, 0, stream)
         n, k = x.shape
         v_pad = padded_vocab or weight_q.shape[0]
         ld = (v_pad + 7) // 8 * 8
-        logits = _used_on(stream, torch.empty((n, ld), dtype=torch.bfloat16, device=x.device))
+        logits = torch.empty((n, ld), dtype=torch.bfloat16, device=x.device)
         rlk_lmhead_logits_fp8(make_desc(n, real_vocab, v_pad, ld, 1), matrix,
                               make_fp8_matrix(weight_q, weight_scale), k, logits, stream)
+    _handed_over(x, stream, logits)
     return logits if ld == v_pad else logits[:, :v_pad]
 
 
@@ -916,16 +929,17 @@ def fused_lmhead_fp8(hidden, weight_q: torch.Tensor, weight_scale: torch.Tensor,
     v_pad = padded_vocab or weight_q.shape[0]
     desc = make_desc(n, real_vocab, v_pad, v_pad, num_vocab_tiles, num_virtual_shards,
                      ignore_index, validate)
-    with _device_of(x):
+    with _call_on(x, stream):
         nbytes = rlk_logp_fused_lmhead_fp8_workspace_bytes(desc)
         if nbytes == 0:
             raise ValueError(f"invalid rlk_logp_desc: {rlk_last_error_detail()}")
         matrix, buffer = _fp8_operand(hidden, nbytes if workspace is None else 0, stream)
         if workspace is None:
             workspace = buffer
-        logp = _used_on(stream, torch.empty(n, dtype=torch.float32, device=x.device))
-        lse = _used_on(stream, torch.empty(n, dtype=torch.float32, device=x.device))
+        logp = torch.empty(n, dtype=torch.float32, device=x.device)
+        lse = torch.empty(n, dtype=torch.float32, device=x.device)
         rlk_logp_fused_lmhead_fp8(desc, matrix,
                                   make_fp8_matrix(weight_q, weight_scale), x.shape[1], targets,
                                   _u8_mask(active_mask), logp, lse, workspace, stream)
+    _handed_over(x, stream, logp, lse)
     return logp, lse
