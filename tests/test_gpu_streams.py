@@ -78,3 +78,24 @@ def check(call, inputs):
 def test_lmhead_calls_beside_a_busy_stream(name, inputs):
     print(f"case {name}", flush=True)
     check(LMHEAD[name], inputs)
+
+
+LOGITS = {
+    "forward": lambda x, t, m, f, **kw: rlk.forward(x, t, m, real_vocab=V, **kw),
+    "backward": lambda x, t, m, f, **kw: rlk.backward(x, t, m, f, f, real_vocab=V, **kw),
+    "forward_ex": lambda x, t, m, f, **kw: rlk.forward_ex(x, t, m, real_vocab=V, **kw),
+    "backward_ex": lambda x, t, m, f, **kw: rlk.backward_ex(x, t, m, f, f, f, real_vocab=V, **kw),
+    "forward_backward": lambda x, t, m, f, **kw: rlk.forward_backward(x, t, m, f, real_vocab=V,
+                                                                      **kw),
+    "forward_backward_ex": lambda x, t, m, f, **kw: rlk.forward_backward_ex(
+        x, t, m, f, real_vocab=V, **kw),
+}
+
+
+@pytest.mark.parametrize("name", LOGITS)
+def test_logits_calls_beside_a_busy_stream(name, inputs):
+    print(f"case {name}", flush=True)
+    c, wq, ws, lse = inputs
+    x = rlk.lmhead_logits_fp8(c.h, wq, ws, real_vocab=V, padded_vocab=V + 4)
+    torch.cuda.synchronize()
+    check(LOGITS[name], (x, c.tgt, c.mask, lse))

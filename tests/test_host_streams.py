@@ -106,3 +106,22 @@ def check(call, seen):
 @pytest.mark.parametrize("name", LMHEAD)
 def test_lmhead_memory_comes_from_the_launch_stream(name, streams):
     check(LMHEAD[name], streams)
+
+
+LOGITS = {
+    "forward": lambda i, **kw: rlk.forward(i["x"], i["t"], real_vocab=V, **kw),
+    "backward": lambda i, **kw: rlk.backward(i["x"], i["t"], None, i["f"], i["f"], real_vocab=V,
+                                             **kw),
+    "forward_ex": lambda i, **kw: rlk.forward_ex(i["x"], i["t"], real_vocab=V, **kw),
+    "backward_ex": lambda i, **kw: rlk.backward_ex(i["x"], i["t"], None, i["f"], i["f"], i["f"],
+                                                   real_vocab=V, **kw),
+    "forward_backward": lambda i, **kw: rlk.forward_backward(i["x"], i["t"], None, i["f"],
+                                                             real_vocab=V, **kw),
+    "forward_backward_ex": lambda i, **kw: rlk.forward_backward_ex(i["x"], i["t"], None, i["f"],
+                                                                   real_vocab=V, **kw),
+}
+
+
+@pytest.mark.parametrize("name", LOGITS)
+def test_logits_memory_comes_from_the_launch_stream(name, streams):
+    check(LOGITS[name], streams)

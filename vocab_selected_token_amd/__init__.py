@@ -443,10 +443,7 @@ def _bytes_for(nbytes: int, device) -> torch.Tensor:
 def workspace_for(desc: rlk_logp_desc, device) -> torch.Tensor:
     """A fresh workspace of rlk_logp_workspace_bytes(desc) bytes for rlk_logp_fwd
     (its contents on entry do not matter)."""
-    n = rlk_logp_workspace_bytes(desc)
-    if n == 0:
-        raise ValueError(f"invalid rlk_logp_desc: {rlk_last_error_detail()}")
-    return torch.empty(n, dtype=torch.uint8, device=device)
+    return _bytes_for(rlk_logp_workspace_bytes(desc), device)
 
 
 def forward(logits: torch.Tensor, targets: torch.Tensor, active_mask=None, *, real_vocab: int,
@@ -459,11 +456,13 @@ def forward(logits: torch.Tensor, targets: torch.Tensor, active_mask=None, *, re
     n = logits.shape[0]
     desc = make_desc(n, real_vocab, padded_vocab or logits.shape[1], logits.stride(0),
                      num_vocab_tiles, num_virtual_shards, ignore_index, validate)
-    logp = torch.empty(n, dtype=torch.float32, device=logits.device)
-    lse = torch.empty(n, dtype=torch.float32, device=logits.device)
-    if workspace is None:
-        workspace = workspace_for(desc, logits.device)
-    rlk_logp_fwd(desc, logits, targets, _u8_mask(active_mask), logp, lse, workspace, stream)
+    with _call_on(logits, stream):
+        logp = torch.empty(n, dtype=torch.float32, device=logits.device)
+        lse = torch.empty(n, dtype=torch.float32, device=logits.device)
+        if workspace is None:
+            workspace = workspace_for(desc, logits.device)
+        rlk_logp_fwd(desc, logits, targets, _u8_mask(active_mask), logp, lse, workspace, stream)
+    _handed_over(logits, stream, logp, lse)
     return logp, lse
 
 
@@ -482,12 +481,14 @@ def backward(logits: torch.Tensor, targets: torch.Tensor, active_mask, lse: torc
     tiles = num_vocab_tiles if num_vocab_tiles is not None else min(64, v_pad)
     desc = make_desc(n, real_vocab, v_pad, logits.stride(0), tiles, 1, ignore_index, validate)
     ld_d = (v_pad + 7) // 8 * 8
-    dl = torch.empty((n, ld_d), dtype=out_dtype, device=logits.device)
-    if workspace is None:
-        workspace = workspace_for(desc, logits.device)
     code = RLK_DTYPE_BF16 if out_dtype == torch.bfloat16 else RLK_DTYPE_F32
-    rlk_logp_bwd(desc, logits, targets, _u8_mask(active_mask), lse, grad_logp, dl, ld_d, code,
-                 workspace, stream)
+    with _call_on(logits, stream):
+        dl = torch.empty((n, ld_d), dtype=out_dtype, device=logits.device)
+        if workspace is None:
+            workspace = workspace_for(desc, logits.device)
+        rlk_logp_bwd(desc, logits, targets, _u8_mask(active_mask), lse, grad_logp, dl, ld_d,
+                     code, workspace, stream)
+    _handed_over(logits, stream, dl)
     return dl[:, :v_pad]
 
 
@@ -501,16 +502,15 @@ def forward_ex(logits: torch.Tensor, targets: torch.Tensor, active_mask=None, *,
     n = logits.shape[0]
     desc = make_desc(n, real_vocab, padded_vocab or logits.shape[1], logits.stride(0),
                      num_vocab_tiles, num_virtual_shards, ignore_index, validate)
-    logp = torch.empty(n, dtype=torch.float32, device=logits.device)
-    lse = torch.empty(n, dtype=torch.float32, device=logits.device)
-    ent = torch.empty(n, dtype=torch.float32, device=logits.device)
-    if workspace is None:
-        nbytes = rlk_logp_ex_workspace_bytes(desc)
-        if nbytes == 0:
-            raise ValueError(f"invalid rlk_logp_desc: {rlk_last_error_detail()}")
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=logits.device)
-    rlk_logp_fwd_ex(desc, logits, targets, _u8_mask(active_mask), logp, lse, ent, workspace,
-                    stream)
+    with _call_on(logits, stream):
+        logp = torch.empty(n, dtype=torch.float32, device=logits.device)
+        lse = torch.empty(n, dtype=torch.float32, device=logits.device)
+        ent = torch.empty(n, dtype=torch.float32, device=logits.device)
+        if workspace is None:
+            workspace = _bytes_for(rlk_logp_ex_workspace_bytes(desc), logits.device)
+        rlk_logp_fwd_ex(desc, logits, targets, _u8_mask(active_mask), logp, lse, ent, workspace,
+                        stream)
+    _handed_over(logits, stream, logp, lse, ent)
     return logp, lse, ent
 
 
@@ -531,12 +531,14 @@ def backward_ex(logits: torch.Tensor, targets: torch.Tensor, active_mask, lse: t
     tiles = num_vocab_tiles if num_vocab_tiles is not None else min(64, v_pad)
     desc = make_desc(n, real_vocab, v_pad, logits.stride(0), tiles, 1, ignore_index, validate)
     ld_d = (v_pad + 7) // 8 * 8
-    dl = torch.empty((n, ld_d), dtype=out_dtype, device=logits.device)
-    if workspace is None:
-        workspace = workspace_for(desc, logits.device)
     code = RLK_DTYPE_BF16 if out_dtype == torch.bfloat16 else RLK_DTYPE_F32
-    rlk_logp_bwd_ex(desc, logits, targets, _u8_mask(active_mask), lse, entropy, grad_logp,
-                    grad_lse, grad_ent, dl, ld_d, code, workspace, stream)
+    with _call_on(logits, stream):
+        dl = torch.empty((n, ld_d), dtype=out_dtype, device=logits.device)
+        if workspace is None:
+            workspace = workspace_for(desc, logits.device)
+        rlk_logp_bwd_ex(desc, logits, targets, _u8_mask(active_mask), lse, entropy, grad_logp,
+                        grad_lse, grad_ent, dl, ld_d, code, workspace, stream)
+    _handed_over(logits, stream, dl)
     return dl[:, :v_pad]
 
 
@@ -616,17 +618,16 @@ def forward_backward(logits: torch.Tensor, targets: torch.Tensor, active_mask,
     desc = make_desc(n, real_vocab, v_pad, logits.stride(0), num_vocab_tiles, num_virtual_shards,
                      ignore_index, validate)
     ld_d = (v_pad + 7) // 8 * 8
-    logp = torch.empty(n, dtype=torch.float32, device=logits.device)
-    lse = torch.empty(n, dtype=torch.float32, device=logits.device)
-    dl = torch.empty((n, ld_d), dtype=out_dtype, device=logits.device)
-    if workspace is None:
-        nbytes = rlk_logp_fwd_bwd_workspace_bytes(desc)
-        if nbytes == 0:
-            raise ValueError(f"invalid rlk_logp_desc: {rlk_last_error_detail()}")
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=logits.device)
     code = RLK_DTYPE_BF16 if out_dtype == torch.bfloat16 else RLK_DTYPE_F32
-    rlk_logp_fwd_bwd(desc, logits, targets, _u8_mask(active_mask), grad_logp, logp, lse, dl, ld_d,
-                     code, workspace, stream)
+    with _call_on(logits, stream):
+        logp = torch.empty(n, dtype=torch.float32, device=logits.device)
+        lse = torch.empty(n, dtype=torch.float32, device=logits.device)
+        dl = torch.empty((n, ld_d), dtype=out_dtype, device=logits.device)
+        if workspace is None:
+            workspace = _bytes_for(rlk_logp_fwd_bwd_workspace_bytes(desc), logits.device)
+        rlk_logp_fwd_bwd(desc, logits, targets, _u8_mask(active_mask), grad_logp, logp, lse, dl,
+                         ld_d, code, workspace, stream)
+    _handed_over(logits, stream, logp, lse, dl)
     return logp, lse, dl[:, :v_pad]
 
 
@@ -649,18 +650,17 @@ def forward_backward_ex(logits: torch.Tensor, targets: torch.Tensor, active_mask
     desc = make_desc(n, real_vocab, v_pad, logits.stride(0), num_vocab_tiles, num_virtual_shards,
                      ignore_index, validate)
     ld_d = (v_pad + 7) // 8 * 8
-    logp = torch.empty(n, dtype=torch.float32, device=logits.device)
-    lse = torch.empty(n, dtype=torch.float32, device=logits.device)
-    ent = torch.empty(n, dtype=torch.float32, device=logits.device)
-    dl = torch.empty((n, ld_d), dtype=out_dtype, device=logits.device)
-    if workspace is None:
-        nbytes = rlk_logp_fwd_bwd_ex_workspace_bytes(desc)
-        if nbytes == 0:
-            raise ValueError(f"invalid rlk_logp_desc: {rlk_last_error_detail()}")
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=logits.device)
     code = RLK_DTYPE_BF16 if out_dtype == torch.bfloat16 else RLK_DTYPE_F32
-    rlk_logp_fwd_bwd_ex(desc, logits, targets, _u8_mask(active_mask), grad_logp, grad_lse,
-                        grad_ent, logp, lse, ent, dl, ld_d, code, workspace, stream)
+    with _call_on(logits, stream):
+        logp = torch.empty(n, dtype=torch.float32, device=logits.device)
+        lse = torch.empty(n, dtype=torch.float32, device=logits.device)
+        ent = torch.empty(n, dtype=torch.float32, device=logits.device)
+        dl = torch.empty((n, ld_d), dtype=out_dtype, device=logits.device)
+        if workspace is None:
+            workspace = _bytes_for(rlk_logp_fwd_bwd_ex_workspace_bytes(desc), logits.device)
+        rlk_logp_fwd_bwd_ex(desc, logits, targets, _u8_mask(active_mask), grad_logp, grad_lse,
+                            grad_ent, logp, lse, ent, dl, ld_d, code, workspace, stream)
+    _handed_over(logits, stream, logp, lse, ent, dl)
     return logp, lse, ent, dl[:, :v_pad]
 
 
