@@ -89,8 +89,9 @@ struct ScanLds {
 // live rows in ascending order.  Returns their number; at(i, r) hears that live row i
 // is row r of the batch.  With `write`, they and the scale go to the workspace; slots
 // from the last live row up to a multiple of 256 hold rows that give dz = 0.  An
-// effective-active row with a target outside [0, V_real) is live with NaN factors:
-// its dz is NaN.
+// effective-active row with a target outside [0, V_real) is live with NaN factors,
+// and so is one whose LSE is not finite (exp(z - inf) would be a plausible 0): its dz is
+// NaN.
 template <int kThr, typename At>
 __device__ __forceinline__ int32_t scan_rows(const RowArgs& a, const LiveRows& live,
                                              ScanLds<kThr>& lds, bool write, At&& at_row) {
@@ -147,9 +148,11 @@ __device__ __forceinline__ int32_t scan_rows(const RowArgs& a, const LiveRows& l
       const float nan = __builtin_nanf("");
       live.idx[at] = r;
       live.tgt[at] = (act && !bad) ? tgt : -1;
-      live.lse[at] = a.lse[r];
-      live.cg[at] = bad ? nan : g / scale;
-      live.cc[at] = bad ? nan : gl / scale - g / scale;
+      const float l = a.lse[r];
+      const bool none = bad || !isfinite(l);
+      live.lse[at] = l;
+      live.cg[at] = none ? nan : g / scale;
+      live.cc[at] = none ? nan : gl / scale - g / scale;
       live.resid[at] = 0.0f;
       if (bad) a.status[0] = 1u;
     }
