@@ -71,7 +71,7 @@ __device__ __forceinline__ uint32_t top_bits(const u32x4& x) {
 }
 
 // x / s, correctly rounded.  With y = 1 / s correctly rounded, q = x y is off by
-// an ulp or two, and one residual step (Markstein), q + (x - q s) y in two fmas,
+// an ulp or two, and one residual step (Markstein), q - (q s - x) y in two fmas,
 // gives the rounded quotient: for every pair of a bf16 x and a scale taken from a
 // bf16 maximum, which is a finite set of mantissas (all 128 x 128 were compared
 // with exact fractions).  The residual's last bit is a number as long as s is
@@ -85,7 +85,7 @@ struct Quotient {
       : s(scale), y(1.0f / scale), step(scale >= 0x1p-60f && scale <= 0x1p+120f) {}
   __device__ __forceinline__ float operator()(float x) const {
     const float q = x * y;
-    return fmaf(fmaf(-q, s, x), y, q);
+    return fmaf(-fmaf(q, s, -x), y, q);  // (the signs as they are, -0 stays -0)
   }
 };
 
