@@ -372,7 +372,8 @@ rlk_status rlk_logp_fused_lmhead(const rlk_logp_desc* desc, const void* hidden,
  *               that no term reaches.  NULL: not wanted, and not computed.
  *   dweight     (device) bf16 [padded_vocab, hidden_dim], 16-byte aligned, out;
  *               +0 on rows >= real_vocab (and everywhere for N == 0).  NULL: not
- *               wanted, and not computed.  At least one of the two must be given.
+ *               wanted, and not computed.  At least one of the two must be given (N == 0
+ *               apart, where dhidden is empty and dweight may be NULL).
  *   workspace   >= rlk_logp_fused_lmhead_bwd_workspace_bytes(desc, hidden_dim,
  *               dhidden != NULL, dweight != NULL), 256-byte aligned; calls that
  *               share one must not overlap.

@@ -45,3 +45,15 @@ def test_lse_that_is_not_finite(n, terms, value):
         c.mask[row] = False
         dh, dw = rlk.fused_lmhead_backward(c.h, c.w, c.tgt, c.mask, lse, g, None, real_vocab=600)
         assert (bits(dh[row]) == 0).all() and dw.float().isfinite().all()
+
+
+def test_no_token_and_a_frozen_head():
+    c, lse = make(5, 64, 300, 300, 8)
+    h = c.h[:0].clone().requires_grad_(True)
+    logp, out = rlk.lmhead_selected_token_logprob(h, c.w, c.tgt[:0], None, real_vocab=300,
+                                                  num_vocab_tiles=1)
+    (logp.sum() + out.sum()).backward()
+    assert h.grad.shape == (0, 64)
+    dh, dw = rlk.fused_lmhead_backward(c.h[:0], c.w, c.tgt[:0], None, lse[:0], c.g[:0],
+                                       real_vocab=300, want_weight=False)
+    assert dh.shape == (0, 64) and dw is None

@@ -910,10 +910,10 @@ rlk_status rlk_logp_fused_lmhead_bwd(const rlk_logp_desc* desc, const void* hidd
                                      void* workspace, size_t workspace_bytes, void* stream_ptr) {
   rlk_status st = check_lmhead_bwd(desc, hidden_dim);
   if (st != RLK_OK) return st;
-  if (!dhidden && !dweight)
-    return fail(RLK_ERR_NULL_POINTER, "at least one of dhidden and dweight must be non-NULL");
   hipStream_t stream = reinterpret_cast<hipStream_t>(stream_ptr);
   const int64_t n = desc->num_tokens;
+  if (n > 0 && !dhidden && !dweight)  // (an empty dhidden has no address)
+    return fail(RLK_ERR_NULL_POINTER, "at least one of dhidden and dweight must be non-NULL");
   hipError_t e;
   if (n == 0) {  // no token: dweight is zero
     if (!dweight) return ok();
