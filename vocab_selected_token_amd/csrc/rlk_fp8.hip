@@ -462,7 +462,7 @@ __global__ __launch_bounds__(kThreads) void fp8_tile(Fp8Operands p, SegmentArgs 
   block_of(blk_begin + xcd_local_block(blockIdx.x, gridDim.x), n_vbs, n_tb, vb, tb);
   vb += vb_begin;
   const int32_t v0 = vb * kBA, t0 = tb * T::kTokens;
-  f32x4 acc[kVS][kTok];
+  f32x4 acc[kVS][kTok] = {};
   // else a block of padding: only logits has them, and stores no sum
   if (!kLogits || v0 < a.row_hi) fp8_product<kTok>(smem, p, a, v0, t0, wave, lane, acc);
   if constexpr (kLogits) {
@@ -540,7 +540,7 @@ __global__ __launch_bounds__(kStreamThreads) void fp8_stream(Fp8Operands p, Segm
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int32_t v0 = v_begin + (int32_t)(blk_begin + blockIdx.x) * kStreamRows;
   const int32_t vw = v0 + wave * 16;
-  f32x4 acc[1][kTok];
+  f32x4 acc[1][kTok] = {};  // outside the rows: zeros, which segments_of_z passes over
   if (v0 < a.row_hi && v0 + kStreamRows > a.row_lo) {
     Fp8Stream<kTok> math;
     math.lds = scales;

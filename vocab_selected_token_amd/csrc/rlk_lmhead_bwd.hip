@@ -336,7 +336,7 @@ __global__ __launch_bounds__(kThreads) void dz_piece(
   int32_t va, tb;
   tile_of(xcd_local_block(blk, used), n_va, n_tb, va, tb);
   const int32_t t0 = tb * kTokens, v0 = va * kBA;  // v0: column inside the piece
-  f32x4 acc[kVS][kTok];
+  f32x4 acc[kVS][kTok] = {};  // a tile of padding: z = 0, of which no dz is made
   if (c0 + v0 < real_vocab) {
     const int64_t row_bytes = (int64_t)hidden_dim * 2;
     const TileOperand wo(reinterpret_cast<const char*>(w) + (int64_t)(c0 + v0) * row_bytes,
