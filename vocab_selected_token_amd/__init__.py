@@ -137,10 +137,17 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+# The handle alone: a Stream object takes ten times as long to make.  It is not part of
+# torch's documented interface, so there may be none.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
-    if stream is None:  # the handle alone: a Stream object takes ten times as long to make
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
-    return stream.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def make_desc(num_tokens: int, real_vocab: int, padded_vocab: int, ld_logits: int,
