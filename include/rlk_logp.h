@@ -377,8 +377,9 @@ rlk_status rlk_logp_fused_lmhead(const rlk_logp_desc* desc, const void* hidden,
  *   workspace   >= rlk_logp_fused_lmhead_bwd_workspace_bytes(desc, hidden_dim,
  *               dhidden != NULL, dweight != NULL), 256-byte aligned; calls that
  *               share one must not overlap.
- * Repeated calls give the same bits.  A row with a bad target gives NaN to its row
- * of dhidden and to all real rows of dweight (RLK_ERR_TARGET_RANGE under
+ * Repeated calls give the same bits.  dz is held relative to the call's largest
+ * finite |g|, |gl|: entries below 2^-126 of that may count as zero.  A row with a bad
+ * target gives NaN to its row of dhidden and to all real rows of dweight (RLK_ERR_TARGET_RANGE under
  * RLK_FLAG_VALIDATE), and so does one whose LSE is not finite. */
 size_t rlk_logp_fused_lmhead_bwd_workspace_bytes(const rlk_logp_desc* desc, int64_t hidden_dim,
                                                  int32_t want_dhidden, int32_t want_dweight);

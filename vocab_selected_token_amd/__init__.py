@@ -802,7 +802,9 @@ def lmhead_selected_token_logprob(hidden: torch.Tensor, weight: torch.Tensor,
     pieces of the vocabulary.  The softmax cross entropy of a token is -logp; a loss
     on logp and LSE hands its gradients to rlk_logp_fused_lmhead_bwd, which computes
     only the gradients that autograd asks for.  hidden: bf16 [N, K] contiguous;
-    weight: bf16 [V_pad, K] contiguous; their gradients are bf16.
+    weight: bf16 [V_pad, K] contiguous; their gradients are bf16.  Where a training step is
+    captured into a HIP graph, no eager autograd graph of the same leaves may be alive: torch
+    ends the process.
     """
     _check_lmhead(hidden, weight, targets, active_mask, real_vocab)
     return _LmheadSelectedTokenLogprob.apply(hidden, weight, targets, active_mask, real_vocab,

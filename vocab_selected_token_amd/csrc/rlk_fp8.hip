@@ -254,7 +254,7 @@ __device__ __forceinline__ uint64_t logits_of(const LogitsOut& o, int32_t v, con
 
 // Stores the kCount logits `x` of token t, columns from v on (a multiple of kCount),
 // as far as the padded vocabulary goes.  kNt: past the caches (1024 tokens x 151936:
-// 349 against 373 us, and no loss to a forward that reads the logits next; nothing
+// 555 against 575 us, and no loss to a forward that reads the logits next; nothing
 // gained where few tokens are streamed).
 template <int kCount, bool kNt, typename T>
 __device__ __forceinline__ void store_logits(const LogitsOut& o, int32_t t, int32_t v,
