@@ -100,7 +100,8 @@ typedef enum rlk_status {
   RLK_ERR_HIP = 9            /* the HIP runtime reported an error                   */
 } rlk_status;
 
-typedef enum rlk_dtype { RLK_DTYPE_F32 = 0, RLK_DTYPE_BF16 = 1 } rlk_dtype;
+/* (fp16 only for what rlk_linear_fwd saves) */
+typedef enum rlk_dtype { RLK_DTYPE_F32 = 0, RLK_DTYPE_BF16 = 1, RLK_DTYPE_F16 = 2 } rlk_dtype;
 
 /* Synchronise `stream` after the launches and turn the device status words
  * into RLK_ERR_TARGET_RANGE (checked first) or RLK_ERR_NONFINITE_LSE. */
@@ -463,6 +464,175 @@ rlk_status rlk_logp_fused_lmhead_fp8(const rlk_logp_desc* desc, const rlk_fp8_ma
                                      const int32_t* targets, const uint8_t* active_mask,
                                      float* logp, float* lse, void* workspace,
                                      size_t workspace_bytes, void* stream);
+
+/* ---- What a sampler does to logits ---------------------------------------------
+ * Penalties for repeated tokens, a bias, a temperature and a grammar's mask: for row r
+ * and column j < V_real, with s = j occurs in the row's history and c = how often it
+ * occurs in the generated part of it,
+ *   x1 = s ? (x > 0 ? x / rho_r : x rho_r) : x
+ *   x2 = x1 - frequency_r c - (c > 0 ? presence_r : 0)
+ *   y  = (x2 + bias_j) / T_r,   and y = -inf where the row's grammar bars j
+ * in fp32.  A barred column's logit is replaced: whatever it holds (NaN, infinity) counts
+ * for nothing.  The pages have no such step; the rows, the columns and the statistics
+ * keep [PR289]'s contract (padding columns are never read for arithmetic). */
+
+/* The rules of a call's N rows (host struct, read during the call only; pointers are
+ * device memory).  Every pointer may be NULL: no such rule.
+ *   repetition, presence, frequency, temperature  float [N] each: rho (positive), the two
+ *               penalties, T (positive); 1, 0, 0 and 1 change nothing.
+ *   history     int32 [history_len] tokens, history_len < 2^31.  Row r's are
+ *               [history_begin[r], history_end[r]), of which those in front of
+ *               history_split[r] are its prompt (history_split NULL: none); rows may share
+ *               tokens (a training row's history is what its sequence holds in front of it).
+ *               Positions outside [0, history_len) are not read, and tokens outside
+ *               [0, V_real) count for nothing.  int64 [N] each, required with a history.
+ *   bias        float [bias_rows, ld_bias], ld_bias >= V_real, added to the logits of row r
+ *               from table row bias_index[r] (int32 [N]; outside the table: no bias).
+ *               bias_index NULL: row r of N, or the only row of a table of one.
+ *   allow       uint32 [allow_rows, ld_allow], ld_allow >= ceil(V_real / 32): column j is
+ *               allowed where bit j % 32 of word j / 32 is set; allow_rows and allow_index
+ *               as for the bias (outside the table: every column is allowed). */
+typedef struct rlk_logit_rules {
+  const float* repetition;
+  const float* presence;
+  const float* frequency;
+  const float* temperature;
+  const int32_t* history;
+  int64_t history_len;
+  const int64_t* history_begin;
+  const int64_t* history_split;
+  const int64_t* history_end;
+  const float* bias;
+  int64_t bias_rows;
+  int64_t ld_bias;
+  const int32_t* bias_index;
+  const uint32_t* allow;
+  int64_t allow_rows;
+  int64_t ld_allow;
+  const int32_t* allow_index;
+} rlk_logit_rules;
+
+/* The processed logits, in one pass.
+ *   desc        num_tokens, real_vocab, padded_vocab, ld_logits as for rlk_logp_fwd, with
+ *               padded_vocab < 2^31 - 65536 (the tiling is validated and not used; flags
+ *               must be 0).
+ *   logits      (device) bf16 [N, ld_logits], 16-byte aligned.
+ *   out         (device) [N, ld_out] of out_dtype, 16-byte aligned: y rounded once; columns
+ *               [V_real, V_pad) are -inf, columns from V_pad on are not touched.  ld_out >=
+ *               V_pad, a multiple of 8.  out may be logits itself (bf16, the same ld); they
+ *               may not overlap otherwise. */
+rlk_status rlk_logits_process(const rlk_logp_desc* desc, const void* logits,
+                              const rlk_logit_rules* rules, void* out, int64_t ld_out,
+                              rlk_dtype out_dtype, void* stream);
+
+/* Selected-token logp and LSE under the processed logits, which are not written: what
+ * rlk_logp_fwd gives of y (not rounded to bf16).
+ *   desc        as for rlk_logp_fwd, with padded_vocab < 2^31 - 65536.  The statistics are
+ *               taken over pieces of 2048 columns and merged in ascending order: the tiling
+ *               and the shards are validated and change nothing.
+ *   logits, targets, active_mask, logp, lse   as for rlk_logp_fwd.  A target that the row's
+ *               grammar bars has logp -inf; a row that is barred altogether has LSE -inf and
+ *               logp NaN (RLK_ERR_NONFINITE_LSE under RLK_FLAG_VALIDATE).
+ *   workspace   >= rlk_logp_processed_workspace_bytes(desc), 256-byte aligned; the status
+ *               words come first.  Calls that share one must not overlap.
+ * Repeated calls give the same bits, and a row the same whatever other rows share the
+ * call. */
+size_t rlk_logp_processed_workspace_bytes(const rlk_logp_desc* desc);
+rlk_status rlk_logp_processed_fwd(const rlk_logp_desc* desc, const void* logits,
+                                  const rlk_logit_rules* rules, const int32_t* targets,
+                                  const uint8_t* active_mask, float* logp, float* lse,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* Its gradient to the raw logits, with p_rj = exp(y_rj - LSE_r):
+ *   dX[r, j] = (a_r g_r ([j == target[r]] - p_rj) + gl_r p_rj) dy/dx
+ *   dy/dx    = (s ? (x > 0 ? 1 / rho_r : rho_r) : 1) / T_r, and 0 where j is barred
+ * (the rules themselves are constants).  A row that no term reaches (not effective-active
+ * or g == 0, and gl == 0) is +0 and its logits and LSE are not read.
+ *   desc, logits, rules, targets, active_mask   as for the forward.
+ *   lse         (device) float [N]: the forward's LSE.
+ *   grad_logp, grad_lse  (device) float [N] each, or NULL for zero; at least one given.
+ *   dlogits, ld_dlogits, dlogits_dtype, bad targets   as for rlk_logp_bwd.
+ *   workspace   >= 256 bytes (the status words), 256-byte aligned. */
+rlk_status rlk_logp_processed_bwd(const rlk_logp_desc* desc, const void* logits,
+                                  const rlk_logit_rules* rules, const int32_t* targets,
+                                  const uint8_t* active_mask, const float* lse,
+                                  const float* grad_logp, const float* grad_lse, void* dlogits,
+                                  int64_t ld_dlogits, rlk_dtype dlogits_dtype, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* ---- Dense products with their epilogue -------------------------------------------
+ *   z = x . weight^T + bias,   out = residual + act(z)
+ * with bf16 operands, z, act and the sum with the residual in fp32, and out rounded to
+ * bf16 once: logits with a bias and a soft cap, or the residual and dense blocks of a
+ * prediction head in front of them.  The pages have no such step. */
+typedef enum rlk_activation {
+  RLK_ACT_NONE = 0,
+  RLK_ACT_RELU = 1,
+  RLK_ACT_GELU = 2,      /* z Phi(z)                                                   */
+  RLK_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2            */
+  RLK_ACT_SILU = 4,      /* z / (1 + exp(-z))                                          */
+  RLK_ACT_SOFTCAP = 5    /* cap tanh(z / cap)                                          */
+} rlk_activation;
+
+/* Problem description (host struct, read during the call only).
+ *   tokens      >= 0 (0 enqueues nothing, but for the weight's and the bias' zero gradients)
+ *   in_dim      a positive multiple of 64, at most 2^21
+ *   out_dim     >= 1, padded_out >= out_dim and < 2^31 - 65536
+ *   ld_out      >= padded_out, a multiple of 8;  ld_residual >= out_dim (any)
+ *   ld_saved    >= out_dim, a multiple of 8
+ *   activation  an rlk_activation; cap: finite and positive for RLK_ACT_SOFTCAP, else unused
+ *   bias_dtype  of the bias and its gradient; unused without them
+ *   saved_dtype RLK_DTYPE_F16 or RLK_DTYPE_F32: what the forward keeps of z.  fp16 (11 bits)
+ *               costs gradients in bf16 nothing that shows; a bias' gradient in fp32 is as
+ *               exact as what is kept                                                   */
+typedef struct rlk_linear_desc {
+  int64_t tokens;
+  int64_t in_dim;
+  int64_t out_dim;
+  int64_t padded_out;
+  int64_t ld_out;
+  int64_t ld_residual;
+  int64_t ld_saved;
+  int32_t activation;
+  int32_t bias_dtype;
+  int32_t saved_dtype;
+  float cap;
+} rlk_linear_desc;
+
+/* Forward.
+ *   x           (device) bf16 [tokens, in_dim], contiguous, 16-byte aligned.
+ *   weight      (device) bf16 [>= out_dim, in_dim], contiguous, 16-byte aligned; rows >=
+ *               out_dim are never read.
+ *   bias        (device) [out_dim] of bias_dtype, or NULL.
+ *   residual    (device) bf16 [tokens, ld_residual], or NULL; it may not overlap out.
+ *   out         (device) bf16 [tokens, ld_out], 16-byte aligned; columns [out_dim, padded_out)
+ *               are -inf (the logits of padding), columns from padded_out on are not touched.
+ *   saved       (device) [tokens, ld_saved] of saved_dtype, 16-byte aligned, out, or NULL: z
+ *               (z / cap for the soft cap; in fp16 clamped to +-65504), which rlk_linear_bwd
+ *               needs unless the activation is RLK_ACT_NONE.  Columns from out_dim on may be
+ *               written.
+ * Repeated calls give the same bits. */
+rlk_status rlk_linear_fwd(const rlk_linear_desc* desc, const void* x, const void* weight,
+                          const void* bias, const void* residual, void* out, void* saved,
+                          void* stream);
+
+/* Gradients: dz = grad_out act'(z), dx = dz . weight, dweight = dz^T . x, dbias = the sum of
+ * dz over the tokens (the residual's gradient is grad_out).  dz is rounded to bf16 once for
+ * the two products; dbias is summed from it in fp32 before that.
+ *   desc        out_dim <= 2^21; padded_out, ld_out and ld_residual are not used.
+ *   saved       the forward's (not used for RLK_ACT_NONE).
+ *   grad_out    (device) bf16 [tokens, ld_grad], ld_grad >= out_dim (any).
+ *   dx          (device) bf16 [tokens, in_dim], dweight bf16 [out_dim, in_dim], both
+ *               contiguous and 16-byte aligned, dbias [out_dim] of bias_dtype; each may be
+ *               NULL (not wanted and not computed), not all three.
+ *   workspace   >= rlk_linear_bwd_workspace_bytes(desc), 256-byte aligned; calls that share
+ *               one must not overlap.
+ * Repeated calls give the same bits. */
+size_t rlk_linear_bwd_workspace_bytes(const rlk_linear_desc* desc);
+rlk_status rlk_linear_bwd(const rlk_linear_desc* desc, const void* x, const void* weight,
+                          const void* saved, const void* grad_out, int64_t ld_grad, void* dx,
+                          void* dweight, void* dbias, void* workspace, size_t workspace_bytes,
+                          void* stream);
 
 /* Host-only geometry (no device access): writes T+1 tile bounds
  * floor(t*V_pad/T) to `bounds` and S+1 shard starts floor(s*T/S) to

@@ -33,6 +33,7 @@ RLK_ERR_HIP = 9
 
 RLK_DTYPE_F32 = 0
 RLK_DTYPE_BF16 = 1
+RLK_DTYPE_F16 = 2
 RLK_FLAG_VALIDATE = 1
 
 EXPORTED = ("rlk_logp_workspace_bytes", "rlk_logp_fwd", "rlk_logp_bwd",
@@ -43,6 +44,9 @@ EXPORTED = ("rlk_logp_workspace_bytes", "rlk_logp_fwd", "rlk_logp_bwd",
             "rlk_logp_fused_lmhead_bwd_workspace_bytes", "rlk_logp_fused_lmhead_bwd",
             "rlk_fp8_quantize", "rlk_lmhead_logits_fp8",
             "rlk_logp_fused_lmhead_fp8_workspace_bytes", "rlk_logp_fused_lmhead_fp8",
+            "rlk_logits_process", "rlk_logp_processed_workspace_bytes",
+            "rlk_logp_processed_fwd", "rlk_logp_processed_bwd",
+            "rlk_linear_fwd", "rlk_linear_bwd_workspace_bytes", "rlk_linear_bwd",
             "rlk_logp_tile_geometry", "rlk_status_string", "rlk_last_error_detail",
             "rlk_logp_fwd_noalloc")
 
@@ -57,6 +61,27 @@ class rlk_logp_desc(ctypes.Structure):  # noqa: N801 - mirrors the C struct name
 class rlk_fp8_matrix(ctypes.Structure):  # noqa: N801 - mirrors the C struct name
     _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p),
                 ("scale_row_stride", ctypes.c_int64), ("scale_col_stride", ctypes.c_int64)]
+
+
+class rlk_logit_rules(ctypes.Structure):  # noqa: N801
+    _fields_ = [("repetition", ctypes.c_void_p), ("presence", ctypes.c_void_p),
+                ("frequency", ctypes.c_void_p), ("temperature", ctypes.c_void_p),
+                ("history", ctypes.c_void_p), ("history_len", ctypes.c_int64),
+                ("history_begin", ctypes.c_void_p), ("history_split", ctypes.c_void_p),
+                ("history_end", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("bias_rows", ctypes.c_int64), ("ld_bias", ctypes.c_int64),
+                ("bias_index", ctypes.c_void_p), ("allow", ctypes.c_void_p),
+                ("allow_rows", ctypes.c_int64), ("ld_allow", ctypes.c_int64),
+                ("allow_index", ctypes.c_void_p)]
+
+
+class rlk_linear_desc(ctypes.Structure):  # noqa: N801
+    _fields_ = [("tokens", ctypes.c_int64), ("in_dim", ctypes.c_int64),
+                ("out_dim", ctypes.c_int64), ("padded_out", ctypes.c_int64),
+                ("ld_out", ctypes.c_int64), ("ld_residual", ctypes.c_int64),
+                ("ld_saved", ctypes.c_int64), ("activation", ctypes.c_int32),
+                ("bias_dtype", ctypes.c_int32), ("saved_dtype", ctypes.c_int32),
+                ("cap", ctypes.c_float)]
 
 
 class RlkError(RuntimeError):
@@ -116,6 +141,22 @@ def _load() -> ctypes.CDLL:
     lib.rlk_logp_fused_lmhead_fp8_workspace_bytes.restype = sz
     lib.rlk_logp_fused_lmhead_fp8.argtypes = [dp, mp, mp, i64, vp, vp, vp, vp, vp, sz, vp]
     lib.rlk_logp_fused_lmhead_fp8.restype = ctypes.c_int
+    rp, lp = ctypes.POINTER(rlk_logit_rules), ctypes.POINTER(rlk_linear_desc)
+    lib.rlk_logits_process.argtypes = [dp, vp, rp, vp, i64, ctypes.c_int, vp]
+    lib.rlk_logits_process.restype = ctypes.c_int
+    lib.rlk_logp_processed_workspace_bytes.argtypes = [dp]
+    lib.rlk_logp_processed_workspace_bytes.restype = sz
+    lib.rlk_logp_processed_fwd.argtypes = [dp, vp, rp, vp, vp, vp, vp, vp, sz, vp]
+    lib.rlk_logp_processed_fwd.restype = ctypes.c_int
+    lib.rlk_logp_processed_bwd.argtypes = [dp, vp, rp, vp, vp, vp, vp, vp, vp, i64, ctypes.c_int,
+                                           vp, sz, vp]
+    lib.rlk_logp_processed_bwd.restype = ctypes.c_int
+    lib.rlk_linear_fwd.argtypes = [lp, vp, vp, vp, vp, vp, vp, vp]
+    lib.rlk_linear_fwd.restype = ctypes.c_int
+    lib.rlk_linear_bwd_workspace_bytes.argtypes = [lp]
+    lib.rlk_linear_bwd_workspace_bytes.restype = sz
+    lib.rlk_linear_bwd.argtypes = [lp, vp, vp, vp, vp, i64, vp, vp, vp, vp, sz, vp]
+    lib.rlk_linear_bwd.restype = ctypes.c_int
     lib.rlk_logp_tile_geometry.argtypes = [i64, i32, i32, vp, vp]
     lib.rlk_logp_tile_geometry.restype = ctypes.c_int
     lib.rlk_status_string.argtypes = [ctypes.c_int]
@@ -305,6 +346,53 @@ def rlk_logp_fused_lmhead_fp8(desc, hidden, weight, hidden_dim: int, targets, ac
                                           hidden_dim, _ptr(targets), _ptr(active_mask),
                                           _ptr(logp), _ptr(lse), _ptr(workspace), ws_bytes,
                                           _stream(stream)))
+
+
+def rlk_logits_process(desc, logits, rules, out, ld_out: int, out_dtype: int,
+                       stream=None) -> None:
+    _check(_lib.rlk_logits_process(ctypes.byref(desc), _ptr(logits), _ref(rules), _ptr(out),
+                                   ld_out, out_dtype, _stream(stream)))
+
+
+def rlk_logp_processed_workspace_bytes(desc: rlk_logp_desc) -> int:
+    return int(_lib.rlk_logp_processed_workspace_bytes(ctypes.byref(desc)))
+
+
+def rlk_logp_processed_fwd(desc, logits, rules, targets, active_mask, logp, lse, workspace,
+                           stream=None) -> None:
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.rlk_logp_processed_fwd(ctypes.byref(desc), _ptr(logits), _ref(rules),
+                                       _ptr(targets), _ptr(active_mask), _ptr(logp), _ptr(lse),
+                                       _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def rlk_logp_processed_bwd(desc, logits, rules, targets, active_mask, lse, grad_logp, grad_lse,
+                           dlogits, ld_dlogits: int, dlogits_dtype: int, workspace,
+                           stream=None) -> None:
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.rlk_logp_processed_bwd(ctypes.byref(desc), _ptr(logits), _ref(rules),
+                                       _ptr(targets), _ptr(active_mask), _ptr(lse),
+                                       _ptr(grad_logp), _ptr(grad_lse), _ptr(dlogits),
+                                       ld_dlogits, dlogits_dtype, _ptr(workspace), ws_bytes,
+                                       _stream(stream)))
+
+
+def rlk_linear_fwd(desc: rlk_linear_desc, x, weight, bias, residual, out, saved,
+                   stream=None) -> None:
+    _check(_lib.rlk_linear_fwd(ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias),
+                               _ptr(residual), _ptr(out), _ptr(saved), _stream(stream)))
+
+
+def rlk_linear_bwd_workspace_bytes(desc: rlk_linear_desc) -> int:
+    return int(_lib.rlk_linear_bwd_workspace_bytes(ctypes.byref(desc)))
+
+
+def rlk_linear_bwd(desc: rlk_linear_desc, x, weight, saved, grad_out, ld_grad: int, dx, dweight,
+                   dbias, workspace, stream=None) -> None:
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.rlk_linear_bwd(ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(saved),
+                               _ptr(grad_out), ld_grad, _ptr(dx), _ptr(dweight), _ptr(dbias),
+                               _ptr(workspace), ws_bytes, _stream(stream)))
 
 
 def rlk_logp_tile_geometry(padded_vocab: int, num_vocab_tiles: int, num_virtual_shards: int = 1):
@@ -952,3 +1040,476 @@ def fused_lmhead_fp8(hidden, weight_q: torch.Tensor, weight_scale: torch.Tensor,
                                   _u8_mask(active_mask), logp, lse, workspace, stream)
     _handed_over(x, stream, logp, lse)
     return logp, lse
+
+
+# -- what a sampler does to logits -------------------------------------------------
+class LogitRules:
+    """The rules of a call's N rows: penalties for repeated tokens, a bias, a temperature and a
+    grammar's mask.  For row r and column j, with s = j occurs in the row's history and c = how
+    often in the generated part of it,
+
+        x1 = (x / repetition if x > 0 else x * repetition) if s else x
+        x2 = x1 - frequency c - (presence if c > 0 else 0)
+        y  = (x2 + bias_j) / temperature,  -inf where the grammar bars j
+
+    Every rule may be absent.  repetition, presence, frequency, temperature: fp32 [N].
+    history: int32 [H] tokens; row r's are history[history_begin[r]:history_end[r]] (int64 [N]
+    each), of which those in front of history_split[r] are its prompt (none without it); rows may
+    share tokens, and tokens outside the vocabulary count for nothing.  bias: fp32 [rows, >= V],
+    allow: int32 bits [rows, >= ceil(V / 32)], bit j % 32 of word j / 32 set where column j is
+    allowed; either with one row (or 1-D) for all, with N, or with an int32 [N] index of the row
+    to take (outside the table: none).
+
+    The tensors are checked here, once, and have to stay as they are made: contents may change
+    between calls.  They are constants: no gradient reaches them."""
+
+    __slots__ = ("tensors", "rows", "device", "struct", "_bias_cols", "_allow_words")
+
+    _VECTORS = ("repetition", "presence", "frequency", "temperature")
+    _BOUNDS = ("history_begin", "history_split", "history_end")
+
+    def __init__(self, *, repetition=None, presence=None, frequency=None, temperature=None,
+                 history=None, history_begin=None, history_split=None, history_end=None,
+                 bias=None, bias_index=None, allow=None, allow_index=None):
+        rows = device = None
+        s = rlk_logit_rules()
+        kept = []
+
+        def vector(name, t, dtype, per_row=True):
+            nonlocal rows, device
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+            if t.dtype != dtype:
+                raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+            if t.dim() != 1 or not t.is_contiguous():
+                raise ValueError(f"{name} must be 1-D and contiguous")
+            if per_row:
+                if rows is None:
+                    rows = t.shape[0]
+                elif t.shape[0] != rows:
+                    raise ValueError(f"{name} has {t.shape[0]} elements, other rules {rows}")
+            seen(name, t)
+            return t.data_ptr() or None
+
+        def seen(name, t):
+            nonlocal device
+            if device is None:
+                device = t.device
+            elif t.device != device:
+                raise ValueError(f"{name} is on {t.device}, other rules on {device}")
+            kept.append(t)
+
+        def table(name, t, dtype, index):
+            nonlocal rows
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+            if t.dtype != dtype:
+                raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+            if t.dim() not in (1, 2) or (t.shape[-1] > 1 and t.stride(-1) != 1):
+                raise ValueError(f"{name} must be 1-D or 2-D with unit column stride")
+            n, width = (1, t.shape[0]) if t.dim() == 1 else t.shape
+            ld = width if n <= 1 else t.stride(0)
+            if n < 1 or ld < width:
+                raise ValueError(f"{name} must have a row, and rows that do not overlap")
+            seen(name, t)
+            if index is None and n > 1:
+                if rows is None:
+                    rows = n
+                elif n != rows:
+                    raise ValueError(f"{name} without an index has {n} rows, other rules {rows}")
+            at = None if index is None else vector(name + "_index", index, torch.int32)
+            return t.data_ptr() or None, n, ld, at, width
+
+        for name, t in zip(self._VECTORS, (repetition, presence, frequency, temperature)):
+            if t is not None:
+                setattr(s, name, vector(name, t, torch.float32))
+        if history is not None:
+            if history_begin is None or history_end is None:
+                raise TypeError("a history needs history_begin and history_end")
+            s.history = vector("history", history, torch.int32, per_row=False)
+            s.history_len = history.shape[0]
+            for name, t in zip(self._BOUNDS, (history_begin, history_split, history_end)):
+                if t is not None:
+                    setattr(s, name, vector(name, t, torch.int64))
+        elif not (history_begin is history_split is history_end is None):
+            raise TypeError("history_begin, history_split and history_end need a history")
+        self._bias_cols = self._allow_words = None
+        if bias is not None:
+            s.bias, s.bias_rows, s.ld_bias, s.bias_index, self._bias_cols = \
+                table("bias", bias, torch.float32, bias_index)
+        elif bias_index is not None:
+            raise TypeError("bias_index needs a bias")
+        if allow is not None:
+            s.allow, s.allow_rows, s.ld_allow, s.allow_index, self._allow_words = \
+                table("allow", allow, torch.int32, allow_index)
+        elif allow_index is not None:
+            raise TypeError("allow_index needs allow")
+        self.tensors, self.rows, self.device, self.struct = tuple(kept), rows, device, s
+
+
+def _check_rules(rules, logits, real_vocab):
+    if not isinstance(rules, LogitRules):
+        raise TypeError("rules must be LogitRules")
+    if rules.rows is not None and rules.rows != logits.shape[0]:
+        raise ValueError(f"the rules have {rules.rows} rows, the logits {logits.shape[0]}")
+    if rules._bias_cols is not None and rules._bias_cols < real_vocab:
+        raise ValueError(f"bias has {rules._bias_cols} columns, fewer than "
+                         f"real_vocab={real_vocab}")
+    if rules._allow_words is not None and rules._allow_words * 32 < real_vocab:
+        raise ValueError(f"allow has {rules._allow_words} words, fewer than "
+                         f"real_vocab={real_vocab} needs")
+    if rules.device is not None and rules.device != logits.device:
+        raise ValueError(f"the rules are on {rules.device}, the logits on {logits.device}")
+
+
+def process_logits(logits: torch.Tensor, rules: LogitRules, *, real_vocab: int,
+                   padded_vocab: int | None = None, out_dtype=torch.bfloat16,
+                   out: torch.Tensor | None = None, stream=None):
+    """The processed logits [N, V_pad] (bf16 or fp32; rows padded to a multiple of 8 columns,
+    columns [real_vocab, V_pad) -inf).  logits: bf16 [N, ld] with unit column stride.  With `out`
+    they are written there, a tensor of out_dtype with at least V_pad columns: the logits
+    themselves, for instance; what lies behind V_pad stays."""
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("out_dtype must be torch.float32 or torch.bfloat16")
+    v_pad = _check_vocab(logits, real_vocab, padded_vocab)
+    _check_rules(rules, logits, real_vocab)
+    n = logits.shape[0]
+    if out is not None:
+        if not isinstance(out, torch.Tensor) or out.dtype != out_dtype:
+            raise TypeError(f"out must be a tensor of {out_dtype}")
+        if out.dim() != 2 or out.shape[0] != n or out.shape[1] < v_pad or out.stride(1) != 1:
+            raise ValueError(f"out must have {n} rows of at least {v_pad} columns, of unit "
+                             "stride")
+    _check_device(logits, out=out)
+    code = RLK_DTYPE_BF16 if out_dtype == torch.bfloat16 else RLK_DTYPE_F32
+    desc = make_desc(n, real_vocab, v_pad, logits.stride(0), 1)
+    with _call_on(logits, stream):
+        if out is None:
+            ld = (v_pad + 7) // 8 * 8
+            y = torch.empty((n, ld), dtype=out_dtype, device=logits.device)
+        else:
+            y, ld = out, out.stride(0)
+        rlk_logits_process(desc, logits, rules.struct, y, ld, code, stream)
+    if out is not None:
+        return out
+    _handed_over(logits, stream, y)
+    return y if ld == v_pad else y[:, :v_pad]
+
+
+def processed_forward(logits: torch.Tensor, targets: torch.Tensor, rules: LogitRules,
+                      active_mask=None, *, real_vocab: int, padded_vocab: int | None = None,
+                      ignore_index: int = -100, validate: bool = False,
+                      workspace: torch.Tensor | None = None, stream=None):
+    """(logp, lse), fp32 [N] each, of the processed logits (see LogitRules), which are not
+    written: forward() of process_logits(), but for the rounding."""
+    v_pad = _check_vocab(logits, real_vocab, padded_vocab)
+    _check_inputs(logits, targets, active_mask)
+    _check_rules(rules, logits, real_vocab)
+    desc = make_desc(logits.shape[0], real_vocab, v_pad, logits.stride(0), 1, 1, ignore_index,
+                     validate)
+    return _run_processed(desc, logits, targets, rules, active_mask, workspace, stream)
+
+
+def _run_processed(desc, logits, targets, rules, active_mask, workspace=None, stream=None):
+    n = logits.shape[0]
+    with _call_on(logits, stream):
+        logp = torch.empty(n, dtype=torch.float32, device=logits.device)
+        lse = torch.empty(n, dtype=torch.float32, device=logits.device)
+        if workspace is None:
+            workspace = _bytes_for(rlk_logp_processed_workspace_bytes(desc), logits.device)
+        rlk_logp_processed_fwd(desc, logits, rules.struct, targets, _u8_mask(active_mask), logp,
+                               lse, workspace, stream)
+    _handed_over(logits, stream, logp, lse)
+    return logp, lse
+
+
+def processed_backward(logits: torch.Tensor, targets: torch.Tensor, rules: LogitRules,
+                       active_mask, lse: torch.Tensor, grad_logp=None, grad_lse=None, *,
+                       real_vocab: int, padded_vocab: int | None = None,
+                       out_dtype=torch.float32, ignore_index: int = -100,
+                       validate: bool = False, workspace: torch.Tensor | None = None,
+                       stream=None):
+    """dlogits [N, V_pad] (fp32 or bf16), to the raw logits, of a loss on processed_forward's
+    logp and LSE; absent gradients are zero."""
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("dlogits dtype must be torch.float32 or torch.bfloat16")
+    if lse is None:
+        raise TypeError("lse must be a torch.Tensor")
+    if grad_logp is None and grad_lse is None:
+        raise TypeError("at least one of grad_logp and grad_lse must be a torch.Tensor")
+    v_pad = _check_vocab(logits, real_vocab, padded_vocab)
+    _check_inputs(logits, targets, active_mask, lse=lse, grad_logp=grad_logp, grad_lse=grad_lse)
+    _check_rules(rules, logits, real_vocab)
+    desc = make_desc(logits.shape[0], real_vocab, v_pad, logits.stride(0), 1, 1, ignore_index,
+                     validate)
+    return _run_processed_backward(desc, logits, targets, rules, active_mask, lse, grad_logp,
+                                   grad_lse, out_dtype, workspace, stream)
+
+
+def _run_processed_backward(desc, logits, targets, rules, active_mask, lse, grad_logp, grad_lse,
+                            out_dtype, workspace=None, stream=None):
+    v_pad = desc.padded_vocab
+    ld = (v_pad + 7) // 8 * 8
+    code = RLK_DTYPE_BF16 if out_dtype == torch.bfloat16 else RLK_DTYPE_F32
+    with _call_on(logits, stream):
+        dl = torch.empty((logits.shape[0], ld), dtype=out_dtype, device=logits.device)
+        if workspace is None:
+            workspace = _bytes_for(256, logits.device)
+        rlk_logp_processed_bwd(desc, logits, rules.struct, targets, _u8_mask(active_mask), lse,
+                               grad_logp, grad_lse, dl, ld, code, workspace, stream)
+    _handed_over(logits, stream, dl)
+    return dl if ld == v_pad else dl[:, :v_pad]
+
+
+class _ProcessedSelectedTokenLogprob(torch.autograd.Function):
+    """(logp, lse) of bf16 logits under the rules, differentiable in the logits; the forward
+    and the backward are rlk_logp_processed_fwd and rlk_logp_processed_bwd."""
+
+    @staticmethod
+    def forward(ctx, logits, targets, rules, active_mask, real_vocab, v_pad, ignore_index):
+        desc = make_desc(logits.shape[0], real_vocab, v_pad, logits.stride(0), 1, 1, ignore_index)
+        logp, lse = _run_processed(desc, logits, targets, rules, active_mask)
+        # (the rules' tensors too: one that is changed in between is refused by autograd)
+        ctx.save_for_backward(logits, targets, active_mask, lse, *rules.tensors)
+        ctx.rules = rules
+        # every column of the gradient is written: +0 from real_vocab on
+        ctx.desc = make_desc(logits.shape[0], real_vocab, logits.shape[1], logits.stride(0), 1, 1,
+                             ignore_index)
+        ctx.set_materialize_grads(False)
+        return logp, lse
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g_logp, g_lse):
+        if g_logp is None and g_lse is None:
+            return (None,) * 7
+
+        def vec(t):
+            return None if t is None else t.contiguous().float()
+        logits, targets, active_mask, lse = ctx.saved_tensors[:4]
+        d = _run_processed_backward(ctx.desc, logits, targets, ctx.rules, active_mask, lse,
+                                    vec(g_logp), vec(g_lse), logits.dtype)
+        return d, None, None, None, None, None, None
+
+
+def processed_selected_token_logprob(logits: torch.Tensor, targets: torch.Tensor,
+                                     rules: LogitRules, active_mask=None, *, real_vocab: int,
+                                     padded_vocab: int | None = None, ignore_index: int = -100):
+    """processed_forward as a differentiable torch function: returns (logp, lse), fp32 [N].
+
+    The log-probability under the distribution that a sampler with these rules draws from,
+    and its gradient to the raw logits (bf16 [N, ld] with unit column stride; the gradient has
+    their shape and dtype).  The rules are constants.  Where a training step is captured into a HIP
+    graph, no eager autograd graph of the same leaves may be alive: torch ends the process."""
+    v_pad = _check_vocab(logits, real_vocab, padded_vocab)
+    _check_inputs(logits, targets, active_mask)
+    _check_rules(rules, logits, real_vocab)
+    for t in rules.tensors:
+        if t.requires_grad:
+            raise ValueError("the rules are constants: none of their tensors may require a "
+                             "gradient")
+    return _ProcessedSelectedTokenLogprob.apply(logits, targets, rules, active_mask, real_vocab,
+                                                v_pad, ignore_index)
+
+
+# -- dense products with their epilogue -----------------------------------------------
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "softcap": 5}
+
+
+_SAVED = {torch.float32: RLK_DTYPE_F32, torch.float16: RLK_DTYPE_F16}
+
+
+def _check_activation(activation, cap):
+    code = ACTIVATIONS.get(activation)
+    if code is None:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, "
+                         f"got {activation!r}")
+    if (cap is not None) != (activation == "softcap"):
+        raise ValueError("cap goes with the activation softcap, and with no other")
+    if cap is not None and not 0.0 < cap < 3e38:
+        raise ValueError(f"cap must be finite and positive, got {cap!r}")
+    return code, 0.0 if cap is None else float(cap)
+
+
+def _check_linear(x, weight, out_dim, bias, **others):
+    """x bf16 [M, K] and weight bf16 [>= out_dim, K], contiguous; bias bf16 or fp32, out_dim or
+    more; others: bf16 [M, out_dim] with unit column stride.  Nones apart; all on x's GPU."""
+    for name, t in (("x", x), ("weight", weight)):
+        _check_logits(t, name)
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    if weight.shape[1] != x.shape[1]:
+        raise ValueError(f"weight has {weight.shape[1]} columns, x {x.shape[1]}")
+    if weight.shape[0] < out_dim:
+        raise ValueError(f"weight has {weight.shape[0]} rows, fewer than {out_dim}")
+    if bias is not None:
+        if not isinstance(bias, torch.Tensor):
+            raise TypeError("bias must be a torch.Tensor")
+        if bias.dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"bias must be torch.bfloat16 or torch.float32, got {bias.dtype}")
+        if bias.dim() != 1 or bias.shape[0] < out_dim or not bias.is_contiguous():
+            raise ValueError(f"bias must be 1-D and contiguous with {out_dim} elements, got "
+                             f"shape {tuple(bias.shape)}")
+    for name, t in others.items():
+        if t is not None:
+            _check_logits(t, name)
+            if tuple(t.shape) != (x.shape[0], out_dim):
+                raise ValueError(f"{name} must have shape {(x.shape[0], out_dim)}, got "
+                                 f"{tuple(t.shape)}")
+    _check_device(x, weight=weight, bias=bias, **others)
+
+
+def _row_stride(t):
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _bias_code(dtype):
+    return RLK_DTYPE_BF16 if dtype == torch.bfloat16 else RLK_DTYPE_F32
+
+
+def _run_linear(x, weight, bias, residual, act, cap, out_dim, padded, save, stream=None):
+    m, k = x.shape
+    ld, ld_saved = (padded + 7) // 8 * 8, (out_dim + 7) // 8 * 8
+    with _call_on(x, stream):
+        y = torch.empty((m, ld), dtype=torch.bfloat16, device=x.device)
+        # (a bias in fp32 has a gradient in fp32, as exact as what is kept of z)
+        exact = bias is not None and bias.dtype == torch.float32
+        saved = torch.empty((m, ld_saved), dtype=torch.float32 if exact else torch.float16,
+                            device=x.device) if save else None
+        desc = rlk_linear_desc(m, k, out_dim, padded, ld,
+                               0 if residual is None else _row_stride(residual), ld_saved, act,
+                               0 if bias is None else _bias_code(bias.dtype),
+                               RLK_DTYPE_F32 if exact else RLK_DTYPE_F16, cap)
+        rlk_linear_fwd(desc, x, weight, bias, residual, y, saved, stream)
+    _handed_over(x, stream, y, saved)
+    return y if ld == padded else y[:, :padded], saved
+
+
+def linear_forward(x: torch.Tensor, weight: torch.Tensor, bias=None, residual=None, *,
+                   activation: str = "none", cap: float | None = None, save: bool = False,
+                   stream=None):
+    """(out, saved): out = residual + act(x . weight^T + bias) in bf16 [M, N], rounded once.
+
+    x: bf16 [M, K], weight: bf16 [N, K], both contiguous, K a multiple of 64; bias: bf16 or fp32
+    [N]; residual: bf16 [M, N] with unit column stride.  activation: none, relu, gelu, gelu_tanh,
+    silu or softcap (cap tanh(z / cap)).  out's rows are padded to a multiple of 8 columns.  With
+    `save`, saved is what linear_backward needs (z in fp16, or in fp32 with a bias in fp32; None
+    for no activation)."""
+    act, cap = _check_activation(activation, cap)
+    _check_logits(weight, "weight")
+    n = weight.shape[0]
+    _check_linear(x, weight, n, bias, residual=residual)
+    return _run_linear(x, weight, bias, residual, act, cap, n, n, save and act != 0, stream)
+
+
+def linear_backward(x: torch.Tensor, weight: torch.Tensor, grad_out: torch.Tensor, saved=None, *,
+                    activation: str = "none", cap: float | None = None, want_x: bool = True,
+                    want_weight: bool = True, want_bias: bool = False,
+                    bias_dtype=torch.float32, workspace: torch.Tensor | None = None,
+                    stream=None):
+    """(dx, dweight, dbias) of linear_forward, in bf16 (dbias in bias_dtype), from its `saved` and
+    grad_out, bf16 [M, N] with unit column stride (which is the residual's gradient).  What is not
+    wanted is not computed and comes back as None."""
+    act, cap = _check_activation(activation, cap)
+    if bias_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("bias_dtype must be torch.float32 or torch.bfloat16")
+    if not (want_x or want_weight or want_bias):
+        raise ValueError("at least one of want_x, want_weight and want_bias must be true")
+    _check_logits(weight, "weight")
+    n = weight.shape[0]
+    if grad_out is None:
+        raise TypeError("grad_out must be a torch.Tensor")
+    _check_linear(x, weight, n, None, grad_out=grad_out)
+    if act != 0:
+        if not isinstance(saved, torch.Tensor) or saved.dtype not in _SAVED:
+            raise TypeError(f"{activation}: the gradient needs what linear_forward saved")
+        if tuple(saved.shape) != (x.shape[0], (n + 7) // 8 * 8) or not saved.is_contiguous():
+            raise ValueError("saved is not what linear_forward saved for this call")
+        _check_device(x, saved=saved)
+    return _run_linear_backward(x, weight, grad_out, saved, act, cap, want_x, want_weight,
+                                bias_dtype if want_bias else None, workspace, stream)
+
+
+def _run_linear_backward(x, weight, grad_out, saved, act, cap, want_x, want_weight, bias_dtype,
+                         workspace=None, stream=None):
+    m, k = x.shape
+    n = weight.shape[0]
+    desc = rlk_linear_desc(m, k, n, n, n, n, (n + 7) // 8 * 8, act,
+                           0 if bias_dtype is None else _bias_code(bias_dtype),
+                           RLK_DTYPE_F16 if saved is None else _SAVED[saved.dtype], cap)
+    with _call_on(x, stream):
+        dx = torch.empty_like(x) if want_x else None
+        dw = torch.empty_like(weight) if want_weight else None
+        db = None if bias_dtype is None else torch.empty(n, dtype=bias_dtype, device=x.device)
+        if workspace is None:
+            nbytes = rlk_linear_bwd_workspace_bytes(desc)
+            if nbytes == 0:
+                raise ValueError(f"invalid rlk_linear_desc: {rlk_last_error_detail()}")
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+        rlk_linear_bwd(desc, x, weight, saved, grad_out, _row_stride(grad_out), dx, dw, db,
+                       workspace, stream)
+    _handed_over(x, stream, dx, dw, db)
+    return dx, dw, db
+
+
+class _HeadLinear(torch.autograd.Function):
+    """residual + act(x . weight^T + bias), differentiable in all four; the forward and the
+    backward are rlk_linear_fwd and rlk_linear_bwd."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, act, cap):
+        n = weight.shape[0]
+        save = act != 0 and any(ctx.needs_input_grad[:3])
+        y, saved = _run_linear(x, weight, bias, residual, act, cap, n, n, save)
+        ctx.save_for_backward(x, weight, saved)
+        ctx.cfg = act, cap, None if bias is None else bias.dtype
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        # what was saved has been checked; the gradient has the output's shape, dtype and device
+        act, cap, bias_dtype = ctx.cfg
+        want_x, want_weight, want_bias, want_residual = ctx.needs_input_grad[:4]
+        dx = dw = db = None
+        if want_x or want_weight or want_bias:
+            x, weight, saved = ctx.saved_tensors
+            if grad.stride(1) != 1 or grad.stride(0) < grad.shape[1]:
+                grad = grad.contiguous()
+            dx, dw, db = _run_linear_backward(x, weight, grad, saved, act, cap, want_x,
+                                              want_weight, bias_dtype if want_bias else None)
+        return dx, dw, db, grad if want_residual else None, None, None
+
+
+def head_linear(x: torch.Tensor, weight: torch.Tensor, bias=None, residual=None, *,
+                activation: str = "none", cap: float | None = None):
+    """linear_forward as a differentiable torch function: returns residual + act(x . weight^T +
+    bias), bf16 [M, N], with gradients for the inputs that ask for one (dx, dweight in bf16,
+    the bias' in its dtype, the residual's is the upstream one).
+
+    This is a prediction head's dense or residual block, in front of the LM-head.  The backward
+    keeps z in 16 bits (32 with a bias in fp32) and rounds dz to bf16 once.  Where a training step is captured into a HIP
+    graph, no eager autograd graph of the same leaves may be alive: torch ends the process."""
+    act, cap = _check_activation(activation, cap)
+    _check_logits(weight, "weight")
+    n = weight.shape[0]
+    _check_linear(x, weight, n, bias, residual=residual)
+    if bias is not None and bias.shape[0] != n:
+        raise ValueError(f"bias must have {n} elements, got {bias.shape[0]}")
+    return _HeadLinear.apply(x, weight, bias, residual, act, cap)
+
+
+def lmhead_logits(hidden: torch.Tensor, weight: torch.Tensor, bias=None, *, real_vocab: int,
+                  padded_vocab: int | None = None, cap: float | None = None, stream=None):
+    """bf16 logits [N, V_pad] of an LM-head, z = hidden . weight^T + bias or, with a cap,
+    cap tanh(z / cap), rounded once, as forward() and its kin take them (their rows are padded to
+    a multiple of 8 columns); columns [real_vocab, V_pad) are -inf.
+
+    hidden: bf16 [N, K] contiguous; weight: bf16 [>= real_vocab, K] contiguous; bias: bf16 or fp32
+    [>= real_vocab].  No gradient: fused_lmhead and head_linear have theirs."""
+    act, cap = _check_activation("none" if cap is None else "softcap", cap)
+    _check_linear(hidden, weight, real_vocab, bias)
+    v_pad = padded_vocab or weight.shape[0]
+    if not 1 <= real_vocab <= v_pad:
+        raise ValueError(f"real_vocab={real_vocab} outside [1, padded_vocab={v_pad}]")
+    return _run_linear(hidden, weight, bias, None, act, cap, real_vocab, v_pad, False, stream)[0]

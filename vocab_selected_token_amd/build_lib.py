@@ -18,7 +18,7 @@ CALIB = PKG / "rlk_calib"  # stream-ceiling probe the benchmark reports beside i
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 HIP_SOURCES = ["rlk_kernels", "rlk_lmhead", "rlk_lmhead_bwd", "rlk_fp8",
-               "rlk_noalloc"]
+               "rlk_noalloc", "rlk_process", "rlk_linear"]
 
 # -ffp-contract=off: only the explicit fmaf calls fuse, so every tile's
 # arithmetic is fixed by the source.  Packed fp32 VALU ops are disabled.

@@ -969,6 +969,404 @@ rlk_status rlk_logp_fused_lmhead_bwd(const rlk_logp_desc* desc, const void* hidd
   return ok();
 }
 
+// ---------------------------------------------------------------------------
+// What a sampler does to logits.
+// ---------------------------------------------------------------------------
+namespace {
+
+// 32-bit columns up to the end of the last block
+constexpr int64_t kMostColumns = kI32Max - 65536;
+
+rlk_status check_columns(int64_t padded) {
+  if (padded > kMostColumns)
+    return fail(RLK_ERR_BAD_SHAPE, "%lld padded columns exceed %lld", (long long)padded,
+                (long long)kMostColumns);
+  return RLK_OK;
+}
+
+// A table of a rule's rows: `name` for its detail texts.
+rlk_status check_table(const char* name, const void* table, int64_t rows, int64_t ld, int64_t least,
+                       const int32_t* index, int64_t n) {
+  if (!table) return RLK_OK;
+  if (rows < 1 || ld < least)
+    return fail(RLK_ERR_BAD_SHAPE, "%s: %lld rows of %lld, needs at least one of %lld", name,
+                (long long)rows, (long long)ld, (long long)least);
+  if (!index && rows != 1 && rows != n)
+    return fail(RLK_ERR_BAD_SHAPE, "%s without an index has %lld rows, neither 1 nor num_tokens="
+                                   "%lld", name, (long long)rows, (long long)n);
+  if (!aligned(table, 4) || !aligned(index, 4))
+    return fail(RLK_ERR_ALIGNMENT, "%s and its index must be 4-byte aligned", name);
+  return RLK_OK;
+}
+
+rlk_status check_rules(const rlk_logp_desc* d, const rlk_logit_rules* r, rlk::RuleArgs* out) {
+  if (!r) return fail(RLK_ERR_NULL_POINTER, "rules is NULL");
+  if (!aligned(r->repetition, 4) || !aligned(r->presence, 4) || !aligned(r->frequency, 4) ||
+      !aligned(r->temperature, 4) || !aligned(r->history, 4))
+    return fail(RLK_ERR_ALIGNMENT, "the penalties, the temperature and the history must be "
+                                   "4-byte aligned");
+  if (r->history) {
+    if (r->history_len < 0 || r->history_len > kI32Max)
+      return fail(RLK_ERR_BAD_SHAPE, "history_len=%lld outside [0, 2^31-1]",
+                  (long long)r->history_len);
+    if (!r->history_begin || !r->history_end)
+      return fail(RLK_ERR_NULL_POINTER, "a history needs history_begin and history_end");
+    if (!aligned(r->history_begin, 8) || !aligned(r->history_split, 8) ||
+        !aligned(r->history_end, 8))
+      return fail(RLK_ERR_ALIGNMENT, "the history's bounds must be 8-byte aligned");
+  }
+  rlk_status st = check_table("bias", r->bias, r->bias_rows, r->ld_bias, d->real_vocab,
+                              r->bias_index, d->num_tokens);
+  if (st != RLK_OK) return st;
+  st = check_table("allow", r->allow, r->allow_rows, r->ld_allow, (d->real_vocab + 31) / 32,
+                   r->allow_index, d->num_tokens);
+  if (st != RLK_OK) return st;
+  *out = rlk::RuleArgs{r->repetition,    r->presence,      r->frequency,   r->temperature,
+                       r->history,       r->history_len,   r->history_begin,
+                       r->history_split, r->history_end,   r->bias,        r->bias_rows,
+                       r->ld_bias,       r->bias_index,    r->allow,       r->allow_rows,
+                       r->ld_allow,      r->allow_index};
+  return RLK_OK;
+}
+
+rlk_status check_dtype(rlk_dtype t, const char* name) {
+  if (t != RLK_DTYPE_F32 && t != RLK_DTYPE_BF16)
+    return fail(RLK_ERR_DTYPE, "%s=%d is neither RLK_DTYPE_F32 nor RLK_DTYPE_BF16", name, (int)t);
+  return RLK_OK;
+}
+
+rlk_status check_out(const rlk_logp_desc* d, int64_t ld, const char* name) {
+  if (ld < d->padded_vocab)
+    return fail(RLK_ERR_BAD_SHAPE, "%s=%lld < padded_vocab=%lld", name, (long long)ld,
+                (long long)d->padded_vocab);
+  if (ld % 8 != 0)
+    return fail(RLK_ERR_ALIGNMENT, "%s=%lld is not a multiple of 8 elements", name, (long long)ld);
+  return RLK_OK;
+}
+
+struct ProcessedLayout {
+  size_t pmax, psum, target_logit, total;
+};
+
+int64_t pieces_of(const rlk_logp_desc* d) {
+  return (d->real_vocab + rlk::kProcessPiece - 1) / rlk::kProcessPiece;
+}
+
+ProcessedLayout processed_layout(const rlk_logp_desc* d) {
+  const size_t n = (size_t)d->num_tokens, part = round256(n * (size_t)pieces_of(d) * sizeof(float));
+  ProcessedLayout l;
+  l.pmax = kStatusBytes;
+  l.psum = l.pmax + part;
+  l.target_logit = l.psum + part;
+  l.total = l.target_logit + round256(n * sizeof(float));
+  return l;
+}
+
+rlk_status check_processed_desc(const rlk_logp_desc* d) {
+  const rlk_status st = check_desc(d);
+  return st != RLK_OK ? st : check_columns(d->padded_vocab);
+}
+
+rlk::ProcessedArgs processed_args(const rlk_logp_desc* d, const void* logits,
+                                  const int32_t* targets, const uint8_t* active_mask,
+                                  void* workspace) {
+  rlk::ProcessedArgs a{};
+  a.logits = logits;
+  a.ld = d->ld_logits;
+  a.num_rows = (int32_t)d->num_tokens;
+  a.real_vocab = (int32_t)d->real_vocab;
+  a.padded_vocab = (int32_t)d->padded_vocab;
+  a.pieces = (int32_t)pieces_of(d);
+  a.targets = targets;
+  a.mask = active_mask;
+  a.ignore_index = d->ignore_index;
+  a.status = reinterpret_cast<uint32_t*>(workspace);
+  return a;
+}
+
+}  // namespace
+
+rlk_status rlk_logits_process(const rlk_logp_desc* desc, const void* logits,
+                              const rlk_logit_rules* rules, void* out, int64_t ld_out,
+                              rlk_dtype out_dtype, void* stream_ptr) {
+  rlk_status st = check_processed_desc(desc);
+  if (st != RLK_OK) return st;
+  if (desc->flags) return fail(RLK_ERR_BAD_SHAPE, "logits have no data errors to validate");
+  st = check_dtype(out_dtype, "out_dtype");
+  if (st != RLK_OK) return st;
+  st = check_out(desc, ld_out, "ld_out");
+  if (st != RLK_OK) return st;
+  rlk::RuleArgs r;
+  st = check_rules(desc, rules, &r);
+  if (st != RLK_OK) return st;
+  if (desc->num_tokens == 0) return ok();
+  if (!logits || !out) return fail(RLK_ERR_NULL_POINTER, "logits and out must be non-NULL");
+  if (!aligned(logits, 16) || !aligned(out, 16))
+    return fail(RLK_ERR_ALIGNMENT, "logits and out must be 16-byte aligned");
+  if (logits == out && (out_dtype != RLK_DTYPE_BF16 || ld_out != desc->ld_logits))
+    return fail(RLK_ERR_BAD_SHAPE, "out can be logits only in bf16 with the same ld");
+  const hipError_t e = rlk::launch_process(
+      logits, desc->ld_logits, (int32_t)desc->num_tokens, (int32_t)desc->real_vocab,
+      (int32_t)desc->padded_vocab, r, out, ld_out, out_dtype == RLK_DTYPE_BF16,
+      reinterpret_cast<hipStream_t>(stream_ptr));
+  if (e != hipSuccess) return hip_fail(e, "process_rows launch");
+  return ok();
+}
+
+size_t rlk_logp_processed_workspace_bytes(const rlk_logp_desc* desc) {
+  if (check_processed_desc(desc) != RLK_OK) return 0;
+  return processed_layout(desc).total;
+}
+
+rlk_status rlk_logp_processed_fwd(const rlk_logp_desc* desc, const void* logits,
+                                  const rlk_logit_rules* rules, const int32_t* targets,
+                                  const uint8_t* active_mask, float* logp, float* lse,
+                                  void* workspace, size_t workspace_bytes, void* stream_ptr) {
+  rlk_status st = check_processed_desc(desc);
+  if (st != RLK_OK) return st;
+  rlk::RuleArgs r;
+  st = check_rules(desc, rules, &r);
+  if (st != RLK_OK) return st;
+  if (desc->num_tokens == 0) return ok();
+  if (!logits || !targets || !logp || !lse)
+    return fail(RLK_ERR_NULL_POINTER, "logits, targets, logp and lse must be non-NULL");
+  const ProcessedLayout lay = processed_layout(desc);
+  if (!workspace) return fail(RLK_ERR_WORKSPACE, "workspace is NULL");
+  if (workspace_bytes < lay.total)
+    return fail(RLK_ERR_WORKSPACE, "workspace_bytes=%zu < required %zu", workspace_bytes,
+                lay.total);
+  if (!aligned(logits, 16)) return fail(RLK_ERR_ALIGNMENT, "logits not 16-byte aligned");
+  if (!aligned(workspace, 256)) return fail(RLK_ERR_ALIGNMENT, "workspace not 256-byte aligned");
+  if (!aligned(targets, 4) || !aligned(logp, 4) || !aligned(lse, 4))
+    return fail(RLK_ERR_ALIGNMENT, "targets, logp and lse must be 4-byte aligned");
+  hipStream_t stream = reinterpret_cast<hipStream_t>(stream_ptr);
+  const bool validate = (desc->flags & RLK_FLAG_VALIDATE) != 0;
+  rlk::ProcessedArgs a = processed_args(desc, logits, targets, active_mask, workspace);
+  char* ws = static_cast<char*>(workspace);
+  a.pmax = reinterpret_cast<float*>(ws + lay.pmax);
+  a.psum = reinterpret_cast<float*>(ws + lay.psum);
+  a.target_logit = reinterpret_cast<float*>(ws + lay.target_logit);
+  a.logp = logp;
+  a.lse = lse;
+  hipError_t e;
+  if (validate) {
+    e = rlk::launch_clear_status(a.status, stream);
+    if (e != hipSuccess) return hip_fail(e, "clear_status launch");
+  }
+  e = rlk::launch_processed_fwd(a, r, stream);
+  if (e != hipSuccess) return hip_fail(e, "processed_stats launch");
+  if (validate) return finish_validate(a.status, stream, true);
+  return ok();
+}
+
+rlk_status rlk_logp_processed_bwd(const rlk_logp_desc* desc, const void* logits,
+                                  const rlk_logit_rules* rules, const int32_t* targets,
+                                  const uint8_t* active_mask, const float* lse,
+                                  const float* grad_logp, const float* grad_lse, void* dlogits,
+                                  int64_t ld_dlogits, rlk_dtype dlogits_dtype, void* workspace,
+                                  size_t workspace_bytes, void* stream_ptr) {
+  rlk_status st = check_processed_desc(desc);
+  if (st != RLK_OK) return st;
+  st = check_dtype(dlogits_dtype, "dlogits_dtype");
+  if (st != RLK_OK) return st;
+  st = check_out(desc, ld_dlogits, "ld_dlogits");
+  if (st != RLK_OK) return st;
+  rlk::RuleArgs r;
+  st = check_rules(desc, rules, &r);
+  if (st != RLK_OK) return st;
+  if (desc->num_tokens == 0) return ok();
+  if (!logits || !targets || !lse || !dlogits)
+    return fail(RLK_ERR_NULL_POINTER, "logits, targets, lse and dlogits must be non-NULL");
+  if (logits == dlogits)  // (a block may write what another still reads)
+    return fail(RLK_ERR_BAD_SHAPE, "dlogits cannot be logits");
+  if (!grad_logp && !grad_lse)
+    return fail(RLK_ERR_NULL_POINTER, "at least one of grad_logp and grad_lse must be non-NULL");
+  if (!workspace) return fail(RLK_ERR_WORKSPACE, "workspace is NULL");
+  if (workspace_bytes < kStatusBytes)
+    return fail(RLK_ERR_WORKSPACE, "workspace_bytes=%zu < %zu", workspace_bytes, kStatusBytes);
+  if (!aligned(logits, 16) || !aligned(dlogits, 16))
+    return fail(RLK_ERR_ALIGNMENT, "logits and dlogits must be 16-byte aligned");
+  if (!aligned(workspace, 256)) return fail(RLK_ERR_ALIGNMENT, "workspace not 256-byte aligned");
+  if (!aligned(targets, 4) || !aligned(lse, 4) || !aligned(grad_logp, 4) || !aligned(grad_lse, 4))
+    return fail(RLK_ERR_ALIGNMENT, "targets, lse and the gradients must be 4-byte aligned");
+  hipStream_t stream = reinterpret_cast<hipStream_t>(stream_ptr);
+  const bool validate = (desc->flags & RLK_FLAG_VALIDATE) != 0;
+  rlk::ProcessedArgs a = processed_args(desc, logits, targets, active_mask, workspace);
+  a.lse = const_cast<float*>(lse);
+  a.grad = grad_logp;
+  a.grad_lse = grad_lse;
+  hipError_t e;
+  if (validate) {
+    e = rlk::launch_clear_status(a.status, stream);
+    if (e != hipSuccess) return hip_fail(e, "clear_status launch");
+  }
+  e = rlk::launch_processed_bwd(a, r, dlogits, ld_dlogits, dlogits_dtype == RLK_DTYPE_BF16,
+                                stream);
+  if (e != hipSuccess) return hip_fail(e, "processed_grad launch");
+  if (validate) return finish_validate(a.status, stream, false);
+  return ok();
+}
+
+// ---------------------------------------------------------------------------
+// Dense products with their epilogue.
+// ---------------------------------------------------------------------------
+namespace {
+
+rlk_status check_linear(const rlk_linear_desc* d, bool backward) {
+  if (!d) return fail(RLK_ERR_NULL_POINTER, "desc is NULL");
+  if (d->tokens < 0 || d->tokens > kMostColumns)
+    return fail(RLK_ERR_BAD_SHAPE, "tokens=%lld outside [0, %lld]", (long long)d->tokens,
+                (long long)kMostColumns);
+  rlk_status st = check_hidden_dim(d->in_dim, rlk::kLmheadSlabK);
+  if (st != RLK_OK) return st;
+  if (d->out_dim < 1 || d->out_dim > (backward ? rlk::kLinearMaxOut : kMostColumns))
+    return fail(RLK_ERR_BAD_SHAPE, "out_dim=%lld outside its range", (long long)d->out_dim);
+  if (d->activation < RLK_ACT_NONE || d->activation > RLK_ACT_SOFTCAP)
+    return fail(RLK_ERR_BAD_SHAPE, "activation=%d is not an rlk_activation", d->activation);
+  if (d->activation == RLK_ACT_SOFTCAP && !(d->cap > 0.0f && d->cap <= 3.0e38f))
+    return fail(RLK_ERR_BAD_SHAPE, "cap=%g must be finite and positive", (double)d->cap);
+  return RLK_OK;
+}
+
+rlk_status check_saved(const rlk_linear_desc* d, const void* saved) {
+  if (d->ld_saved < d->out_dim)
+    return fail(RLK_ERR_BAD_SHAPE, "ld_saved=%lld < out_dim=%lld", (long long)d->ld_saved,
+                (long long)d->out_dim);
+  if (d->saved_dtype != RLK_DTYPE_F16 && d->saved_dtype != RLK_DTYPE_F32)
+    return fail(RLK_ERR_DTYPE, "saved_dtype=%d is neither RLK_DTYPE_F16 nor RLK_DTYPE_F32",
+                d->saved_dtype);
+  if (d->ld_saved % 8 != 0 || !aligned(saved, 16))
+    return fail(RLK_ERR_ALIGNMENT, "saved must be 16-byte aligned, ld_saved=%lld a multiple of 8",
+                (long long)d->ld_saved);
+  return RLK_OK;
+}
+
+rlk_status check_bias(const rlk_linear_desc* d, const void* bias) {
+  if (!bias) return RLK_OK;
+  const rlk_status st = check_dtype((rlk_dtype)d->bias_dtype, "bias_dtype");
+  if (st != RLK_OK) return st;
+  if (!aligned(bias, d->bias_dtype == RLK_DTYPE_BF16 ? 2 : 4))
+    return fail(RLK_ERR_ALIGNMENT, "the bias must be aligned to its elements");
+  return RLK_OK;
+}
+
+rlk::LinearArgs linear_args(const rlk_linear_desc* d, const void* x, const void* weight) {
+  rlk::LinearArgs a{};
+  a.x = x;
+  a.weight = weight;
+  a.bias_bf16 = d->bias_dtype == RLK_DTYPE_BF16;
+  a.tokens = (int32_t)d->tokens;
+  a.in_dim = (int32_t)d->in_dim;
+  a.out_dim = (int32_t)d->out_dim;
+  a.activation = d->activation;
+  a.cap = d->activation == RLK_ACT_SOFTCAP ? d->cap : 1.0f;
+  a.ld_saved = d->ld_saved;
+  a.saved_f32 = d->saved_dtype == RLK_DTYPE_F32;
+  return a;
+}
+
+}  // namespace
+
+rlk_status rlk_linear_fwd(const rlk_linear_desc* desc, const void* x, const void* weight,
+                          const void* bias, const void* residual, void* out, void* saved,
+                          void* stream_ptr) {
+  rlk_status st = check_linear(desc, false);
+  if (st != RLK_OK) return st;
+  if (desc->padded_out < desc->out_dim)
+    return fail(RLK_ERR_BAD_SHAPE, "padded_out=%lld < out_dim=%lld", (long long)desc->padded_out,
+                (long long)desc->out_dim);
+  st = check_columns(desc->padded_out);
+  if (st != RLK_OK) return st;
+  if (desc->ld_out < desc->padded_out)
+    return fail(RLK_ERR_BAD_SHAPE, "ld_out=%lld < padded_out=%lld", (long long)desc->ld_out,
+                (long long)desc->padded_out);
+  if (desc->ld_out % 8 != 0)
+    return fail(RLK_ERR_ALIGNMENT, "ld_out=%lld is not a multiple of 8 elements",
+                (long long)desc->ld_out);
+  st = check_bias(desc, bias);
+  if (st != RLK_OK) return st;
+  if (saved) {
+    st = check_saved(desc, saved);
+    if (st != RLK_OK) return st;
+  }
+  if (residual && desc->ld_residual < desc->out_dim)
+    return fail(RLK_ERR_BAD_SHAPE, "ld_residual=%lld < out_dim=%lld",
+                (long long)desc->ld_residual, (long long)desc->out_dim);
+  if (desc->tokens == 0) return ok();
+  if (!x || !weight || !out)
+    return fail(RLK_ERR_NULL_POINTER, "x, weight and out must be non-NULL");
+  if (!aligned(x, 16) || !aligned(weight, 16) || !aligned(out, 16))
+    return fail(RLK_ERR_ALIGNMENT, "x, weight and out must be 16-byte aligned");
+  if (!aligned(residual, 2)) return fail(RLK_ERR_ALIGNMENT, "residual must be 2-byte aligned");
+  if (out == residual || out == x || out == weight)
+    return fail(RLK_ERR_BAD_SHAPE, "out cannot be one of the inputs");
+  rlk::LinearArgs a = linear_args(desc, x, weight);
+  a.bias = bias;
+  a.residual = residual;
+  a.ld_residual = desc->ld_residual;
+  a.padded_out = (int32_t)desc->padded_out;
+  a.out = out;
+  a.ld_out = desc->ld_out;
+  a.saved = saved;
+  const hipError_t e = rlk::launch_linear_fwd(a, reinterpret_cast<hipStream_t>(stream_ptr));
+  if (e != hipSuccess) return hip_fail(e, "linear launch");
+  return ok();
+}
+
+size_t rlk_linear_bwd_workspace_bytes(const rlk_linear_desc* desc) {
+  if (check_linear(desc, true) != RLK_OK) return 0;
+  return rlk::linear_bwd_layout(desc->tokens, desc->in_dim, desc->out_dim).total;
+}
+
+rlk_status rlk_linear_bwd(const rlk_linear_desc* desc, const void* x, const void* weight,
+                          const void* saved, const void* grad_out, int64_t ld_grad, void* dx,
+                          void* dweight, void* dbias, void* workspace, size_t workspace_bytes,
+                          void* stream_ptr) {
+  rlk_status st = check_linear(desc, true);
+  if (st != RLK_OK) return st;
+  st = check_bias(desc, dbias);
+  if (st != RLK_OK) return st;
+  if (ld_grad < desc->out_dim)
+    return fail(RLK_ERR_BAD_SHAPE, "ld_grad=%lld < out_dim=%lld", (long long)ld_grad,
+                (long long)desc->out_dim);
+  const bool need_saved = desc->activation != RLK_ACT_NONE;
+  if (desc->tokens > 0) {  // (empty tensors have no address)
+    if (!x || !weight || !grad_out)
+      return fail(RLK_ERR_NULL_POINTER, "x, weight and grad_out must be non-NULL");
+    if (!dx && !dweight && !dbias)
+      return fail(RLK_ERR_NULL_POINTER, "at least one of dx, dweight and dbias must be non-NULL");
+    if (need_saved && !saved)
+      return fail(RLK_ERR_NULL_POINTER, "this activation's gradient needs what the forward saved");
+    if (need_saved) {
+      st = check_saved(desc, saved);
+      if (st != RLK_OK) return st;
+    }
+  }
+  if (!aligned(x, 16) || !aligned(weight, 16) || !aligned(dx, 16) || !aligned(dweight, 16))
+    return fail(RLK_ERR_ALIGNMENT, "x, weight, dx and dweight must be 16-byte aligned");
+  if (!aligned(grad_out, 2)) return fail(RLK_ERR_ALIGNMENT, "grad_out must be 2-byte aligned");
+  const rlk::LinearBwdLayout lay =
+      rlk::linear_bwd_layout(desc->tokens, desc->in_dim, desc->out_dim);
+  if (!workspace) return fail(RLK_ERR_WORKSPACE, "workspace is NULL");
+  if (workspace_bytes < lay.total)
+    return fail(RLK_ERR_WORKSPACE, "workspace_bytes=%zu < required %zu", workspace_bytes,
+                lay.total);
+  if (!aligned(workspace, 256)) return fail(RLK_ERR_ALIGNMENT, "workspace not 256-byte aligned");
+  rlk::LinearBwdArgs a{};
+  a.f = linear_args(desc, x, weight);
+  a.f.saved = need_saved ? const_cast<void*>(saved) : nullptr;
+  a.dy = grad_out;
+  a.ld_dy = ld_grad;
+  a.dx = desc->tokens > 0 ? dx : nullptr;
+  a.dweight = dweight;
+  a.dbias = dbias;
+  a.workspace = static_cast<char*>(workspace);
+  a.layout = lay;
+  const hipError_t e = rlk::launch_linear_bwd(a, reinterpret_cast<hipStream_t>(stream_ptr));
+  if (e != hipSuccess) return hip_fail(e, "linear_bwd launch");
+  return ok();
+}
+
 const char* rlk_status_string(rlk_status s) {
   switch (s) {
     case RLK_OK: return "RLK_OK";

@@ -585,24 +585,12 @@ __global__ __launch_bounds__(128) void segments_of_z(ZOut zo, SegmentArgs a, int
   write_segments<1>(a, acc, xch, vb, t0, wv, 0, lane);
 }
 
-// Launches `blocks` blocks in pieces of at most the launch limit.
-template <typename F>
-hipError_t in_launches(int64_t blocks, int threads, F&& launch) {
-  const int64_t most = launch_thread_limit() / threads;
-  for (int64_t b = 0; b < blocks; b += most) {
-    launch(b, dim3((unsigned)(blocks - b < most ? blocks - b : most)));
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
-}
-
 template <bool kLogits, int kTok>
 hipError_t launch_stream(const Fp8Operands& p, const SegmentArgs& sa, const LogitsOut& lo,
                          const ZOut& zo, int32_t v_begin, int32_t columns, hipStream_t stream) {
-  return in_launches(columns / kStreamRows, kStreamThreads, [&](int64_t b, dim3 grid) {
-    hipLaunchKernelGGL((fp8_stream<kLogits, kTok>), grid, dim3(kStreamThreads), 0, stream, p, sa, lo, zo,
-                       v_begin, b);
+  return in_launches(columns / kStreamRows, kStreamThreads, [&](int64_t b, int64_t nb) {
+    hipLaunchKernelGGL((fp8_stream<kLogits, kTok>), dim3((unsigned)nb), dim3(kStreamThreads), 0,
+                       stream, p, sa, lo, zo, v_begin, b);
   });
 }
 
@@ -610,9 +598,9 @@ template <bool kLogits, int kTok>
 hipError_t launch_tile(const Fp8Operands& p, const SegmentArgs& sa, const LogitsOut& lo,
                        int32_t vb_begin, int32_t n_vbs, hipStream_t stream) {
   const int32_t n_tb = (sa.num_tokens + 64 * kTok - 1) / (64 * kTok);
-  return in_launches((int64_t)n_vbs * n_tb, kThreads, [&](int64_t b, dim3 grid) {
-    hipLaunchKernelGGL((fp8_tile<kLogits, kTok>), grid, dim3(kThreads), 0, stream, p, sa, lo,
-                       n_tb, vb_begin, n_vbs, b);
+  return in_launches((int64_t)n_vbs * n_tb, kThreads, [&](int64_t b, int64_t nb) {
+    hipLaunchKernelGGL((fp8_tile<kLogits, kTok>), dim3((unsigned)nb), dim3(kThreads), 0, stream,
+                       p, sa, lo, n_tb, vb_begin, n_vbs, b);
   });
 }
 
@@ -648,8 +636,9 @@ hipError_t launch_product(const Fp8Operands& p, const SegmentArgs& sa, const Log
     e = launch_stream<kLogits, 4>(p, sa, lo, zo, v, columns, stream);
   if (e != hipSuccess || kLogits) return e;
   const int32_t n_tg = (n + 15) / 16;
-  return in_launches((int64_t)n_vbs * n_tg, 128, [&](int64_t b, dim3 grid) {
-    hipLaunchKernelGGL(segments_of_z, grid, dim3(128), 0, stream, zo, sa, vb_begin, n_tg, b);
+  return in_launches((int64_t)n_vbs * n_tg, 128, [&](int64_t b, int64_t nb) {
+    hipLaunchKernelGGL(segments_of_z, dim3((unsigned)nb), dim3(128), 0, stream, zo, sa, vb_begin,
+                       n_tg, b);
   });
 }
 
@@ -669,13 +658,13 @@ hipError_t launch_fp8_quantize(const Fp8QuantizeArgs& a, hipStream_t stream) {
                              : (a.rows * col_blocks + 16 * kRowBlocks - 1) / (16 * kRowBlocks);
   const u32x4* x = reinterpret_cast<const u32x4*>(a.x);
   uint64_t* q = reinterpret_cast<uint64_t*>(a.q);
-  return in_launches(items, 256, [&](int64_t b, dim3 grid) {
+  return in_launches(items, 256, [&](int64_t b, int64_t nb) {
     if (wide)
-      hipLaunchKernelGGL(quantize_blocks, grid, dim3(256), 0, stream, x, a.ld / 8, a.rows,
-                         col_blocks, q, a.scale, a.scale_row_stride, a.scale_col_stride, b);
+      hipLaunchKernelGGL(quantize_blocks, dim3((unsigned)nb), dim3(256), 0, stream, x, a.ld / 8,
+                         a.rows, col_blocks, q, a.scale, a.scale_row_stride, a.scale_col_stride, b);
     else
-      hipLaunchKernelGGL(quantize_rows, grid, dim3(256), 0, stream, x, a.ld / 8, a.rows,
-                         col_blocks, q, a.scale, a.scale_row_stride, a.scale_col_stride, b);
+      hipLaunchKernelGGL(quantize_rows, dim3((unsigned)nb), dim3(256), 0, stream, x, a.ld / 8,
+                         a.rows, col_blocks, q, a.scale, a.scale_row_stride, a.scale_col_stride, b);
   });
 }
 

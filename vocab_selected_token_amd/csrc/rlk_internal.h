@@ -216,6 +216,86 @@ struct LmheadBwdArgs {
   uint32_t* status;
 };
 
+// What a sampler does to logits (rlk_logits_rules).
+struct RuleArgs {
+  const float* repetition;  // [num_rows] each, or null: 1, 0, 0, 1
+  const float* presence;
+  const float* frequency;
+  const float* temperature;
+  const int32_t* history;  // null: none
+  int64_t history_len;
+  const int64_t* history_begin;  // [num_rows]
+  const int64_t* history_split;  // null: no prompt
+  const int64_t* history_end;
+  const float* bias;  // [bias_rows][ld_bias], or null
+  int64_t bias_rows, ld_bias;
+  const int32_t* bias_index;  // null: row r, or the only one
+  const uint32_t* allow;  // [allow_rows][ld_allow], a bit per column, or null
+  int64_t allow_rows, ld_allow;
+  const int32_t* allow_index;
+};
+
+constexpr int32_t kProcessPiece = 2048;  // columns whose statistics are one partial
+
+struct ProcessedArgs {
+  const void* logits;  // bf16 [num_rows, ld]
+  int64_t ld;
+  int32_t num_rows;
+  int32_t real_vocab;
+  int32_t padded_vocab;
+  int32_t pieces;  // ceil(real_vocab / kProcessPiece)
+  const int32_t* targets;
+  const uint8_t* mask;  // may be null
+  int32_t ignore_index;
+  float* pmax;  // [num_rows][pieces]
+  float* psum;
+  float* target_logit;  // [num_rows]
+  float* logp;
+  float* lse;
+  const float* grad;      // null = zero
+  const float* grad_lse;  // null = zero
+  uint32_t* status;
+};
+
+// A dense product with its epilogue: out = residual + act(x . weight^T + bias).
+enum Activation : int32_t { kActNone, kActRelu, kActGelu, kActGeluTanh, kActSilu, kActSoftcap };
+constexpr int64_t kLinearMaxOut = int64_t{1} << 21;  // with a backward pass
+
+struct LinearArgs {
+  const void* x;       // bf16 [tokens, in_dim]
+  const void* weight;  // bf16 [out_dim, in_dim]
+  const void* bias;    // [out_dim], or null
+  bool bias_bf16;
+  const void* residual;  // bf16 [tokens, ld_residual], or null
+  int64_t ld_residual;
+  int32_t tokens, in_dim, out_dim, padded_out;
+  int32_t activation;
+  float cap;
+  void* out;  // bf16 [tokens, ld_out]
+  int64_t ld_out;
+  void* saved;  // fp16 or float [tokens, ld_saved], or null
+  bool saved_f32;
+  int64_t ld_saved;
+};
+
+// Byte offsets into the workspace of the backward pass.
+struct LinearBwdLayout {
+  int32_t rows, cols;  // of dz: tokens and out_dim rounded up to 64
+  int32_t row_blocks;  // partials of the bias' gradient
+  size_t dz, x_tail, w_tail, bias_part, total;
+};
+
+struct LinearBwdArgs {
+  LinearArgs f;   // x, weight, sizes, activation, saved
+  const void* dy;  // bf16 [tokens, ld_dy]
+  int64_t ld_dy;
+  void* dx;       // bf16 [tokens, in_dim], or null
+  void* dweight;  // bf16 [out_dim, in_dim], or null
+  void* dbias;    // [out_dim], or null
+  char* workspace;
+  LinearBwdLayout layout;
+};
+
 // Most threads one launch may have.  A dispatch holds its grid size in 32 bits
 // of threads: at 2^32 the launch fails, and above it the size wraps around and
 // the kernel silently runs on a fraction of the grid.  Every launcher splits
@@ -223,6 +303,19 @@ struct LmheadBwdArgs {
 // RLK_MAX_LAUNCH_THREADS environment variable says so at the process's first
 // launch -- a hook for tests, which check that any split gives the same bits).
 int64_t launch_thread_limit();
+
+// Launches `blocks` blocks of `threads` in pieces of at most that limit: launch(first block,
+// how many).
+template <typename F>
+hipError_t in_launches(int64_t blocks, int threads, F&& launch) {
+  const int64_t most = launch_thread_limit() / threads;
+  for (int64_t b = 0; b < blocks; b += most) {
+    launch(b, blocks - b < most ? blocks - b : most);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
 
 // The allocation-free forward's workspace: a device array of the library's own,
 // one per GPU, of this many bytes (status words plus 2 * N * T fp32 partials:
@@ -270,6 +363,15 @@ hipError_t launch_stage1(const Stage1Args& a, hipStream_t stream);
 hipError_t launch_stage2(const Stage2Args& a, hipStream_t stream);
 hipError_t launch_bwd(const BwdArgs& a, hipStream_t stream);
 hipError_t launch_fwd_bwd(const FwdBwdArgs& a, hipStream_t stream);
+hipError_t launch_process(const void* logits, int64_t ld, int32_t num_rows, int32_t real_vocab,
+                          int32_t padded_vocab, const RuleArgs& rules, void* out, int64_t ld_out,
+                          bool out_bf16, hipStream_t stream);
+hipError_t launch_processed_fwd(const ProcessedArgs& a, const RuleArgs& rules, hipStream_t stream);
+hipError_t launch_processed_bwd(const ProcessedArgs& a, const RuleArgs& rules, void* dlogits,
+                                int64_t ld_d, bool out_bf16, hipStream_t stream);
+hipError_t launch_linear_fwd(const LinearArgs& a, hipStream_t stream);
+LinearBwdLayout linear_bwd_layout(int64_t tokens, int64_t in_dim, int64_t out_dim);
+hipError_t launch_linear_bwd(const LinearBwdArgs& a, hipStream_t stream);
 hipError_t launch_clear_status(uint32_t* status, hipStream_t stream);
 
 }  // namespace rlk

@@ -1,0 +1,667 @@
+// rlk_linear.hip -- dense products with bias, activation and residual in the epilogue, and
+// their gradients, for gfx950:
+//   z = x . W^T + b,   y = residual + act(z)
+//   dz = dy act'(z),   dx = dz . W,   dW = dz^T . x,   db = sum over tokens of dz
+// (the residual's gradient is dy).  y is rounded to bf16 once; z, the activation and the
+// residual's sum are fp32.
+//
+// The tile product of rlk_tile.h does the work: W's rows as operand A and x's as B give
+// C[out][token], so that a lane holds 4 consecutive outputs of one token.  Up to 64 tokens
+// linear_few streams the weight instead.
+//
+// What the backward pass needs of z (z / cap for the soft cap) is kept in fp16, for its 11 bits,
+// clamped to +-65504, where every activation here has reached its last slope: the rounding,
+// 2^-11 relative, moves act'(z) by a fraction of what rounding dz to bf16 does.  A bias in
+// fp32 has a gradient in fp32, which that rounding would show in (1e-4 relative): z is kept in
+// fp32 then.
+//
+// Sums are fp32 in a fixed order: repeated calls give the same bits.  No atomics.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "rlk_internal.h"
+#include "rlk_rows.h"
+#include "rlk_tile.h"
+
+namespace rlk {
+namespace {
+
+static_assert(kBK == kLmheadSlabK, "slab width shared with the boundary");
+
+typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ float bf16_float(uint16_t b) {
+  return __uint_as_float((uint32_t)b << 16);
+}
+__device__ __forceinline__ float rcp_hw(float x) { return __builtin_amdgcn_rcpf(x); }
+
+// ---------------------------------------------------------------------------
+// The activations.  exp2 and the reciprocal are the hardware's (1 step of fp32), which
+// rounding to bf16 hides.
+// ---------------------------------------------------------------------------
+constexpr float kGeluC = 0.7978845608028654f;       // sqrt(2 / pi)
+constexpr float kGeluA = 0.044715f;
+constexpr float kInvSqrt2Pi = 0.3989422804014327f;
+
+__device__ __forceinline__ float sigmoid(float z) {
+  return rcp_hw(1.0f + exp2_hw(-z * kLog2e));
+}
+// The normal distribution's Phi(z).
+__device__ __forceinline__ float normal_cdf(float z) {
+  return 0.5f * erfcf(z * -0.7071067811865476f);
+}
+// tanh: below 2^-6 its series (the next term is 2/15 u^4 < 2^-26 of it), where 1 - e would
+// cancel.
+__device__ __forceinline__ float tanh_of(float u) {
+  const float a = fabsf(u), e = exp2_hw(a * (-2.0f * kLog2e));
+  const float t = a < 0.015625f ? fmaf(a * a * a, -1.0f / 3.0f, a) : (1.0f - e) * rcp_hw(1.0f + e);
+  return copysignf(t, u);
+}
+
+template <int kAct>
+__device__ __forceinline__ float act_of(float z, float cap, float inv_cap) {
+  if constexpr (kAct == kActRelu) return z < 0.0f ? 0.0f : z;  // (NaN stays)
+  if constexpr (kAct == kActSilu) return z * sigmoid(z);
+  if constexpr (kAct == kActGelu) return z * normal_cdf(z);
+  if constexpr (kAct == kActGeluTanh)  // (1 + tanh(u)) / 2 = sigmoid(2u)
+    return z * sigmoid(2.0f * kGeluC * (z + kGeluA * z * z * z));
+  if constexpr (kAct == kActSoftcap) return cap * tanh_of(z * inv_cap);
+  return z;
+}
+
+// act'(z) from what was kept: z, or z / cap.
+__device__ __forceinline__ float slope_of(int act, float z) {
+  switch (act) {
+    case kActRelu: return z > 0.0f ? 1.0f : 0.0f;
+    case kActSilu: {
+      const float s = sigmoid(z);
+      return s * (1.0f + z * (1.0f - s));
+    }
+    case kActGelu: return normal_cdf(z) + z * kInvSqrt2Pi * exp2_hw(-0.5f * kLog2e * z * z);
+    case kActGeluTanh: {
+      const float s = sigmoid(2.0f * kGeluC * (z + kGeluA * z * z * z));
+      return s + z * s * (1.0f - s) * 2.0f * kGeluC * (1.0f + 3.0f * kGeluA * z * z);
+    }
+    case kActSoftcap: {  // 1 - tanh^2, without the difference
+      const float e = exp2_hw(fabsf(z) * (-2.0f * kLog2e)), r = rcp_hw(1.0f + e);
+      return 4.0f * e * r * r;
+    }
+  }
+  return 1.0f;
+}
+
+__device__ __forceinline__ uint16_t fp16_bits(float z) {
+  const _Float16 h = (_Float16)(z > 65504.0f ? 65504.0f : z < -65504.0f ? -65504.0f : z);
+  return __builtin_bit_cast(uint16_t, h);
+}
+
+// finish(act): the call's activation, one for all of its outputs.
+template <typename Finish>
+__device__ __forceinline__ void with_activation(const LinearArgs& a, Finish&& finish) {
+  const float cap = a.cap, inv_cap = 1.0f / a.cap;
+  switch (a.activation) {
+    case kActRelu: return finish([](float z) { return act_of<kActRelu>(z, 0.0f, 0.0f); });
+    case kActGelu: return finish([](float z) { return act_of<kActGelu>(z, 0.0f, 0.0f); });
+    case kActGeluTanh: return finish([](float z) { return act_of<kActGeluTanh>(z, 0.0f, 0.0f); });
+    case kActSilu: return finish([](float z) { return act_of<kActSilu>(z, 0.0f, 0.0f); });
+    case kActSoftcap:
+      return finish([=](float z) { return act_of<kActSoftcap>(z, cap, inv_cap); });
+  }
+  finish([](float z) { return z; });
+}
+
+// The bias of 4 consecutive outputs (0 from out_dim on).
+__device__ __forceinline__ f32x4 bias_of(const LinearArgs& a, int32_t n) {
+  f32x4 b = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (!a.bias) return b;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (n + e < a.out_dim)
+      b[e] = a.bias_bf16 ? bf16_float(static_cast<const uint16_t*>(a.bias)[n + e])
+                         : static_cast<const float*>(a.bias)[n + e];
+  return b;
+}
+
+constexpr uint16_t kNegInfBf16 = 0xFF80;
+
+// 8 outputs of a token from output n on: those behind out_dim are -inf up to padded_out.
+__device__ __forceinline__ void put_out(const LinearArgs& a, int32_t m, int32_t n,
+                                        const u32x4& x) {
+  if (m >= a.tokens || n >= a.padded_out) return;
+  uint16_t* out = static_cast<uint16_t*>(a.out) + m * a.ld_out + n;
+  union {
+    u32x4 x;
+    uint16_t e[8];
+  } o;
+  o.x = x;
+  if (n + 8 > a.out_dim) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (n + e >= a.out_dim) o.e[e] = kNegInfBf16;
+  }
+  if (n + 8 <= a.padded_out) {
+    *reinterpret_cast<u32x4*>(out) = o.x;
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (n + e < a.padded_out) out[e] = o.e[e];
+}
+
+// ---------------------------------------------------------------------------
+// linear_tiles: 32 kVSn outputs x 16 kTok kWB tokens a block.
+// ---------------------------------------------------------------------------
+template <int kVSn, int kTok, int kWB>
+struct Shape {
+  static constexpr int kA = 32 * kVSn, kB = 16 * kTok * kWB;
+  static constexpr int kWavesN = 2 * kWB, kThr = 64 * kWavesN;
+  static constexpr int kLds = 2 * (kA + kB) * kRowBytes;
+  static constexpr int kOwn = 512 * kVSn * kTok;  // bytes of a wave's rows
+  static_assert(kLds >= kWavesN * kOwn, "the rows fit");
+  typedef TileOperandOf<kA / (kWavesN * kRowsPerLoad)> OperandA;
+  typedef TileOperandOf<kB / (kWavesN * kRowsPerLoad)> OperandB;
+  typedef TileOperandTOf<kA, kWavesN> OperandAT;
+  typedef TileOperandTOf<kB, kWavesN> OperandBT;
+};
+
+template <int kVSn, int kTok, int kWB>
+__global__ __launch_bounds__((Shape<kVSn, kTok, kWB>::kThr), 2) void linear_tiles(LinearArgs a,
+                                                                               int32_t n_a,
+                                                                               int32_t n_b,
+                                                                               int64_t blk_begin) {
+  typedef Shape<kVSn, kTok, kWB> S;
+  __shared__ __attribute__((aligned(16))) char smem[S::kLds];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  int32_t ta, tb;
+  tile_of(blk_begin + xcd_local_block(blockIdx.x, gridDim.x), n_a, n_b, ta, tb);
+  const int32_t n0 = ta * S::kA, m0 = tb * S::kB;
+  const int64_t row_bytes = (int64_t)a.in_dim * 2;
+  f32x4 acc[kVSn][kTok] = {};
+  if (n0 < a.out_dim) {  // (else a tile of padding)
+    const typename S::OperandA wo(static_cast<const char*>(a.weight) + n0 * row_bytes, row_bytes,
+                                  min(S::kA, a.out_dim - n0), 0, wave, lane);
+    const typename S::OperandB xo(static_cast<const char*>(a.x) + m0 * row_bytes, row_bytes,
+                                  min(S::kB, a.tokens - m0), 0, wave, lane);
+    tile_product<kWB>(smem, wo, xo, 0, a.in_dim / kBK, wave, lane, acc);
+  }
+  const int32_t nw = n0 + wave / kWB * (16 * kVSn), mw = m0 + wave % kWB * (16 * kTok);
+  char* own = smem + wave * S::kOwn;
+#pragma unroll
+  for (int vs = 0; vs < kVSn; ++vs) {
+    const f32x4 b = bias_of(a, nw + vs * 16 + 4 * (lane >> 4));
+#pragma unroll
+    for (int ts = 0; ts < kTok; ++ts) acc[vs][ts] += b;
+  }
+  const float by = a.activation == kActSoftcap ? 1.0f / a.cap : 1.0f;
+  if (a.saved && a.saved_f32) {
+#pragma unroll
+    for (int ts = 0; ts < kTok; ++ts) {
+      const int32_t m = mw + ts * 16 + (lane & 15);
+      if (m >= a.tokens) continue;
+      float* to = static_cast<float*>(a.saved) + m * a.ld_saved;
+#pragma unroll
+      for (int vs = 0; vs < kVSn; ++vs) {
+        const int32_t n = nw + vs * 16 + 4 * (lane >> 4);
+        if (n < a.ld_saved) *reinterpret_cast<f32x4*>(to + n) = acc[vs][ts] * by;
+      }
+    }
+  } else if (a.saved) {
+    store_rows<kTok, kVSn>(
+        smem, wave, lane,
+        [&](int vs, int ts) __attribute__((always_inline)) {
+          union {
+            uint16_t e[4];
+            uint64_t x;
+          } o;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o.e[e] = fp16_bits(acc[vs][ts][e] * by);
+          return o.x;
+        },
+        [&](int r, int c, const u32x4& x) __attribute__((always_inline)) {
+          const int32_t m = mw + r, n = nw + c * 8;
+          if (m < a.tokens && n < a.ld_saved)
+            *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.saved) + m * a.ld_saved + n) = x;
+        });
+  }
+  if (a.residual) {
+    // in by whole rows, to where the accumulators will find it
+    const uint16_t* res = static_cast<const uint16_t*>(a.residual);
+    const bool wide = a.ld_residual % 8 == 0 && (reinterpret_cast<uintptr_t>(res) & 15) == 0;
+    whole_rows<kTok, kVSn>(own, lane, [&](int r, int c, u32x4* at)
+                                          __attribute__((always_inline)) {
+      const int32_t m = mw + r, n = nw + c * 8;
+      union {
+        u32x4 x;
+        uint16_t e[8];
+      } o;
+      o.x = u32x4{0, 0, 0, 0};
+      if (m < a.tokens) {
+        const uint16_t* from = res + m * a.ld_residual + n;
+        if (wide && n + 8 <= a.out_dim) {
+          o.x = *reinterpret_cast<const u32x4*>(from);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (n + e < a.out_dim) o.e[e] = from[e];
+        }
+      }
+      *at = o.x;
+    });
+  }
+  const bool add = a.residual != nullptr;
+  with_activation(a, [&](auto&& act) __attribute__((always_inline)) {
+    store_rows<kTok, kVSn>(
+        smem, wave, lane,
+        [&](int vs, int ts) __attribute__((always_inline)) {
+          union {
+            uint16_t e[4];
+            uint64_t x;
+          } o, r;
+          r.x = add ? *reinterpret_cast<const uint64_t*>(row_slot<kVSn>(own, lane, vs, ts)) : 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            o.e[e] = bf16_bits(act(acc[vs][ts][e]) + bf16_float(r.e[e]));
+          return o.x;
+        },
+        [&](int r, int c, const u32x4& x) __attribute__((always_inline)) {
+          put_out(a, mw + r, nw + c * 8, x);
+        });
+  });
+}
+
+// ---------------------------------------------------------------------------
+// linear_few: up to 64 tokens (16 kTok), whose time the weight's bytes bound.  A block takes
+// 16 kRT outputs; its eight waves take every eighth slab of 64 of the sum each, operands
+// straight from memory to registers, kDepth slabs ahead, and meet only at the end, where the
+// eight sums are added in order.
+// ---------------------------------------------------------------------------
+constexpr int kFewWaves = 8;
+constexpr int kDepth = 3;
+
+template <int kTok, int kRT>
+__global__ __launch_bounds__(64 * kFewWaves) void linear_few(LinearArgs a, int64_t blk_begin) {
+  constexpr int kRows = 16 * kRT, kTokens = 16 * kTok;
+  __shared__ f32x4 part[kFewWaves][kTokens][kRows / 4];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int32_t n0 = (int32_t)(blk_begin + blockIdx.x) * kRows;
+  const int fr = lane & 15, fc = lane >> 4;
+  if (n0 < a.out_dim) {
+    const uint16_t *w[kRT], *x[kTok];
+#pragma unroll
+    for (int rt = 0; rt < kRT; ++rt)
+      w[rt] = static_cast<const uint16_t*>(a.weight) +
+              (int64_t)min(n0 + rt * 16 + fr, a.out_dim - 1) * a.in_dim + fc * 8;
+#pragma unroll
+    for (int ts = 0; ts < kTok; ++ts)
+      x[ts] = static_cast<const uint16_t*>(a.x) +
+              (int64_t)min(ts * 16 + fr, a.tokens - 1) * a.in_dim + fc * 8;
+    f32x4 acc[kRT][kTok] = {};
+    bf16x8 wf[kDepth][kRT][2], xf[kDepth][kTok][2];
+    const int nslab = a.in_dim / kBK;
+    auto load = [&](int s, int at) __attribute__((always_inline)) {
+      // past the end the last slab is loaded again, unused
+      const int64_t k = (int64_t)min(s, nslab - 1) * kBK;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int rt = 0; rt < kRT; ++rt)
+          wf[at][rt][h] = *reinterpret_cast<const bf16x8*>(w[rt] + k + h * 32);
+#pragma unroll
+        for (int ts = 0; ts < kTok; ++ts)
+          xf[at][ts][h] = *reinterpret_cast<const bf16x8*>(x[ts] + k + h * 32);
+      }
+    };
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) load(wave + d * kFewWaves, d);
+    for (int s = wave; s < nslab; s += kDepth * kFewWaves) {
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d) {
+        if (s + d * kFewWaves < nslab) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int rt = 0; rt < kRT; ++rt)
+#pragma unroll
+              for (int ts = 0; ts < kTok; ++ts)
+                acc[rt][ts] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[d][rt][h], xf[d][ts][h],
+                                                                      acc[rt][ts], 0, 0, 0);
+        }
+        load(s + (d + kDepth) * kFewWaves, d);
+      }
+    }
+#pragma unroll
+    for (int rt = 0; rt < kRT; ++rt)
+#pragma unroll
+      for (int ts = 0; ts < kTok; ++ts) part[wave][ts * 16 + fr][rt * 4 + fc] = acc[rt][ts];
+  }
+  __syncthreads();
+  const int m = threadIdx.x / (kRows / 4), at = threadIdx.x % (kRows / 4);
+  const int32_t n = n0 + at * 4;
+  static_assert(kTokens * kRows / 4 <= 64 * kFewWaves, "a thread takes 4 outputs of a token");
+  if (m >= min(kTokens, a.tokens) || n >= a.padded_out) return;
+  uint16_t* out = static_cast<uint16_t*>(a.out) + m * a.ld_out + n;
+  union {
+    uint16_t e[4];
+    uint64_t x;
+  } o;
+  o.x = 0xFF80FF80FF80FF80ull;
+  if (n < a.out_dim) {
+    f32x4 z = part[0][m][at];
+#pragma unroll
+    for (int i = 1; i < kFewWaves; ++i) z += part[i][m][at];
+    z += bias_of(a, n);
+    if (a.saved) {
+      const float by = a.activation == kActSoftcap ? 1.0f / a.cap : 1.0f;
+      if (a.saved_f32) {
+        *reinterpret_cast<f32x4*>(static_cast<float*>(a.saved) + m * a.ld_saved + n) = z * by;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o.e[e] = fp16_bits(z[e] * by);
+        *reinterpret_cast<uint64_t*>(static_cast<uint16_t*>(a.saved) + m * a.ld_saved + n) = o.x;
+      }
+    }
+    with_activation(a, [&](auto&& act) __attribute__((always_inline)) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z[e] = act(z[e]);
+    });
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool on = n + e < a.out_dim;
+      if (on && a.residual)
+        z[e] += bf16_float(static_cast<const uint16_t*>(a.residual)[m * a.ld_residual + n + e]);
+      o.e[e] = on ? bf16_bits(z[e]) : kNegInfBf16;
+    }
+  }
+  if (n + 4 <= a.padded_out) {
+    *reinterpret_cast<uint64_t*>(out) = o.x;
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (n + e < a.padded_out) out[e] = o.e[e];
+}
+
+// ---------------------------------------------------------------------------
+// linear_dz: dz = dy act'(z) in bf16, its rows and columns filled up with zeros to multiples
+// of 64, and what 64 tokens add to db.  A block takes 64 tokens x 512 outputs, each of its
+// four waves 16 tokens, a lane 8 outputs.  The blocks behind copy x's and W's last rows, those
+// behind the last whole 64, followed by zeros: the slabs of dW's and dx's sums that they do not
+// fill.
+// ---------------------------------------------------------------------------
+constexpr int kDzRows = 64, kDzCols = 512;
+
+struct TailArgs {
+  const u32x4* x;  // the first of the last rows
+  const u32x4* w;
+  int32_t x_rows, w_rows;  // how many (0: no such slab)
+  int32_t ldc;             // 16-byte chunks per row
+  int32_t blocks;          // that copy each of them
+};
+
+__global__ __launch_bounds__(256) void linear_dz(LinearBwdArgs a, TailArgs t, int64_t n_dz,
+                                                 int64_t blk_begin) {
+  __shared__ float sums[3][kDzCols];
+  const LinearBwdLayout& l = a.layout;
+  int64_t blk = blk_begin + blockIdx.x;
+  if (blk >= n_dz) {
+    blk -= n_dz;
+    const bool of_w = t.x_rows == 0 || blk >= t.blocks;
+    const int64_t i = (blk % t.blocks) * 256 + threadIdx.x;
+    u32x4* to = reinterpret_cast<u32x4*>(a.workspace + (of_w ? l.w_tail : l.x_tail));
+    if (i < (int64_t)kBK * t.ldc)
+      to[i] = i < (int64_t)(of_w ? t.w_rows : t.x_rows) * t.ldc ? (of_w ? t.w : t.x)[i]
+                                                               : u32x4{0, 0, 0, 0};
+    return;
+  }
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int32_t n_cols = (l.cols + kDzCols - 1) / kDzCols;
+  const int32_t rb = (int32_t)(blk / n_cols);
+  const int32_t n = (int32_t)(blk % n_cols) * kDzCols + lane * 8;
+  const LinearArgs& f = a.f;
+  const uint16_t* dy = static_cast<const uint16_t*>(a.dy);
+  const bool wide = a.ld_dy % 8 == 0 && (reinterpret_cast<uintptr_t>(dy) & 15) == 0 &&
+                    n + 8 <= f.out_dim;
+  float sum[8] = {};
+  if (n < l.cols) {
+#pragma unroll 4
+    for (int i = 0; i < kDzRows / 4; ++i) {
+      const int32_t m = rb * kDzRows + wave * (kDzRows / 4) + i;
+      union {
+        u32x4 x;
+        uint16_t e[8];
+        _Float16 h[8];
+      } g, h;
+      g.x = u32x4{0, 0, 0, 0};
+      float z[8] = {};
+      if (m < f.tokens) {
+        const uint16_t* from = dy + m * a.ld_dy + n;
+        if (wide) {
+          g.x = *reinterpret_cast<const u32x4*>(from);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (n + e < f.out_dim) g.e[e] = from[e];
+        }
+        if (f.saved && n < f.out_dim) {
+          if (f.saved_f32) {
+            const f32x4* at = reinterpret_cast<const f32x4*>(static_cast<const float*>(f.saved) +
+                                                             m * f.ld_saved + n);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = at[e / 4][e % 4];
+          } else {
+            h.x = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(f.saved) +
+                                                  m * f.ld_saved + n);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = (float)h.h[e];
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        // (columns behind out_dim hold anything in z)
+        const float d = n + e < f.out_dim
+                            ? bf16_float(g.e[e]) * slope_of(f.activation, z[e])
+                            : 0.0f;
+        sum[e] += d;
+        g.e[e] = bf16_bits(d);
+      }
+      *reinterpret_cast<u32x4*>(a.workspace + l.dz + ((int64_t)m * l.cols + n) * 2) = g.x;
+    }
+  }
+  if (!a.dbias) return;
+  if (wave > 0)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sums[wave - 1][lane * 8 + e] = sum[e];
+  __syncthreads();
+  if (wave != 0 || n >= l.cols) return;
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] += sums[i][lane * 8 + e];
+  f32x4* to = reinterpret_cast<f32x4*>(a.workspace + l.bias_part +
+                                       ((int64_t)rb * l.cols + n) * 4);
+  to[0] = f32x4{sum[0], sum[1], sum[2], sum[3]};
+  to[1] = f32x4{sum[4], sum[5], sum[6], sum[7]};
+}
+
+// ---------------------------------------------------------------------------
+// linear_grads: dx, dW and db in one launch, so that the last blocks of one fill the chip
+// beside the next.  Blocks [0, n_dx) are dx's (A = W by its rows, the sum's index; B = dz: C[in]
+// [token]), the next n_dw dW's (A = x and B = dz by their rows: C[in][out]), the rest db's.
+// ---------------------------------------------------------------------------
+template <int kVSn, int kTok, int kWB>
+__global__ __launch_bounds__((Shape<kVSn, kTok, kWB>::kThr), 2) void linear_grads(
+    LinearBwdArgs a, int64_t n_dx, int64_t n_dw, int64_t blk_begin) {
+  typedef Shape<kVSn, kTok, kWB> S;
+  __shared__ __attribute__((aligned(16))) char smem[S::kLds];
+  const LinearBwdLayout& l = a.layout;
+  const LinearArgs& f = a.f;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  int64_t blk = blk_begin + blockIdx.x;
+  if (blk >= n_dx + n_dw) {
+    const int64_t n = (blk - n_dx - n_dw) * S::kThr + threadIdx.x;
+    if (n >= f.out_dim) return;
+    const float* part = reinterpret_cast<const float*>(a.workspace + l.bias_part) + n;
+    float sum = 0.0f;
+#pragma unroll 8
+    for (int32_t i = 0; i < l.row_blocks; ++i) sum += part[(int64_t)i * l.cols];
+    if (f.bias_bf16)
+      static_cast<uint16_t*>(a.dbias)[n] = bf16_bits(sum);
+    else
+      static_cast<float*>(a.dbias)[n] = sum;
+    return;
+  }
+  const bool is_dx = blk < n_dx;
+  const int32_t n_k = (f.in_dim + S::kA - 1) / S::kA;
+  int32_t ta, tb;
+  if (is_dx)
+    tile_of(xcd_local_block(blk, n_dx), n_k, (f.tokens + S::kB - 1) / S::kB, ta, tb);
+  else
+    tile_of(xcd_local_block(blk - n_dx, n_dw), n_k, (f.out_dim + S::kB - 1) / S::kB, ta, tb);
+  const int32_t k0 = ta * S::kA, b0 = tb * S::kB;
+  const int64_t k_bytes = (int64_t)f.in_dim * 2, dz_bytes = (int64_t)l.cols * 2;
+  const char* dz = a.workspace + l.dz;
+  const int32_t rows = is_dx ? f.out_dim : f.tokens;  // of the operand by its rows
+  const typename S::OperandAT ao(
+      static_cast<const char*>(is_dx ? f.weight : f.x) + k0 * 2, k_bytes,
+      min(S::kA, f.in_dim - k0), a.workspace + (is_dx ? l.w_tail : l.x_tail) + k0 * 2,
+      rows % kBK ? rows / kBK : -1, wave, lane);
+  f32x4 acc[kVSn][kTok];
+  if (is_dx) {
+    const typename S::OperandB bo(dz + b0 * dz_bytes, dz_bytes, min(S::kB, l.rows - b0), 0, wave,
+                                  lane);
+    tile_product<kWB>(smem, ao, bo, 0, l.cols / kBK, wave, lane, acc);
+  } else {
+    const typename S::OperandBT bo(dz + b0 * 2, dz_bytes, min(S::kB, l.cols - b0), nullptr, -1,
+                                   wave, lane);
+    tile_product<kWB>(smem, ao, bo, 0, l.rows / kBK, wave, lane, acc);
+  }
+  const int32_t kw = k0 + wave / kWB * (16 * kVSn), bw = b0 + wave % kWB * (16 * kTok);
+  const int32_t last = is_dx ? f.tokens : f.out_dim;
+  uint16_t* out = static_cast<uint16_t*>(is_dx ? a.dx : a.dweight);
+  store_rows<kTok, kVSn>(
+      smem, wave, lane,
+      [&](int vs, int ts) __attribute__((always_inline)) {
+        union {
+          uint16_t e[4];
+          uint64_t x;
+        } o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o.e[e] = bf16_bits(acc[vs][ts][e]);
+        return o.x;
+      },
+      [&](int r, int c, const u32x4& x) __attribute__((always_inline)) {
+        const int32_t row = bw + r, k = kw + c * 8;
+        if (row < last && k < f.in_dim)
+          *reinterpret_cast<u32x4*>(out + (int64_t)row * f.in_dim + k) = x;
+      });
+}
+
+size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+int64_t tiles_of(int64_t a, int64_t b, int64_t edge_a, int64_t edge_b) {
+  return ((a + edge_a - 1) / edge_a) * ((b + edge_b - 1) / edge_b);
+}
+
+template <int kVSn, int kTok, int kWB>
+hipError_t launch_tiles(const LinearArgs& a, hipStream_t stream) {
+  typedef Shape<kVSn, kTok, kWB> S;
+  const int32_t n_a = (a.padded_out + S::kA - 1) / S::kA, n_b = (a.tokens + S::kB - 1) / S::kB;
+  return in_launches((int64_t)n_a * n_b, S::kThr, [&](int64_t b, int64_t nb) {
+    hipLaunchKernelGGL((linear_tiles<kVSn, kTok, kWB>), dim3((unsigned)nb), dim3(S::kThr), 0,
+                       stream, a, n_a, n_b, b);
+  });
+}
+
+template <int kTok, int kRT>
+hipError_t launch_few(const LinearArgs& a, hipStream_t stream) {
+  const int64_t blocks = ((int64_t)a.padded_out + 16 * kRT - 1) / (16 * kRT);
+  return in_launches(blocks, 64 * kFewWaves, [&](int64_t b, int64_t nb) {
+    hipLaunchKernelGGL((linear_few<kTok, kRT>), dim3((unsigned)nb), dim3(64 * kFewWaves), 0,
+                       stream, a, b);
+  });
+}
+
+template <int kVSn, int kTok, int kWB>
+hipError_t launch_grads(const LinearBwdArgs& a, hipStream_t stream) {
+  typedef Shape<kVSn, kTok, kWB> S;
+  const LinearArgs& f = a.f;
+  const int64_t n_dx = a.dx ? tiles_of(f.in_dim, f.tokens, S::kA, S::kB) : 0;
+  const int64_t n_dw = a.dweight ? tiles_of(f.in_dim, f.out_dim, S::kA, S::kB) : 0;
+  const int64_t n_db = a.dbias ? ((int64_t)f.out_dim + S::kThr - 1) / S::kThr : 0;
+  return in_launches(n_dx + n_dw + n_db, S::kThr, [&](int64_t b, int64_t nb) {
+    hipLaunchKernelGGL((linear_grads<kVSn, kTok, kWB>), dim3((unsigned)nb), dim3(S::kThr), 0,
+                       stream, a, n_dx, n_dw, b);
+  });
+}
+
+}  // namespace
+
+constexpr int32_t kLinearFewTokens = 64;
+
+hipError_t launch_linear_fwd(const LinearArgs& a, hipStream_t stream) {
+  if (a.tokens <= kLinearFewTokens) {
+    if (a.tokens <= 16) return launch_few<1, 1>(a, stream);
+    if (a.tokens <= 32) return launch_few<2, 1>(a, stream);
+    return launch_few<4, 1>(a, stream);
+  }
+  if (tiles_of(a.out_dim, a.tokens, 256, 256) >= 192) return launch_tiles<8, 4, 4>(a, stream);
+  return launch_tiles<4, 4, 2>(a, stream);
+}
+
+LinearBwdLayout linear_bwd_layout(int64_t tokens, int64_t in_dim, int64_t out_dim) {
+  LinearBwdLayout l{};
+  const int64_t rows = (tokens + kBK - 1) / kBK * kBK, cols = (out_dim + kBK - 1) / kBK * kBK;
+  l.rows = (int32_t)rows;
+  l.cols = (int32_t)cols;
+  l.row_blocks = (int32_t)(rows / kDzRows);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += round256(bytes);
+    return here;
+  };
+  l.dz = take((size_t)rows * cols * 2);
+  l.x_tail = take((size_t)kBK * in_dim * 2);
+  l.w_tail = take((size_t)kBK * in_dim * 2);
+  l.bias_part = take((size_t)l.row_blocks * cols * 4);
+  l.total = at;
+  return l;
+}
+
+hipError_t launch_linear_bwd(const LinearBwdArgs& a, hipStream_t stream) {
+  const LinearArgs& f = a.f;
+  const LinearBwdLayout& l = a.layout;
+  if (f.tokens == 0) {  // no token: no gradient, and db's sums have no term
+    if (a.dweight) {
+      const hipError_t e =
+          launch_fill_zero(a.dweight, (int64_t)f.out_dim * f.in_dim * 2, stream);
+      if (e != hipSuccess) return e;
+    }
+    LinearBwdArgs of_db = a;
+    of_db.dweight = nullptr;
+    return launch_grads<4, 4, 2>(of_db, stream);
+  }
+  TailArgs t;
+  t.ldc = f.in_dim / 8;
+  t.x_rows = a.dweight ? f.tokens % kBK : 0;
+  t.w_rows = a.dx ? f.out_dim % kBK : 0;
+  t.x = static_cast<const u32x4*>(f.x) + (int64_t)(f.tokens / kBK * kBK) * t.ldc;
+  t.w = static_cast<const u32x4*>(f.weight) + (int64_t)(f.out_dim / kBK * kBK) * t.ldc;
+  t.blocks = (int32_t)(((int64_t)kBK * t.ldc + 255) / 256);
+  const int64_t n_dz = (int64_t)l.row_blocks * ((l.cols + kDzCols - 1) / kDzCols);
+  const int64_t tails = (t.x_rows ? t.blocks : 0) + (t.w_rows ? t.blocks : 0);
+  hipError_t e = in_launches(n_dz + tails, 256, [&](int64_t b, int64_t nb) {
+    hipLaunchKernelGGL(linear_dz, dim3((unsigned)nb), dim3(256), 0, stream, a, t, n_dz, b);
+  });
+  if (e != hipSuccess) return e;
+  const int64_t big = (a.dx ? tiles_of(f.in_dim, f.tokens, 256, 256) : 0) +
+                      (a.dweight ? tiles_of(f.in_dim, f.out_dim, 256, 256) : 0);
+  return big >= 192 ? launch_grads<8, 4, 4>(a, stream) : launch_grads<4, 4, 2>(a, stream);
+}
+
+}  // namespace rlk

@@ -276,18 +276,6 @@ __global__ __launch_bounds__(256) void gather_rows(GatherArgs a, RowArgs rows, c
   }
 }
 
-// Work index -> (tile of A, tile of B): strips of 4 A tiles, B-major inside, so
-// that the blocks resident on one XCD share operand rows (see lmhead_segments).
-__device__ __forceinline__ void tile_of(int64_t blk, int32_t n_a, int32_t n_b, int32_t& ta,
-                                        int32_t& tb) {
-  constexpr int32_t kGroup = 4;
-  const int64_t strip = blk / ((int64_t)kGroup * n_b);
-  const int32_t r_in = (int32_t)(blk - strip * kGroup * n_b);
-  const int32_t strip_w = min(kGroup, n_a - (int32_t)strip * kGroup);
-  ta = (int32_t)strip * kGroup + r_in % strip_w;
-  tb = r_in / strip_w;
-}
-
 // dz of one column from its logit (nl = -LSE log2 e), before its rounding to bf16;
 // what the rounding takes is kept where the column is the target's.
 __device__ __forceinline__ float plain_dz(float z, float nl, float cc) {
@@ -789,18 +777,6 @@ __global__ __launch_bounds__(256) void fill_zero(u32x4* __restrict__ out, int64_
                                                  int64_t begin) {
   const int64_t i = begin + (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (i < n) out[i] = u32x4{0, 0, 0, 0};
-}
-
-// Launches `blocks` blocks in pieces of at most the launch limit.
-template <typename F>
-hipError_t in_launches(int64_t blocks, int threads, F&& launch) {
-  const int64_t most = launch_thread_limit() / threads;
-  for (int64_t b = 0; b < blocks; b += most) {
-    launch(b, blocks - b < most ? blocks - b : most);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
 }
 
 size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }

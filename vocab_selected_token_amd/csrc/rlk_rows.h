@@ -12,28 +12,42 @@ __device__ __forceinline__ uint16_t bf16_bits(float x) {
   return __builtin_bit_cast(uint16_t, b);
 }
 
-// A wave's 16 kTok rows (of operand B) x 128 columns (of A) in bf16, through LDS: 8
-// bytes a lane as the accumulators lie, out in 16-byte pieces of whole 256-byte rows.
-// pack(vs, ts) gives 4 columns; put(row, chunk, x) stores 8 of them.  smem: 4096 kTok
+// Where 4 columns (of A, 4 * (lane / 16) on in its 16-row tile vs) of a wave's row
+// ts * 16 + lane % 16 (of B) lie in LDS, 2 bytes each: rows of 32 kVSn bytes, chunk c of row
+// r at c ^ (r % (2 kVSn)), so that 16 rows spread over all banks.
+template <int kVSn>
+__device__ __forceinline__ char* row_slot(char* own, int lane, int vs, int ts) {
+  const int r = ts * 16 + (lane & 15), c = vs * 2 + (lane >> 5);
+  return own + r * (32 * kVSn) + (c ^ (r & (2 * kVSn - 1))) * 16 + ((lane >> 4) & 1) * 8;
+}
+
+// A wave's 16 kTok rows in 16-byte pieces of whole rows: visit(row, chunk, its place in LDS).
+template <int kTok, int kVSn, typename Visit>
+__device__ __forceinline__ void whole_rows(char* own, int lane, Visit&& visit) {
+  constexpr int kChunks = 2 * kVSn, kRowsAt = 64 / kChunks;
+#pragma unroll
+  for (int j = 0; j < 16 * kTok / kRowsAt; ++j) {
+    const int r = j * kRowsAt + lane / kChunks, at = lane % kChunks;
+    visit(r, at ^ (r & (kChunks - 1)),
+          reinterpret_cast<u32x4*>(own + r * (32 * kVSn) + at * 16));
+  }
+}
+
+// A wave's 16 kTok rows (of operand B) x 16 kVSn columns (of A) in bf16, through LDS: 8
+// bytes a lane as the accumulators lie, out in 16-byte pieces of whole rows.
+// pack(vs, ts) gives 4 columns; put(row, chunk, x) stores 8 of them.  smem: 512 kTok kVSn
 // bytes a wave, free; each wave uses its own part.
-template <int kTok, typename Pack, typename Put>
+template <int kTok, int kVSn = kVS, typename Pack, typename Put>
 __device__ __forceinline__ void store_rows(char* smem, int wave, int lane, Pack&& pack,
                                            Put&& put) {
-  char* own = smem + wave * (16 * kTok * 256);
+  char* own = smem + wave * (16 * kTok * 32 * kVSn);
 #pragma unroll
   for (int ts = 0; ts < kTok; ++ts)
 #pragma unroll
-    for (int vs = 0; vs < kVS; ++vs) {
-      // chunk c of row r lies at c ^ (r % 16): 16 rows spread over all banks
-      const int r = ts * 16 + (lane & 15), c = vs * 2 + (lane >> 5);
-      *reinterpret_cast<uint64_t*>(own + r * 256 + (c ^ (lane & 15)) * 16 +
-                                   ((lane >> 4) & 1) * 8) = pack(vs, ts);
-    }
-#pragma unroll
-  for (int j = 0; j < 4 * kTok; ++j) {
-    const int r = j * 4 + (lane >> 4), c = (lane & 15) ^ (r & 15);
-    put(r, c, *reinterpret_cast<const u32x4*>(own + r * 256 + (lane & 15) * 16));
-  }
+    for (int vs = 0; vs < kVSn; ++vs)
+      *reinterpret_cast<uint64_t*>(row_slot<kVSn>(own, lane, vs, ts)) = pack(vs, ts);
+  whole_rows<kTok, kVSn>(own, lane, [&](int r, int c, const u32x4* x)
+                                        __attribute__((always_inline)) { put(r, c, *x); });
 }
 
 }  // namespace

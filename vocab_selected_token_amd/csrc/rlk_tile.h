@@ -90,6 +90,18 @@ __device__ __forceinline__ int64_t xcd_local_block(int64_t b, int64_t nb) {
   return x * per + (x < rem ? x : rem) + l;
 }
 
+// Work index -> (tile of A, tile of B): strips of 4 A tiles, B-major inside, so
+// that the blocks resident on one XCD share operand rows (see lmhead_segments).
+__device__ __forceinline__ void tile_of(int64_t blk, int32_t n_a, int32_t n_b, int32_t& ta,
+                                        int32_t& tb) {
+  constexpr int32_t kGroup = 4;
+  const int64_t strip = blk / ((int64_t)kGroup * n_b);
+  const int32_t r_in = (int32_t)(blk - strip * kGroup * n_b);
+  const int32_t strip_w = min(kGroup, n_a - (int32_t)strip * kGroup);
+  ta = (int32_t)strip * kGroup + r_in % strip_w;
+  tb = r_in / strip_w;
+}
+
 // One operand's slab loads.  Wave w moves rows [32w, 32w + 32), 8 rows per
 // instruction; lane i of instruction j fetches row 32w + 8j + i/8 at the chunk
 // that belongs at LDS position i%8.  The resource starts at `first` and covers
@@ -99,6 +111,7 @@ __device__ __forceinline__ int64_t xcd_local_block(int64_t b, int64_t nb) {
 // for tiles of fewer rows.)
 template <int kLoadsT>
 struct TileOperandOf {
+  static constexpr int kLoads = kLoadsT;
   __amdgpu_buffer_rsrc_t rsrc;
   uint32_t off[kLoadsT];  // byte offsets from the resource's base
 
@@ -148,36 +161,41 @@ __device__ __forceinline__ s16x4 transposed_read(lds_s16x4 __restrict__ at) {
 
 typedef TileOperandOf<kLoads> TileOperand;
 
-// An operand whose rows are the sum's index: row k of the slab holds B[0..255][k].
-// Wave w moves rows [8w, 8w + 8) of a slab, 2 per instruction; lane i of
-// instruction j fetches row 8w + 2j + i/32 at the chunk that belongs at position
+// An operand whose rows are the sum's index: row k of the slab holds B[0..255][k]
+// (kCols of them).  Of 256, wave w moves rows [8w, 8w + 8) of a slab, 2 per instruction;
+// lane i of instruction j fetches row 8w + 2j + i/32 at the chunk that belongs at position
 // i%32.  Columns from `cols` (a multiple of 8) on are never read: clamped.  Slab
 // tail_slab, if any, is read at `tail` (64 whole rows) instead: the one that the
 // last rows do not fill.
-struct TileOperandT {
+template <int kCols, int kWavesT>
+struct TileOperandTOf {
   const char* first;
   const char* tail;
   int tail_slab;
   int64_t slab_bytes;
-  uint32_t off[kLoads];
 
-  static constexpr int kRowBytesT = kBB * 2;
+  static constexpr int kRowBytesT = kCols * 2;
   static constexpr int kReadsPerFragment = 2;
+  static constexpr int kChunks = kCols / 8;            // of 16 bytes, per row
+  static constexpr int kRowsPerLoadT = 64 / kChunks;   // rows per load instruction
+  static constexpr int kRowsPerWaveT = kBK / kWavesT;
+  static constexpr int kLoads = kRowsPerWaveT / kRowsPerLoadT;
+  uint32_t off[kLoads];
 
   static __device__ __forceinline__ int swizzle(int row) {
     return ((row & 3) << 1) | (((row >> 3) & 1) << 3);
   }
 
-  __device__ __forceinline__ TileOperandT(const void* first_, int64_t row_bytes, int32_t cols,
-                                          const void* tail_, int tail_slab_, int wave, int lane)
+  __device__ __forceinline__ TileOperandTOf(const void* first_, int64_t row_bytes, int32_t cols,
+                                            const void* tail_, int tail_slab_, int wave, int lane)
       : first(static_cast<const char*>(first_)),
         tail(static_cast<const char*>(tail_)),
         tail_slab(tail_slab_),
         slab_bytes(kBK * row_bytes) {
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
-      const int row = wave * (kBK / kWaves) + j * 2 + (lane >> 5);
-      const int c = min((lane & 31) ^ swizzle(row), cols / 8 - 1);
+      const int row = wave * kRowsPerWaveT + j * kRowsPerLoadT + lane / kChunks;
+      const int c = min((lane % kChunks) ^ swizzle(row), cols / 8 - 1);
       off[j] = (uint32_t)(row * row_bytes + c * 16);
     }
   }
@@ -188,11 +206,11 @@ struct TileOperandT {
     const char* at = first + ((slab * slab_bytes & ~from_tail) | ((tail - first) & from_tail));
     const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<char*>(at), 0, (int)slab_bytes, kBufferWord3);
-    char* base = stage + wave * (kBK / kWaves) * kRowBytesT;
+    char* base = stage + wave * kRowsPerWaveT * kRowBytesT;
 #pragma unroll
     for (int j = 0; j < kLoads; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)(base + j * 2 * kRowBytesT), 16,
-                                               off[j], 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rsrc, (lds_ptr)(base + j * kRowsPerLoadT * kRowBytesT), 16, off[j], 0, 0, 0);
   }
 
   static __device__ __forceinline__ bf16x8 fragment(const char* stage, int row, int ks, int lane) {
@@ -211,22 +229,26 @@ struct TileOperandT {
   }
 };
 
+typedef TileOperandTOf<kBB, kWaves> TileOperandT;
+
 // LDS of a tile whose B has 64 kTok rows (each wave takes 16 kTok of them).
 template <int kTok>
 constexpr int kStageBytes = kSlabBytes + 64 * kTok * kRowBytes;
 
 // acc = the product over the slabs [slab0, slab0 + nslab) (nslab >= 1) of the
-// operands' rows.  smem: two stages, free for other use on return (every
-// load has landed and every wave has passed the last barrier).
-template <int kTok, typename OperandB>
-__device__ __forceinline__ void tile_product(char* smem, const TileOperand& A,
-                                             const OperandB& B, int slab0, int nslab, int wave,
-                                             int lane, f32x4 (&acc)[kVS][kTok]) {
-  constexpr int kStage = kStageBytes<kTok>;
-  const int wv = wave >> 2;  // half of A's rows
-  const int wt = wave & 3;   // quarter of B's rows
+// operands' rows, by waves of 16 kVSn rows of A x 16 kTok of B, kWB of them along B and two
+// along A.  smem: two stages, free for other use on return (every load has landed and
+// every wave has passed the last barrier).
+template <int kWB = 4, int kVSn, int kTok, typename OperandA, typename OperandB>
+__device__ __forceinline__ void tile_product(char* smem, const OperandA& A, const OperandB& B,
+                                             int slab0, int nslab, int wave, int lane,
+                                             f32x4 (&acc)[kVSn][kTok]) {
+  constexpr int kSlabA = 2 * 16 * kVSn * kRowBytes;
+  constexpr int kStage = kSlabA + kWB * 16 * kTok * kRowBytes;
+  const int wv = wave / kWB;  // half of A's rows
+  const int wt = wave % kWB;  // part of B's rows
 #pragma unroll
-  for (int a = 0; a < kVS; ++a)
+  for (int a = 0; a < kVSn; ++a)
 #pragma unroll
     for (int b = 0; b < kTok; ++b)
 #pragma unroll
@@ -237,33 +259,36 @@ __device__ __forceinline__ void tile_product(char* smem, const TileOperand& A,
   auto issue = [&](int slab, int stage) __attribute__((always_inline)) {
     char* base = smem + stage * kStage;
     A.issue(base, wave, slab0 + slab);
-    B.issue(base + kSlabBytes, wave, slab0 + slab);
+    B.issue(base + kSlabA, wave, slab0 + slab);
   };
-  auto fetch = [&](const char* As, int ks, bf16x8 (&af)[kVS], bf16x8 (&bf)[kTok])
+  auto fetch = [&](const char* As, int ks, bf16x8 (&af)[kVSn], bf16x8 (&bf)[kTok])
       __attribute__((always_inline)) {
-    const char* Bs = As + kSlabBytes;
+    const char* Bs = As + kSlabA;
 #pragma unroll
-    for (int vs = 0; vs < kVS; ++vs)
-      af[vs] = TileOperand::fragment(As, wv * 128 + vs * 16, ks, lane);
+    for (int vs = 0; vs < kVSn; ++vs)
+      af[vs] = OperandA::fragment(As, wv * (16 * kVSn) + vs * 16, ks, lane);
 #pragma unroll
     for (int ts = 0; ts < kTok; ++ts)
       bf[ts] = OperandB::fragment(Bs, wt * (16 * kTok) + ts * 16, ks, lane);
   };
-  auto mma = [&](const bf16x8 (&af)[kVS], const bf16x8 (&bf)[kTok]) __attribute__((always_inline)) {
+  auto mma = [&](const bf16x8 (&af)[kVSn], const bf16x8 (&bf)[kTok])
+      __attribute__((always_inline)) {
 #pragma unroll
-    for (int vs = 0; vs < kVS; ++vs)
+    for (int vs = 0; vs < kVSn; ++vs)
 #pragma unroll
       for (int ts = 0; ts < kTok; ++ts)
         acc[vs][ts] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[vs], bf[ts], acc[vs][ts], 0, 0, 0);
   };
   // Instruction order inside a k-step: 4 MFMAs, then one LDS read (and, after the
-  // barrier, one slab load) per 2 MFMAs -- per MFMA, where B's fragments take two
-  // reads, and in narrower tiles -- then the remaining MFMAs.  The reads thus overlap
+  // barrier, one slab load) per 2 MFMAs -- per MFMA, where fragments take two reads,
+  // and in narrower tiles -- then the remaining MFMAs.  The reads thus overlap
   // the MFMAs that do not need them.
-  constexpr int kReads = kVS + OperandB::kReadsPerFragment * kTok, kMfmas = kVS * kTok, kLead = 4;
-  constexpr int kPer = OperandB::kReadsPerFragment == 1 && kTok == kTS ? 2 : 1;
-  constexpr int kSlabLoads = kLoads + kTok;
-  static_assert(kLead + kPer * kReads <= kMfmas, "the reads fit inside the step");
+  constexpr int kReads = OperandA::kReadsPerFragment * kVSn + OperandB::kReadsPerFragment * kTok,
+                kMfmas = kVSn * kTok;
+  constexpr int kPer = 4 + 2 * kReads <= kMfmas ? 2 : 1;
+  constexpr int kSpare = kMfmas - kPer * kReads, kLead = kSpare < 4 ? kSpare : 4;
+  constexpr int kSlabLoads = OperandA::kLoads + OperandB::kLoads;
+  static_assert(kSpare >= 0, "the reads fit inside the step");
   static_assert(kSlabLoads <= kReads, "one load per read at most");
   auto order_step = [&](bool with_loads) __attribute__((always_inline)) {
     __builtin_amdgcn_sched_group_barrier(0x008, kLead, 0);  // MFMA
@@ -273,14 +298,14 @@ __device__ __forceinline__ void tile_product(char* smem, const TileOperand& A,
       if (with_loads && i < kSlabLoads) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // VMEM
       __builtin_amdgcn_sched_group_barrier(0x008, kPer, 0);
     }
-    __builtin_amdgcn_sched_group_barrier(0x008, kMfmas - kLead - kPer * kReads, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, kSpare - kLead, 0);
   };
 
   issue(0, 0);
   if (nslab > 1) issue(1, 1);
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
-  bf16x8 a0[kVS], b0[kTok], a1[kVS], b1[kTok];
+  bf16x8 a0[kVSn], b0[kTok], a1[kVSn], b1[kTok];
   fetch(smem, 0, a0, b0);
   for (int s = 0; s < nslab; ++s) {
     const char* cur = smem + (s & 1) * kStage;
