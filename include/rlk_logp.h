@@ -608,8 +608,8 @@ typedef struct rlk_linear_desc {
  *   out         (device) bf16 [tokens, ld_out], 16-byte aligned; columns [out_dim, padded_out)
  *               are -inf (the logits of padding), columns from padded_out on are not touched.
  *   saved       (device) [tokens, ld_saved] of saved_dtype, 16-byte aligned, out, or NULL: z
- *               (z / cap for the soft cap; in fp16 clamped to +-65504), which rlk_linear_bwd
- *               needs unless the activation is RLK_ACT_NONE.  Columns from out_dim on may be
+ *               (z / cap for the soft cap) clamped to +-65504, which rlk_linear_bwd needs
+ *               unless the activation is RLK_ACT_NONE.  Columns from out_dim on may be
  *               written.
  * Repeated calls give the same bits. */
 rlk_status rlk_linear_fwd(const rlk_linear_desc* desc, const void* x, const void* weight,

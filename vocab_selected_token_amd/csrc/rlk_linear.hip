@@ -21,6 +21,7 @@
 
 #include "rlk_internal.h"
 #include "rlk_rows.h"
+#include "rlk_stream.h"
 #include "rlk_tile.h"
 
 namespace rlk {
@@ -70,29 +71,48 @@ __device__ __forceinline__ float act_of(float z, float cap, float inv_cap) {
 }
 
 // act'(z) from what was kept: z, or z / cap.
-__device__ __forceinline__ float slope_of(int act, float z) {
-  switch (act) {
-    case kActRelu: return z > 0.0f ? 1.0f : 0.0f;
-    case kActSilu: {
-      const float s = sigmoid(z);
-      return s * (1.0f + z * (1.0f - s));
-    }
-    case kActGelu: return normal_cdf(z) + z * kInvSqrt2Pi * exp2_hw(-0.5f * kLog2e * z * z);
-    case kActGeluTanh: {
-      const float s = sigmoid(2.0f * kGeluC * (z + kGeluA * z * z * z));
-      return s + z * s * (1.0f - s) * 2.0f * kGeluC * (1.0f + 3.0f * kGeluA * z * z);
-    }
-    case kActSoftcap: {  // 1 - tanh^2, without the difference
-      const float e = exp2_hw(fabsf(z) * (-2.0f * kLog2e)), r = rcp_hw(1.0f + e);
-      return 4.0f * e * r * r;
-    }
+template <int kAct>
+__device__ __forceinline__ float slope_of(float z) {
+  if constexpr (kAct == kActRelu) return z > 0.0f ? 1.0f : 0.0f;
+  if constexpr (kAct == kActSilu) {
+    const float s = sigmoid(z);
+    return s * (1.0f + z * (1.0f - s));
+  }
+  if constexpr (kAct == kActGelu)
+    return normal_cdf(z) + z * kInvSqrt2Pi * exp2_hw(-0.5f * kLog2e * z * z);
+  if constexpr (kAct == kActGeluTanh) {
+    const float s = sigmoid(2.0f * kGeluC * (z + kGeluA * z * z * z));
+    return s + z * s * (1.0f - s) * 2.0f * kGeluC * (1.0f + 3.0f * kGeluA * z * z);
+  }
+  if constexpr (kAct == kActSoftcap) {  // 1 - tanh^2, without the difference
+    const float e = exp2_hw(fabsf(z) * (-2.0f * kLog2e)), r = rcp_hw(1.0f + e);
+    return 4.0f * e * r * r;
   }
   return 1.0f;
 }
 
+// use(slope): the slope of the call's activation, one for all of its outputs.
+template <typename Use>
+__device__ __forceinline__ void with_slope(int activation, Use&& use) {
+  switch (activation) {
+    case kActRelu: return use(slope_of<kActRelu>);
+    case kActGelu: return use(slope_of<kActGelu>);
+    case kActGeluTanh: return use(slope_of<kActGeluTanh>);
+    case kActSilu: return use(slope_of<kActSilu>);
+    case kActSoftcap: return use(slope_of<kActSoftcap>);
+  }
+  use(slope_of<kActNone>);
+}
+
+// What is kept of z, before its rounding (NaN stays).
+__device__ __forceinline__ float clamped(float z) {
+  return z > 65504.0f ? 65504.0f : z < -65504.0f ? -65504.0f : z;
+}
 __device__ __forceinline__ uint16_t fp16_bits(float z) {
-  const _Float16 h = (_Float16)(z > 65504.0f ? 65504.0f : z < -65504.0f ? -65504.0f : z);
-  return __builtin_bit_cast(uint16_t, h);
+  return __builtin_bit_cast(uint16_t, (_Float16)clamped(z));
+}
+__device__ __forceinline__ f32x4 clamped(const f32x4& z) {
+  return f32x4{clamped(z[0]), clamped(z[1]), clamped(z[2]), clamped(z[3])};
 }
 
 // finish(act): the call's activation, one for all of its outputs.
@@ -203,7 +223,7 @@ __global__ __launch_bounds__((Shape<kVSn, kTok, kWB>::kThr), 2) void linear_tile
 #pragma unroll
       for (int vs = 0; vs < kVSn; ++vs) {
         const int32_t n = nw + vs * 16 + 4 * (lane >> 4);
-        if (n < a.ld_saved) *reinterpret_cast<f32x4*>(to + n) = acc[vs][ts] * by;
+        if (n < a.ld_saved) *reinterpret_cast<f32x4*>(to + n) = clamped(acc[vs][ts] * by);
       }
     }
   } else if (a.saved) {
@@ -270,77 +290,8 @@ __global__ __launch_bounds__((Shape<kVSn, kTok, kWB>::kThr), 2) void linear_tile
   });
 }
 
-// ---------------------------------------------------------------------------
-// linear_few: up to 64 tokens (16 kTok), whose time the weight's bytes bound.  A block takes
-// 16 kRT outputs; its eight waves take every eighth slab of 64 of the sum each, operands
-// straight from memory to registers, kDepth slabs ahead, and meet only at the end, where the
-// eight sums are added in order.
-// ---------------------------------------------------------------------------
-constexpr int kFewWaves = 8;
-constexpr int kDepth = 3;
-
-template <int kTok, int kRT>
-__global__ __launch_bounds__(64 * kFewWaves) void linear_few(LinearArgs a, int64_t blk_begin) {
-  constexpr int kRows = 16 * kRT, kTokens = 16 * kTok;
-  __shared__ f32x4 part[kFewWaves][kTokens][kRows / 4];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int32_t n0 = (int32_t)(blk_begin + blockIdx.x) * kRows;
-  const int fr = lane & 15, fc = lane >> 4;
-  if (n0 < a.out_dim) {
-    const uint16_t *w[kRT], *x[kTok];
-#pragma unroll
-    for (int rt = 0; rt < kRT; ++rt)
-      w[rt] = static_cast<const uint16_t*>(a.weight) +
-              (int64_t)min(n0 + rt * 16 + fr, a.out_dim - 1) * a.in_dim + fc * 8;
-#pragma unroll
-    for (int ts = 0; ts < kTok; ++ts)
-      x[ts] = static_cast<const uint16_t*>(a.x) +
-              (int64_t)min(ts * 16 + fr, a.tokens - 1) * a.in_dim + fc * 8;
-    f32x4 acc[kRT][kTok] = {};
-    bf16x8 wf[kDepth][kRT][2], xf[kDepth][kTok][2];
-    const int nslab = a.in_dim / kBK;
-    auto load = [&](int s, int at) __attribute__((always_inline)) {
-      // past the end the last slab is loaded again, unused
-      const int64_t k = (int64_t)min(s, nslab - 1) * kBK;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int rt = 0; rt < kRT; ++rt)
-          wf[at][rt][h] = *reinterpret_cast<const bf16x8*>(w[rt] + k + h * 32);
-#pragma unroll
-        for (int ts = 0; ts < kTok; ++ts)
-          xf[at][ts][h] = *reinterpret_cast<const bf16x8*>(x[ts] + k + h * 32);
-      }
-    };
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d) load(wave + d * kFewWaves, d);
-    for (int s = wave; s < nslab; s += kDepth * kFewWaves) {
-#pragma unroll
-      for (int d = 0; d < kDepth; ++d) {
-        if (s + d * kFewWaves < nslab) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int rt = 0; rt < kRT; ++rt)
-#pragma unroll
-              for (int ts = 0; ts < kTok; ++ts)
-                acc[rt][ts] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[d][rt][h], xf[d][ts][h],
-                                                                      acc[rt][ts], 0, 0, 0);
-        }
-        load(s + (d + kDepth) * kFewWaves, d);
-      }
-    }
-#pragma unroll
-    for (int rt = 0; rt < kRT; ++rt)
-#pragma unroll
-      for (int ts = 0; ts < kTok; ++ts) part[wave][ts * 16 + fr][rt * 4 + fc] = acc[rt][ts];
-  }
-  __syncthreads();
-  const int m = threadIdx.x / (kRows / 4), at = threadIdx.x % (kRows / 4);
-  const int32_t n = n0 + at * 4;
-  static_assert(kTokens * kRows / 4 <= 64 * kFewWaves, "a thread takes 4 outputs of a token");
-  if (m >= min(kTokens, a.tokens) || n >= a.padded_out) return;
+// 4 outputs of token m from output n (a multiple of 4) on: the rest of the epilogue.
+__device__ __forceinline__ void finish4(const LinearArgs& a, int32_t m, int32_t n, f32x4 z) {
   uint16_t* out = static_cast<uint16_t*>(a.out) + m * a.ld_out + n;
   union {
     uint16_t e[4];
@@ -348,14 +299,12 @@ __global__ __launch_bounds__(64 * kFewWaves) void linear_few(LinearArgs a, int64
   } o;
   o.x = 0xFF80FF80FF80FF80ull;
   if (n < a.out_dim) {
-    f32x4 z = part[0][m][at];
-#pragma unroll
-    for (int i = 1; i < kFewWaves; ++i) z += part[i][m][at];
     z += bias_of(a, n);
     if (a.saved) {
       const float by = a.activation == kActSoftcap ? 1.0f / a.cap : 1.0f;
       if (a.saved_f32) {
-        *reinterpret_cast<f32x4*>(static_cast<float*>(a.saved) + m * a.ld_saved + n) = z * by;
+        *reinterpret_cast<f32x4*>(static_cast<float*>(a.saved) + m * a.ld_saved + n) =
+            clamped(z * by);
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) o.e[e] = fp16_bits(z[e] * by);
@@ -384,13 +333,115 @@ __global__ __launch_bounds__(64 * kFewWaves) void linear_few(LinearArgs a, int64
 }
 
 // ---------------------------------------------------------------------------
+// linear_few: up to 64 tokens (16 kTok), whose time the weight's bytes bound.  A block takes
+// 16 outputs; its four waves take every fourth slab of 64 of the sum each, operands
+// straight from memory to registers, kDepth slabs ahead, and meet only at the end, where the
+// four sums are added in order.
+// ---------------------------------------------------------------------------
+constexpr int kFewWaves = 4;
+constexpr int kDepth = 4;
+
+template <int kTok>
+__global__ __launch_bounds__(64 * kFewWaves) void linear_few(LinearArgs a, int64_t blk_begin) {
+  constexpr int kTokens = 16 * kTok;
+  __shared__ f32x4 part[kFewWaves][kTokens][4];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int32_t n0 = (int32_t)(blk_begin + blockIdx.x) * 16;
+  const int fr = lane & 15, fc = lane >> 4;
+  if (n0 < a.out_dim) {
+    const uint16_t *w, *x[kTok];
+    w = static_cast<const uint16_t*>(a.weight) +
+        (int64_t)min(n0 + fr, a.out_dim - 1) * a.in_dim + fc * 8;
+#pragma unroll
+    for (int ts = 0; ts < kTok; ++ts)
+      x[ts] = static_cast<const uint16_t*>(a.x) +
+              (int64_t)min(ts * 16 + fr, a.tokens - 1) * a.in_dim + fc * 8;
+    f32x4 acc[kTok] = {};
+    bf16x8 wf[kDepth][2], xf[kDepth][kTok][2];
+    const int nslab = a.in_dim / kBK;
+    const int turn = (int)((uint32_t)blockIdx.x % (uint32_t)nslab);
+    auto load = [&](int s, int at) __attribute__((always_inline)) {
+      // past the end the last slab is loaded again, unused
+      const int t = min(s, nslab - 1) + turn;
+      const int64_t k = (int64_t)(t < nslab ? t : t - nslab) * kBK;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        wf[at][h] = *reinterpret_cast<const bf16x8*>(w + k + h * 32);
+#pragma unroll
+        for (int ts = 0; ts < kTok; ++ts)
+          xf[at][ts][h] = *reinterpret_cast<const bf16x8*>(x[ts] + k + h * 32);
+      }
+    };
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) load(wave + d * kFewWaves, d);
+    for (int s = wave; s < nslab; s += kDepth * kFewWaves) {
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d) {
+        if (s + d * kFewWaves < nslab) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int ts = 0; ts < kTok; ++ts)
+              acc[ts] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[d][h], xf[d][ts][h], acc[ts],
+                                                                0, 0, 0);
+        }
+        load(s + (d + kDepth) * kFewWaves, d);
+      }
+    }
+#pragma unroll
+    for (int ts = 0; ts < kTok; ++ts) part[wave][ts * 16 + fr][fc] = acc[ts];
+  }
+  __syncthreads();
+  const int m = threadIdx.x / 4, at = threadIdx.x % 4;
+  static_assert(kTokens * 4 <= 64 * kFewWaves, "a thread takes 4 outputs of a token");
+  if (m >= min(kTokens, a.tokens) || n0 + at * 4 >= a.padded_out) return;
+  f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (n0 < a.out_dim) {
+    z = part[0][m][at];
+#pragma unroll
+    for (int i = 1; i < kFewWaves; ++i) z += part[i][m][at];
+  }
+  finish4(a, m, n0 + at * 4, z);
+}
+
+// ---------------------------------------------------------------------------
+// linear_stream: up to 64 tokens and a weight of many rows: the stream product, 64 kRT outputs a
+// block, the whole sum.  Each block begins its sum at another slab and goes around: the weight's
+// rows are a power of two apart, and blocks in step would all ask the same few memory
+// channels (16 tokens x 4096 x 151936: 255 us in step, 218 so, 5.7 TB/s; 64 tokens 283 and 248).
+// ---------------------------------------------------------------------------
+template <int kTok, int kRT>
+__global__ __launch_bounds__(kStreamThreads) void linear_stream(LinearArgs a, int64_t blk_begin) {
+  __shared__ StreamLds<kTok> lds;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int64_t blk = blk_begin + blockIdx.x;
+  const int32_t n0 = (int32_t)blk * (kStreamRows * kRT);
+  f32x4 acc[kRT][kTok] = {};
+  Bf16Stream math;
+  if (n0 < a.out_dim)
+    stream_product<kRT, kStreamThreads, true>(
+        lds, static_cast<const char*>(a.weight), static_cast<const char*>(a.x),
+        (uint32_t)a.in_dim * 2, 0, a.out_dim, a.tokens, n0, math, acc,
+        (int)(blk % (a.in_dim / kBK)));
+#pragma unroll
+  for (int rt = 0; rt < kRT; ++rt)
+#pragma unroll
+    for (int ts = 0; ts < kTok; ++ts) {
+      const int32_t m = ts * 16 + (lane & 15), n = n0 + (wave * kRT + rt) * 16 + 4 * (lane >> 4);
+      if (m < a.tokens && n < a.padded_out) finish4(a, m, n, acc[rt][ts]);
+    }
+}
+
+// ---------------------------------------------------------------------------
 // linear_dz: dz = dy act'(z) in bf16, its rows and columns filled up with zeros to multiples
-// of 64, and what 64 tokens add to db.  A block takes 64 tokens x 512 outputs, each of its
-// four waves 16 tokens, a lane 8 outputs.  The blocks behind copy x's and W's last rows, those
+// of 64, and what 64 tokens add to db.  A block takes 64 tokens x 128 outputs, a thread 4 tokens
+// x 8 outputs, whose loads go out together.  The blocks behind copy x's and W's last rows, those
 // behind the last whole 64, followed by zeros: the slabs of dW's and dx's sums that they do not
 // fill.
 // ---------------------------------------------------------------------------
-constexpr int kDzRows = 64, kDzCols = 512;
+constexpr int kDzRows = 64, kDzCols = 128;
 
 struct TailArgs {
   const u32x4* x;  // the first of the last rows
@@ -402,7 +453,7 @@ struct TailArgs {
 
 __global__ __launch_bounds__(256) void linear_dz(LinearBwdArgs a, TailArgs t, int64_t n_dz,
                                                  int64_t blk_begin) {
-  __shared__ float sums[3][kDzCols];
+  __shared__ float sums[16][kDzCols + 4];
   const LinearBwdLayout& l = a.layout;
   int64_t blk = blk_begin + blockIdx.x;
   if (blk >= n_dz) {
@@ -415,76 +466,74 @@ __global__ __launch_bounds__(256) void linear_dz(LinearBwdArgs a, TailArgs t, in
                                                                : u32x4{0, 0, 0, 0};
     return;
   }
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int group = threadIdx.x >> 4, at = (threadIdx.x & 15) * 8;
   const int32_t n_cols = (l.cols + kDzCols - 1) / kDzCols;
-  const int32_t rb = (int32_t)(blk / n_cols);
-  const int32_t n = (int32_t)(blk % n_cols) * kDzCols + lane * 8;
+  const int32_t rb = (int32_t)(blk / n_cols), c0 = (int32_t)(blk % n_cols) * kDzCols;
+  const int32_t n = c0 + at;
   const LinearArgs& f = a.f;
   const uint16_t* dy = static_cast<const uint16_t*>(a.dy);
   const bool wide = a.ld_dy % 8 == 0 && (reinterpret_cast<uintptr_t>(dy) & 15) == 0 &&
                     n + 8 <= f.out_dim;
+  union Eight {
+    u32x4 x;
+    uint16_t e[8];
+    _Float16 h[8];
+  };
   float sum[8] = {};
   if (n < l.cols) {
-#pragma unroll 4
-    for (int i = 0; i < kDzRows / 4; ++i) {
-      const int32_t m = rb * kDzRows + wave * (kDzRows / 4) + i;
-      union {
-        u32x4 x;
-        uint16_t e[8];
-        _Float16 h[8];
-      } g, h;
-      g.x = u32x4{0, 0, 0, 0};
-      float z[8] = {};
-      if (m < f.tokens) {
-        const uint16_t* from = dy + m * a.ld_dy + n;
-        if (wide) {
-          g.x = *reinterpret_cast<const u32x4*>(from);
-        } else {
+    Eight g[4], h[4];
+    f32x4 z[4][2];
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (n + e < f.out_dim) g.e[e] = from[e];
-        }
-        if (f.saved && n < f.out_dim) {
-          if (f.saved_f32) {
-            const f32x4* at = reinterpret_cast<const f32x4*>(static_cast<const float*>(f.saved) +
-                                                             m * f.ld_saved + n);
+    for (int i = 0; i < 4; ++i) {
+      const int32_t m = rb * kDzRows + i * 16 + group;
+      g[i].x = h[i].x = u32x4{0, 0, 0, 0};
+      z[i][0] = z[i][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (m >= f.tokens || n >= f.out_dim) continue;
+      const uint16_t* from = dy + m * a.ld_dy + n;
+      if (wide) {
+        g[i].x = *reinterpret_cast<const u32x4*>(from);
+      } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] = at[e / 4][e % 4];
-          } else {
-            h.x = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(f.saved) +
-                                                  m * f.ld_saved + n);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] = (float)h.h[e];
-          }
-        }
+        for (int e = 0; e < 8; ++e)
+          if (n + e < f.out_dim) g[i].e[e] = from[e];
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        // (columns behind out_dim hold anything in z)
-        const float d = n + e < f.out_dim
-                            ? bf16_float(g.e[e]) * slope_of(f.activation, z[e])
-                            : 0.0f;
-        sum[e] += d;
-        g.e[e] = bf16_bits(d);
+      if (!f.saved) continue;
+      if (f.saved_f32) {
+        const f32x4* kept = reinterpret_cast<const f32x4*>(static_cast<const float*>(f.saved) +
+                                                           m * f.ld_saved + n);
+        z[i][0] = kept[0];
+        z[i][1] = kept[1];
+      } else {
+        h[i].x = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(f.saved) +
+                                                 m * f.ld_saved + n);
       }
-      *reinterpret_cast<u32x4*>(a.workspace + l.dz + ((int64_t)m * l.cols + n) * 2) = g.x;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int32_t m = rb * kDzRows + i * 16 + group;
+      with_slope(f.activation, [&](auto&& slope) __attribute__((always_inline)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float kept = f.saved_f32 ? z[i][e / 4][e % 4] : (float)h[i].h[e];
+          // (columns behind out_dim hold anything in z)
+          const float d = n + e < f.out_dim ? bf16_float(g[i].e[e]) * slope(kept) : 0.0f;
+          sum[e] += d;
+          g[i].e[e] = bf16_bits(d);
+        }
+      });
+      *reinterpret_cast<u32x4*>(a.workspace + l.dz + ((int64_t)m * l.cols + n) * 2) = g[i].x;
     }
   }
   if (!a.dbias) return;
-  if (wave > 0)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sums[wave - 1][lane * 8 + e] = sum[e];
+  for (int e = 0; e < 8; ++e) sums[group][at + e] = sum[e];
   __syncthreads();
-  if (wave != 0 || n >= l.cols) return;
+  if (threadIdx.x >= kDzCols || c0 + (int32_t)threadIdx.x >= l.cols) return;
+  float all = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 3; ++i)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sum[e] += sums[i][lane * 8 + e];
-  f32x4* to = reinterpret_cast<f32x4*>(a.workspace + l.bias_part +
-                                       ((int64_t)rb * l.cols + n) * 4);
-  to[0] = f32x4{sum[0], sum[1], sum[2], sum[3]};
-  to[1] = f32x4{sum[4], sum[5], sum[6], sum[7]};
+  for (int i = 0; i < 16; ++i) all += sums[i][threadIdx.x];
+  reinterpret_cast<float*>(a.workspace + l.bias_part)[(int64_t)rb * l.cols + c0 + threadIdx.x] =
+      all;
 }
 
 // ---------------------------------------------------------------------------
@@ -577,12 +626,23 @@ hipError_t launch_tiles(const LinearArgs& a, hipStream_t stream) {
   });
 }
 
-template <int kTok, int kRT>
+// Up to 64 tokens.  A weight of few rows needs every block's waves on one sum; one of many is
+// read fastest by blocks of 128 rows, where that leaves enough of them.  Of linear_few, blocks of 64
+// and of 128 rows, 16 tokens x 4096 x 8192 outputs take 19.6, 20.0 and 35.5 us, x 16384 37.6, 25.6 and
+// 37.0, x 24576 55, 43.5 and 38.9; 64 tokens x 4096 x 4096 23.6, 26.6 and 43, x 8192 44.6, 28.0 and 44.
+template <int kTok>
 hipError_t launch_few(const LinearArgs& a, hipStream_t stream) {
-  const int64_t blocks = ((int64_t)a.padded_out + 16 * kRT - 1) / (16 * kRT);
-  return in_launches(blocks, 64 * kFewWaves, [&](int64_t b, int64_t nb) {
-    hipLaunchKernelGGL((linear_few<kTok, kRT>), dim3((unsigned)nb), dim3(64 * kFewWaves), 0,
-                       stream, a, b);
+  const int64_t n = a.padded_out;
+  auto stream_blocks = [&](auto kernel, int rows) {
+    return in_launches((n + rows - 1) / rows, kStreamThreads, [&](int64_t b, int64_t nb) {
+      hipLaunchKernelGGL(kernel, dim3((unsigned)nb), dim3(kStreamThreads), 0, stream, a, b);
+    });
+  };
+  if (n > 16384) return stream_blocks(linear_stream<kTok, 2>, 2 * kStreamRows);
+  if (n > (kTok == 1 ? 8192 : 4096)) return stream_blocks(linear_stream<kTok, 1>, kStreamRows);
+  return in_launches((n + 15) / 16, 64 * kFewWaves, [&](int64_t b, int64_t nb) {
+    hipLaunchKernelGGL(linear_few<kTok>, dim3((unsigned)nb), dim3(64 * kFewWaves), 0, stream, a,
+                       b);
   });
 }
 
@@ -605,9 +665,9 @@ constexpr int32_t kLinearFewTokens = 64;
 
 hipError_t launch_linear_fwd(const LinearArgs& a, hipStream_t stream) {
   if (a.tokens <= kLinearFewTokens) {
-    if (a.tokens <= 16) return launch_few<1, 1>(a, stream);
-    if (a.tokens <= 32) return launch_few<2, 1>(a, stream);
-    return launch_few<4, 1>(a, stream);
+    if (a.tokens <= 16) return launch_few<1>(a, stream);
+    if (a.tokens <= 32) return launch_few<2>(a, stream);
+    return launch_few<4>(a, stream);
   }
   if (tiles_of(a.out_dim, a.tokens, 256, 256) >= 192) return launch_tiles<8, 4, 4>(a, stream);
   return launch_tiles<4, 4, 2>(a, stream);

@@ -45,12 +45,13 @@ struct StreamLds {
 // w: the weight's rows [row_lo, row_hi) (some of them in the block; others are not read:
 // the row is clamped), row_bytes each, a multiple of 128; h: num_tokens rows.  `math`
 // multiplies a slab and may stage data of its own beside the hidden states.
-// Every wave of the block calls it; on return all have done with `lds`.
-template <int kRT = 1, int kThr = kStreamThreads, int kTok, typename Math>
+// Every wave of the block calls it; on return all have done with `lds`.  With kTurn the sum begins
+// at slab `turn` (< the number of slabs) and goes around.
+template <int kRT = 1, int kThr = kStreamThreads, bool kTurn = false, int kTok, typename Math>
 __device__ __forceinline__ void stream_product(StreamLds<kTok>& lds, const char* w, const char* h,
                                                uint32_t row_bytes, int32_t row_lo, int32_t row_hi,
                                                int32_t num_tokens, int32_t v0, Math& math,
-                                               f32x4 (&acc)[kRT][kTok]) {
+                                               f32x4 (&acc)[kRT][kTok], int turn = 0) {
 #if defined(__HIP_DEVICE_COMPILE__)  // the host pass cannot instantiate the target's builtins
   typedef StreamLds<kTok> T;
   constexpr int kCopies = kBuf * T::kBytes / 16 / kThr;  // per thread and stage
@@ -76,6 +77,12 @@ __device__ __forceinline__ void stream_product(StreamLds<kTok>& lds, const char*
                    row_bytes +
                fc * 16;
 
+  // where slab s of the sum lies in a row
+  auto place = [&](int s) __attribute__((always_inline)) {
+    if constexpr (!kTurn) return (uint32_t)s * kRowBytes;
+    const int at = s + turn;
+    return (uint32_t)(at < nslab ? at : at - nslab) * kRowBytes;
+  };
   u32x4 copy[kCopies];
   auto load_stage = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
@@ -86,7 +93,7 @@ __device__ __forceinline__ void stream_product(StreamLds<kTok>& lds, const char*
           u32x4, __builtin_amdgcn_raw_buffer_load_b128(
                      hrs,
                      (uint32_t)min(r, num_tokens - 1) * row_bytes +
-                         (uint32_t)min(s + i, nslab - 1) * kRowBytes + c * 16,
+                         place(min(s + i, nslab - 1)) + c * 16,
                      0, 0));
     }
     math.load_stage(s);
@@ -109,7 +116,7 @@ __device__ __forceinline__ void stream_product(StreamLds<kTok>& lds, const char*
 
   i32x4 a[kBuf][kRT][2];
   auto load = [&](int slab, int at) __attribute__((always_inline)) {
-    const uint32_t off = (uint32_t)slab * kRowBytes;
+    const uint32_t off = place(slab);
 #pragma unroll
     for (int rt = 0; rt < kRT; ++rt)
 #pragma unroll
