@@ -1063,47 +1063,51 @@ class LogitRules:
     The tensors are checked here, once, and have to stay as they are made: contents may change
     between calls.  They are constants: no gradient reaches them."""
 
-    __slots__ = ("tensors", "rows", "device", "struct", "_bias_cols", "_allow_words")
-
-    _VECTORS = ("repetition", "presence", "frequency", "temperature")
-    _BOUNDS = ("history_begin", "history_split", "history_end")
+    __slots__ = ("tensors", "rows", "device", "struct", "bias_columns", "allow_words")
 
     def __init__(self, *, repetition=None, presence=None, frequency=None, temperature=None,
                  history=None, history_begin=None, history_split=None, history_end=None,
                  bias=None, bias_index=None, allow=None, allow_index=None):
-        rows = device = None
-        s = rlk_logit_rules()
-        kept = []
-
-        def vector(name, t, dtype, per_row=True):
-            nonlocal rows, device
+        if history is None:
+            if not (history_begin is history_split is history_end is None):
+                raise TypeError("history_begin, history_split and history_end need a history")
+        elif history_begin is None or history_end is None:
+            raise TypeError("a history needs history_begin and history_end")
+        if bias is None and bias_index is not None:
+            raise TypeError("bias_index needs a bias")
+        if allow is None and allow_index is not None:
+            raise TypeError("allow_index needs allow")
+        f32, i32, i64 = torch.float32, torch.int32, torch.int64
+        rows, kept, at = None, [], {}
+        for name, t, dtype in (("repetition", repetition, f32), ("presence", presence, f32),
+                               ("frequency", frequency, f32), ("temperature", temperature, f32),
+                               ("history_begin", history_begin, i64),
+                               ("history_split", history_split, i64),
+                               ("history_end", history_end, i64),
+                               ("bias_index", bias_index, i32), ("allow_index", allow_index, i32),
+                               ("history", history, i32)):
+            if t is None:
+                continue
             if not isinstance(t, torch.Tensor):
                 raise TypeError(f"{name} must be a torch.Tensor")
-            if t.dtype != dtype:
+            if t.dtype is not dtype:
                 raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
             if t.dim() != 1 or not t.is_contiguous():
                 raise ValueError(f"{name} must be 1-D and contiguous")
-            if per_row:
+            if t is not history:
                 if rows is None:
                     rows = t.shape[0]
                 elif t.shape[0] != rows:
                     raise ValueError(f"{name} has {t.shape[0]} elements, other rules {rows}")
-            seen(name, t)
-            return t.data_ptr() or None
-
-        def seen(name, t):
-            nonlocal device
-            if device is None:
-                device = t.device
-            elif t.device != device:
-                raise ValueError(f"{name} is on {t.device}, other rules on {device}")
             kept.append(t)
-
-        def table(name, t, dtype, index):
-            nonlocal rows
+            at[name] = t.data_ptr()
+        for name, t, dtype, index in (("bias", bias, f32, bias_index),
+                                      ("allow", allow, i32, allow_index)):
+            if t is None:
+                continue
             if not isinstance(t, torch.Tensor):
                 raise TypeError(f"{name} must be a torch.Tensor")
-            if t.dtype != dtype:
+            if t.dtype is not dtype:
                 raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
             if t.dim() not in (1, 2) or (t.shape[-1] > 1 and t.stride(-1) != 1):
                 raise ValueError(f"{name} must be 1-D or 2-D with unit column stride")
@@ -1111,40 +1115,24 @@ class LogitRules:
             ld = width if n <= 1 else t.stride(0)
             if n < 1 or ld < width:
                 raise ValueError(f"{name} must have a row, and rows that do not overlap")
-            seen(name, t)
             if index is None and n > 1:
                 if rows is None:
                     rows = n
                 elif n != rows:
                     raise ValueError(f"{name} without an index has {n} rows, other rules {rows}")
-            at = None if index is None else vector(name + "_index", index, torch.int32)
-            return t.data_ptr() or None, n, ld, at, width
-
-        for name, t in zip(self._VECTORS, (repetition, presence, frequency, temperature)):
-            if t is not None:
-                setattr(s, name, vector(name, t, torch.float32))
+            kept.append(t)
+            at[name], at[name + "_rows"], at["ld_" + name] = t.data_ptr(), n, ld
+            at[name + "_columns"] = width
+        self.bias_columns = at.pop("bias_columns", None)
+        self.allow_words = at.pop("allow_columns", None)
         if history is not None:
-            if history_begin is None or history_end is None:
-                raise TypeError("a history needs history_begin and history_end")
-            s.history = vector("history", history, torch.int32, per_row=False)
-            s.history_len = history.shape[0]
-            for name, t in zip(self._BOUNDS, (history_begin, history_split, history_end)):
-                if t is not None:
-                    setattr(s, name, vector(name, t, torch.int64))
-        elif not (history_begin is history_split is history_end is None):
-            raise TypeError("history_begin, history_split and history_end need a history")
-        self._bias_cols = self._allow_words = None
-        if bias is not None:
-            s.bias, s.bias_rows, s.ld_bias, s.bias_index, self._bias_cols = \
-                table("bias", bias, torch.float32, bias_index)
-        elif bias_index is not None:
-            raise TypeError("bias_index needs a bias")
-        if allow is not None:
-            s.allow, s.allow_rows, s.ld_allow, s.allow_index, self._allow_words = \
-                table("allow", allow, torch.int32, allow_index)
-        elif allow_index is not None:
-            raise TypeError("allow_index needs allow")
-        self.tensors, self.rows, self.device, self.struct = tuple(kept), rows, device, s
+            at["history_len"] = history.shape[0]
+        device = kept[0].device if kept else None
+        for t in kept:
+            if t.device != device:
+                raise ValueError(f"the rules are on {t.device} and on {device}")
+        self.tensors, self.rows, self.device = tuple(kept), rows, device
+        self.struct = rlk_logit_rules(**at)
 
 
 def _check_rules(rules, logits, real_vocab):
@@ -1152,11 +1140,11 @@ def _check_rules(rules, logits, real_vocab):
         raise TypeError("rules must be LogitRules")
     if rules.rows is not None and rules.rows != logits.shape[0]:
         raise ValueError(f"the rules have {rules.rows} rows, the logits {logits.shape[0]}")
-    if rules._bias_cols is not None and rules._bias_cols < real_vocab:
-        raise ValueError(f"bias has {rules._bias_cols} columns, fewer than "
+    if rules.bias_columns is not None and rules.bias_columns < real_vocab:
+        raise ValueError(f"bias has {rules.bias_columns} columns, fewer than "
                          f"real_vocab={real_vocab}")
-    if rules._allow_words is not None and rules._allow_words * 32 < real_vocab:
-        raise ValueError(f"allow has {rules._allow_words} words, fewer than "
+    if rules.allow_words is not None and rules.allow_words * 32 < real_vocab:
+        raise ValueError(f"allow has {rules.allow_words} words, fewer than "
                          f"real_vocab={real_vocab} needs")
     if rules.device is not None and rules.device != logits.device:
         raise ValueError(f"the rules are on {rules.device}, the logits on {logits.device}")
@@ -1496,6 +1484,10 @@ def head_linear(x: torch.Tensor, weight: torch.Tensor, bias=None, residual=None,
     _check_linear(x, weight, n, bias, residual=residual)
     if bias is not None and bias.shape[0] != n:
         raise ValueError(f"bias must have {n} elements, got {bias.shape[0]}")
+    if not torch.is_grad_enabled() or not (
+            x.requires_grad or weight.requires_grad or (bias is not None and bias.requires_grad)
+            or (residual is not None and residual.requires_grad)):
+        return _run_linear(x, weight, bias, residual, act, cap, n, n, False)[0]
     return _HeadLinear.apply(x, weight, bias, residual, act, cap)
 
 

@@ -29,7 +29,8 @@ namespace {
 
 static_assert(kBK == kLmheadSlabK, "slab width shared with the boundary");
 
-typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+// 16 bytes at any element's address
+typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(2)));
 
 __device__ __forceinline__ float bf16_float(uint16_t b) {
   return __uint_as_float((uint32_t)b << 16);
@@ -47,9 +48,24 @@ constexpr float kInvSqrt2Pi = 0.3989422804014327f;
 __device__ __forceinline__ float sigmoid(float z) {
   return rcp_hw(1.0f + exp2_hw(-z * kLog2e));
 }
-// The normal distribution's Phi(z).
-__device__ __forceinline__ float normal_cdf(float z) {
-  return 0.5f * erfcf(z * -0.7071067811865476f);
+// exp(-z^2 / 2).
+__device__ __forceinline__ float bell(float z) { return exp2_hw(z * z * (-0.5f * kLog2e)); }
+// The normal distribution's Phi(z), bell = exp(-z^2 / 2): Phi(-a) = bell P(t), t = 1 / (1 + 0.3 a),
+// with P fitted to erfcx(a / sqrt 2) / 2 over 0 <= a <= 14 for the least relative error
+// (1.5e-7; behind, bell is 0).  Half the instructions of the library's erfcf, whose share of 1024
+// tokens x 2048 x 151936 was a fifth (GELU 819 us, SiLU 648).
+__device__ __forceinline__ float normal_cdf(float z, float bell) {
+  const float t = rcp_hw(fmaf(0.3f, fabsf(z), 1.0f));
+  float p = 0.035674773156642914f;
+  p = fmaf(p, t, -0.1572030782699585f);
+  p = fmaf(p, t, 0.20635350048542023f);
+  p = fmaf(p, t, -0.05368363857269287f);
+  p = fmaf(p, t, 0.12856163084506989f);
+  p = fmaf(p, t, 0.09991349279880524f);
+  p = fmaf(p, t, 0.12075395882129669f);
+  p = fmaf(p, t, 0.11962930113077164f);
+  const float q = p * t * bell;
+  return z < 0.0f ? q : 1.0f - q;
 }
 // tanh: below 2^-6 its series (the next term is 2/15 u^4 < 2^-26 of it), where 1 - e would
 // cancel.
@@ -63,7 +79,7 @@ template <int kAct>
 __device__ __forceinline__ float act_of(float z, float cap, float inv_cap) {
   if constexpr (kAct == kActRelu) return z < 0.0f ? 0.0f : z;  // (NaN stays)
   if constexpr (kAct == kActSilu) return z * sigmoid(z);
-  if constexpr (kAct == kActGelu) return z * normal_cdf(z);
+  if constexpr (kAct == kActGelu) return z * normal_cdf(z, bell(z));
   if constexpr (kAct == kActGeluTanh)  // (1 + tanh(u)) / 2 = sigmoid(2u)
     return z * sigmoid(2.0f * kGeluC * (z + kGeluA * z * z * z));
   if constexpr (kAct == kActSoftcap) return cap * tanh_of(z * inv_cap);
@@ -78,8 +94,10 @@ __device__ __forceinline__ float slope_of(float z) {
     const float s = sigmoid(z);
     return s * (1.0f + z * (1.0f - s));
   }
-  if constexpr (kAct == kActGelu)
-    return normal_cdf(z) + z * kInvSqrt2Pi * exp2_hw(-0.5f * kLog2e * z * z);
+  if constexpr (kAct == kActGelu) {
+    const float b = bell(z);
+    return normal_cdf(z, b) + z * kInvSqrt2Pi * b;
+  }
   if constexpr (kAct == kActGeluTanh) {
     const float s = sigmoid(2.0f * kGeluC * (z + kGeluA * z * z * z));
     return s + z * s * (1.0f - s) * 2.0f * kGeluC * (1.0f + 3.0f * kGeluA * z * z);
@@ -247,7 +265,6 @@ __global__ __launch_bounds__((Shape<kVSn, kTok, kWB>::kThr), 2) void linear_tile
   if (a.residual) {
     // in by whole rows, to where the accumulators will find it
     const uint16_t* res = static_cast<const uint16_t*>(a.residual);
-    const bool wide = a.ld_residual % 8 == 0 && (reinterpret_cast<uintptr_t>(res) & 15) == 0;
     whole_rows<kTok, kVSn>(own, lane, [&](int r, int c, u32x4* at)
                                           __attribute__((always_inline)) {
       const int32_t m = mw + r, n = nw + c * 8;
@@ -258,8 +275,8 @@ __global__ __launch_bounds__((Shape<kVSn, kTok, kWB>::kThr), 2) void linear_tile
       o.x = u32x4{0, 0, 0, 0};
       if (m < a.tokens) {
         const uint16_t* from = res + m * a.ld_residual + n;
-        if (wide && n + 8 <= a.out_dim) {
-          o.x = *reinterpret_cast<const u32x4*>(from);
+        if (n + 8 <= a.out_dim) {
+          o.x = *reinterpret_cast<const u32x4u*>(from);
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
@@ -278,10 +295,16 @@ __global__ __launch_bounds__((Shape<kVSn, kTok, kWB>::kThr), 2) void linear_tile
             uint16_t e[4];
             uint64_t x;
           } o, r;
-          r.x = add ? *reinterpret_cast<const uint64_t*>(row_slot<kVSn>(own, lane, vs, ts)) : 0;
+          float y[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            o.e[e] = bf16_bits(act(acc[vs][ts][e]) + bf16_float(r.e[e]));
+          for (int e = 0; e < 4; ++e) y[e] = act(acc[vs][ts][e]);
+          if (add) {
+            r.x = *reinterpret_cast<const uint64_t*>(row_slot<kVSn>(own, lane, vs, ts));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] += bf16_float(r.e[e]);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o.e[e] = bf16_bits(y[e]);
           return o.x;
         },
         [&](int r, int c, const u32x4& x) __attribute__((always_inline)) {
@@ -472,8 +495,6 @@ __global__ __launch_bounds__(256) void linear_dz(LinearBwdArgs a, TailArgs t, in
   const int32_t n = c0 + at;
   const LinearArgs& f = a.f;
   const uint16_t* dy = static_cast<const uint16_t*>(a.dy);
-  const bool wide = a.ld_dy % 8 == 0 && (reinterpret_cast<uintptr_t>(dy) & 15) == 0 &&
-                    n + 8 <= f.out_dim;
   union Eight {
     u32x4 x;
     uint16_t e[8];
@@ -490,8 +511,8 @@ __global__ __launch_bounds__(256) void linear_dz(LinearBwdArgs a, TailArgs t, in
       z[i][0] = z[i][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
       if (m >= f.tokens || n >= f.out_dim) continue;
       const uint16_t* from = dy + m * a.ld_dy + n;
-      if (wide) {
-        g[i].x = *reinterpret_cast<const u32x4*>(from);
+      if (n + 8 <= f.out_dim) {
+        g[i].x = *reinterpret_cast<const u32x4u*>(from);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -616,6 +637,37 @@ int64_t tiles_of(int64_t a, int64_t b, int64_t edge_a, int64_t edge_b) {
   return ((a + edge_a - 1) / edge_a) * ((b + edge_b - 1) / edge_b);
 }
 
+// The tiles, and what a slab of the sum takes (us, 4096 in) with 1, 2, ... of them on each of the
+// chip's 256 CUs, up to as many as fit: many small tiles fill the chip where few large ones would
+// not, and multiply more slowly where there is work for both.
+struct TileCost {
+  int a, b, fit;
+  double time[5];
+};
+constexpr TileCost kTileCosts[] = {{256, 256, 1, {1.45}},
+                                   {128, 128, 2, {0.65, 1.0}},
+                                   {128, 64, 3, {0.55, 0.65, 0.81}},
+                                   {64, 64, 5, {0.46, 0.50, 0.60, 0.75, 0.95}}};
+
+// Which of them: blocks(edge of A, edge of B) tiles in all.  Of the four, 4096 x 4096 x 4096 take 124,
+// 136, 160 and 200 us, 1024 x 4096 x 4096 94, 46, 42 and 48, 512 x 4096 x 4096 93, 43, 38 and 32, 777 x
+// 1088 x 2501 35, 16, 12.2 and 12.0, 333 x 2048 x 50021 110, 86, 100 and 115.
+template <typename Blocks>
+int best_tile(Blocks&& blocks) {
+  int best = 0;
+  double least = 0.0;
+  for (int i = 0; i < 4; ++i) {
+    const TileCost& c = kTileCosts[i];
+    const int64_t n = blocks(c.a, c.b), full = n / (256 * c.fit), rest = n % (256 * c.fit);
+    const double cost = (double)full * c.time[c.fit - 1] + (rest ? c.time[(rest - 1) / 256] : 0.0);
+    if (i == 0 || cost < least) {
+      least = cost;
+      best = i;
+    }
+  }
+  return best;
+}
+
 template <int kVSn, int kTok, int kWB>
 hipError_t launch_tiles(const LinearArgs& a, hipStream_t stream) {
   typedef Shape<kVSn, kTok, kWB> S;
@@ -669,8 +721,12 @@ hipError_t launch_linear_fwd(const LinearArgs& a, hipStream_t stream) {
     if (a.tokens <= 32) return launch_few<2>(a, stream);
     return launch_few<4>(a, stream);
   }
-  if (tiles_of(a.out_dim, a.tokens, 256, 256) >= 192) return launch_tiles<8, 4, 4>(a, stream);
-  return launch_tiles<4, 4, 2>(a, stream);
+  switch (best_tile([&](int ea, int eb) { return tiles_of(a.padded_out, a.tokens, ea, eb); })) {
+    case 0: return launch_tiles<8, 4, 4>(a, stream);
+    case 1: return launch_tiles<4, 4, 2>(a, stream);
+    case 2: return launch_tiles<4, 2, 2>(a, stream);
+    default: return launch_tiles<2, 2, 2>(a, stream);
+  }
 }
 
 LinearBwdLayout linear_bwd_layout(int64_t tokens, int64_t in_dim, int64_t out_dim) {
@@ -719,9 +775,15 @@ hipError_t launch_linear_bwd(const LinearBwdArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL(linear_dz, dim3((unsigned)nb), dim3(256), 0, stream, a, t, n_dz, b);
   });
   if (e != hipSuccess) return e;
-  const int64_t big = (a.dx ? tiles_of(f.in_dim, f.tokens, 256, 256) : 0) +
-                      (a.dweight ? tiles_of(f.in_dim, f.out_dim, 256, 256) : 0);
-  return big >= 192 ? launch_grads<8, 4, 4>(a, stream) : launch_grads<4, 4, 2>(a, stream);
+  switch (best_tile([&](int ea, int eb) {
+    return (a.dx ? tiles_of(f.in_dim, f.tokens, ea, eb) : 0) +
+           (a.dweight ? tiles_of(f.in_dim, f.out_dim, ea, eb) : 0);
+  })) {
+    case 0: return launch_grads<8, 4, 4>(a, stream);
+    case 1: return launch_grads<4, 4, 2>(a, stream);
+    case 2: return launch_grads<4, 2, 2>(a, stream);
+    default: return launch_grads<2, 2, 2>(a, stream);
+  }
 }
 
 }  // namespace rlk

@@ -182,9 +182,12 @@ struct TileOperandTOf {
   static constexpr int kLoads = kRowsPerWaveT / kRowsPerLoadT;
   uint32_t off[kLoads];
 
+  // (64 columns: rows are half as long as the banks, so odd rows lie apart from even ones)
   static __device__ __forceinline__ int swizzle(int row) {
+    if constexpr (kChunks == 8) return (row & 2) | (((row >> 3) & 1) << 2);
     return ((row & 3) << 1) | (((row >> 3) & 1) << 3);
   }
+  static_assert(kChunks >= 8, "a chunk stays in its row");
 
   __device__ __forceinline__ TileOperandTOf(const void* first_, int64_t row_bytes, int32_t cols,
                                             const void* tail_, int tail_slab_, int wave, int lane)
@@ -282,15 +285,16 @@ __device__ __forceinline__ void tile_product(char* smem, const OperandA& A, cons
   // Instruction order inside a k-step: 4 MFMAs, then one LDS read (and, after the
   // barrier, one slab load) per 2 MFMAs -- per MFMA, where fragments take two reads,
   // and in narrower tiles -- then the remaining MFMAs.  The reads thus overlap
-  // the MFMAs that do not need them.
+  // the MFMAs that do not need them.  (With fewer MFMAs than reads the order is left to the
+  // compiler.)
   constexpr int kReads = OperandA::kReadsPerFragment * kVSn + OperandB::kReadsPerFragment * kTok,
                 kMfmas = kVSn * kTok;
   constexpr int kPer = 4 + 2 * kReads <= kMfmas ? 2 : 1;
   constexpr int kSpare = kMfmas - kPer * kReads, kLead = kSpare < 4 ? kSpare : 4;
   constexpr int kSlabLoads = OperandA::kLoads + OperandB::kLoads;
-  static_assert(kSpare >= 0, "the reads fit inside the step");
-  static_assert(kSlabLoads <= kReads, "one load per read at most");
+  static_assert(kSpare < 0 || kSlabLoads <= kReads, "one load per read at most");
   auto order_step = [&](bool with_loads) __attribute__((always_inline)) {
+    if constexpr (kSpare < 0) return;
     __builtin_amdgcn_sched_group_barrier(0x008, kLead, 0);  // MFMA
 #pragma unroll
     for (int i = 0; i < kReads; ++i) {
