@@ -383,7 +383,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void linear_few(LinearArgs a, int64
     f32x4 acc[kTok] = {};
     bf16x8 wf[kDepth][2], xf[kDepth][kTok][2];
     const int nslab = a.in_dim / kBK;
-    const int turn = (int)((uint32_t)blockIdx.x % (uint32_t)nslab);
+    const int turn = (int)((blk_begin + blockIdx.x) % nslab);
     auto load = [&](int s, int at) __attribute__((always_inline)) {
       // past the end the last slab is loaded again, unused
       const int t = min(s, nslab - 1) + turn;
