@@ -1078,15 +1078,16 @@ class LogitRules:
         if allow is None and allow_index is not None:
             raise TypeError("allow_index needs allow")
         f32, i32, i64 = torch.float32, torch.int32, torch.int64
-        rows, kept, at = None, [], {}
+        rows = where = None
+        kept, ptrs = [], []
         for name, t, dtype in (("repetition", repetition, f32), ("presence", presence, f32),
                                ("frequency", frequency, f32), ("temperature", temperature, f32),
-                               ("history_begin", history_begin, i64),
+                               ("history", history, i32), ("history_begin", history_begin, i64),
                                ("history_split", history_split, i64),
                                ("history_end", history_end, i64),
-                               ("bias_index", bias_index, i32), ("allow_index", allow_index, i32),
-                               ("history", history, i32)):
+                               ("bias_index", bias_index, i32), ("allow_index", allow_index, i32)):
             if t is None:
+                ptrs.append(None)
                 continue
             if not isinstance(t, torch.Tensor):
                 raise TypeError(f"{name} must be a torch.Tensor")
@@ -1096,14 +1097,20 @@ class LogitRules:
                 raise ValueError(f"{name} must be 1-D and contiguous")
             if t is not history:
                 if rows is None:
-                    rows = t.shape[0]
-                elif t.shape[0] != rows:
-                    raise ValueError(f"{name} has {t.shape[0]} elements, other rules {rows}")
+                    rows = t.numel()
+                elif t.numel() != rows:
+                    raise ValueError(f"{name} has {t.numel()} elements, other rules {rows}")
+            if where is None:
+                where = t.get_device()
+            elif t.get_device() != where:
+                raise ValueError(f"{name} is on {t.device}, another rule on {kept[0].device}")
             kept.append(t)
-            at[name] = t.data_ptr()
+            ptrs.append(t.data_ptr())
+        tables = []
         for name, t, dtype, index in (("bias", bias, f32, bias_index),
                                       ("allow", allow, i32, allow_index)):
             if t is None:
+                tables.append((None, 0, 0, None))
                 continue
             if not isinstance(t, torch.Tensor):
                 raise TypeError(f"{name} must be a torch.Tensor")
@@ -1120,19 +1127,19 @@ class LogitRules:
                     rows = n
                 elif n != rows:
                     raise ValueError(f"{name} without an index has {n} rows, other rules {rows}")
+            if where is None:
+                where = t.get_device()
+            elif t.get_device() != where:
+                raise ValueError(f"{name} is on {t.device}, another rule on {kept[0].device}")
             kept.append(t)
-            at[name], at[name + "_rows"], at["ld_" + name] = t.data_ptr(), n, ld
-            at[name + "_columns"] = width
-        self.bias_columns = at.pop("bias_columns", None)
-        self.allow_words = at.pop("allow_columns", None)
-        if history is not None:
-            at["history_len"] = history.shape[0]
-        device = kept[0].device if kept else None
-        for t in kept:
-            if t.device != device:
-                raise ValueError(f"the rules are on {t.device} and on {device}")
-        self.tensors, self.rows, self.device = tuple(kept), rows, device
-        self.struct = rlk_logit_rules(**at)
+            tables.append((t.data_ptr(), n, ld, width))
+        (bias_ptr, bias_rows, ld_bias, self.bias_columns), \
+            (allow_ptr, allow_rows, ld_allow, self.allow_words) = tables
+        self.tensors, self.rows = tuple(kept), rows
+        self.device = kept[0].device if kept else None
+        self.struct = rlk_logit_rules(
+            *ptrs[:5], 0 if history is None else history.numel(), *ptrs[5:8], bias_ptr, bias_rows,
+            ld_bias, ptrs[8], allow_ptr, allow_rows, ld_allow, ptrs[9])
 
 
 def _check_rules(rules, logits, real_vocab):
