@@ -580,7 +580,7 @@ typedef enum rlk_activation {
  *   out_dim     >= 1, padded_out >= out_dim and < 2^31 - 65536
  *   ld_out      >= padded_out, a multiple of 8;  ld_residual >= out_dim (any)
  *   ld_saved    >= out_dim, a multiple of 8
- *   activation  an rlk_activation; cap: finite and positive for RLK_ACT_SOFTCAP, else unused
+ *   activation  an rlk_activation; cap: in [1e-30, 1e30] for RLK_ACT_SOFTCAP, else unused
  *   bias_dtype  of the bias and its gradient; unused without them
  *   saved_dtype RLK_DTYPE_F16 or RLK_DTYPE_F32: what the forward keeps of z.  fp16 (11 bits)
  *               costs gradients in bf16 nothing that shows; a bias' gradient in fp32 is as
@@ -604,14 +604,14 @@ typedef struct rlk_linear_desc {
  *   weight      (device) bf16 [>= out_dim, in_dim], contiguous, 16-byte aligned; rows >=
  *               out_dim are never read.
  *   bias        (device) [out_dim] of bias_dtype, or NULL.
- *   residual    (device) bf16 [tokens, ld_residual], or NULL; it may not overlap out.
+ *   residual    (device) bf16 [tokens, ld_residual], or NULL.
  *   out         (device) bf16 [tokens, ld_out], 16-byte aligned; columns [out_dim, padded_out)
  *               are -inf (the logits of padding), columns from padded_out on are not touched.
  *   saved       (device) [tokens, ld_saved] of saved_dtype, 16-byte aligned, out, or NULL: z
  *               (z / cap for the soft cap) clamped to +-65504, which rlk_linear_bwd needs
  *               unless the activation is RLK_ACT_NONE.  Columns from out_dim on may be
  *               written.
- * Repeated calls give the same bits. */
+ * No output may overlap an input or another output.  Repeated calls give the same bits. */
 rlk_status rlk_linear_fwd(const rlk_linear_desc* desc, const void* x, const void* weight,
                           const void* bias, const void* residual, void* out, void* saved,
                           void* stream);
@@ -627,7 +627,7 @@ rlk_status rlk_linear_fwd(const rlk_linear_desc* desc, const void* x, const void
  *               NULL (not wanted and not computed), not all three.
  *   workspace   >= rlk_linear_bwd_workspace_bytes(desc), 256-byte aligned; calls that share
  *               one must not overlap.
- * Repeated calls give the same bits. */
+ * No output may overlap an input or another output.  Repeated calls give the same bits. */
 size_t rlk_linear_bwd_workspace_bytes(const rlk_linear_desc* desc);
 rlk_status rlk_linear_bwd(const rlk_linear_desc* desc, const void* x, const void* weight,
                           const void* saved, const void* grad_out, int64_t ld_grad, void* dx,

@@ -203,3 +203,27 @@ def test_no_tokens():
     dx, dw, db = rlk.linear_backward(x, w, y, saved, activation="silu", want_bias=True)
     assert dx.shape == (0, 64) and (bits(dw) == 0).all() and (bits(db) == 0).all()
     assert rlk.lmhead_logits(x, w, real_vocab=9).shape == (0, 9)
+
+
+@pytest.mark.parametrize("m", [1, 70])
+def test_the_smallest_and_the_largest_cap(m):
+    """x picks one column of the weight, so z is exact.  At 1e30 z / cap stays normal and the soft
+    cap is z but for four roundings (1 / cap, z / cap, tanh's quotient, the product) of 2^-23 at
+    most, its slope 4 (1/2)^2 but for three; at 1e-30 they are +-cap but for four and 0."""
+    torch.manual_seed(4)
+    w = (torch.rand(96, 64, device=DEV) + 0.5) * torch.randn(96, 64, device=DEV).sign()
+    w = w.bfloat16()
+    x = torch.zeros(m, 64, dtype=torch.bfloat16, device=DEV)
+    x[:, 5] = 1.0
+    z = w[:, 5].double().expand(m, -1)
+    dy = torch.randn(m, 96, device=DEV).bfloat16()
+    for cap, want, slope in ((1e30, z, 1.0), (1e-30, z.sign() * 1e-30, 0.0)):
+        y, saved = rlk.linear_forward(x, w, torch.zeros(96, device=DEV), activation="softcap",
+                                      cap=cap, save=True)
+        assert ((y.double() - want).abs() <= want.abs() * (2.0 ** -8 + 2.0 ** -20)).all()
+        _, _, db = rlk.linear_backward(x, w, dy, saved, activation="softcap", cap=cap,
+                                       want_bias=True)
+        exact = dy.double().sum(0) * slope
+        # (the sum of m terms: m roundings of 2^-24)
+        bound = dy.double().abs().sum(0) * slope * (2.0 ** -20 + m * 2.0 ** -24)
+        assert ((db.double() - exact).abs() <= bound).all()

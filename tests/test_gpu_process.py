@@ -218,6 +218,23 @@ def test_in_place_and_what_lies_behind():
                        bits(want))
 
 
+def test_autograd_sees_what_is_written_in_place():
+    """A backward pass that saved the logits refuses them once they are processed in place."""
+    c = C.make_case(5, 1000, 1008, 3, DEV, "all")
+    for inner in (lambda x: rlk.processed_selected_token_logprob(x, c.tgt, rules(c), c.mask,
+                                                                 real_vocab=c.v)[0],
+                  lambda x: rlk.selected_token_logprob(x, c.tgt, c.mask, real_vocab=c.v)):
+        x = c.x.clone().requires_grad_()
+        logp = inner(x)
+        logp = logp if isinstance(logp, torch.Tensor) else logp[0]
+        g = torch.ones_like(logp)
+        torch.autograd.grad(logp, x, g, retain_graph=True)
+        with torch.no_grad():
+            rlk.process_logits(x, rules(c), real_vocab=c.v, out=x)
+        with pytest.raises(RuntimeError, match="inplace"):
+            torch.autograd.grad(logp, x, g)
+
+
 def test_a_row_has_the_same_bits_alone():
     c = C.make_case(40, 20001, 20008, 13, DEV, "all")
     y = rlk.process_logits(c.x, rules(c), real_vocab=c.v, padded_vocab=c.pad)

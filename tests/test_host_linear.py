@@ -89,6 +89,32 @@ def test_backward_refuses():
     assert rlk.rlk_linear_bwd_workspace_bytes(desc(in_dim=1)) == 0
 
 
+def test_outputs_stand_apart():
+    """An output that is an input, or another output, would be written while it is read."""
+    a, b, c, e = (FakeTensor(PTR + i * 0x1000000) for i in range(4))
+    for kw in (dict(out=X), dict(out=W), dict(out=OUT, saved=OUT), dict(saved=X), dict(saved=W),
+               dict(residual=a, saved=a), dict(bias=a, out=a), dict(bias=a, saved=a)):
+        refused(forward, rlk.RLK_ERR_BAD_SHAPE, **kw)
+    ws = FakeTensor(0x30000000, 1 << 20)
+    apart = dict(saved=a, dy=b, dx=c, dw=e, db=None, ws=ws)
+    for kw in (dict(dx=X), dict(dx=W), dict(dx=a), dict(dx=b), dict(dw=X), dict(dw=W),
+               dict(dw=a), dict(dw=b), dict(dw=c), dict(db=c), dict(db=e), dict(db=W),
+               dict(dx=ws), dict(dy=ws), dict(saved=ws)):
+        refused(backward, rlk.RLK_ERR_BAD_SHAPE, **{**apart, **kw})
+
+
+@pytest.mark.parametrize("cap", [1e-39, 9e-31, 2e30, 3e38])
+def test_caps_whose_quotients_leave_fp32_are_refused(cap):
+    refused(forward, rlk.RLK_ERR_BAD_SHAPE, d=desc(activation=5, cap=cap))
+    refused(backward, rlk.RLK_ERR_BAD_SHAPE, d=desc(activation=5, cap=cap))
+    x = torch.zeros(5, 64, dtype=torch.bfloat16)
+    for call in (rlk.linear_forward, rlk.head_linear):
+        with pytest.raises(ValueError, match="cap must"):
+            call(x, x, activation="softcap", cap=cap)
+    with pytest.raises(ValueError, match="cap must"):
+        rlk.lmhead_logits(x, x, cap=cap, real_vocab=5)
+
+
 def test_conveniences_check_tensors():
     bf = dict(dtype=torch.bfloat16)
     x, w, b = torch.zeros(5, 64, **bf), torch.zeros(9, 64, **bf), torch.zeros(9)

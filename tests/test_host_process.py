@@ -190,6 +190,14 @@ def test_conveniences_check_their_tensors():
         rlk.processed_backward(x, t, r, None, None, f, real_vocab=v)
 
 
+def test_out_that_requires_a_gradient_is_refused():
+    x = torch.zeros(4, 104, dtype=torch.bfloat16, requires_grad=True)
+    with pytest.raises(ValueError, match="requires a gradient"):
+        rlk.process_logits(x, rlk.LogitRules(), real_vocab=100, out=x)
+    with torch.no_grad(), pytest.raises(ValueError, match="GPU memory"):
+        rlk.process_logits(x, rlk.LogitRules(), real_vocab=100, out=x)
+
+
 @pytest.mark.parametrize("kind", C.KINDS)
 def test_the_formula_against_differences(kind):
     """dx of the plain form against central differences of its logp and LSE, in 64 bits: the

@@ -1175,6 +1175,8 @@ def process_logits(logits: torch.Tensor, rules: LogitRules, *, real_vocab: int,
         if out.dim() != 2 or out.shape[0] != n or out.shape[1] < v_pad or out.stride(1) != 1:
             raise ValueError(f"out must have {n} rows of at least {v_pad} columns, of unit "
                              "stride")
+        if out.requires_grad and torch.is_grad_enabled():
+            raise ValueError("out requires a gradient, and process_logits has none")
     _check_device(logits, out=out)
     code = RLK_DTYPE_BF16 if out_dtype == torch.bfloat16 else RLK_DTYPE_F32
     desc = make_desc(n, real_vocab, v_pad, logits.stride(0), 1)
@@ -1186,6 +1188,9 @@ def process_logits(logits: torch.Tensor, rules: LogitRules, *, real_vocab: int,
             y, ld = out, out.stride(0)
         rlk_logits_process(desc, logits, rules.struct, y, ld, code, stream)
     if out is not None:
+        # (autograd refuses a backward pass that has saved what was there)
+        if not out.is_inference():
+            torch.autograd.graph.increment_version(out)
         return out
     _handed_over(logits, stream, y)
     return y if ld == v_pad else y[:, :v_pad]
@@ -1294,8 +1299,8 @@ def processed_selected_token_logprob(logits: torch.Tensor, targets: torch.Tensor
 
     The log-probability under the distribution that a sampler with these rules draws from,
     and its gradient to the raw logits (bf16 [N, ld] with unit column stride; the gradient has
-    their shape and dtype).  The rules are constants.  Where a training step is captured into a HIP
-    graph, no eager autograd graph of the same leaves may be alive: torch ends the process."""
+    their shape and dtype).  The rules are constants.  Where a training step is captured into a
+    HIP graph, no eager autograd graph of the same leaves may be alive: torch ends the process."""
     v_pad = _check_vocab(logits, real_vocab, padded_vocab)
     _check_inputs(logits, targets, active_mask)
     _check_rules(rules, logits, real_vocab)
@@ -1321,8 +1326,8 @@ def _check_activation(activation, cap):
                          f"got {activation!r}")
     if (cap is not None) != (activation == "softcap"):
         raise ValueError("cap goes with the activation softcap, and with no other")
-    if cap is not None and not 0.0 < cap < 3e38:
-        raise ValueError(f"cap must be finite and positive, got {cap!r}")
+    if cap is not None and not 1e-30 <= cap <= 1e30:
+        raise ValueError(f"cap must be finite and in [1e-30, 1e30], got {cap!r}")
     return code, 0.0 if cap is None else float(cap)
 
 
@@ -1483,8 +1488,9 @@ def head_linear(x: torch.Tensor, weight: torch.Tensor, bias=None, residual=None,
     the bias' in its dtype, the residual's is the upstream one).
 
     This is a prediction head's dense or residual block, in front of the LM-head.  The backward
-    keeps z in 16 bits (32 with a bias in fp32) and rounds dz to bf16 once.  Where a training step is captured into a HIP
-    graph, no eager autograd graph of the same leaves may be alive: torch ends the process."""
+    keeps z in 16 bits (32 with a bias in fp32) and rounds dz to bf16 once.  Where a training step
+    is captured into a HIP graph, no eager autograd graph of the same leaves may be alive: torch
+    ends the process."""
     act, cap = _check_activation(activation, cap)
     _check_logits(weight, "weight")
     n = weight.shape[0]

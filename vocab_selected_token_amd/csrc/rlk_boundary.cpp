@@ -16,6 +16,8 @@
 #include <stdio.h>
 
 #include <stdlib.h>
+#include <algorithm>
+#include <initializer_list>
 #include <string>
 
 #include "rlk_internal.h"
@@ -1223,8 +1225,9 @@ rlk_status check_linear(const rlk_linear_desc* d, bool backward) {
     return fail(RLK_ERR_BAD_SHAPE, "out_dim=%lld outside its range", (long long)d->out_dim);
   if (d->activation < RLK_ACT_NONE || d->activation > RLK_ACT_SOFTCAP)
     return fail(RLK_ERR_BAD_SHAPE, "activation=%d is not an rlk_activation", d->activation);
-  if (d->activation == RLK_ACT_SOFTCAP && !(d->cap > 0.0f && d->cap <= 3.0e38f))
-    return fail(RLK_ERR_BAD_SHAPE, "cap=%g must be finite and positive", (double)d->cap);
+  // (1 / cap, and z / cap of all but the smallest z, are normal numbers)
+  if (d->activation == RLK_ACT_SOFTCAP && !(d->cap >= 1e-30f && d->cap <= 1e30f))
+    return fail(RLK_ERR_BAD_SHAPE, "cap=%g outside [1e-30, 1e30]", (double)d->cap);
   return RLK_OK;
 }
 
@@ -1247,6 +1250,18 @@ rlk_status check_bias(const rlk_linear_desc* d, const void* bias) {
   if (st != RLK_OK) return st;
   if (!aligned(bias, d->bias_dtype == RLK_DTYPE_BF16 ? 2 : 4))
     return fail(RLK_ERR_ALIGNMENT, "the bias must be aligned to its elements");
+  return RLK_OK;
+}
+
+// No output (NULLs apart) may be an input or another output.
+rlk_status check_apart(std::initializer_list<const void*> outputs,
+                       std::initializer_list<const void*> inputs) {
+  for (auto o = outputs.begin(); o != outputs.end(); ++o) {
+    if (!*o) continue;
+    if (std::find(inputs.begin(), inputs.end(), *o) != inputs.end() ||
+        std::find(o + 1, outputs.end(), *o) != outputs.end())
+      return fail(RLK_ERR_BAD_SHAPE, "an output cannot be an input or another output");
+  }
   return RLK_OK;
 }
 
@@ -1298,8 +1313,8 @@ rlk_status rlk_linear_fwd(const rlk_linear_desc* desc, const void* x, const void
   if (!aligned(x, 16) || !aligned(weight, 16) || !aligned(out, 16))
     return fail(RLK_ERR_ALIGNMENT, "x, weight and out must be 16-byte aligned");
   if (!aligned(residual, 2)) return fail(RLK_ERR_ALIGNMENT, "residual must be 2-byte aligned");
-  if (out == residual || out == x || out == weight)
-    return fail(RLK_ERR_BAD_SHAPE, "out cannot be one of the inputs");
+  st = check_apart({out, saved}, {x, weight, bias, residual});
+  if (st != RLK_OK) return st;
   rlk::LinearArgs a = linear_args(desc, x, weight);
   a.bias = bias;
   a.residual = residual;
@@ -1352,6 +1367,9 @@ rlk_status rlk_linear_bwd(const rlk_linear_desc* desc, const void* x, const void
     return fail(RLK_ERR_WORKSPACE, "workspace_bytes=%zu < required %zu", workspace_bytes,
                 lay.total);
   if (!aligned(workspace, 256)) return fail(RLK_ERR_ALIGNMENT, "workspace not 256-byte aligned");
+  st = check_apart({dx, dweight, dbias, workspace},
+                   {x, weight, need_saved ? saved : nullptr, grad_out});
+  if (st != RLK_OK) return st;
   rlk::LinearBwdArgs a{};
   a.f = linear_args(desc, x, weight);
   a.f.saved = need_saved ? const_cast<void*>(saved) : nullptr;

@@ -649,9 +649,9 @@ constexpr TileCost kTileCosts[] = {{256, 256, 1, {1.45}},
                                    {128, 64, 3, {0.55, 0.65, 0.81}},
                                    {64, 64, 5, {0.46, 0.50, 0.60, 0.75, 0.95}}};
 
-// Which of them: blocks(edge of A, edge of B) tiles in all.  Of the four, 4096 x 4096 x 4096 take 124,
-// 136, 160 and 200 us, 1024 x 4096 x 4096 94, 46, 42 and 48, 512 x 4096 x 4096 93, 43, 38 and 32, 777 x
-// 1088 x 2501 35, 16, 12.2 and 12.0, 333 x 2048 x 50021 110, 86, 100 and 115.
+// Which of them: blocks(edge of A, edge of B) tiles in all.  Of the four, 4096 x 4096 x 4096
+// take 124, 136, 160 and 200 us, 1024 x 4096 x 4096 94, 46, 42 and 48, 512 x 4096 x 4096 93, 43,
+// 38 and 32, 777 x 1088 x 2501 35, 16, 12.2 and 12.0, 333 x 2048 x 50021 110, 86, 100 and 115.
 template <typename Blocks>
 int best_tile(Blocks&& blocks) {
   int best = 0;
@@ -679,9 +679,10 @@ hipError_t launch_tiles(const LinearArgs& a, hipStream_t stream) {
 }
 
 // Up to 64 tokens.  A weight of few rows needs every block's waves on one sum; one of many is
-// read fastest by blocks of 128 rows, where that leaves enough of them.  Of linear_few, blocks of 64
-// and of 128 rows, 16 tokens x 4096 x 8192 outputs take 19.6, 20.0 and 35.5 us, x 16384 37.6, 25.6 and
-// 37.0, x 24576 55, 43.5 and 38.9; 64 tokens x 4096 x 4096 23.6, 26.6 and 43, x 8192 44.6, 28.0 and 44.
+// read fastest by blocks of 128 rows, where that leaves enough of them.  Of linear_few, blocks of
+// 64 and of 128 rows, 16 tokens x 4096 x 8192 outputs take 19.6, 20.0 and 35.5 us, x 16384 37.6,
+// 25.6 and 37.0, x 24576 55, 43.5 and 38.9; 64 tokens x 4096 x 4096 23.6, 26.6 and 43, x 8192
+// 44.6, 28.0 and 44.
 template <int kTok>
 hipError_t launch_few(const LinearArgs& a, hipStream_t stream) {
   const int64_t n = a.padded_out;
