@@ -31,6 +31,8 @@ static_assert(kBK == kLmheadSlabK, "slab width shared with the boundary");
 
 // 16 bytes at any element's address
 typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint16_t u16x4u __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 
 __device__ __forceinline__ float bf16_float(uint16_t b) {
   return __uint_as_float((uint32_t)b << 16);
@@ -67,12 +69,13 @@ __device__ __forceinline__ float normal_cdf(float z, float bell) {
   const float q = p * t * bell;
   return z < 0.0f ? q : 1.0f - q;
 }
-// tanh: below 2^-6 its series (the next term is 2/15 u^4 < 2^-26 of it), where 1 - e would
-// cancel.
-__device__ __forceinline__ float tanh_of(float u) {
-  const float a = fabsf(u), e = exp2_hw(a * (-2.0f * kLog2e));
-  const float t = a < 0.015625f ? fmaf(a * a * a, -1.0f / 3.0f, a) : (1.0f - e) * rcp_hw(1.0f + e);
-  return copysignf(t, u);
+// cap tanh(u), u = z / cap: cap - 2 cap / (1 + exp(2u)); below 2^-4, where that would cancel, the
+// series z (1 - u^2 / 3 + 2 u^4 / 15), whose next term is 2^-28 of it.
+__device__ __forceinline__ float soft_cap(float z, float cap, float inv_cap) {
+  const float u = z * inv_cap, q = u * u;
+  const float far = fmaf(-2.0f * cap, rcp_hw(1.0f + exp2_hw(u * (2.0f * kLog2e))), cap);
+  const float near = z * fmaf(fmaf(q, 2.0f / 15.0f, -1.0f / 3.0f), q, 1.0f);
+  return fabsf(u) < 0.0625f ? near : far;
 }
 
 template <int kAct>
@@ -82,7 +85,7 @@ __device__ __forceinline__ float act_of(float z, float cap, float inv_cap) {
   if constexpr (kAct == kActGelu) return z * normal_cdf(z, bell(z));
   if constexpr (kAct == kActGeluTanh)  // (1 + tanh(u)) / 2 = sigmoid(2u)
     return z * sigmoid(2.0f * kGeluC * (z + kGeluA * z * z * z));
-  if constexpr (kAct == kActSoftcap) return cap * tanh_of(z * inv_cap);
+  if constexpr (kAct == kActSoftcap) return soft_cap(z, cap, inv_cap);
   return z;
 }
 
@@ -231,11 +234,45 @@ __global__ __launch_bounds__((Shape<kVSn, kTok, kWB>::kThr), 2) void linear_tile
   }
   const int32_t nw = n0 + wave / kWB * (16 * kVSn), mw = m0 + wave % kWB * (16 * kTok);
   char* own = smem + wave * S::kOwn;
+  const bool inside = nw + 16 * kVSn <= a.out_dim;  // (all of the wave's outputs)
+  auto add_bias = [&](auto&& at) __attribute__((always_inline)) {
+    constexpr int kBatch = kVSn < 4 ? kVSn : 4;
 #pragma unroll
-  for (int vs = 0; vs < kVSn; ++vs) {
-    const f32x4 b = bias_of(a, nw + vs * 16 + 4 * (lane >> 4));
+    for (int vs = 0; vs < kVSn; vs += kBatch) {
+      f32x4 b[kBatch];
 #pragma unroll
-    for (int ts = 0; ts < kTok; ++ts) acc[vs][ts] += b;
+      for (int i = 0; i < kBatch; ++i) b[i] = at(nw + (vs + i) * 16 + 4 * (lane >> 4));
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+        for (int ts = 0; ts < kTok; ++ts) acc[vs + i][ts] += b[i];
+    }
+  };
+  if (a.bias) {
+    if (!inside)
+      add_bias([&](int32_t n) { return bias_of(a, n); });
+    else if (a.bias_bf16)
+      add_bias([&](int32_t n) {
+        const u16x4u b = *reinterpret_cast<const u16x4u*>(
+            static_cast<const uint16_t*>(a.bias) + n);
+        return f32x4{bf16_float(b[0]), bf16_float(b[1]), bf16_float(b[2]), bf16_float(b[3])};
+      });
+    else
+      add_bias([&](int32_t n) {
+        return (f32x4)*reinterpret_cast<const f32x4u*>(static_cast<const float*>(a.bias) + n);
+      });
+  }
+  // The residual comes in by whole rows, all on their way before z's copy goes out (tokens from
+  // the last on again: they are not written).  A wave at the outputs' end takes them later.
+  const uint16_t* res = static_cast<const uint16_t*>(a.residual);
+  const bool ahead = res && inside;
+  u32x4 held[kVSn * kTok / 2];
+  if (ahead) {
+    int j = 0;
+    whole_rows<kTok, kVSn>(own, lane, [&](int r, int c, u32x4*) __attribute__((always_inline)) {
+      held[j++] = *reinterpret_cast<const u32x4u*>(res + min(mw + r, a.tokens - 1) *
+                                                   a.ld_residual + nw + c * 8);
+    });
   }
   const float by = a.activation == kActSoftcap ? 1.0f / a.cap : 1.0f;
   if (a.saved && a.saved_f32) {
@@ -268,9 +305,12 @@ __global__ __launch_bounds__((Shape<kVSn, kTok, kWB>::kThr), 2) void linear_tile
             *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.saved) + m * a.ld_saved + n) = x;
         });
   }
-  if (a.residual) {
-    // in by whole rows, to where the accumulators will find it
-    const uint16_t* res = static_cast<const uint16_t*>(a.residual);
+  if (ahead) {
+    int j = 0;
+    whole_rows<kTok, kVSn>(own, lane, [&](int, int, u32x4* at) __attribute__((always_inline)) {
+      *at = held[j++];
+    });
+  } else if (res) {
     whole_rows<kTok, kVSn>(own, lane, [&](int r, int c, u32x4* at)
                                           __attribute__((always_inline)) {
       const int32_t m = mw + r, n = nw + c * 8;
@@ -280,19 +320,14 @@ __global__ __launch_bounds__((Shape<kVSn, kTok, kWB>::kThr), 2) void linear_tile
       } o;
       o.x = u32x4{0, 0, 0, 0};
       if (m < a.tokens) {
-        const uint16_t* from = res + m * a.ld_residual + n;
-        if (n + 8 <= a.out_dim) {
-          o.x = *reinterpret_cast<const u32x4u*>(from);
-        } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (n + e < a.out_dim) o.e[e] = from[e];
-        }
+        for (int e = 0; e < 8; ++e)
+          if (n + e < a.out_dim) o.e[e] = res[m * a.ld_residual + n + e];
       }
       *at = o.x;
     });
   }
-  const bool add = a.residual != nullptr;
+  const bool add = res != nullptr;
   with_activation(a, [&](auto&& act) __attribute__((always_inline)) {
     store_rows<kTok, kVSn>(
         smem, wave, lane,
