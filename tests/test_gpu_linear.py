@@ -227,3 +227,24 @@ def test_the_smallest_and_the_largest_cap(m):
         # (the sum of m terms: m roundings of 2^-24)
         bound = dy.double().abs().sum(0) * slope * (2.0 ** -20 + m * 2.0 ** -24)
         assert ((db.double() - exact).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("m", [1000, 850])
+def test_a_last_round_in_half_tiles(m):
+    """1320 of the largest tiles are five rounds of the chip and 40 more, of which the half behind
+    the last token (850: from 896 on) has nothing to do."""
+    n, k = 84480, 64
+    c = C.make_case(m, k, n, "silu", 9 + m, DEV, BF16, True)
+    y, saved = rlk.linear_forward(c.x, c.w, c.bias, c.residual, activation="silu", save=True)
+    for at in range(0, n, 16896):  # the bounds by pieces
+        here = slice(at, at + 16896)
+        piece = C.Case(c.x, c.w[here], c.bias[here], c.residual[:, here], c.dy[:, here], "silu")
+        assert C.worst(y[:, here], *C.forward64(piece)) <= 1.0
+        z, ez = C.product64(piece)
+        # (fp16's half step)
+        assert ((saved[:, here].double() - z).abs() <= ez + 2.0 ** -11 * (z.abs() + ez)
+                + 2.0 ** -25).all()
+    # the same bits as of the last outputs alone, which take other tiles
+    last, _ = rlk.linear_forward(c.x, c.w[-4096:].contiguous(), c.bias[-4096:].contiguous(),
+                                 c.residual[:, -4096:], activation="silu")
+    assert torch.equal(bits(y[:, -4096:]), bits(last))

@@ -193,10 +193,10 @@ __device__ __forceinline__ void put_out(const LinearArgs& a, int32_t m, int32_t 
 // linear_tiles: 32 kVSn outputs x 16 kTok kWB tokens a block, by the tile product; then bias,
 // activation, residual and z's copy on a lane's 4 outputs, and whole rows out through LDS.
 // Bound by the matrix cores and by what stands beside them: a slab of the 256 x 256 tile takes
-// 1.45 us, which is 1.48 PFLOP/s, and a tile 20 us more for its first loads, its epilogue and its
-// stores, which nothing hides at one block a CU.  1024 x 2048 x 151936: 640 us without an
-// activation (1.0 PFLOP/s), 684-745 with the soft cap; 4096 x 4096 x 4096: 124 us (1.11), with a
-// residual, SiLU and z kept 142.
+// 1.45 us, which is 1.48 PFLOP/s, and a tile 12-20 us more for its first loads, its epilogue and
+// its stores, which nothing hides at one block a CU.  1024 x 2048 x 151936: 606 us without an
+// activation (1.05 PFLOP/s), 651 with the soft cap; 4096 x 4096 x 4096: 109 us (1.26), with a
+// bias, a residual, SiLU and z kept 117.
 // ---------------------------------------------------------------------------
 template <int kVSn, int kTok, int kWB>
 struct Shape {
@@ -204,6 +204,7 @@ struct Shape {
   static constexpr int kWavesN = 2 * kWB, kThr = 64 * kWavesN;
   static constexpr int kLds = 2 * (kA + kB) * kRowBytes;
   static constexpr int kOwn = 512 * kVSn * kTok;  // bytes of a wave's rows
+  static constexpr bool kSplits = kB == 256;      // see launch_tiles
   static_assert(kLds >= kWavesN * kOwn, "the rows fit");
   typedef TileOperandOf<kA / (kWavesN * kRowsPerLoad)> OperandA;
   typedef TileOperandOf<kB / (kWavesN * kRowsPerLoad)> OperandB;
@@ -212,17 +213,11 @@ struct Shape {
 };
 
 template <int kVSn, int kTok, int kWB>
-__global__ __launch_bounds__((Shape<kVSn, kTok, kWB>::kThr), 2) void linear_tiles(LinearArgs a,
-                                                                               int32_t n_a,
-                                                                               int32_t n_b,
-                                                                               int64_t blk_begin) {
+__device__ __forceinline__ void linear_tile(const LinearArgs& a, char* smem, int32_t n0,
+                                            int32_t m0) {
   typedef Shape<kVSn, kTok, kWB> S;
-  __shared__ __attribute__((aligned(16))) char smem[S::kLds];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  int32_t ta, tb;
-  tile_of(blk_begin + xcd_local_block(blockIdx.x, gridDim.x), n_a, n_b, ta, tb);
-  const int32_t n0 = ta * S::kA, m0 = tb * S::kB;
   const int64_t row_bytes = (int64_t)a.in_dim * 2;
   f32x4 acc[kVSn][kTok] = {};
   if (n0 < a.out_dim) {  // (else a tile of padding)
@@ -352,6 +347,28 @@ __global__ __launch_bounds__((Shape<kVSn, kTok, kWB>::kThr), 2) void linear_tile
           put_out(a, mw + r, nw + c * 8, x);
         });
   });
+}
+
+// Blocks [0, n_whole) take a tile each, the others half a tile's tokens.
+template <int kVSn, int kTok, int kWB>
+__global__ __launch_bounds__((Shape<kVSn, kTok, kWB>::kThr), 2) void linear_tiles(
+    LinearArgs a, int32_t n_a, int32_t n_b, int64_t n_whole, int64_t blk_begin) {
+  typedef Shape<kVSn, kTok, kWB> S;
+  __shared__ __attribute__((aligned(16))) char smem[S::kLds];
+  // (the halves are the last to be dispatched)
+  const uint32_t whole =
+      (uint32_t)max((int64_t)0, min(n_whole - blk_begin, (int64_t)gridDim.x));
+  int32_t ta, tb;
+  if (blockIdx.x < whole) {
+    tile_of(blk_begin + xcd_local_block(blockIdx.x, whole), n_a, n_b, ta, tb);
+    linear_tile<kVSn, kTok, kWB>(a, smem, ta * S::kA, tb * S::kB);
+  } else if constexpr (S::kSplits) {
+    const int64_t at = blk_begin + whole - n_whole +
+                       xcd_local_block(blockIdx.x - whole, gridDim.x - whole);
+    tile_of(n_whole + at / 2, n_a, n_b, ta, tb);
+    const int32_t m0 = tb * S::kB + (int32_t)(at % 2) * (S::kB / 2);
+    if (m0 < a.tokens) linear_tile<kVSn, kTok / 2, kWB>(a, smem, ta * S::kA, m0);
+  }
 }
 
 // 4 outputs of token m from output n (a multiple of 4) on: the rest of the epilogue.
@@ -712,13 +729,18 @@ int best_tile(Blocks&& blocks) {
   return best;
 }
 
+// Of the largest tiles one fits a CU.  What they leave for a last round, if it is at most half
+// of one, goes in halves of a tile, to twice as many CUs (1024 x 2048 x 151936, 9.3 rounds:
+// 617 -> 606 us; 1024 x 2048 x 33280, 2.03: 159 -> 140; 1024 x 1024 x 21504, 1.3: 60.5 -> 50.8).
 template <int kVSn, int kTok, int kWB>
 hipError_t launch_tiles(const LinearArgs& a, hipStream_t stream) {
   typedef Shape<kVSn, kTok, kWB> S;
   const int32_t n_a = (a.padded_out + S::kA - 1) / S::kA, n_b = (a.tokens + S::kB - 1) / S::kB;
-  return in_launches((int64_t)n_a * n_b, S::kThr, [&](int64_t b, int64_t nb) {
+  const int64_t n = (int64_t)n_a * n_b, rest = n % 256;
+  const int64_t halves = S::kSplits && n > 256 && rest <= 128 ? rest : 0;
+  return in_launches(n + halves, S::kThr, [&](int64_t b, int64_t nb) {
     hipLaunchKernelGGL((linear_tiles<kVSn, kTok, kWB>), dim3((unsigned)nb), dim3(S::kThr), 0,
-                       stream, a, n_a, n_b, b);
+                       stream, a, n_a, n_b, n - halves, b);
   });
 }
 
