@@ -2,7 +2,7 @@
 one seeded case and saves the output bits to the path it is given.  The library reads
 RLK_MAX_LAUNCH_THREADS once per process.
 
-    python -m tests.head_child OUT.pt
+    python -m tests.head_child OUT.pt [halves]
 """
 from __future__ import annotations
 
@@ -45,7 +45,15 @@ def run_all():
     return out
 
 
+def run_halves():
+    """A product whose last 40 of 1320 tiles go in halves; sums of its rows' bits."""
+    c = L.make_case(1000, 64, 84480, "silu", 5, DEV)
+    y, _ = rlk.linear_forward(c.x, c.w, c.bias, c.residual, activation="silu")
+    torch.cuda.synchronize()
+    return {"halves": (bits(y).sum(1).to(torch.int32),)}
+
+
 if __name__ == "__main__":
     print("head child: running", flush=True)
-    torch.save(run_all(), sys.argv[1])
+    torch.save(run_halves() if sys.argv[2:] == ["halves"] else run_all(), sys.argv[1])
     print("head child: done", flush=True)

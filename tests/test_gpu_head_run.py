@@ -14,7 +14,7 @@ import torch
 import vocab_selected_token_amd as rlk
 from tests import linear_cases as L
 from tests import process_cases as P
-from tests.head_child import run_all
+from tests.head_child import run_all, run_halves
 from tests.test_gpu_streams import check as check_beside_a_busy_stream
 
 pytestmark = pytest.mark.gpu
@@ -298,6 +298,21 @@ def test_split_launches_give_the_same_bits(tmp_path):
         for key in ref:
             for a, b in zip(ref[key], got[key]):
                 assert torch.equal(a, b), f"{key} differs with a {limit}-thread launch limit"
+
+
+def test_split_launches_of_half_tiles(tmp_path):
+    """Blocks of 512 threads: the second launch begins with whole tiles (after 1000 blocks), and
+    among the halves (after 1290)."""
+    (want,) = run_halves()["halves"]
+    for blocks in (1000, 1290):
+        print(f"launch limit {blocks} blocks (child process)", flush=True)
+        out = tmp_path / f"halves_{blocks}.pt"
+        env = dict(os.environ, RLK_MAX_LAUNCH_THREADS=str(512 * blocks))
+        r = subprocess.run([sys.executable, "-u", "-m", "tests.head_child", str(out), "halves"],
+                           cwd=ROOT, env=env, capture_output=True, text=True, timeout=100)
+        assert r.returncode == 0, f"{r.stdout[-2000:]}\n{r.stderr[-3000:]}"
+        (got,) = torch.load(out, weights_only=True)["halves"]
+        assert torch.equal(got, want)
 
 
 def test_rows_past_4_gib():
