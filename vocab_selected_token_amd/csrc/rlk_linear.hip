@@ -151,16 +151,31 @@ __device__ __forceinline__ void with_activation(const LinearArgs& a, Finish&& fi
   finish([](float z) { return z; });
 }
 
-// The bias of 4 consecutive outputs (0 from out_dim on).
-__device__ __forceinline__ f32x4 bias_of(const LinearArgs& a, int32_t n) {
-  f32x4 b = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (!a.bias) return b;
+__device__ __forceinline__ f32x4 floats_of(const u16x4u& b) {
+  return f32x4{bf16_float(b[0]), bf16_float(b[1]), bf16_float(b[2]), bf16_float(b[3])};
+}
+// 4 consecutive elements from n on (0 from `end` on).
+__device__ __forceinline__ f32x4 four_of(const uint16_t* from, int32_t n, int32_t end) {
+  if (n + 4 <= end) return floats_of(*reinterpret_cast<const u16x4u*>(from + n));
+  f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int e = 0; e < 4; ++e)
-    if (n + e < a.out_dim)
-      b[e] = a.bias_bf16 ? bf16_float(static_cast<const uint16_t*>(a.bias)[n + e])
-                         : static_cast<const float*>(a.bias)[n + e];
-  return b;
+    if (n + e < end) x[e] = bf16_float(from[n + e]);
+  return x;
+}
+__device__ __forceinline__ f32x4 four_of(const float* from, int32_t n, int32_t end) {
+  if (n + 4 <= end) return *reinterpret_cast<const f32x4u*>(from + n);
+  f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (n + e < end) x[e] = from[n + e];
+  return x;
+}
+// The bias of 4 consecutive outputs.
+__device__ __forceinline__ f32x4 bias_of(const LinearArgs& a, int32_t n) {
+  if (!a.bias) return f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  return a.bias_bf16 ? four_of(static_cast<const uint16_t*>(a.bias), n, a.out_dim)
+                     : four_of(static_cast<const float*>(a.bias), n, a.out_dim);
 }
 
 constexpr uint16_t kNegInfBf16 = 0xFF80;
@@ -248,9 +263,8 @@ __device__ __forceinline__ void linear_tile(const LinearArgs& a, char* smem, int
       add_bias([&](int32_t n) { return bias_of(a, n); });
     else if (a.bias_bf16)
       add_bias([&](int32_t n) {
-        const u16x4u b = *reinterpret_cast<const u16x4u*>(
-            static_cast<const uint16_t*>(a.bias) + n);
-        return f32x4{bf16_float(b[0]), bf16_float(b[1]), bf16_float(b[2]), bf16_float(b[3])};
+        return floats_of(
+            *reinterpret_cast<const u16x4u*>(static_cast<const uint16_t*>(a.bias) + n));
       });
     else
       add_bias([&](int32_t n) {
@@ -371,8 +385,23 @@ __global__ __launch_bounds__((Shape<kVSn, kTok, kWB>::kThr), 2) void linear_tile
   }
 }
 
-// 4 outputs of token m from output n (a multiple of 4) on: the rest of the epilogue.
-__device__ __forceinline__ void finish4(const LinearArgs& a, int32_t m, int32_t n, f32x4 z) {
+// What the epilogue adds to 4 outputs of token m from output n (a multiple of 4) on.
+struct Added {
+  f32x4 bias, residual;
+};
+__device__ __forceinline__ Added added_to(const LinearArgs& a, int32_t m, int32_t n) {
+  Added o;
+  o.bias = bias_of(a, n);
+  o.residual = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  if (a.residual)
+    o.residual = four_of(static_cast<const uint16_t*>(a.residual) + m * a.ld_residual, n,
+                         a.out_dim);
+  return o;
+}
+
+// Those outputs: the rest of the epilogue.
+__device__ __forceinline__ void finish4(const LinearArgs& a, int32_t m, int32_t n, f32x4 z,
+                                        const Added& add) {
   uint16_t* out = static_cast<uint16_t*>(a.out) + m * a.ld_out + n;
   union {
     uint16_t e[4];
@@ -380,7 +409,7 @@ __device__ __forceinline__ void finish4(const LinearArgs& a, int32_t m, int32_t 
   } o;
   o.x = 0xFF80FF80FF80FF80ull;
   if (n < a.out_dim) {
-    z += bias_of(a, n);
+    if (a.bias) z += add.bias;
     if (a.saved) {
       const float by = a.activation == kActSoftcap ? 1.0f / a.cap : 1.0f;
       if (a.saved_f32) {
@@ -398,10 +427,8 @@ __device__ __forceinline__ void finish4(const LinearArgs& a, int32_t m, int32_t 
     });
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const bool on = n + e < a.out_dim;
-      if (on && a.residual)
-        z[e] += bf16_float(static_cast<const uint16_t*>(a.residual)[m * a.ld_residual + n + e]);
-      o.e[e] = on ? bf16_bits(z[e]) : kNegInfBf16;
+      if (a.residual) z[e] += add.residual[e];
+      o.e[e] = n + e < a.out_dim ? bf16_bits(z[e]) : kNegInfBf16;
     }
   }
   if (n + 4 <= a.padded_out) {
@@ -431,6 +458,12 @@ __global__ __launch_bounds__(64 * kFewWaves) void linear_few(LinearArgs a, int64
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int32_t n0 = (int32_t)(blk_begin + blockIdx.x) * 16;
   const int fr = lane & 15, fc = lane >> 4;
+  // 4 outputs of a token in the end: what is added to them is on its way first
+  const int m = threadIdx.x / 4, at = threadIdx.x % 4;
+  static_assert(kTokens * 4 <= 64 * kFewWaves, "a thread takes 4 outputs of a token");
+  const bool mine = m < min(kTokens, a.tokens) && n0 + at * 4 < a.padded_out;
+  Added add = {};
+  if (mine) add = added_to(a, m, n0 + at * 4);
   if (n0 < a.out_dim) {
     const uint16_t *w, *x[kTok];
     w = static_cast<const uint16_t*>(a.weight) +
@@ -475,16 +508,14 @@ __global__ __launch_bounds__(64 * kFewWaves) void linear_few(LinearArgs a, int64
     for (int ts = 0; ts < kTok; ++ts) part[wave][ts * 16 + fr][fc] = acc[ts];
   }
   __syncthreads();
-  const int m = threadIdx.x / 4, at = threadIdx.x % 4;
-  static_assert(kTokens * 4 <= 64 * kFewWaves, "a thread takes 4 outputs of a token");
-  if (m >= min(kTokens, a.tokens) || n0 + at * 4 >= a.padded_out) return;
+  if (!mine) return;
   f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
   if (n0 < a.out_dim) {
     z = part[0][m][at];
 #pragma unroll
     for (int i = 1; i < kFewWaves; ++i) z += part[i][m][at];
   }
-  finish4(a, m, n0 + at * 4, z);
+  finish4(a, m, n0 + at * 4, z, add);
 }
 
 // ---------------------------------------------------------------------------
@@ -512,7 +543,7 @@ __global__ __launch_bounds__(kStreamThreads) void linear_stream(LinearArgs a, in
 #pragma unroll
     for (int ts = 0; ts < kTok; ++ts) {
       const int32_t m = ts * 16 + (lane & 15), n = n0 + (wave * kRT + rt) * 16 + 4 * (lane >> 4);
-      if (m < a.tokens && n < a.padded_out) finish4(a, m, n, acc[rt][ts]);
+      if (m < a.tokens && n < a.padded_out) finish4(a, m, n, acc[rt][ts], added_to(a, m, n));
     }
 }
 
