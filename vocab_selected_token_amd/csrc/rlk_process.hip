@@ -178,8 +178,10 @@ struct Counter {
   }
 };
 
-// A row's logits and its grammar's bits, as buffers: a lane's offset is fixed, a span's is
-// uniform, and what lies behind the last real column reads as 0.
+// A row's logits and its grammar's bits, as buffers: what lies behind the last real column reads
+// as 0.  A load's whole position stands in its vector offset: a buffer's bounds are compared with
+// that one, and a position in the scalar offset, which can lie behind the row by itself, is not
+// sure to be held to them.
 struct RowBuffers {
   __amdgpu_buffer_rsrc_t logits, allow;
 };
@@ -190,15 +192,20 @@ struct Piece {
   uint32_t bits[kPieceChunks];  // which of a chunk's columns are allowed (with a grammar)
 };
 
+__device__ __forceinline__ void load_bits(Piece& p, int i, const RowBuffers& b, int32_t c0,
+                                          int lane) {
+#if defined(__HIP_DEVICE_COMPILE__)  // the host pass cannot instantiate the target's builtins
+  p.bits[i] = __builtin_amdgcn_raw_buffer_load_b8(
+      b.allow, (uint32_t)c0 / 8 + (uint32_t)lane + i * 64, 0, 0);
+#endif
+}
 __device__ __forceinline__ void load_chunk(Piece& p, int i, const RowBuffers& b, bool allow,
                                            int32_t c0, int lane) {
-#if defined(__HIP_DEVICE_COMPILE__)  // the host pass cannot instantiate the target's builtins
+#if defined(__HIP_DEVICE_COMPILE__)
   p.raw[i] = __builtin_bit_cast(
-      u32x4, __builtin_amdgcn_raw_buffer_load_b128(b.logits, (uint32_t)lane * 16 + i * 1024,
-                                                   (uint32_t)c0 * 2, 0));
-  if (allow)
-    p.bits[i] = __builtin_amdgcn_raw_buffer_load_b8(b.allow, (uint32_t)lane + i * 64,
-                                                    (uint32_t)c0 / 8, 0);
+      u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                 b.logits, (uint32_t)c0 * 2 + (uint32_t)lane * 16 + i * 1024, 0, 0));
+  if (allow) load_bits(p, i, b, c0, lane);
 #endif
 }
 
@@ -327,12 +334,9 @@ __device__ __forceinline__ void for_spans(const Part& part, int32_t real_vocab,
     b.allow = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(o.allow), 0,
                                                 (int)(((uint32_t)real_vocab + 7) / 8),
                                                 kBufferWord3);
-#if defined(__HIP_DEVICE_COMPILE__)
 #pragma unroll
     for (int i = 0; i < kPieceChunks; ++i)
-      p.bits[i] = __builtin_amdgcn_raw_buffer_load_b8(
-          b.allow, (uint32_t)lane + i * 64, (uint32_t)(part.c0 + wave * kPiece) / 8, 0);
-#endif
+      load_bits(p, i, b, part.c0 + wave * kPiece, lane);
   }
   auto spans = [&](auto&& count, uint32_t* own) __attribute__((always_inline)) {
     for (int32_t c0 = part.c0; c0 < part.c1; c0 += kSpan) {
