@@ -1095,7 +1095,7 @@ class LogitRules:
                 raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
             if t.dim() != 1 or not t.is_contiguous():
                 raise ValueError(f"{name} must be 1-D and contiguous")
-            if t is not history:
+            if name != "history":  # (whose tensor may be an index too)
                 if rows is None:
                     rows = t.numel()
                 elif t.numel() != rows:
