@@ -609,8 +609,9 @@ typedef struct rlk_linear_desc {
  *               are -inf (the logits of padding), columns from padded_out on are not touched.
  *   saved       (device) [tokens, ld_saved] of saved_dtype, 16-byte aligned, out, or NULL: z
  *               (z / cap for the soft cap) clamped to +-65504, which rlk_linear_bwd needs
- *               unless the activation is RLK_ACT_NONE.  Columns from out_dim on may be
- *               written.
+ *               unless the activation is RLK_ACT_NONE; in fp16 a positive z of RLK_ACT_RELU
+ *               keeps at least the smallest positive value, 2^-24, for its slope.  Columns
+ *               from out_dim on may be written.
  * No output may overlap an input or another output.  Repeated calls give the same bits. */
 rlk_status rlk_linear_fwd(const rlk_linear_desc* desc, const void* x, const void* weight,
                           const void* bias, const void* residual, void* out, void* saved,

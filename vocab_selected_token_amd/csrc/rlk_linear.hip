@@ -129,8 +129,18 @@ __device__ __forceinline__ void with_slope(int activation, Use&& use) {
 __device__ __forceinline__ float clamped(float z) {
   return z > 65504.0f ? 65504.0f : z < -65504.0f ? -65504.0f : z;
 }
-__device__ __forceinline__ uint16_t fp16_bits(float z) {
-  return __builtin_bit_cast(uint16_t, (_Float16)clamped(z));
+// In fp16 a positive z keeps at least `least`: under ReLU the smallest positive value, since its
+// slope is z's sign, which rounding to 0 would take from z up to 2^-25.
+__device__ __forceinline__ float least_kept(const LinearArgs& a) {
+  return a.activation == kActRelu ? 0x1p-24f : 0.0f;
+}
+__device__ __forceinline__ uint16_t fp16_bits(float z, float least) {
+#if defined(__HIP_DEVICE_COMPILE__)  // the host pass cannot instantiate the target's builtins
+  const float kept = z > 0.0f ? __builtin_amdgcn_fmed3f(z, least, 65504.0f) : clamped(z);
+  return __builtin_bit_cast(uint16_t, (_Float16)kept);
+#else
+  return 0;
+#endif
 }
 __device__ __forceinline__ f32x4 clamped(const f32x4& z) {
   return f32x4{clamped(z[0]), clamped(z[1]), clamped(z[2]), clamped(z[3])};
@@ -297,6 +307,7 @@ __device__ __forceinline__ void linear_tile(const LinearArgs& a, char* smem, int
       }
     }
   } else if (a.saved) {
+    const float least = least_kept(a);
     store_rows<kTok, kVSn>(
         smem, wave, lane,
         [&](int vs, int ts) __attribute__((always_inline)) {
@@ -305,7 +316,7 @@ __device__ __forceinline__ void linear_tile(const LinearArgs& a, char* smem, int
             uint64_t x;
           } o;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o.e[e] = fp16_bits(acc[vs][ts][e] * by);
+          for (int e = 0; e < 4; ++e) o.e[e] = fp16_bits(acc[vs][ts][e] * by, least);
           return o.x;
         },
         [&](int r, int c, const u32x4& x) __attribute__((always_inline)) {
@@ -417,7 +428,7 @@ __device__ __forceinline__ void finish4(const LinearArgs& a, int32_t m, int32_t 
             clamped(z * by);
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o.e[e] = fp16_bits(z[e] * by);
+        for (int e = 0; e < 4; ++e) o.e[e] = fp16_bits(z[e] * by, least_kept(a));
         *reinterpret_cast<uint64_t*>(static_cast<uint16_t*>(a.saved) + m * a.ld_saved + n) = o.x;
       }
     }
