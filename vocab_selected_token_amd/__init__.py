@@ -1452,6 +1452,12 @@ def _run_linear_backward(x, weight, grad_out, saved, act, cap, want_x, want_weig
     return dx, dw, db
 
 
+def _forward_mode():
+    """Whether tensors may have tangents.  The level is not part of torch's documented interface;
+    where it is gone, they may."""
+    return getattr(torch.autograd.forward_ad, "_current_level", 0) >= 0
+
+
 class _HeadLinear(torch.autograd.Function):
     """residual + act(x . weight^T + bias), differentiable in all four; the forward and the
     backward are rlk_linear_fwd and rlk_linear_bwd."""
@@ -1497,9 +1503,10 @@ def head_linear(x: torch.Tensor, weight: torch.Tensor, bias=None, residual=None,
     _check_linear(x, weight, n, bias, residual=residual)
     if bias is not None and bias.shape[0] != n:
         raise ValueError(f"bias must have {n} elements, got {bias.shape[0]}")
-    if not torch.is_grad_enabled() or not (
+    # (forward mode is torch's to refuse: a tensor with a tangent need not require a gradient)
+    if not _forward_mode() and (not torch.is_grad_enabled() or not (
             x.requires_grad or weight.requires_grad or (bias is not None and bias.requires_grad)
-            or (residual is not None and residual.requires_grad)):
+            or (residual is not None and residual.requires_grad))):
         return _run_linear(x, weight, bias, residual, act, cap, n, n, False)[0]
     return _HeadLinear.apply(x, weight, bias, residual, act, cap)
 
