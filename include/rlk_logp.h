@@ -519,8 +519,8 @@ typedef struct rlk_logit_rules {
  *   logits      (device) bf16 [N, ld_logits], 16-byte aligned.
  *   out         (device) [N, ld_out] of out_dtype, 16-byte aligned: y rounded once; columns
  *               [V_real, V_pad) are -inf, columns from V_pad on are not touched.  ld_out >=
- *               V_pad, a multiple of 8.  out may be logits itself (bf16, the same ld); they
- *               may not overlap otherwise. */
+ *               V_pad, a multiple of 8.  out may be logits itself (bf16, the same ld);
+ *               otherwise no byte of the two may be the same (refused). */
 rlk_status rlk_logits_process(const rlk_logp_desc* desc, const void* logits,
                               const rlk_logit_rules* rules, void* out, int64_t ld_out,
                               rlk_dtype out_dtype, void* stream);
@@ -551,7 +551,8 @@ rlk_status rlk_logp_processed_fwd(const rlk_logp_desc* desc, const void* logits,
  *   desc, logits, rules, targets, active_mask   as for the forward.
  *   lse         (device) float [N]: the forward's LSE.
  *   grad_logp, grad_lse  (device) float [N] each, or NULL for zero; at least one given.
- *   dlogits, ld_dlogits, dlogits_dtype, bad targets   as for rlk_logp_bwd.
+ *   dlogits, ld_dlogits, dlogits_dtype, bad targets   as for rlk_logp_bwd; no byte of
+ *               dlogits may be one of logits (refused).
  *   workspace   >= 256 bytes (the status words), 256-byte aligned. */
 rlk_status rlk_logp_processed_bwd(const rlk_logp_desc* desc, const void* logits,
                                   const rlk_logit_rules* rules, const int32_t* targets,

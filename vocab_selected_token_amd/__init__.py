@@ -1162,8 +1162,8 @@ def process_logits(logits: torch.Tensor, rules: LogitRules, *, real_vocab: int,
                    out: torch.Tensor | None = None, stream=None):
     """The processed logits [N, V_pad] (bf16 or fp32; rows padded to a multiple of 8 columns,
     columns [real_vocab, V_pad) -inf).  logits: bf16 [N, ld] with unit column stride.  With `out`
-    they are written there, a tensor of out_dtype with at least V_pad columns: the logits
-    themselves, for instance; what lies behind V_pad stays."""
+    they are written there, a tensor of out_dtype with at least V_pad columns, whose rows lie
+    beside those of the logits or are the logits themselves; what lies behind V_pad stays."""
     if out_dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("out_dtype must be torch.float32 or torch.bfloat16")
     v_pad = _check_vocab(logits, real_vocab, padded_vocab)

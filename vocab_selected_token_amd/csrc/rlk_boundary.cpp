@@ -1046,6 +1046,34 @@ rlk_status check_out(const rlk_logp_desc* d, int64_t ld, const char* name) {
   return RLK_OK;
 }
 
+typedef __int128 wide;  // (a stride may be any number)
+
+// `n` rows of `width` elements of `size` bytes each, `ld` (>= width) elements apart.
+struct Rows {
+  wide first, end, width, stride;  // in bytes
+  Rows(const void* at, int64_t n, int64_t width_, int64_t ld, int size)
+      : first(reinterpret_cast<uintptr_t>(at)),
+        end(first + (n - 1) * (wide)ld * size + (wide)width_ * size),
+        width((wide)width_ * size),
+        stride((wide)ld * size) {}
+};
+
+// Whether two of as many rows each share a byte (with different strides: whether their extents do).
+bool overlap(const Rows& x, const Rows& y) {
+  if (y.first >= x.end || x.first >= y.end) return false;
+  if (x.stride != y.stride) return true;
+  // y's rows lie this far behind those of x
+  const wide by = ((y.first - x.first) % x.stride + x.stride) % x.stride;
+  return by < x.width || by + y.width > x.stride;
+}
+
+// What a pass over the logits' rows writes, `padded_vocab` of `ld` columns: beside them.
+bool over_logits(const rlk_logp_desc* d, const void* logits, const void* out, int64_t ld,
+                 rlk_dtype dtype) {
+  return overlap(Rows(logits, d->num_tokens, d->real_vocab, d->ld_logits, 2),
+                 Rows(out, d->num_tokens, d->padded_vocab, ld, dtype == RLK_DTYPE_BF16 ? 2 : 4));
+}
+
 struct ProcessedLayout {
   size_t pmax, psum, target_logit, total;
 };
@@ -1107,6 +1135,8 @@ rlk_status rlk_logits_process(const rlk_logp_desc* desc, const void* logits,
     return fail(RLK_ERR_ALIGNMENT, "logits and out must be 16-byte aligned");
   if (logits == out && (out_dtype != RLK_DTYPE_BF16 || ld_out != desc->ld_logits))
     return fail(RLK_ERR_BAD_SHAPE, "out can be logits only in bf16 with the same ld");
+  if (logits != out && over_logits(desc, logits, out, ld_out, out_dtype))
+    return fail(RLK_ERR_BAD_SHAPE, "out overlaps the logits and is not the logits");
   const hipError_t e = rlk::launch_process(
       logits, desc->ld_logits, (int32_t)desc->num_tokens, (int32_t)desc->real_vocab,
       (int32_t)desc->padded_vocab, r, out, ld_out, out_dtype == RLK_DTYPE_BF16,
@@ -1179,8 +1209,9 @@ rlk_status rlk_logp_processed_bwd(const rlk_logp_desc* desc, const void* logits,
   if (desc->num_tokens == 0) return ok();
   if (!logits || !targets || !lse || !dlogits)
     return fail(RLK_ERR_NULL_POINTER, "logits, targets, lse and dlogits must be non-NULL");
-  if (logits == dlogits)  // (a block may write what another still reads)
-    return fail(RLK_ERR_BAD_SHAPE, "dlogits cannot be logits");
+  // (a block may write what another still reads)
+  if (over_logits(desc, logits, dlogits, ld_dlogits, dlogits_dtype))
+    return fail(RLK_ERR_BAD_SHAPE, "dlogits cannot be logits or overlap them");
   if (!grad_logp && !grad_lse)
     return fail(RLK_ERR_NULL_POINTER, "at least one of grad_logp and grad_lse must be non-NULL");
   if (!workspace) return fail(RLK_ERR_WORKSPACE, "workspace is NULL");
