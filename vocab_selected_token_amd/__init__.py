@@ -452,6 +452,16 @@ def _check_device(base, **tensors):
             raise ValueError(f"{name} is on {t.device}, the logits on {base.device}")
 
 
+def _check_workspace(workspace, base):
+    """The caller's own: the C entry points see no more than its address and size."""
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if workspace.device != base.device:
+        raise ValueError(f"workspace is on {workspace.device}, the inputs on {base.device}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+
+
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
 _MASK = (torch.uint8, torch.bool)
@@ -556,6 +566,8 @@ def forward(logits: torch.Tensor, targets: torch.Tensor, active_mask=None, *, re
         lse = torch.empty(n, dtype=torch.float32, device=logits.device)
         if workspace is None:
             workspace = workspace_for(desc, logits.device)
+        else:
+            _check_workspace(workspace, logits)
         rlk_logp_fwd(desc, logits, targets, _u8_mask(active_mask), logp, lse, workspace, stream)
     _handed_over(logits, stream, logp, lse)
     return logp, lse
@@ -581,6 +593,8 @@ def backward(logits: torch.Tensor, targets: torch.Tensor, active_mask, lse: torc
         dl = torch.empty((n, ld_d), dtype=out_dtype, device=logits.device)
         if workspace is None:
             workspace = workspace_for(desc, logits.device)
+        else:
+            _check_workspace(workspace, logits)
         rlk_logp_bwd(desc, logits, targets, _u8_mask(active_mask), lse, grad_logp, dl, ld_d,
                      code, workspace, stream)
     _handed_over(logits, stream, dl)
@@ -603,6 +617,8 @@ def forward_ex(logits: torch.Tensor, targets: torch.Tensor, active_mask=None, *,
         ent = torch.empty(n, dtype=torch.float32, device=logits.device)
         if workspace is None:
             workspace = _bytes_for(rlk_logp_ex_workspace_bytes(desc), logits.device)
+        else:
+            _check_workspace(workspace, logits)
         rlk_logp_fwd_ex(desc, logits, targets, _u8_mask(active_mask), logp, lse, ent, workspace,
                         stream)
     _handed_over(logits, stream, logp, lse, ent)
@@ -631,6 +647,8 @@ def backward_ex(logits: torch.Tensor, targets: torch.Tensor, active_mask, lse: t
         dl = torch.empty((n, ld_d), dtype=out_dtype, device=logits.device)
         if workspace is None:
             workspace = workspace_for(desc, logits.device)
+        else:
+            _check_workspace(workspace, logits)
         rlk_logp_bwd_ex(desc, logits, targets, _u8_mask(active_mask), lse, entropy, grad_logp,
                         grad_lse, grad_ent, dl, ld_d, code, workspace, stream)
     _handed_over(logits, stream, dl)
@@ -720,6 +738,8 @@ def forward_backward(logits: torch.Tensor, targets: torch.Tensor, active_mask,
         dl = torch.empty((n, ld_d), dtype=out_dtype, device=logits.device)
         if workspace is None:
             workspace = _bytes_for(rlk_logp_fwd_bwd_workspace_bytes(desc), logits.device)
+        else:
+            _check_workspace(workspace, logits)
         rlk_logp_fwd_bwd(desc, logits, targets, _u8_mask(active_mask), grad_logp, logp, lse, dl,
                          ld_d, code, workspace, stream)
     _handed_over(logits, stream, logp, lse, dl)
@@ -753,6 +773,8 @@ def forward_backward_ex(logits: torch.Tensor, targets: torch.Tensor, active_mask
         dl = torch.empty((n, ld_d), dtype=out_dtype, device=logits.device)
         if workspace is None:
             workspace = _bytes_for(rlk_logp_fwd_bwd_ex_workspace_bytes(desc), logits.device)
+        else:
+            _check_workspace(workspace, logits)
         rlk_logp_fwd_bwd_ex(desc, logits, targets, _u8_mask(active_mask), grad_logp, grad_lse,
                             grad_ent, logp, lse, ent, dl, ld_d, code, workspace, stream)
     _handed_over(logits, stream, logp, lse, ent, dl)
@@ -801,6 +823,8 @@ def _run_lmhead(desc, hidden, weight, targets, active_mask, workspace=None, stre
         lse = torch.empty(n, dtype=torch.float32, device=hidden.device)
         if workspace is None:
             workspace = _bytes_for(rlk_logp_fused_lmhead_workspace_bytes(desc), hidden.device)
+        else:
+            _check_workspace(workspace, hidden)
         rlk_logp_fused_lmhead(desc, hidden, weight, k, targets, _u8_mask(active_mask), logp, lse,
                               workspace, stream)
     _handed_over(hidden, stream, logp, lse)
@@ -838,6 +862,8 @@ def _run_lmhead_backward(desc, hidden, weight, targets, active_mask, lse, grad_l
         if workspace is None:
             workspace = _bytes_for(rlk_logp_fused_lmhead_bwd_workspace_bytes(
                 desc, k, want_hidden, want_weight), hidden.device)
+        else:
+            _check_workspace(workspace, hidden)
         rlk_logp_fused_lmhead_bwd(desc, hidden, weight, k, targets, _u8_mask(active_mask), lse,
                                   grad_logp, grad_lse, dh, dw, workspace, stream)
     _handed_over(hidden, stream, dh, dw)
@@ -1030,6 +1056,8 @@ def fused_lmhead_fp8(hidden, weight_q: torch.Tensor, weight_scale: torch.Tensor,
         nbytes = rlk_logp_fused_lmhead_fp8_workspace_bytes(desc)
         if nbytes == 0:
             raise ValueError(f"invalid rlk_logp_desc: {rlk_last_error_detail()}")
+        if workspace is not None:
+            _check_workspace(workspace, x)
         matrix, buffer = _fp8_operand(hidden, nbytes if workspace is None else 0, stream)
         if workspace is None:
             workspace = buffer
@@ -1217,6 +1245,8 @@ def _run_processed(desc, logits, targets, rules, active_mask, workspace=None, st
         lse = torch.empty(n, dtype=torch.float32, device=logits.device)
         if workspace is None:
             workspace = _bytes_for(rlk_logp_processed_workspace_bytes(desc), logits.device)
+        else:
+            _check_workspace(workspace, logits)
         rlk_logp_processed_fwd(desc, logits, rules.struct, targets, _u8_mask(active_mask), logp,
                                lse, workspace, stream)
     _handed_over(logits, stream, logp, lse)
@@ -1255,6 +1285,8 @@ def _run_processed_backward(desc, logits, targets, rules, active_mask, lse, grad
         dl = torch.empty((logits.shape[0], ld), dtype=out_dtype, device=logits.device)
         if workspace is None:
             workspace = _bytes_for(256, logits.device)
+        else:
+            _check_workspace(workspace, logits)
         rlk_logp_processed_bwd(desc, logits, rules.struct, targets, _u8_mask(active_mask), lse,
                                grad_logp, grad_lse, dl, ld, code, workspace, stream)
     _handed_over(logits, stream, dl)
@@ -1446,6 +1478,8 @@ def _run_linear_backward(x, weight, grad_out, saved, act, cap, want_x, want_weig
             if nbytes == 0:
                 raise ValueError(f"invalid rlk_linear_desc: {rlk_last_error_detail()}")
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+        else:
+            _check_workspace(workspace, x)
         rlk_linear_bwd(desc, x, weight, saved, grad_out, _row_stride(grad_out), dx, dw, db,
                        workspace, stream)
     _handed_over(x, stream, dx, dw, db)
