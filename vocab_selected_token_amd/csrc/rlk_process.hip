@@ -357,13 +357,14 @@ __device__ __forceinline__ void for_spans(const Part& part, int32_t real_vocab,
 }
 
 // exp(y - base) for many y of one base: exp2(y L - hi), L = log2 e, in one fma, which is exact
-// up to its one rounding; what hi took from base L goes into the factor, once.  A base too far
-// out for the product takes the difference first.
+// up to its one rounding; what hi took from base L goes into the factor, once.  Below 2^24 that
+// is at most 1, half a step of hi < 2^25; a base farther out, whose hi may be off by more than an
+// exponential holds, takes the difference first.
 struct ExpFrom {
   float base, hi, factor;
   bool near;
   __device__ __forceinline__ explicit ExpFrom(float b) : base(b) {
-    near = fabsf(b) < 1e30f;
+    near = fabsf(b) < 0x1p24f;
     hi = b * kLog2e;
     factor = near ? exp2_hw(-fmaf(b, kLog2e, -hi)) : 1.0f;
   }
