@@ -1404,6 +1404,9 @@ def _run_linear(x, weight, bias, residual, act, cap, out_dim, padded, save, stre
     ld, ld_saved = (padded + 7) // 8 * 8, (out_dim + 7) // 8 * 8
     with _call_on(x, stream):
         y = torch.empty((m, ld), dtype=torch.bfloat16, device=x.device)
+        if ld != padded:
+            # (not a view: torch refuses to change one in place that a function returns)
+            y.as_strided_((m, padded), (ld, 1))
         # (a bias in fp32 has a gradient in fp32, as exact as what is kept of z)
         exact = bias is not None and bias.dtype == torch.float32
         saved = torch.empty((m, ld_saved), dtype=torch.float32 if exact else torch.float16,
@@ -1414,7 +1417,7 @@ def _run_linear(x, weight, bias, residual, act, cap, out_dim, padded, save, stre
                                RLK_DTYPE_F32 if exact else RLK_DTYPE_F16, cap)
         rlk_linear_fwd(desc, x, weight, bias, residual, y, saved, stream)
     _handed_over(x, stream, y, saved)
-    return y if ld == padded else y[:, :padded], saved
+    return y, saved
 
 
 def linear_forward(x: torch.Tensor, weight: torch.Tensor, bias=None, residual=None, *,
