@@ -1080,6 +1080,9 @@ class LogitRules:
         x2 = x1 - frequency c - (presence if c > 0 else 0)
         y  = (x2 + bias_j) / temperature,  -inf where the grammar bars j
 
+    in this order (an engine that adds its bias or divides by its temperature first draws from
+    another distribution).
+
     Every rule may be absent.  repetition, presence, frequency, temperature: fp32 [N].
     history: int32 [H] tokens; row r's are history[history_begin[r]:history_end[r]] (int64 [N]
     each), of which those in front of history_split[r] are its prompt (none without it); rows may
@@ -1191,7 +1194,8 @@ def process_logits(logits: torch.Tensor, rules: LogitRules, *, real_vocab: int,
     """The processed logits [N, V_pad] (bf16 or fp32; rows padded to a multiple of 8 columns,
     columns [real_vocab, V_pad) -inf).  logits: bf16 [N, ld] with unit column stride.  With `out`
     they are written there, a tensor of out_dtype with at least V_pad columns, whose rows lie
-    beside those of the logits or are the logits themselves; what lies behind V_pad stays."""
+    beside those of the logits or are the logits themselves; what lies behind V_pad stays.  No
+    gradient: processed_selected_token_logprob has one."""
     if out_dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("out_dtype must be torch.float32 or torch.bfloat16")
     v_pad = _check_vocab(logits, real_vocab, padded_vocab)
@@ -1429,7 +1433,9 @@ def linear_forward(x: torch.Tensor, weight: torch.Tensor, bias=None, residual=No
     [N]; residual: bf16 [M, N] with unit column stride.  activation: none, relu, gelu, gelu_tanh,
     silu or softcap (cap tanh(z / cap)).  out's rows are padded to a multiple of 8 columns.  With
     `save`, saved is what linear_backward needs (z in fp16, or in fp32 with a bias in fp32; None
-    for no activation)."""
+    for no activation).  fp16 moves the activation's slope by 2^-11.6 at most, which shows beside
+    the rounding of dz to bf16 only where the slope is below 0.05.  No gradient: head_linear has
+    them."""
     act, cap = _check_activation(activation, cap)
     _check_logits(weight, "weight")
     n = weight.shape[0]
@@ -1531,7 +1537,8 @@ def head_linear(x: torch.Tensor, weight: torch.Tensor, bias=None, residual=None,
     the bias' in its dtype, the residual's is the upstream one).
 
     This is a prediction head's dense or residual block, in front of the LM-head.  The backward
-    keeps z in 16 bits (32 with a bias in fp32) and rounds dz to bf16 once.  Where a training step
+    keeps z in 16 bits (32 with a bias in fp32, which may be zeros; see linear_forward) and rounds
+    dz to bf16 once.  Where a training step
     is captured into a HIP graph, no eager autograd graph of the same leaves may be alive: torch
     ends the process."""
     act, cap = _check_activation(activation, cap)

@@ -10,10 +10,17 @@
 // linear_few streams the weight instead.
 //
 // What the backward pass needs of z (z / cap for the soft cap) is kept in fp16, for its 11 bits,
-// clamped to +-65504, where every activation here has reached its last slope: the rounding,
-// 2^-11 relative, moves act'(z) by a fraction of what rounding dz to bf16 does.  A bias in
-// fp32 has a gradient in fp32, which that rounding would show in (1e-4 relative): z is kept in
-// fp32 then.
+// clamped to +-65504, where every activation here has reached its last slope.  The rounding, 2^-11
+// relative, moves act'(z) by at most 2^-12 (the soft cap's by 2^-11.6): less than rounding dz to
+// bf16, 2^-8 of it, wherever |act'(z)| > 0.05.  Where the slope all but vanishes it is more: GELU's
+// moves by 0.7% of itself at z = -4 and 1.2% at -5 (by tanh 0.9 and 1.6), SiLU's by 0.4% at -10,
+// the soft cap's by 0.4% at |z / cap| = 4 and 0.8% at 8.  A bias in fp32 has a gradient in fp32,
+// which that rounding would show in (1e-4 relative): z is kept in fp32 then, and by the C call
+// wherever it is asked to.
+//
+// dz is rounded to bf16 for its two products, whose matrix instructions take operands of 16 bits
+// (those of fp32 operands have a small part of their rate); with the results' own rounding dx and
+// dW are off by 0.0023 of their size, where products of an fp32 dz would be off by 0.0017.
 //
 // Sums are fp32 in a fixed order: repeated calls give the same bits.  No atomics.
 #include <hip/hip_runtime.h>
@@ -54,7 +61,7 @@ __device__ __forceinline__ float sigmoid(float z) {
 __device__ __forceinline__ float bell(float z) { return exp2_hw(z * z * (-0.5f * kLog2e)); }
 // The normal distribution's Phi(z), bell = exp(-z^2 / 2): Phi(-a) = bell P(t), t = 1 / (1 + 0.3 a),
 // with P fitted to erfcx(a / sqrt 2) / 2 over 0 <= a <= 14 for the least relative error
-// (1.5e-7; behind, bell is 0).  Half the instructions of the library's erfcf, whose share of 1024
+// (1.7e-7; behind, bell is 0).  Half the instructions of the library's erfcf, whose share of 1024
 // tokens x 2048 x 151936 was a fifth (GELU 819 us, SiLU 648).
 __device__ __forceinline__ float normal_cdf(float z, float bell) {
   const float t = rcp_hw(fmaf(0.3f, fabsf(z), 1.0f));
@@ -217,11 +224,13 @@ __device__ __forceinline__ void put_out(const LinearArgs& a, int32_t m, int32_t 
 // ---------------------------------------------------------------------------
 // linear_tiles: 32 kVSn outputs x 16 kTok kWB tokens a block, by the tile product; then bias,
 // activation, residual and z's copy on a lane's 4 outputs, and whole rows out through LDS.
-// Bound by the matrix cores and by what stands beside them: a slab of the 256 x 256 tile takes
-// 1.45 us, which is 1.48 PFLOP/s, and a tile 12-20 us more for its first loads, its epilogue and
-// its stores, which nothing hides at one block a CU.  1024 x 2048 x 151936: 606 us without an
-// activation (1.05 PFLOP/s), 651 with the soft cap; 4096 x 4096 x 4096: 109 us (1.26), with a
-// bias, a residual, SiLU and z kept 117.
+// Bound by what stands beside the matrix cores, which are busy 41-44% of the time in the large
+// cases (8% at 777 x 1088 x 2501): a slab of the 256 x 256 tile takes 1.45 us, which is 1.48
+// PFLOP/s, and a tile 12-20 us more for its first loads, its epilogue and its stores, which
+// nothing hides at one block a CU; small tiles wait for their slabs.  In a row of calls 1024 x
+// 2048 x 151936 takes 606-625 us without an activation (1.02-1.05 PFLOP/s) and 651-661 with the soft cap, 4096 x
+// 4096 x 4096 109-111 us (1.24-1.26) and 117-123 with a bias, a residual, SiLU and z kept; single
+// calls under a trace 679-717 with the soft cap and 133-140 with everything.
 // ---------------------------------------------------------------------------
 template <int kVSn, int kTok, int kWB>
 struct Shape {
@@ -456,7 +465,7 @@ __device__ __forceinline__ void finish4(const LinearArgs& a, int32_t m, int32_t 
 // 16 outputs; its four waves take every fourth slab of 64 of the sum each, operands
 // straight from memory to registers, kDepth slabs ahead, and meet only at the end, where the
 // four sums are added in order.  What the epilogue adds is fetched first.  One token x 4096 x
-// 4096 with bias and residual: 8.0 us (4.2 TB/s, of which the launch's start and end take a
+// 4096 with bias and residual: 8.0-8.2 us (4.1 TB/s, of which the launch's start and end take a
 // third; fetched last, 8.8).
 // ---------------------------------------------------------------------------
 constexpr int kFewWaves = 4;
@@ -564,8 +573,9 @@ __global__ __launch_bounds__(kStreamThreads) void linear_stream(LinearArgs a, in
 // of 64, and what 64 tokens add to db.  A block takes 64 tokens x 128 outputs, a thread 4 tokens
 // x 8 outputs, whose loads go out together.  The blocks behind copy x's and W's last rows, those
 // behind the last whole 64, followed by zeros: the slabs of dW's and dx's sums that they do not
-// fill.  Bound by its bytes: 4096 x 4096 23 us (4.4 TB/s); 777 x 2501 11 us, mostly a launch's own
-// time (rows that are not 16-byte aligned are read by whole vectors at their elements' addresses).
+// fill.  Bound by its bytes: 4096 x 4096 23-24 us (4.2-4.4 TB/s); 777 x 2501 with z in fp32 11 us,
+// of which the smallest launch's 5.4 are one half and 3 would do for the bytes (rows that are
+// not 16-byte aligned are read by whole vectors at their elements' addresses).
 // ---------------------------------------------------------------------------
 constexpr int kDzRows = 64, kDzCols = 128;
 
@@ -662,9 +672,10 @@ __global__ __launch_bounds__(256) void linear_dz(LinearBwdArgs a, TailArgs t, in
 
 // ---------------------------------------------------------------------------
 // linear_grads: dx, dW and db in one launch, so that the last blocks of one fill the chip
-// beside the next (4096 x 4096 x 4096: 205-215 us, 1.28-1.34 PFLOP/s; the library's two products
-// 247).  Blocks [0, n_dx) are dx's (A = W by its rows, the sum's index; B = dz: C[in]
-// [token]), the next n_dw dW's (A = x and B = dz by their rows: C[in][out]), the rest db's.
+// beside the next (4096 x 4096 x 4096: 205-215 us in a row of calls, 1.28-1.34 PFLOP/s, and 219-226
+// in single ones; the library's two products 247).  Blocks [0, n_dx) are dx's (A = W by its rows,
+// the sum's index; B = dz: C[in][token]), the next n_dw dW's (A = x and B = dz by their rows:
+// C[in][out]), the rest db's.
 // ---------------------------------------------------------------------------
 template <int kVSn, int kTok, int kWB>
 __global__ __launch_bounds__((Shape<kVSn, kTok, kWB>::kThr), 2) void linear_grads(

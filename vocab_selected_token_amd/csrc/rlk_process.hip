@@ -23,13 +23,13 @@
 // are worked on; where none of a wave's 512 columns is counted the penalties are skipped.
 //
 // What bounds it: arithmetic and the chain of a span, not yet memory alone.  The statistics of 4096
-// rows x 151936 with 2048 tokens of history each take 431 us (2.9 TB/s; the vector units are busy
-// 65% of it, with 17 instructions a column, half of them for penalties: nearly every 512
-// columns hold some token), the gradient 555 us (4.5 TB/s); with short histories, 1024 rows, 83 and
-// 110 us (3.7 and 5.7 TB/s); 512 rows processed 75 us (4.2 TB/s).  The logits are read through
-// buffers, whose bounds stand in for a test of every load, and a span's are on their way while
-// the one before is worked on (with 64-bit addresses, tests and shuffles through LDS the statistics
-// took 625 us).
+// rows x 151936 with 2048 tokens of history each take 422-436 us (2.9 TB/s; the vector units are
+// busy 68% of it, with 17 instructions a column, half of them for penalties: nearly every 512
+// columns hold some token), the gradient 544-557 us (4.5 TB/s); with short histories, 1024 rows,
+// 85-95 and 109-112 us (3.3-3.7 and 5.6 TB/s); 512 rows processed 73-75 us (4.3 TB/s).  The logits
+// are read through buffers, whose bounds stand in for a test of every load, and a span's are on
+// their way while the one before is worked on (with 64-bit addresses, tests and shuffles through
+// LDS the statistics took 625 us).
 //
 // Sums are fp32 within a piece and fp64 over the pieces, in a fixed order; a row's results
 // do not depend on what other rows share the call.  No atomics on results.
