@@ -1094,7 +1094,7 @@ class LogitRules:
     The tensors are checked here, once, and have to stay as they are made: contents may change
     between calls.  They are constants: no gradient reaches them."""
 
-    __slots__ = ("tensors", "rows", "device", "struct", "bias_columns", "allow_words")
+    __slots__ = ("tensors", "names", "rows", "device", "struct", "bias_columns", "allow_words")
 
     def __init__(self, *, repetition=None, presence=None, frequency=None, temperature=None,
                  history=None, history_begin=None, history_split=None, history_end=None,
@@ -1110,7 +1110,7 @@ class LogitRules:
             raise TypeError("allow_index needs allow")
         f32, i32, i64 = torch.float32, torch.int32, torch.int64
         rows = where = None
-        kept, ptrs = [], []
+        kept, names, ptrs = [], [], []
         for name, t, dtype in (("repetition", repetition, f32), ("presence", presence, f32),
                                ("frequency", frequency, f32), ("temperature", temperature, f32),
                                ("history", history, i32), ("history_begin", history_begin, i64),
@@ -1136,6 +1136,7 @@ class LogitRules:
             elif t.get_device() != where:
                 raise ValueError(f"{name} is on {t.device}, another rule on {kept[0].device}")
             kept.append(t)
+            names.append(name)
             ptrs.append(t.data_ptr())
         tables = []
         for name, t, dtype, index in (("bias", bias, f32, bias_index),
@@ -1163,10 +1164,11 @@ class LogitRules:
             elif t.get_device() != where:
                 raise ValueError(f"{name} is on {t.device}, another rule on {kept[0].device}")
             kept.append(t)
+            names.append(name)
             tables.append((t.data_ptr(), n, ld, width))
         (bias_ptr, bias_rows, ld_bias, self.bias_columns), \
             (allow_ptr, allow_rows, ld_allow, self.allow_words) = tables
-        self.tensors, self.rows = tuple(kept), rows
+        self.tensors, self.names, self.rows = tuple(kept), tuple(names), rows
         self.device = kept[0].device if kept else None
         self.struct = rlk_logit_rules(
             *ptrs[:5], 0 if history is None else history.numel(), *ptrs[5:8], bias_ptr, bias_rows,
@@ -1322,9 +1324,20 @@ class _ProcessedSelectedTokenLogprob(torch.autograd.Function):
 
         def vec(t):
             return None if t is None else t.contiguous().float()
-        logits, targets, active_mask, lse = ctx.saved_tensors[:4]
-        d = _run_processed_backward(ctx.desc, logits, targets, ctx.rules, active_mask, lse,
-                                    vec(g_logp), vec(g_lse), logits.dtype)
+        logits, targets, active_mask, lse, *of_rules = ctx.saved_tensors
+        desc, rules = ctx.desc, ctx.rules
+        # Hooks on saved tensors hand back others (copies from host memory, for instance), in
+        # any layout, and the rules as they were: checked as the call's own were.
+        if logits.stride() != (desc.ld_logits, 1) or \
+                any(a is not b for a, b in zip(of_rules, rules.tensors)):
+            rules = LogitRules(**{k: t.contiguous() for k, t in zip(rules.names, of_rules)})
+            if logits.stride() != (desc.ld_logits, 1):
+                wide = logits.new_empty((logits.shape[0], desc.ld_logits))
+                logits = wide[:, :logits.shape[1]].copy_(logits)
+            _check_inputs(logits, targets, active_mask, lse=lse)
+            _check_rules(rules, logits, desc.real_vocab)
+        d = _run_processed_backward(desc, logits, targets, rules, active_mask, lse, vec(g_logp),
+                                    vec(g_lse), logits.dtype)
         return d, None, None, None, None, None, None
 
 
@@ -1522,7 +1535,8 @@ class _HeadLinear(torch.autograd.Function):
         want_x, want_weight, want_bias, want_residual = ctx.needs_input_grad[:4]
         dx = dw = db = None
         if want_x or want_weight or want_bias:
-            x, weight, saved = ctx.saved_tensors
+            # (hooks on saved tensors may hand back another layout)
+            x, weight, saved = (None if t is None else t.contiguous() for t in ctx.saved_tensors)
             if grad.stride(1) != 1 or grad.stride(0) < grad.shape[1]:
                 grad = grad.contiguous()
             dx, dw, db = _run_linear_backward(x, weight, grad, saved, act, cap, want_x,
