@@ -58,6 +58,20 @@ def test_products_are_given_contiguous_tensors(copy, streams, monkeypatch):  # n
     assert len(tensors) > 3 and all(t.is_contiguous() for t in tensors[:3])
 
 
+@pytest.mark.parametrize("copy", COPIES)
+def test_the_lmhead_is_given_contiguous_tensors(copy, streams, monkeypatch):  # noqa: F811
+    calls = []
+    monkeypatch.setattr(rlk, "rlk_logp_fused_lmhead_bwd", lambda *a: calls.append(a))
+    x = torch.zeros(N, K, **BF16).requires_grad_()
+    w = torch.zeros(512, K, **BF16).requires_grad_()
+    with saved_tensors_hooks(COPIES[copy], lambda t: t):
+        logp, _ = rlk.lmhead_selected_token_logprob(x, w, torch.zeros(N, dtype=torch.int32),
+                                                    real_vocab=500, num_vocab_tiles=2)
+    torch.autograd.grad(logp.sum(), (x, w))
+    (_, hidden, weight, *_), = calls
+    assert hidden.is_contiguous() and weight.is_contiguous()
+
+
 def bits(t):
     return t.contiguous().view(torch.int16 if t.element_size() == 2 else torch.int32)
 

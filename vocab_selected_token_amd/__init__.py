@@ -900,7 +900,9 @@ class _LmheadSelectedTokenLogprob(torch.autograd.Function):
 
         def vec(t):
             return None if t is None else t.contiguous().float()
-        hidden, weight, targets, active_mask, lse = ctx.saved_tensors
+        # (hooks on saved tensors may hand back another layout)
+        hidden, weight, targets, active_mask, lse = (
+            None if t is None else t.contiguous() for t in ctx.saved_tensors)
         dh, dw = _run_lmhead_backward(ctx.desc, hidden, weight, targets, active_mask, lse,
                                       vec(g_logp), vec(g_lse), want_hidden, want_weight)
         return dh, dw, None, None, None, None, None, None
